@@ -14,6 +14,9 @@ import os
 import numpy as np
 
 from . import build as _build
+from .paged import (BAD_PAGE, BAD_SEQUENCE, NO_PAGE, BeamPlan, PagedBatch, PagedCache, PagePlan,  # noqa: F401
+                    host_log_sum, paged_attention, paged_attention_work, paged_store)
+from .paged import SIGNATURES as _PAGED_SIGNATURES
 
 CK_FLAG_STOP_TOKENS = 1
 PATH_AUTO, PATH_STEP, PATH_KERNELS = 0, 1, 2
@@ -87,6 +90,7 @@ def lib() -> ctypes.CDLL:
             "ck_host_probability": ([u64, u64], u64),
             "ck_version": ([], ctypes.c_char_p),
         }
+        sig.update(_PAGED_SIGNATURES)
         for name, (args, res) in sig.items():
             f = getattr(L, name)
             f.argtypes = args

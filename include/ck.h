@@ -342,6 +342,138 @@ int ck_state_upload(void* dev_state, const void* host, size_t len, void* stream)
 int ck_matrow(const uint8_t* dev_W, size_t pitch, const uint32_t* dev_scale, uint32_t rows,
               uint32_t cols, const int64_t* dev_x, int64_t* dev_y, void* stream);
 
+/* ---------------------------------------------------------------- a cache in pages
+ * Runs that are served together can keep their keys and values in one pool of pages instead
+ * of one state each: a page holds `page` positions, a sequence lists its pages in a table,
+ * and sequences with a common beginning share its pages.  The words are the cache's ("The
+ * attention cache": int32, 16 fraction bits, every store checked).  The calls below are
+ * single operators, like ck_matrow: device pointers, no allocation, no synchronisation, and
+ * they may be captured into a CUDA graph.  dev_work buffers are scratch (256-byte aligned,
+ * the size from the *_work function); calls that share one must not overlap on the GPU.
+ *
+ * A pool is i32 [pages][layers][kv_heads][page][head_dim], one for keys and one for values,
+ * 16-byte aligned.  Limits: head_dim a power of two from 4 to 128; page a power of two from 8
+ * to 256; layers <= 4095; kv_heads <= 4096; pages <= 2^24; a sequence of at most 2^20 - 1
+ * positions. */
+typedef struct ck_paged_cache {
+  int32_t* dev_k;
+  int32_t* dev_v;
+  uint32_t pages, layers, kv_heads, page, head_dim;
+} ck_paged_cache;
+
+#define CK_NO_PAGE 0xFFFFFFFFu /* a table entry without a page; a parent of no row */
+
+/* New tokens of several sequences.  Sequence s owns rows dev_start[s] .. dev_start[s+1] - 1
+ * (ascending, dev_start[0] .. dev_start[seqs], none above `rows`); its cache holds dev_len[s]
+ * positions, those of its new rows included, so that the last row is at position dev_len[s]
+ * - 1.  A row whose position would be negative holds nothing: no store, zero attention.  Rows
+ * that no sequence owns are left as they were.  dev_table: u32 [seqs][stride], the pages of
+ * each sequence in order.  max_new and max_len bound the sequences' new rows and lengths (the
+ * launch is sized by them, the arrays are read on the device); a sequence beyond them, or
+ * longer than stride * page, is skipped.
+ * dev_status: u64 [seqs], set to all ones by the caller; each sequence's first failure lowers
+ * it to position << 44 | layer << 32 | phase << 24 | element (as a state's first error key),
+ * with phase 6, 7 or 8 for a word that does not fit 32 bits (the wrapped word is stored), 2
+ * for a table entry outside the pool (it is not written, and reads as zeros) and 1 for a
+ * sequence that is skipped. */
+typedef struct ck_paged_batch {
+  const uint32_t* dev_start;
+  const uint32_t* dev_len;
+  const uint32_t* dev_table;
+  uint64_t* dev_status;
+  uint32_t seqs, rows, stride, max_new, max_len;
+} ck_paged_batch;
+
+#define CK_PAGED_BAD_SEQUENCE 1u
+#define CK_PAGED_BAD_PAGE 2u
+
+/* Phases 6 to 8 of every new row ("The forward pass, in order"): queries and keys are rotated
+ * by the row's position, the checked keys and values go into their sequence's pages of
+ * `layer`, the rotated queries to dev_q_out.  dev_q, dev_k, dev_v: i64 rows of heads *
+ * head_dim and kv_heads * head_dim words, `stride` words from row to row (so the three parts
+ * of a stacked matrix row can be given), 16-byte aligned with even strides; dev_q_out i64
+ * [rows][heads * head_dim], which may not overlap the inputs.  The first `rot` elements of
+ * each head are rotated (a multiple of 4 up to head_dim, 0 for none): pairs (2j, 2j + 1), or
+ * (j, j + rot / 2) with `half` set.  dev_rope: i32 [rope_rows][rot / 2][2] (cos, sin) with 24
+ * fraction bits; a scaled or lengthened context is a table of scaled angles.  A position past
+ * the table skips its row (phase 1).  Errors: 9, 10. */
+int ck_paged_store(const ck_paged_cache* cache, uint32_t layer, const ck_paged_batch* batch,
+                   const int64_t* dev_q, size_t q_stride, const int64_t* dev_k, size_t k_stride,
+                   const int64_t* dev_v, size_t v_stride, uint32_t heads, const int32_t* dev_rope,
+                   uint32_t rope_rows, uint32_t rot, int half, int64_t* dev_q_out, void* stream);
+
+/* Phase 9 ("Attention, stage by stage") of every new row over its sequence's pages of
+ * `layer`, positions 0 up to its own: dev_q the rotated queries i64 [rows][heads * head_dim]
+ * (q_stride words from row to row), dev_out i64 [rows][heads * head_dim], both 16-byte
+ * aligned; heads a multiple of kv_heads, head h reading key head h / (heads / kv_heads).
+ * dev_exp: the exponential table u32 [4097], entry 0 = 2^30 and none larger; inv_sqrt: one
+ * over the square root of the head size, 24 fraction bits.  Errors: 4 (work_len), 9, 10. */
+int ck_paged_attention_work(const ck_paged_cache* cache, const ck_paged_batch* batch, uint32_t heads,
+                            size_t* out);
+int ck_paged_attention(const ck_paged_cache* cache, uint32_t layer, const ck_paged_batch* batch,
+                       const int64_t* dev_q, size_t q_stride, uint32_t heads, const uint32_t* dev_exp,
+                       uint32_t inv_sqrt, int64_t* dev_out, void* dev_work, size_t work_len, void* stream);
+
+/* Reorders, forks, frees and grows sequences.  Output row r takes over the sequence of input
+ * row dev_parent[r] (CK_NO_PAGE: the row is empty), dev_len_in positions long, and receives
+ * pages for dev_grow[r] more; several rows may name one parent, and an input row that none
+ * names gives its pages back.  Whole pages are shared.  A part-filled page, where the next
+ * position goes, belongs to one sequence: it stays with the lowest output row that holds it
+ * (with none if another row holds it whole), and every other row gets a page of its own with
+ * the filled positions of all layers copied.  Free are the pages in no output row and not
+ * marked in dev_held (u8 [pages], nonzero: held by others; may be null); they are handed out
+ * in ascending order, row after row.  The call keeps no counts: the tables say what is in use.
+ * Outputs: dev_table_out u32 [rows][stride] (CK_NO_PAGE behind a row's pages), dev_len_out u32
+ * [rows] (the length grown), dev_status u32 [rows]: 0, or the row is empty: 3 (a parent
+ * outside the input rows, a table entry outside the pool), 7 (longer than stride * page), 4
+ * (the free pages ran out before this row: its request and those of the rows before it exceed
+ * them).  The outputs may not overlap the inputs.  Limits: rows_in, rows <= 65536, stride <=
+ * 2^17.  Errors: 4 (work_len), 9, 10. */
+int ck_pages_work(const ck_paged_cache* cache, uint32_t rows, uint32_t stride, size_t* out);
+int ck_pages_fork(const ck_paged_cache* cache, uint32_t rows_in, const uint32_t* dev_len_in,
+                  const uint32_t* dev_table_in, uint32_t rows, const uint32_t* dev_parent,
+                  const uint32_t* dev_grow, uint32_t stride, const uint8_t* dev_held,
+                  uint32_t* dev_len_out, uint32_t* dev_table_out, uint32_t* dev_status, void* dev_work,
+                  size_t work_len, void* stream);
+
+/* Packs a pool: the pages of the rows (ceil(dev_len / page) of each) move to the lowest page
+ * numbers, those already there stay, and the others fill the holes in ascending order.  Every
+ * live row of the pool must be given.  dev_table_out u32 [rows][stride]; *dev_used the number
+ * of pages in use; dev_status u32 [rows] as above (3, 7: the row's table comes out empty and
+ * its pages count as free).  Errors: 4 (work_len), 9, 10. */
+int ck_pages_compact(const ck_paged_cache* cache, uint32_t rows, const uint32_t* dev_len,
+                     const uint32_t* dev_table_in, uint32_t stride, uint32_t* dev_table_out,
+                     uint32_t* dev_used, uint32_t* dev_status, void* dev_work, size_t work_len,
+                     void* stream);
+
+/* ---------------------------------------------------------------- beam search
+ * One step of `groups` searches of `beams` beams each: of every search's beams times the
+ * vocabulary, the `beams` continuations of the highest score, in descending order, equal ones
+ * in the order of (beam, token).  dev_logits i64 [groups * beams][logits_stride] (the first
+ * `vocab` used), dev_scores i64 the beams' sums of log-probabilities (16 fraction bits).  A
+ * continuation's score is its beam's minus (D + lnZ), D = min(m - logit, 2^62) below the
+ * beam's largest logit m and lnZ the logarithm of the sum of the table's exponentials
+ * EXP[min(D >> 8, 4096)] over the vocabulary ("Sampling", temperature one): with Z' = max(Z,
+ * 2^30), n = floor(log2 Z') - 30, y = Z' >> n, t = ((y - 2^30) << 30) / (y + 2^30), T = (t * t)
+ * >> 30, c_7 = a_7, c_i = a_i + ((c_(i+1) * T) >> 30), a_i = round(2^30 / (2 i + 1)):
+ *   lnZ = (n * 744261118 + 2 * ((t * c_0) >> 30) + 2^13) >> 14.
+ * A beam with a nonzero dev_done has ended: it is one candidate with its own score, behind its
+ * own vocabulary, and carries on with done_token.  A beam whose score is not within (-2^61,
+ * 2^61) is dead and gives none.  Outputs, per search in order: dev_scores_out, dev_parent
+ * (the row the continuation extends, 0 .. groups * beams - 1, as ck_pages_fork takes it),
+ * dev_token, dev_done_out (ended before, or, with CK_FLAG_STOP_TOKENS in flags, its token is
+ * 1 or 2).  Where a search has fewer candidates: the lowest int64, CK_NO_PAGE, done_token, 0.
+ * The outputs may not overlap the inputs.  Limits: beams 1 to 64, vocab 1 to 2^20, groups *
+ * beams <= 65536, done_token < vocab.  Errors: 4 (work_len), 9, 10. */
+int ck_beam_work(uint32_t groups, uint32_t beams, uint32_t vocab, size_t* out);
+int ck_beam_select(const int64_t* dev_logits, size_t logits_stride, uint32_t groups, uint32_t beams,
+                   uint32_t vocab, const int64_t* dev_scores, const uint8_t* dev_done,
+                   const uint32_t* dev_exp, uint32_t flags, uint32_t done_token, int64_t* dev_scores_out,
+                   uint32_t* dev_parent, uint32_t* dev_token, uint8_t* dev_done_out, void* dev_work,
+                   size_t work_len, void* stream);
+/* A host build of lnZ above, for tests without a GPU. */
+int64_t ck_host_log_sum(uint64_t z);
+
 /* ---------------------------------------------------------------- host-side checks
  * Host builds of device routines, for tests without a GPU: floor square root of a u64,
  * and truncating signed division of n by d (1 <= d < 2^32) through the precomputed

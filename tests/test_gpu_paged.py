@@ -1,0 +1,546 @@
+"""The paged cache's operators and beam search on the GPU against plain integer implementations
+(the CPU oracle's steps and Python's integers).  All of it is integer work: tolerance 0."""
+import numpy as np
+import pytest
+
+import oracle
+import synth
+
+pytestmark = pytest.mark.gpu
+
+MIN = -2**63
+EXP = synth.exp_table()
+
+
+@pytest.fixture(scope="module")
+def ck():
+    import torch
+    import fixed_point_int8_gb300 as ck
+    from fixed_point_int8_gb300 import build
+    build.build()
+    torch.cuda.init()
+    return ck
+
+
+def cuda(a):
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+class Setup:
+    """A pool of random words, tables of scattered pages, and a batch's new rows."""
+
+    def __init__(self, ck, lens, news, heads, kv_heads, hd, page, layers=2, seed=0, lead=0, tail=0, spare=3,
+                 spread=2.0, max_len=None):
+        import torch
+        self.rng = rng = np.random.default_rng(seed)
+        self.lens, self.news, self.heads, self.kv, self.hd, self.page = lens, news, heads, kv_heads, hd, page
+        n_pages = [-(-n // page) for n in lens]
+        stride = max(n_pages) + 1
+        ids = rng.permutation(sum(n_pages) + spare)
+        self.table = np.full((len(lens), stride), -1, np.int32)
+        at = 0
+        for i, n in enumerate(n_pages):
+            self.table[i, :n] = ids[at:at + n]
+            at += n
+        self.pages = len(ids)
+        shape = (self.pages, layers, kv_heads, page, hd)
+        self.k = (rng.standard_normal(shape) * spread * 65536).astype(np.int32)
+        self.v = (rng.standard_normal(shape) * spread * 65536).astype(np.int32)
+        self.starts = (np.cumsum([0] + list(news)) + lead).astype(np.int32)
+        self.rows = int(self.starts[-1]) + tail
+        self.cache = ck.PagedCache(cuda(self.k), cuda(self.v))
+        self.batch = ck.PagedBatch(cuda(self.table), cuda(np.array(lens, np.int32)), cuda(self.starts), None,
+                                   self.rows, max(max(news), 1), max_len or max(max(lens), 1))
+
+    def words(self, pool, layer, s, kvh, n):
+        """Positions 0 .. n-1 of sequence s as [n][hd]."""
+        t = np.arange(n)
+        return pool[self.table[s, t // self.page], layer, kvh, t % self.page]
+
+    def attention(self, layer, q, inv, exp=EXP, fill=0):
+        out = np.full((self.rows, self.heads * self.hd), fill, np.int64)
+        for s, (n, length) in enumerate(zip(self.news, self.lens)):
+            for j in range(n):
+                row, pos = self.starts[s] + j, length - n + j
+                for h in range(self.heads):
+                    kvh, c = h // (self.heads // self.kv), slice(h * self.hd, (h + 1) * self.hd)
+                    if pos < 0:
+                        out[row, c] = 0
+                        continue
+                    out[row, c] = plain_attention(q[row, c], self.words(self.k, layer, s, kvh, pos + 1),
+                                                  self.words(self.v, layer, s, kvh, pos + 1), inv, exp)
+        return out
+
+
+def plain_attention(q, K, V, inv, exp=EXP):
+    """One head of one row with wrapping 64-bit words."""
+    with np.errstate(over="ignore"):
+        K, V = K.astype(np.int64), V.astype(np.int64)
+        s = (((K * q[None, :]).sum(-1) >> 16) * np.int64(inv)) >> 24
+        d = (np.uint64(int(s.max()) & (2**64 - 1)) - s.view(np.uint64)) >> np.uint64(8)
+        e = exp[np.minimum(d, np.uint64(4096)).astype(np.int64)].astype(np.int64)
+        p = (e << 24) // int(e.sum())
+        return (p[:, None] * V).sum(0) >> 24
+
+
+def test_plain_attention_is_the_oracles():
+    rng = np.random.default_rng(3)
+    for n, hd, spread in ((1, 4, 1), (37, 64, 65536), (5, 128, 2**31 - 1)):
+        q = rng.integers(-2**20, 2**20, hd)
+        K, V = (rng.integers(-spread, spread + 1, (n, hd)).astype(np.int32) for _ in range(2))
+        want = oracle.attention_head(q, K, V, synth.inv_sqrt_head(hd), EXP)
+        want = want[0] if isinstance(want, tuple) else want
+        assert np.array_equal(plain_attention(q, K, V, synth.inv_sqrt_head(hd)), want)
+
+
+# ---------------------------------------------------------------- attention
+
+# lens, news, heads, kv heads, head, page: single tokens and chunks, one position, tables that end
+# inside a page, shared key heads, a sequence without new rows, one with more rows than positions
+ATTENTION = [
+    ([1], [1], 1, 1, 4, 8),
+    ([33], [1], 8, 4, 8, 16),
+    ([1, 2, 15, 16, 17, 100], [1] * 6, 4, 4, 16, 16),
+    ([257, 64], [1, 1], 8, 2, 64, 32),
+    ([300], [1], 3, 3, 128, 256),
+    ([1025], [1], 32, 32, 64, 64),
+    ([2500], [1], 4, 1, 128, 16),
+    ([0, 5, 9], [1, 0, 2], 2, 2, 32, 8),
+    ([3], [5], 2, 1, 8, 8),
+    ([130, 67], [130, 3], 4, 2, 64, 16),
+    ([200], [200], 2, 2, 128, 32),
+    ([77, 300, 12], [20, 129, 12], 4, 4, 32, 64),
+    ([513], [65], 8, 1, 64, 64),
+    ([700], [40], 6, 2, 16, 8),
+    ([260], [129], 2, 2, 4, 16),
+]
+
+
+@pytest.mark.parametrize("lens,news,heads,kv,hd,page", ATTENTION)
+def test_attention_against_the_plain_form(ck, lens, news, heads, kv, hd, page):
+    s = Setup(ck, lens, news, heads, kv, hd, page, seed=hd + len(lens))
+    q = (s.rng.standard_normal((s.rows, heads * hd)) * 65536).astype(np.int64)
+    inv = synth.inv_sqrt_head(hd)
+    for layer in (0, 1):
+        rc, out = ck.paged_attention(s.cache, layer, s.batch, cuda(q), cuda(EXP.view(np.int32)), inv)
+        assert rc == 0
+        assert np.array_equal(out.cpu().numpy(), s.attention(layer, q, inv))
+    assert s.batch.errors() == [None] * len(lens)
+
+
+@pytest.mark.parametrize("new", [1, 70])
+@pytest.mark.parametrize("q_spread,kv_spread", [(2**62, 65536), (65536, 2**31 - 1), (2**31, 2**31 - 1),
+                                                (2**22, 2**23), (2**23 + 5, 2**23 + 5), (1, 1), (0, 65536)])
+def test_attention_over_the_whole_range_of_values(ck, new, q_spread, kv_spread):
+    """Queries to 63 bits and cached words to 32, wrapping products among them."""
+    s = Setup(ck, [150], [new], 4, 2, 64, 16, seed=1)
+    s.k[:] = s.rng.integers(-kv_spread - 1, kv_spread + 1, s.k.shape)
+    s.v[:] = s.rng.integers(-kv_spread - 1, kv_spread + 1, s.v.shape)
+    s.cache.k.copy_(cuda(s.k))
+    s.cache.v.copy_(cuda(s.v))
+    q = s.rng.integers(-q_spread, q_spread + 1, (s.rows, 256))
+    inv = synth.inv_sqrt_head(64)
+    rc, out = ck.paged_attention(s.cache, 1, s.batch, cuda(q), cuda(EXP.view(np.int32)), inv)
+    assert rc == 0
+    assert np.array_equal(out.cpu().numpy(), s.attention(1, q, inv))
+
+
+@pytest.mark.parametrize("new", [1, 130])
+def test_attention_with_equal_and_with_single_scores(ck, new):
+    """Every score the same, and one score far above all others (its probability is 2^24)."""
+    s = Setup(ck, [200], [new], 2, 2, 64, 16, seed=2)
+    inv = synth.inv_sqrt_head(64)
+    exp = EXP.copy()
+    exp[4096] = 0
+    for kind in ("equal", "single"):
+        s.k[:] = 0
+        if kind == "single":
+            s.k[s.table[0, 0], :, :, 3] = 1 << 20
+        s.cache.k.copy_(cuda(s.k))
+        q = np.full((s.rows, 128), 1 << 18, np.int64)
+        rc, out = ck.paged_attention(s.cache, 0, s.batch, cuda(q), cuda(exp.view(np.int32)), inv)
+        assert rc == 0
+        assert np.array_equal(out.cpu().numpy(), s.attention(0, q, inv, exp))
+
+
+def test_attention_leaves_rows_of_no_sequence_and_strided_queries(ck):
+    """Rows before the first sequence and behind the last stay as they were; queries are a
+    column range of wider rows."""
+    import torch
+    s = Setup(ck, [40, 90], [2, 3], 4, 2, 32, 8, lead=2, tail=3)
+    wide = (s.rng.standard_normal((s.rows, 300)) * 65536).astype(np.int64)
+    q = cuda(wide)[:, 64:192]
+    out = torch.full((s.rows, 128), 7, dtype=torch.int64, device="cuda")
+    rc, got = ck.paged_attention(s.cache, 0, s.batch, q, cuda(EXP.view(np.int32)), 1 << 21, out=out)
+    assert rc == 0 and got is out
+    assert np.array_equal(out.cpu().numpy(), s.attention(0, wide[:, 64:192], 1 << 21, fill=7))
+
+
+# ---------------------------------------------------------------- stores
+
+def plain_store(s, layer, q, k, v, rope, half):
+    """Rotated queries, pools and first failures."""
+    rot, hd = 2 * rope.shape[1], s.hd
+    pairs = [(j, j + rot // 2) if half else (2 * j, 2 * j + 1) for j in range(rot // 2)]
+    qo, pk, pv = np.zeros_like(q), s.k.copy(), s.v.copy()
+    status = [None] * len(s.lens)
+
+    def turn(x, pos):
+        y = [int(w) for w in x]
+        for j, (a, b) in enumerate(pairs):
+            y[a], y[b] = oracle.rotate(int(x[a]), int(x[b]), int(rope[pos, j, 0]), int(rope[pos, j, 1]))
+        return y
+
+    def i32(w):
+        return (w + 2**31) % 2**32 - 2**31
+
+    for i, (n, length) in enumerate(zip(s.news, s.lens)):
+        for j in range(n):
+            row, pos = s.starts[i] + j, length - n + j
+            if pos < 0:
+                continue
+            fails = []
+            for h in range(s.heads):
+                qo[row, h * hd:(h + 1) * hd] = turn(q[row, h * hd:(h + 1) * hd], pos)
+            for h in range(s.kv):
+                raw = [int(w) for w in k[row, h * hd:(h + 1) * hd]]
+                fails += [(pos, layer, 6, h * hd + e) for e, w in enumerate(raw) if i32(w) != w]
+                fails += [(pos, layer, 7, h * hd + e) for e, w in enumerate(v[row, h * hd:(h + 1) * hd])
+                          if i32(int(w)) != w]
+                turned = turn([i32(w) for w in raw], pos)
+                fails += [(pos, layer, 8, h * hd + e) for e, w in enumerate(turned) if i32(w) != w]
+                at = s.table[i, pos // s.page], layer, h, pos % s.page
+                pk[at] = [i32(w) for w in turned]
+                pv[at] = [i32(int(w)) for w in v[row, h * hd:(h + 1) * hd]]
+            if fails:
+                status[i] = min(fails + ([status[i]] if status[i] else []))
+    return qo, pk, pv, status
+
+
+def rope_of(positions, rot, base=10000.0, stretch=1.0, magnitude=1.0):
+    """Angles of positions divided by `stretch`, cosine and sine times a magnitude."""
+    angle = np.arange(positions)[:, None] / stretch * base**(-np.arange(0, rot, 2) / max(rot, 1))
+    return np.rint(np.stack((np.cos(angle), np.sin(angle)), -1) * magnitude * 2**24).astype(np.int32)
+
+
+STORE = [
+    ([1], [1], 1, 1, 4, 8, 4, False, {}),
+    ([133], [1], 32, 32, 128, 16, 128, False, {}),
+    ([50, 7, 31], [50, 0, 9], 8, 4, 8, 16, 8, True, {}),
+    ([40, 64], [33, 64], 6, 2, 64, 32, 32, True, {}),
+    ([40, 64], [33, 64], 6, 2, 64, 32, 48, False, {"stretch": 4.0, "magnitude": 1.1386}),
+    ([17], [17], 4, 1, 16, 8, 0, False, {}),
+    ([3, 9], [5, 2], 2, 2, 32, 8, 32, True, {"base": 500000.0}),
+]
+
+
+@pytest.mark.parametrize("lens,news,heads,kv,hd,page,rot,half,scaled", STORE)
+def test_store_against_the_plain_form(ck, lens, news, heads, kv, hd, page, rot, half, scaled):
+    s = Setup(ck, lens, news, heads, kv, hd, page, seed=rot, lead=1, tail=2)
+    cols = (heads + 2 * kv) * hd
+    qkv = (s.rng.standard_normal((s.rows, cols)) * 65536).astype(np.int64)
+    rope = rope_of(max(lens), rot, **scaled)
+    parts = np.split(qkv, [heads * hd, (heads + kv) * hd], axis=1)
+    import torch
+    out = torch.zeros(s.rows, heads * hd, dtype=torch.int64, device="cuda")
+    dev = cuda(qkv).split((heads * hd, kv * hd, kv * hd), -1)
+    rc, q = ck.paged_store(s.cache, 1, s.batch, *dev, cuda(rope), half=half, out=out)
+    assert rc == 0
+    qo, pk, pv, status = plain_store(s, 1, *parts, rope, half)
+    assert np.array_equal(q.cpu().numpy(), qo)
+    assert np.array_equal(s.cache.k.cpu().numpy(), pk) and np.array_equal(s.cache.v.cpu().numpy(), pv)
+    assert s.batch.errors() == status == [None] * len(lens)
+
+
+@pytest.mark.parametrize("half", [False, True])
+def test_store_reports_the_first_word_that_does_not_fit(ck, half):
+    s = Setup(ck, [20, 30, 40], [20, 6, 4], 2, 2, 16, 8)
+    q, k, v = ((s.rng.standard_normal((s.rows, 32)) * 65536).astype(np.int64) for _ in range(3))
+    k[3, 5] = 2**31            # a key before its rotation, position 3 of the first sequence
+    v[3, 1] = -2**31 - 1       # a value of the same position
+    k[2, 8:12] = 2**31 - 1     # fits, but not every rotation of it does
+    v[21, 31] = 2**40          # position 25 of the second
+    v[26, :] = 2**31 - 1       # the third fits exactly
+    q[4] = 2**62
+    rope = rope_of(40, 16)
+    rc, out = ck.paged_store(s.cache, 0, s.batch, cuda(q), cuda(k), cuda(v), cuda(rope), half=half)
+    qo, pk, pv, status = plain_store(s, 0, q, k, v, rope, half)
+    assert rc == 0 and status[0] and status[1] == (25, 0, 7, 31) and status[2] is None
+    assert s.batch.errors() == status
+    assert np.array_equal(out.cpu().numpy(), qo) and np.array_equal(s.cache.k.cpu().numpy(), pk)
+    assert np.array_equal(s.cache.v.cpu().numpy(), pv)
+
+
+# ---------------------------------------------------------------- sequences and pages that do not fit
+
+def test_bad_sequences_and_pages_are_reported_and_the_others_done(ck):
+    """A length beyond the launch's bound, a table entry outside the pool, a position past the
+    rotary table: nothing outside the pool is touched, and the other sequences come out right."""
+    import torch
+    s = Setup(ck, [20, 30, 25, 12], [2, 2, 2, 2], 2, 2, 16, 8)
+    q = (s.rng.standard_normal((s.rows, 32)) * 65536).astype(np.int64)
+    kv = [(s.rng.standard_normal((s.rows, 32)) * 65536).astype(np.int64) for _ in range(2)]
+    want = s.attention(0, q, 1 << 22, fill=5)
+    lens = np.array([20, 31, 25, 12], np.int32)          # the second is past max_len
+    table = s.table.copy()
+    table[2, 1] = s.pages                                 # positions 8 .. 15 of the third
+    s.batch.lens.copy_(cuda(lens))
+    s.batch.table.copy_(cuda(table))
+    out = torch.full((s.rows, 32), 5, dtype=torch.int64, device="cuda")
+    rc, _ = ck.paged_attention(s.cache, 0, s.batch, cuda(q), cuda(EXP.view(np.int32)), 1 << 22, out=out)
+    assert rc == 0
+    got = out.cpu().numpy()
+    assert np.array_equal(got[[0, 1, 6, 7]], want[[0, 1, 6, 7]]) and (got[2:4] == 5).all()
+    assert s.batch.errors() == [None, (0, 0, 1, 0), (8, 0, 2, 0), None]
+    # the words of a page outside the pool read as zeros
+    k, v = s.k.copy(), s.v.copy()
+    for pool in (k, v):
+        pool[s.table[2, 1]] = 0
+    s.k, s.v = k, v
+    assert np.array_equal(got[4:6], s.attention(0, q, 1 << 22)[4:6])
+    s.batch.status.fill_(-1)
+    table[3, 1] = 2**31 - 1                               # positions 8 .. 15 of the fourth
+    s.batch.table.copy_(cuda(table))
+    before = s.cache.k.clone(), s.cache.v.clone()
+    rc, _ = ck.paged_store(s.cache, 0, s.batch, cuda(q), cuda(kv[0]), cuda(kv[1]), cuda(rope_of(24, 16)))
+    assert rc == 0
+    assert s.batch.errors() == [None, (0, 0, 1, 0), (24, 0, 1, 0), (10, 0, 2, 0)]
+    changed = {int(p) for p in torch.nonzero((s.cache.k != before[0]).flatten(1).any(1)).flatten()}
+    assert changed == {int(s.table[0, 2]), int(s.table[2, 2])}
+
+
+# ---------------------------------------------------------------- page tables
+
+def plain_fork(lens, table, parent, grow, pages, page, held=()):
+    rows, stride = len(parent), table.shape[1]
+    status, kept, old = [0] * rows, [[] for _ in range(rows)], [None] * rows
+    for r, p in enumerate(parent):
+        if p == -1:
+            continue
+        if not 0 <= p < len(lens):
+            status[r] = 3
+            continue
+        n = int(lens[p])
+        if n + int(grow[r]) > min(stride * page, 2**20 - 1):
+            status[r] = 7
+            continue
+        if any(not 0 <= w < pages for w in table[p][:-(-n // page)]):
+            status[r] = 3
+            continue
+        old[r] = n
+        kept[r] = [int(w) for w in table[p][:n // page]]
+    used = {w for row in kept for w in row}
+    holder = {}
+    for r in range(rows):
+        if old[r] is not None and old[r] % page:
+            holder.setdefault(int(table[parent[r]][old[r] // page]), r)
+    for w, r in holder.items():
+        if w not in used:
+            kept[r].append(w)
+    free = [w for w in range(pages) if w not in used and w not in holder and w not in set(held)]
+    asked, copies, out_lens = 0, [], [0] * rows
+    for r in range(rows):
+        if old[r] is None:
+            continue
+        need = -(-(old[r] + int(grow[r])) // page) - len(kept[r])
+        mine = free[asked:asked + need]
+        asked += need
+        if len(mine) < need:
+            status[r], kept[r] = 4, []
+            continue
+        if old[r] % page and len(kept[r]) == old[r] // page:
+            copies.append((int(table[parent[r]][old[r] // page]), mine[0], old[r] % page))
+        kept[r] += mine
+        out_lens[r] = old[r] + int(grow[r])
+    out = np.full((rows, stride), -1, np.int32)
+    for r in range(rows):
+        out[r, :len(kept[r])] = kept[r]
+    return out, out_lens, status, copies
+
+
+def check_fork(ck, k, v, lens, table, parent, grow, page, held=None):
+    pages = k.shape[0]
+    cache = ck.PagedCache(cuda(k), cuda(v))
+    plan = ck.PagePlan(cache, max(len(parent), 1), table.shape[1])
+    h = None if held is None else cuda(np.isin(np.arange(pages), held).astype(np.uint8))
+    rc, got = plan.fork(cuda(np.array(parent, np.int32)), cuda(np.array(lens, np.int32)),
+                        cuda(table.astype(np.int32)), cuda(np.array(grow, np.int32)), held=h)
+    assert rc == 0
+    out, out_lens, status, copies = plain_fork(lens, table, parent, grow, pages, page, held or ())
+    assert got.status.tolist() == status
+    assert got.lens.tolist() == out_lens
+    assert np.array_equal(got.table.cpu().numpy(), out)
+    for src, dst, n in copies:
+        k[dst, :, :, :n], v[dst, :, :, :n] = k[src, :, :, :n], v[src, :, :, :n]
+    assert np.array_equal(cache.k.cpu().numpy(), k) and np.array_equal(cache.v.cpu().numpy(), v)
+    return out, out_lens
+
+
+def pools(rng, pages, layers, kv, page, hd):
+    return [rng.integers(-2**31, 2**31, (pages, layers, kv, page, hd)).astype(np.int32) for _ in range(2)]
+
+
+def test_fork_shares_copies_frees_and_grows(ck):
+    rng = np.random.default_rng(5)
+    page = 8
+    k, v = pools(rng, 40, 3, 2, page, 16)
+    table = np.full((4, 9), -1)
+    lens = [21, 16, 5, 0]
+    table[0, :3], table[1, :2], table[2, :1] = [30, 2, 7], [30, 9], [11]
+    # three children of row 0, one of row 1 (its pages are whole), none of row 2, one of the empty row,
+    # an empty row, a parent that does not exist
+    parent, grow = [0, 1, 0, 0, 3, -1, 4], [1, 1, 4, 50, 9, 3, 1]
+    check_fork(ck, k, v, lens, table, parent, grow, page)
+    # a page that is whole for one row and part-filled for another: every part-filled row copies
+    table[1, 1] = 7
+    check_fork(ck, k, v, lens, table, [0, 1, 0], [0, 0, 1], page)
+    # too long, and a table entry outside the pool
+    table[2, 0] = 40
+    check_fork(ck, k, v, lens, table, [0, 2, 1], [52, 1, 1], page)
+    # pages of others, and a pool that runs out in the middle
+    table[2, 0] = 11
+    check_fork(ck, k, v, lens, table, [0, 0, 2, 1], [1, 1, 40, 1], page, held=list(range(12, 38)))
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_fork_step_after_step(ck, seed):
+    """A search's reordering over many steps: tables and pools follow the plain form, and every
+    row's cache reads as its ancestors wrote it."""
+    rng = np.random.default_rng(seed)
+    page, layers, kv, hd = [(8, 1, 1, 4), (16, 2, 3, 8), (32, 1, 2, 64), (8, 3, 1, 128), (16, 5, 4, 8), (64, 1, 1, 16)][seed]
+    rows = [4, 70, 33, 1, 1100, 8][seed]
+    stride, pages = 40 // page + 3, rows * 4 + 40
+    k, v = pools(rng, pages, layers, kv, page, hd)
+    table, lens = np.full((rows, stride), -1), [0] * rows
+    parent = list(range(rows))
+    for step in range(5):
+        grow = [int(rng.integers(0, 8)) for _ in range(rows)]
+        table, lens = check_fork(ck, k, v, lens, table, parent, grow, page)
+        parent = [int(p) for p in rng.integers(-1, rows, rows)]
+
+
+def test_compact_packs_the_pages_in_use(ck):
+    rng = np.random.default_rng(6)
+    page = 8
+    for pages, rows, share in ((40, 5, True), (5000, 300, False), (1, 1, False), (64, 2, False)):
+        k, v = pools(rng, pages, 2, 1, page, 8)
+        stride = 6
+        lens = [int(rng.integers(0, page * stride + 1)) for _ in range(rows)]
+        if pages == 1:
+            lens = [3]
+        table, ids = np.full((rows, stride), -1, np.int32), rng.permutation(pages)
+        at = 0
+        for r in range(rows):
+            n = -(-lens[r] // page)
+            table[r, :n] = ids[at:at + n]
+            at += n
+        if share:
+            table[1, :], lens[1] = table[0, :], lens[0]
+            lens[2] = page * stride + 1                    # too long
+            table[4, 0], lens[4] = pages, max(1, lens[4])  # outside the pool
+        cache = ck.PagedCache(cuda(k), cuda(v))
+        rc, got = ck.PagePlan(cache, rows, stride).compact(cuda(np.array(lens, np.int32)), cuda(table))
+        assert rc == 0
+        status = [0] * rows
+        if share:
+            status[2], status[4] = 7, 3
+        mine = [[int(w) for w in table[r][:-(-lens[r] // page)]] if not status[r] else [] for r in range(rows)]
+        used = sorted({w for row in mine for w in row})
+        low = [w for w in range(len(used)) if w not in set(used)]
+        to = {w: w for w in used if w < len(used)}
+        to.update(zip([w for w in used if w >= len(used)], low))
+        want = np.full((rows, stride), -1, np.int32)
+        for r in range(rows):
+            want[r, :len(mine[r])] = [to[w] for w in mine[r]]
+        for src, dst in to.items():
+            k[dst], v[dst] = k[src], v[src]
+        assert got.status.tolist() == status and int(got.used) == len(used)
+        assert np.array_equal(got.table.cpu().numpy(), want)
+        assert np.array_equal(cache.k.cpu().numpy(), k) and np.array_equal(cache.v.cpu().numpy(), v)
+
+
+# ---------------------------------------------------------------- beam search
+
+LN2 = 744261118
+
+
+def plain_log_sum(z):
+    z = max(z, 2**30)
+    n = z.bit_length() - 31
+    y = z >> n
+    t = ((y - 2**30) << 30) // (y + 2**30)
+    square, c = (t * t) >> 30, 0
+    for i in range(7, -1, -1):
+        c = (2**31 // (2 * i + 1) + 1) // 2 + ((c * square) >> 30)
+    return (n * LN2 + 2 * ((t * c) >> 30) + 2**13) >> 14
+
+
+def plain_beam(logits, scores, done, groups, beams, done_token, stop):
+    out = []
+    vocab = logits.shape[1]
+    for g in range(groups):
+        found = []
+        for r in range(g * beams, (g + 1) * beams):
+            old = int(scores[r])
+            if not -2**61 < old < 2**61:
+                continue
+            if done[r]:
+                found.append((-old, r, vocab))
+                continue
+            row = logits[r].astype(object)
+            d = np.minimum(max(row) - row, 2**62)
+            z = sum(int(EXP[min(int(x) >> 8, 4096)]) for x in d)
+            near = sorted(range(vocab), key=lambda i: (d[i], i))[:beams]
+            found += [(int(d[i]) + plain_log_sum(z) - old, r, i) for i in near]
+        found = sorted(found)[:beams]
+        for cost, r, i in found:
+            ended = i == vocab or (stop and i in (1, 2))
+            out.append((-cost, r, done_token if i == vocab else i, int(ended)))
+        out += [(MIN, -1, done_token, 0)] * (beams - len(found))
+    return out
+
+
+def check_beam(ck, logits, scores, done, groups, beams, done_token=0, stop=True, stride=None):
+    vocab = logits.shape[1]
+    dev = cuda(logits)
+    if stride:
+        import torch
+        wide = torch.full((logits.shape[0], stride), 2**63 - 1, dtype=torch.int64, device="cuda")
+        wide[:, :vocab] = dev
+        dev = wide[:, :vocab]
+    rc, got = ck.BeamPlan(groups, beams, vocab).select(dev, cuda(np.array(scores, np.int64)),
+                                                       cuda(np.array(done, np.uint8)), cuda(EXP.view(np.int32)),
+                                                       stop_tokens=stop, done_token=done_token)
+    assert rc == 0
+    got = list(zip(got.scores.tolist(), got.parent.tolist(), got.token.tolist(), got.done.tolist()))
+    assert got == plain_beam(logits, scores, done, groups, beams, done_token, stop)
+
+
+@pytest.mark.parametrize("groups,beams,vocab", [(1, 1, 1), (1, 4, 3), (2, 3, 7), (1, 4, 512), (3, 8, 1000), (2, 64, 333),
+                                                (5, 5, 4099), (1, 33, 20011), (2, 2, 32000), (1, 1, 32000)])
+def test_beam_selection_against_the_plain_form(ck, groups, beams, vocab):
+    rng = np.random.default_rng(beams + vocab)
+    rows = groups * beams
+    logits = (rng.standard_normal((rows, vocab)) * 3 * 65536).astype(np.int64)
+    scores = -rng.integers(0, 10 << 16, rows)
+    check_beam(ck, logits, scores, np.zeros(rows), groups, beams)
+    done = rng.random(rows) < 0.3
+    scores[rng.random(rows) < 0.2] = MIN
+    check_beam(ck, logits, scores, done, groups, beams, done_token=vocab - 1, stop=False)
+    check_beam(ck, logits // 65536, scores, done, groups, beams, stride=vocab + 3)     # many ties
+
+
+def test_beam_selection_at_the_edges(ck):
+    """All logits equal, extremes of 64 bits, the first step (one live beam), a search of dead
+    beams, scores at the bounds, ascending and descending logits."""
+    rng = np.random.default_rng(9)
+    for vocab in (40, 5000):
+        check_beam(ck, np.zeros((4, vocab), np.int64), [0, -5, -5, -10**9], [0, 0, 0, 0], 1, 4)
+        logits = rng.integers(-2**63, 2**63, (8, vocab))
+        logits[0, 5], logits[0, 7], logits[1, :] = 2**63 - 1, MIN, MIN
+        check_beam(ck, logits, [0, MIN, MIN, MIN, 2**61, -2**61, 2**61 - 1, 1 - 2**61], [0] * 8, 2, 4)
+        check_beam(ck, logits, [MIN] * 4 + [0] * 4, [0, 1, 0, 1] * 2, 2, 4)
+        ramp = np.arange(vocab)[None, :] * np.array([1, -1, 300, -300])[:, None]
+        check_beam(ck, ramp.astype(np.int64), [0, 0, 0, 0], [0] * 4, 1, 4)
+        check_beam(ck, ramp.astype(np.int64), [0, 0, 0, 0], [0] * 4, 4, 1)

@@ -1,0 +1,192 @@
+"""What the paged cache's operators and beam search refuse, and their host routines: no GPU
+needed (every refusal is decided from the arguments alone, before any device call)."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+
+
+@pytest.fixture(scope="module")
+def ck():
+    import fixed_point_int8_gb300 as ck
+    from fixed_point_int8_gb300 import build
+    build.build()
+    return ck
+
+
+def plain_log_sum(z):
+    z = max(z, 2**30)
+    n = z.bit_length() - 31
+    y = z >> n
+    t = ((y - 2**30) << 30) // (y + 2**30)
+    square, c = (t * t) >> 30, 0
+    for i in range(7, -1, -1):
+        c = (2**31 // (2 * i + 1) + 1) // 2 + ((c * square) >> 30)
+    return (n * 744261118 + 2 * ((t * c) >> 30) + 2**13) >> 14
+
+
+def test_log_sum_is_the_logarithm(ck):
+    """The integer series against its definition and against the real logarithm: y is cut to 30
+    fraction bits (2^-30 relative), each of at most 16 cut products loses below 2^-30, the series
+    after t^15 leaves t^17 / 17 * 2 * 9/8 < 2^-29, and the last step rounds to half of 2^-16."""
+    rng = np.random.default_rng(1)
+    zs = [0, 1, 2**30 - 1, 2**30, 2**30 + 1, 2**31 - 1, 2**31, 2**50, 2**50 - 1, 2**52]
+    zs += [2**int(e) + int(r) for e, r in zip(rng.integers(30, 51, 2000), rng.integers(0, 2**30, 2000))]
+    for z in zs:
+        got = ck.host_log_sum(z)
+        assert got == plain_log_sum(z), z
+        real = math.log(max(z, 2**30) / 2**30)
+        assert abs(got / 2**16 - real) <= 2**-17 + 40 * 2**-30, z
+
+
+ADDR = 1 << 20  # stands for an aligned device address: nothing reads it
+
+
+def call(ck, name, good, **changed):
+    args = dict(good)
+    for key, value in changed.items():
+        assert key in args
+        args[key] = value
+    return getattr(ck.lib(), name)(*args.values())
+
+
+def cache(ck, **changed):
+    f = dict(dev_k=ADDR, dev_v=2 * ADDR, pages=8, layers=2, kv_heads=2, page=16, head_dim=32)
+    f.update(changed)
+    return ck.paged._Cache(*f.values())
+
+
+def batch(ck, **changed):
+    f = dict(dev_start=ADDR, dev_len=ADDR, dev_table=ADDR, dev_status=ADDR, seqs=3, rows=6, stride=4, max_new=2,
+             max_len=64)
+    f.update(changed)
+    return ck.paged._Batch(*f.values())
+
+
+BAD_CACHES = [dict(dev_k=None), dict(dev_v=None), dict(dev_k=ADDR + 8), dict(dev_v=ADDR + 4), dict(pages=0),
+              dict(pages=2**24 + 1), dict(layers=0), dict(layers=4096), dict(kv_heads=0), dict(kv_heads=4097),
+              dict(page=4), dict(page=24), dict(page=512), dict(head_dim=2), dict(head_dim=48), dict(head_dim=256)]
+BAD_BATCHES = [dict(dev_start=None), dict(dev_len=None), dict(dev_table=None), dict(dev_status=None),
+               dict(dev_status=ADDR + 4), dict(dev_table=ADDR + 2), dict(seqs=0), dict(seqs=65536), dict(rows=0),
+               dict(rows=2**20 + 1), dict(stride=0), dict(stride=2**17 + 1), dict(max_new=0), dict(max_new=7),
+               dict(max_len=0), dict(max_len=2**20)]
+
+
+def store_args(ck):
+    return dict(cache=cache(ck), layer=1, batch=batch(ck), q=4 * ADDR, q_stride=128, k=5 * ADDR, k_stride=64,
+                v=6 * ADDR, v_stride=64, heads=4, rope=7 * ADDR, rope_rows=64, rot=32, half=0, out=8 * ADDR, stream=None)
+
+
+def attention_args(ck):
+    return dict(cache=cache(ck), layer=1, batch=batch(ck), q=4 * ADDR, q_stride=128, heads=4, exp=ADDR, inv=1,
+                out=8 * ADDR, work=16 * ADDR, work_len=2**40, stream=None)
+
+
+@pytest.mark.parametrize("bad", BAD_CACHES + BAD_BATCHES, ids=str)
+def test_wrong_caches_and_batches_are_refused(ck, bad):
+    key = "cache" if bad.keys() & {n for n, _ in ck.paged._Cache._fields_} else "batch"
+    value = cache(ck, **bad) if key == "cache" else batch(ck, **bad)
+    assert call(ck, "ck_paged_store", store_args(ck), **{key: value}) == 10
+    assert call(ck, "ck_paged_attention", attention_args(ck), **{key: value}) == 10
+
+
+@pytest.mark.parametrize("bad", [dict(cache=None), dict(layer=2), dict(batch=None), dict(q=None), dict(k=None),
+                                 dict(v=None), dict(rope=None), dict(out=None), dict(q=4 * ADDR + 8),
+                                 dict(out=8 * ADDR + 8), dict(rope=ADDR + 8), dict(q_stride=126), dict(q_stride=129),
+                                 dict(k_stride=62), dict(v_stride=65), dict(heads=0), dict(heads=65537),
+                                 dict(rope_rows=0), dict(rot=6), dict(rot=36), dict(q_stride=2**40),
+                                 dict(out=4 * ADDR), dict(out=5 * ADDR + 16), dict(out=6 * ADDR - 16)], ids=str)
+def test_wrong_stores_are_refused(ck, bad):
+    assert call(ck, "ck_paged_store", store_args(ck), **bad) == 10
+
+
+@pytest.mark.parametrize("bad", [dict(cache=None), dict(layer=2), dict(batch=None), dict(q=None), dict(exp=None),
+                                 dict(out=None), dict(work=None), dict(q=4 * ADDR + 8), dict(out=ADDR + 8),
+                                 dict(work=ADDR + 128), dict(exp=ADDR + 2), dict(q_stride=126), dict(q_stride=129),
+                                 dict(heads=3), dict(heads=0), dict(heads=65538), dict(out=4 * ADDR + 32)], ids=str)
+def test_wrong_attention_calls_are_refused(ck, bad):
+    assert call(ck, "ck_paged_attention", attention_args(ck), **bad) == 10
+
+
+def test_work_sizes_are_refused_for_wrong_arguments(ck):
+    n = ctypes.c_size_t()
+    out = ctypes.byref(n)
+    L = ck.lib()
+    assert L.ck_pages_work(cache(ck), 4, 4, None) == 10
+    for c, rows, stride in ((cache(ck, page=7), 4, 4), (cache(ck), 0, 4), (cache(ck), 65537, 4), (cache(ck), 4, 0),
+                            (cache(ck), 4, 2**17 + 1), (None, 4, 4)):
+        assert L.ck_pages_work(c, rows, stride, out) == 10
+    assert L.ck_pages_work(cache(ck), 4, 4, out) == 0 and n.value > 0
+    for groups, beams, vocab in ((0, 1, 1), (1, 0, 1), (1, 65, 1), (1, 1, 0), (1, 1, 2**20 + 1), (1025, 64, 9)):
+        assert L.ck_beam_work(groups, beams, vocab, out) == 10
+    assert L.ck_beam_work(1, 1, 1, None) == 10
+    assert L.ck_beam_work(1024, 64, 9, out) == 0 and n.value > 0
+    assert L.ck_paged_attention_work(cache(ck), batch(ck), 3, out) == 10
+    assert L.ck_paged_attention_work(cache(ck), batch(ck), 4, None) == 10
+
+
+def fork_args(ck):
+    return dict(cache=cache(ck), rows_in=4, len_in=ADDR, table_in=2 * ADDR, rows=4, parent=3 * ADDR, grow=4 * ADDR,
+                stride=4, held=None, len_out=5 * ADDR, table_out=6 * ADDR, status=7 * ADDR, work=8 * ADDR,
+                work_len=ADDR, stream=None)
+
+
+@pytest.mark.parametrize("bad", [dict(cache=None), dict(rows_in=0), dict(rows=0), dict(rows_in=65537), dict(rows=65537),
+                                 dict(stride=0), dict(stride=2**17 + 1), dict(len_in=None), dict(table_in=None),
+                                 dict(parent=None), dict(grow=None), dict(len_out=None), dict(table_out=None),
+                                 dict(status=None), dict(work=None), dict(work=8 * ADDR + 4), dict(table_out=2 * ADDR),
+                                 dict(table_out=2 * ADDR + 60), dict(len_out=ADDR), dict(status=5 * ADDR),
+                                 dict(len_out=8 * ADDR), dict(parent=ADDR + 2), dict(held=8 * ADDR)], ids=str)
+def test_wrong_forks_are_refused(ck, bad):
+    assert call(ck, "ck_pages_fork", fork_args(ck), **bad) == 10
+
+
+def test_short_scratch_is_refused(ck):
+    assert call(ck, "ck_pages_fork", fork_args(ck), work_len=64) == 4
+    assert call(ck, "ck_pages_compact", compact_args(ck), work_len=64) == 4
+    assert call(ck, "ck_beam_select", beam_args(ck), work_len=64) == 4
+
+
+def compact_args(ck):
+    return dict(cache=cache(ck), rows=4, len=ADDR, table_in=2 * ADDR, stride=4, table_out=3 * ADDR, used=4 * ADDR,
+                status=5 * ADDR, work=8 * ADDR, work_len=ADDR, stream=None)
+
+
+@pytest.mark.parametrize("bad", [dict(cache=None), dict(rows=0), dict(rows=65537), dict(len=None), dict(table_in=None),
+                                 dict(stride=0), dict(table_out=None), dict(used=None), dict(status=None),
+                                 dict(work=None), dict(work=ADDR * 8 + 16), dict(table_out=2 * ADDR + 4),
+                                 dict(used=3 * ADDR), dict(status=ADDR)], ids=str)
+def test_wrong_packings_are_refused(ck, bad):
+    assert call(ck, "ck_pages_compact", compact_args(ck), **bad) == 10
+
+
+def beam_args(ck):
+    return dict(logits=ADDR, stride=100, groups=2, beams=4, vocab=100, scores=2 * ADDR, done=3 * ADDR, exp=4 * ADDR,
+                flags=1, done_token=2, scores_out=5 * ADDR, parent=6 * ADDR, token=7 * ADDR, done_out=8 * ADDR,
+                work=9 * ADDR, work_len=ADDR, stream=None)
+
+
+@pytest.mark.parametrize("bad", [dict(logits=None), dict(logits=ADDR + 4), dict(stride=99), dict(groups=0), dict(beams=0),
+                                 dict(beams=65), dict(vocab=0), dict(scores=None), dict(done=None), dict(exp=None),
+                                 dict(flags=2), dict(done_token=100), dict(scores_out=None), dict(parent=None),
+                                 dict(token=None), dict(done_out=None), dict(work=None), dict(scores_out=2 * ADDR),
+                                 dict(done_out=3 * ADDR), dict(token=6 * ADDR + 4), dict(scores_out=ADDR + 8)], ids=str)
+def test_wrong_selections_are_refused(ck, bad):
+    assert call(ck, "ck_beam_select", beam_args(ck), **bad) == 10
+
+
+def test_the_binding_checks_tensors(ck):
+    """Types, shapes, strides and devices that the library cannot see."""
+    import torch
+    pool = torch.zeros(3, 1, 2, 8, 4, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        ck.PagedCache(pool, pool)                                   # not on a CUDA device
+    with pytest.raises(ValueError):
+        ck.PagedCache(pool.long(), pool.long())
+    with pytest.raises(ValueError):
+        ck.PagedBatch(torch.zeros(2, 3, dtype=torch.int64), pool, pool, None, 1, 1, 1)
+    for t, rows in ((torch.zeros(2, 3), 2), (torch.zeros(2, 3, dtype=torch.int64), 3),
+                    (torch.zeros(3, 2, dtype=torch.int64).t(), 2)):
+        with pytest.raises(ValueError):
+            ck.paged._check_rows("q", t, rows, 0)
