@@ -136,6 +136,403 @@ __global__ void __launch_bounds__(kRowsThreads) k_pattn_rows(const PAttnParams p
   }
 }
 
+// ------------------------------------------------------------------ a few queries a key head
+
+// A cluster of blocks takes up to R queries (rows x heads that share a key head) of one sequence
+// and one key head, each block a range of positions, so that every key and value word is read
+// once: scores into the block's scratch, maximum and sum exchanged through distributed shared
+// memory, weighted values summed over the cluster.  HBM bounds it once the positions are many;
+// below, the chain of the two exchanges.  Lanes: hd / 4 a position, four elements each; kBatch
+// positions a lane group in flight.
+constexpr int kBatch = 8, kNarrow = 128;
+
+struct FewParams {
+  PAttnParams a;
+  uint32_t cap;          // positions a block takes at most
+  uint32_t ids;          // table entries a block holds
+  uint32_t sc_smem;      // the scores lie in shared memory
+};
+
+__device__ __forceinline__ uint32_t smem_of(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ unsigned long long peer_word(const void* p, uint32_t rank) {
+  uint32_t a;
+  unsigned long long v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_of(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
+  return v;
+}
+
+struct FewLayout {
+  uint32_t vpre, part, q, red, ids, sc, size;
+};
+template <int NT, int R>
+__host__ __device__ inline FewLayout few_layout(uint32_t hd, uint32_t ids, uint32_t cap, bool sc_smem) {
+  FewLayout w;
+  uint32_t off = 0;
+  w.vpre = off; off += kBatch * NT * 16;
+  w.part = off; off += (NT / 32) * R * hd * 8;
+  w.q = off; off += R * hd * 8;
+  w.red = off; off += ((NT / 32) + 2) * R * 8;
+  w.ids = off; off += (ids * 4 + 15) & ~15u;
+  w.sc = off; off += sc_smem ? R * cap * 8 : 0;
+  w.size = off;
+  return w;
+}
+
+// Sums d[0 .. kBatch) over the LPP lanes of a group; lane `sub` ends with the sum of batch
+// entry *which.  The first steps halve what a lane carries, so that 8 sums cost 8 exchanges.
+template <int LPP>
+__device__ __forceinline__ unsigned long long group_sums(unsigned long long (&d)[kBatch], uint32_t sub,
+                                                         uint32_t* which) {
+  uint32_t w = 0;
+#pragma unroll
+  for (int n = kBatch / 2, o = LPP / 2; n > 0; n >>= 1, o >>= 1) {
+    const bool up = sub & o;
+    w = 2 * w + up;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const unsigned long long got = __shfl_xor_sync(0xffffffffu, up ? d[i] : d[i + n], o);
+      d[i] = (up ? d[i + n] : d[i]) + got;
+    }
+  }
+#pragma unroll
+  for (int o = LPP / kBatch / 2; o > 0; o >>= 1) d[0] += __shfl_xor_sync(0xffffffffu, d[0], o);
+  *which = w;
+  return d[0];
+}
+
+// LPP: lanes a position (8, 16 or 32), 0 for fewer (head sizes below 32).
+template <int LPP, int R, int NT>
+__global__ void __launch_bounds__(NT) k_pattn_few(const FewParams f) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  const PAttnParams& p = f.a;
+  const uint32_t hd = p.pool.hd, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t C = cluster_size(), rank = cluster_rank();
+  const uint32_t seq = blockIdx.x / C, kvh = blockIdx.y, v0 = blockIdx.z * R;
+  const Sequence sq = load_sequence(p.batch, seq, p.pool.page_shift);
+  if (!sq.ok) {  // (the whole cluster leaves)
+    if (tid == 0 && rank == 0) note(p.batch, seq, err_key(0, p.pool.layer, CK_PAGED_BAD_SEQUENCE, 0));
+    return;
+  }
+  const uint32_t group = p.heads / p.pool.kv_heads, queries = sq.count * group;
+  if (v0 >= queries) return;
+  const uint32_t nv = min((uint32_t)R, queries - v0);
+  // positions each query sees: those up to its row's own
+  uint32_t np[R], top = 0;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const uint32_t up = (v0 + r) / group + sq.len;  // position + count
+    np[r] = r < nv && up >= sq.count ? up - sq.count + 1 : 0;
+    top = max(top, np[r]);
+  }
+  const uint32_t per = (top + C - 1) / C, c0 = min(top, rank * per), n = min(top, c0 + per) - c0;
+  const FewLayout w = few_layout<NT, R>(hd, f.ids, f.cap, f.sc_smem);
+  int4* vpre = reinterpret_cast<int4*>(smem + w.vpre);
+  unsigned long long* part = reinterpret_cast<unsigned long long*>(smem + w.part);
+  int64_t* q_s = reinterpret_cast<int64_t*>(smem + w.q);
+  unsigned long long* red = reinterpret_cast<unsigned long long*>(smem + w.red);
+  unsigned long long* xm = red + (NT / 32) * R;
+  unsigned long long* xz = xm + R;
+  uint32_t* ids = reinterpret_cast<uint32_t*>(smem + w.ids);
+  const size_t block = ((size_t)blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
+  long long* sc = f.sc_smem ? reinterpret_cast<long long*>(smem + w.sc) : p.scores + block * R * f.cap;
+
+  const uint32_t shift = p.pool.page_shift, mask = (1u << shift) - 1, page0 = c0 >> shift;
+  const uint32_t* table = p.batch.table + (size_t)seq * p.batch.stride;
+  for (uint32_t i = tid; n != 0 && i <= ((c0 + n - 1) >> shift) - page0; i += NT) {
+    const uint32_t id = table[page0 + i];
+    ids[i] = id;
+    if (id >= p.pool.pages) note(p.batch, seq, err_key((page0 + i) << shift, p.pool.layer, CK_PAGED_BAD_PAGE, 0));
+  }
+  int wide = 0;
+  for (uint32_t i = tid; i < R * hd; i += NT) {
+    const uint32_t r = i / hd, v = v0 + r;
+    int64_t x = 0;
+    if (r < nv)
+      x = p.q[(size_t)(sq.first + v / group) * p.q_stride + (size_t)(kvh * group + v % group) * hd + i % hd];
+    q_s[i] = x;
+    wide |= x != (int32_t)x;
+  }
+  wide = __syncthreads_or(wide);
+
+  const uint32_t lpp = LPP ? LPP : hd / 4, ppw = 32 / lpp, sub = lane % lpp, slot = lane / lpp, e0 = 4 * sub;
+  const uint32_t step = (NT / 32) * ppw, round = step * kBatch;
+  // position c0 + i of the pool, this lane's four words (zeros outside the range or the pool)
+  auto at = [&](const int32_t* pool, uint32_t i) -> const int4* {
+    if (i >= n) return nullptr;
+    const uint32_t t = c0 + i, id = ids[(t >> shift) - page0];
+    if (id >= p.pool.pages) return nullptr;
+    return reinterpret_cast<const int4*>(pool + page_word(p.pool, id, kvh) + (size_t)(t & mask) * hd + e0);
+  };
+  // the first values travel while the scores are formed
+#pragma unroll
+  for (int b = 0; b < kBatch; ++b) {
+    const int4* src = at(p.pool.v, b * step + warp * ppw + slot);
+    if (src)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_of(vpre + b * NT + tid)), "l"(src)
+                   : "memory");
+    else
+      vpre[b * NT + tid] = make_int4(0, 0, 0, 0);
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+
+  // scores
+  long long m[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) m[r] = LLONG_MIN;
+  auto score = [&](int r, uint32_t i, unsigned long long d) {
+    if (i >= n) return;
+    const long long v = wmul((long long)d >> 16, (int64_t)p.inv_sqrt) >> 24;
+    sc[(size_t)r * f.cap + i] = v;
+    if (c0 + i < np[r]) m[r] = max(m[r], v);
+  };
+  for (uint32_t base = 0; base < n; base += round) {
+    int4 k4[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int4* src = at(p.pool.k, base + b * step + warp * ppw + slot);
+      k4[b] = src ? __ldg(src) : make_int4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int64_t q0 = q_s[r * hd + e0], q1 = q_s[r * hd + e0 + 1], q2 = q_s[r * hd + e0 + 2],
+                    q3 = q_s[r * hd + e0 + 3];
+      unsigned long long d[kBatch];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b)  // the low words as signed 32-bit factors
+        d[b] = (unsigned long long)((long long)(int32_t)q0 * k4[b].x) +
+               (unsigned long long)((long long)(int32_t)q1 * k4[b].y) +
+               (unsigned long long)((long long)(int32_t)q2 * k4[b].z) +
+               (unsigned long long)((long long)(int32_t)q3 * k4[b].w);
+      if (wide) {  // and what is left of the queries above them, times 2^32
+        const uint32_t h0 = (uint32_t)((q0 - (int32_t)q0) >> 32), h1 = (uint32_t)((q1 - (int32_t)q1) >> 32),
+                       h2 = (uint32_t)((q2 - (int32_t)q2) >> 32), h3 = (uint32_t)((q3 - (int32_t)q3) >> 32);
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+          d[b] += (unsigned long long)(h0 * (uint32_t)k4[b].x + h1 * (uint32_t)k4[b].y + h2 * (uint32_t)k4[b].z +
+                                       h3 * (uint32_t)k4[b].w)
+                  << 32;
+      }
+      if constexpr (LPP >= kBatch) {
+        uint32_t b;
+        const unsigned long long s = group_sums<LPP>(d, sub, &b);
+        if (sub % (LPP / kBatch) == 0) score(r, base + b * step + warp * ppw + slot, s);
+      } else {
+        for (uint32_t o = lpp >> 1; o > 0; o >>= 1) {
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b) d[b] += __shfl_xor_sync(0xffffffffu, d[b], o);
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+          if (sub == 0) score(r, base + b * step + warp * ppw + slot, d[b]);
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m[r] = max(m[r], __shfl_xor_sync(0xffffffffu, m[r], o));
+    if (lane == 0) red[warp * R + r] = (unsigned long long)m[r];
+  }
+  __syncthreads();
+  if (tid < R) {
+    long long v = LLONG_MIN;
+    for (int k = 0; k < (NT / 32); ++k) v = max(v, (long long)red[k * R + tid]);
+    xm[tid] = (unsigned long long)v;
+  }
+  if (C > 1) cluster_sync();
+  else __syncthreads();
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    m[r] = (long long)xm[r];
+    for (uint32_t k = 0; k < C && C > 1; ++k) m[r] = max(m[r], (long long)peer_word(xm + r, k));
+  }
+  // exponentials and their sums
+  unsigned long long z[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    z[r] = 0;
+    const uint32_t seen = np[r] > c0 ? min(n, np[r] - c0) : 0;
+    long long* s = sc + (size_t)r * f.cap;
+    for (uint32_t i = tid; i < n; i += NT) {
+      const uint32_t e = i < seen ? exponential(p.exp_tab, (unsigned long long)m[r] - (unsigned long long)s[i]) : 0;
+      s[i] = e;
+      z[r] += e;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) z[r] += __shfl_xor_sync(0xffffffffu, z[r], o);
+    if (lane == 0) red[warp * R + r] = z[r];
+  }
+  __syncthreads();
+  if (tid < R) {
+    unsigned long long v = 0;
+    for (int k = 0; k < (NT / 32); ++k) v += red[k * R + tid];
+    xz[tid] = v;
+  }
+  if (C > 1) cluster_sync();
+  else __syncthreads();
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    z[r] = C > 1 ? 0 : xz[r];
+    for (uint32_t k = 0; k < C && C > 1; ++k) z[r] += peer_word(xz + r, k);
+    if (z[r] < kOne) z[r] = kOne;
+    const float rz = rcp_estimate((float)z[r]);
+    long long* s = sc + (size_t)r * f.cap;
+    for (uint32_t i = tid; i < n; i += NT)
+      s[i] = (long long)div_by_estimate((unsigned long long)s[i] << 24, z[r], rz);
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();
+  // weighted values
+  unsigned long long a[R][4];
+#pragma unroll
+  for (int r = 0; r < R; ++r) a[r][0] = a[r][1] = a[r][2] = a[r][3] = 0;
+  for (uint32_t base = 0; base < n; base += round) {
+    int4 v4[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      if (base == 0) {
+        v4[b] = vpre[b * NT + tid];
+      } else {
+        const int4* src = at(p.pool.v, base + b * step + warp * ppw + slot);
+        v4[b] = src ? __ldg(src) : make_int4(0, 0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const uint32_t i = base + b * step + warp * ppw + slot;
+        const long long pb = i < n ? (int32_t)sc[(size_t)r * f.cap + i] : 0;  // P <= 2^24
+        a[r][0] += (unsigned long long)(pb * v4[b].x);
+        a[r][1] += (unsigned long long)(pb * v4[b].y);
+        a[r][2] += (unsigned long long)(pb * v4[b].z);
+        a[r][3] += (unsigned long long)(pb * v4[b].w);
+      }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    for (uint32_t o = 16; o >= lpp; o >>= 1) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) a[r][j] += __shfl_xor_sync(0xffffffffu, a[r][j], o);
+    }
+    if (slot == 0) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) part[((size_t)warp * R + r) * hd + e0 + j] = a[r][j];
+    }
+  }
+  __syncthreads();
+  for (uint32_t i = tid; i < R * hd; i += NT) {
+    unsigned long long t = 0;
+    for (int k = 0; k < (NT / 32); ++k) t += part[(size_t)k * R * hd + i];
+    part[i] = t;  // (only this thread reads or writes entry i of any warp)
+  }
+  if (C > 1) cluster_sync();
+  // a slice of the outputs each block
+  for (uint32_t i = rank * NT + tid; i < nv * hd; i += C * NT) {
+    unsigned long long t = 0;
+    if (C > 1)
+      for (uint32_t k = 0; k < C; ++k) t += peer_word(part + i, k);
+    else
+      t = part[i];
+    const uint32_t v = v0 + i / hd;
+    p.out[((size_t)(sq.first + v / group) * p.heads + kvh * group + v % group) * hd + i % hd] = (long long)t >> 24;
+  }
+  if (C > 1) cluster_sync();  // no block leaves while another reads its sums
+}
+
+struct FewPlan {
+  bool use;
+  uint32_t NT, R, C, z, cap, ids;
+  bool sc_smem;
+  uint32_t smem;
+  uint64_t work;
+};
+
+template <int NT>
+uint32_t few_smem(uint32_t R, uint32_t hd, uint32_t ids, uint32_t cap, bool sc_smem) {
+  return R == 1   ? few_layout<NT, 1>(hd, ids, cap, sc_smem).size
+         : R == 2 ? few_layout<NT, 2>(hd, ids, cap, sc_smem).size
+                  : few_layout<NT, 4>(hd, ids, cap, sc_smem).size;
+}
+
+FewPlan plan_few(const ck_paged_cache& c, const ck_paged_batch& b, uint32_t heads, const DeviceFacts& f) {
+  FewPlan w = {};
+  const uint64_t queries = (uint64_t)b.max_new * (heads / c.kv_heads);
+  if (queries > 16) return w;
+  w.R = queries == 1 ? 1 : queries == 2 ? 2 : 4;
+  w.z = (uint32_t)((queries + w.R - 1) / w.R);
+  // blocks of a cluster: until two an SM are there, while each has 256 positions
+  const uint64_t items = (uint64_t)b.seqs * c.kv_heads * w.z;
+  w.C = 1;
+  while (w.C < 8 && items * w.C < 2ull * f.sms && b.max_len / (2 * w.C) >= 256) w.C *= 2;
+  w.NT = items * w.C >= 4ull * f.sms ? kNarrow : 256;
+  w.cap = (b.max_len + w.C - 1) / w.C;
+  w.ids = w.cap / c.page + 2;
+  auto smem = [&](bool sc) {
+    return w.NT == 256 ? few_smem<256>(w.R, c.head_dim, w.ids, w.cap, sc)
+                       : few_smem<kNarrow>(w.R, c.head_dim, w.ids, w.cap, sc);
+  };
+  w.sc_smem = smem(true) <= (uint32_t)f.optin / 2 - 2048;
+  w.smem = smem(w.sc_smem);
+  w.work = w.sc_smem ? 0 : 8ull * w.cap * w.R * items * w.C;
+  w.use = w.smem <= (uint32_t)f.optin;
+  return w;
+}
+
+template <int LPP, int R, int NT>
+cudaError_t launch_few(const FewParams& p, const FewPlan& w, const DeviceFacts& f, cudaStream_t s) {
+  static std::atomic<bool> ready[64];
+  if (!ready[f.dev].load(std::memory_order_relaxed)) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(k_pattn_few<LPP, R, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, f.optin);
+    if (e != cudaSuccess) return e;
+    ready[f.dev].store(true, std::memory_order_relaxed);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.a.batch.seqs * w.C, p.a.pool.kv_heads, w.z);
+  cfg.blockDim = dim3(NT);
+  cfg.dynamicSmemBytes = w.smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = w.C;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_pattn_few<LPP, R, NT>, p);
+}
+
+template <int R, int NT>
+cudaError_t launch_few_lpp(const FewParams& p, const FewPlan& w, const DeviceFacts& f, cudaStream_t s) {
+  switch (p.a.pool.hd) {
+    case 128: return launch_few<32, R, NT>(p, w, f, s);
+    case 64: return launch_few<16, R, NT>(p, w, f, s);
+    case 32: return launch_few<8, R, NT>(p, w, f, s);
+    default: return launch_few<0, R, NT>(p, w, f, s);
+  }
+}
+
+template <int NT>
+cudaError_t launch_few_r(const FewParams& p, const FewPlan& w, const DeviceFacts& f, cudaStream_t s) {
+  return w.R == 1   ? launch_few_lpp<1, NT>(p, w, f, s)
+         : w.R == 2 ? launch_few_lpp<2, NT>(p, w, f, s)
+                    : launch_few_lpp<4, NT>(p, w, f, s);
+}
+
 // Blocks of k_pattn_rows: four an SM are resident; fewer when there are fewer items.
 uint32_t rows_blocks(const ck_paged_batch& b, uint32_t heads, int sms) {
   const uint64_t items = (uint64_t)b.rows * heads;
@@ -155,7 +552,9 @@ int ck_paged_attention_work(const ck_paged_cache* cache, const ck_paged_batch* b
     return CK_INVALID_ARGUMENT;
   DeviceFacts f;
   CKP_CUDA(device_facts(&f));
-  *out = align256(8ull * rows_blocks(*batch, heads, f.sms) * batch->max_len);
+  const FewPlan few = plan_few(*cache, *batch, heads, f);
+  *out = align256(few.use ? few.work : 8ull * rows_blocks(*batch, heads, f.sms) * batch->max_len);
+  if (*out == 0) *out = 256;  // never an empty buffer
   return CK_OK;
 }
 
@@ -186,7 +585,14 @@ int ck_paged_attention(const ck_paged_cache* cache, uint32_t layer, const ck_pag
   p.exp_tab = dev_exp;
   p.out = dev_out;
   p.scores = static_cast<long long*>(dev_work);
-  k_pattn_rows<<<rows_blocks(*batch, heads, f.sms), kRowsThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const FewPlan few = plan_few(*cache, *batch, heads, f);
+  if (few.use) {
+    const FewParams fp = {p, few.cap, few.ids, few.sc_smem};
+    CKP_CUDA(few.NT == 256 ? launch_few_r<256>(fp, few, f, s) : launch_few_r<kNarrow>(fp, few, f, s));
+    return CK_OK;
+  }
+  k_pattn_rows<<<rows_blocks(*batch, heads, f.sms), kRowsThreads, 0, s>>>(p);
   CKP_CUDA(cudaGetLastError());
   return CK_OK;
 }
