@@ -3,20 +3,19 @@
 // is a table lookup of the distance to the maximum and the probability a floored quotient, so
 // neither can be rescaled when a maximum or a sum changes: the scores are kept and gone through
 // three times.  All sums wrap in 64 bits, so any split of them gives the same bits.
-#include "ck_paged.cuh"
+#include "ck_paged_attention.cuh"
 
 namespace ck {
 namespace {
 
-struct PAttnParams {
-  PoolView pool;
-  BatchView batch;
-  const int64_t* q;
-  size_t q_stride;
-  uint32_t heads, inv_sqrt;
-  const uint32_t* exp_tab;
-  int64_t* out;
+struct RowsParams {
+  PAttnParams a;
   long long* scores;     // [blocks][max_len]
+  // not null: only rows of the tiles marked here ([sequence][key head][tile of 128 queries]),
+  // of which there are *any
+  const uint32_t* any;
+  const uint32_t* away;
+  uint32_t tiles;
 };
 
 constexpr int kRowsThreads = 256, kRowsWarps = kRowsThreads / 32;
@@ -30,7 +29,9 @@ __device__ __forceinline__ uint32_t exponential(const uint32_t* tab, unsigned lo
 
 // One (row, head) at a time a block, whatever the values and the lengths: the products are
 // 64-bit, the scores of the row lie in the block's part of the scratch.
-__global__ void __launch_bounds__(kRowsThreads) k_pattn_rows(const PAttnParams p) {
+__global__ void __launch_bounds__(kRowsThreads) k_pattn_rows(const RowsParams f) {
+  const PAttnParams& p = f.a;
+  if (f.away && *f.any == 0) return;
   __shared__ int64_t q_s[128];
   __shared__ unsigned long long part[kRowsWarps][128];
   __shared__ long long red[kRowsWarps];
@@ -38,7 +39,7 @@ __global__ void __launch_bounds__(kRowsThreads) k_pattn_rows(const PAttnParams p
   const uint32_t lpp = hd / 4, ppw = 32 / lpp;  // lanes a position (four elements each)
   const uint32_t sub = lane % lpp, slot = lane / lpp, e0 = sub * 4;
   const uint32_t mask = (1u << p.pool.page_shift) - 1;
-  long long* sc = p.scores + (size_t)blockIdx.x * p.batch.max_len;
+  long long* sc = f.scores + (size_t)blockIdx.x * p.batch.max_len;
   const uint64_t items = (uint64_t)p.batch.rows * p.heads;
   for (uint64_t item = blockIdx.x; item < items; item += gridDim.x) {
     const uint32_t row = (uint32_t)(item / p.heads), h = (uint32_t)(item - (uint64_t)row * p.heads);
@@ -50,6 +51,10 @@ __global__ void __launch_bounds__(kRowsThreads) k_pattn_rows(const PAttnParams p
     if (!sq.ok) {
       if (tid == 0) note(p.batch, s, err_key(0, p.pool.layer, CK_PAGED_BAD_SEQUENCE, 0));
       continue;
+    }
+    if (f.away) {
+      const uint32_t group = p.heads / p.pool.kv_heads, query = (row - sq.first) * group + h % group;
+      if (!f.away[((size_t)s * p.pool.kv_heads + h / group) * f.tiles + query / 128]) continue;
     }
     int64_t* out = p.out + ((size_t)row * p.heads + h) * hd;
     const uint32_t up = row - sq.first + sq.len;
@@ -145,9 +150,11 @@ __global__ void __launch_bounds__(kRowsThreads) k_pattn_rows(const PAttnParams p
 // below, the chain of the two exchanges.  Lanes: hd / 4 a position, four elements each; kBatch
 // positions a lane group in flight.
 constexpr int kBatch = 8, kNarrow = 128;
+constexpr uint32_t kFewQueries = 16;
 
 struct FewParams {
   PAttnParams a;
+  long long* scores;     // [blocks][R][cap], where they do not fit shared memory
   uint32_t cap;          // positions a block takes at most
   uint32_t ids;          // table entries a block holds
   uint32_t sc_smem;      // the scores lie in shared memory
@@ -248,7 +255,7 @@ __global__ void __launch_bounds__(NT) k_pattn_few(const FewParams f) {
   unsigned long long* xz = xm + R;
   uint32_t* ids = reinterpret_cast<uint32_t*>(smem + w.ids);
   const size_t block = ((size_t)blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
-  long long* sc = f.sc_smem ? reinterpret_cast<long long*>(smem + w.sc) : p.scores + block * R * f.cap;
+  long long* sc = f.sc_smem ? reinterpret_cast<long long*>(smem + w.sc) : f.scores + block * R * f.cap;
 
   const uint32_t shift = p.pool.page_shift, mask = (1u << shift) - 1, page0 = c0 >> shift;
   const uint32_t* table = p.batch.table + (size_t)seq * p.batch.stride;
@@ -472,7 +479,6 @@ uint32_t few_smem(uint32_t R, uint32_t hd, uint32_t ids, uint32_t cap, bool sc_s
 FewPlan plan_few(const ck_paged_cache& c, const ck_paged_batch& b, uint32_t heads, const DeviceFacts& f) {
   FewPlan w = {};
   const uint64_t queries = (uint64_t)b.max_new * (heads / c.kv_heads);
-  if (queries > 16) return w;
   w.R = queries == 1 ? 1 : queries == 2 ? 2 : 4;
   w.z = (uint32_t)((queries + w.R - 1) / w.R);
   // blocks of a cluster: until two an SM are there, while each has 256 positions
@@ -489,7 +495,7 @@ FewPlan plan_few(const ck_paged_cache& c, const ck_paged_batch& b, uint32_t head
   w.sc_smem = smem(true) <= (uint32_t)f.optin / 2 - 2048;
   w.smem = smem(w.sc_smem);
   w.work = w.sc_smem ? 0 : 8ull * w.cap * w.R * items * w.C;
-  w.use = w.smem <= (uint32_t)f.optin;
+  w.use = w.smem <= (uint32_t)f.optin && w.z <= 65535;
   return w;
 }
 
@@ -533,10 +539,35 @@ cudaError_t launch_few_r(const FewParams& p, const FewPlan& w, const DeviceFacts
                     : launch_few_lpp<4, NT>(p, w, f, s);
 }
 
-// Blocks of k_pattn_rows: four an SM are resident; fewer when there are fewer items.
-uint32_t rows_blocks(const ck_paged_batch& b, uint32_t heads, int sms) {
-  const uint64_t items = (uint64_t)b.rows * heads;
-  return (uint32_t)std::min<uint64_t>(items, 4ull * sms);
+// Which kernel a call takes, by the queries a key head has at most (rows x heads that share it):
+// a few go to k_pattn_few, more of head size 64 or 128 to the tensor cores, with k_pattn_rows
+// behind them for tiles with values beyond their digits; small heads in any number to
+// k_pattn_few as long as its grid holds them.
+struct AttentionPlan {
+  FewPlan few;
+  TilesPlan tiles;
+  uint32_t rows_blocks;
+  uint64_t work;
+};
+AttentionPlan attention_plan(const ck_paged_cache& c, const ck_paged_batch& b, uint32_t heads, const DeviceFacts& f) {
+  AttentionPlan w = {};
+  const uint64_t queries = (uint64_t)b.max_new * (heads / c.kv_heads);
+  if (queries > kFewQueries) w.tiles = plan_tiles(c, b, heads, f);
+  if (!w.tiles.use) w.few = plan_few(c, b, heads, f);
+  if (w.few.use) {
+    w.work = std::max<uint64_t>(align256(w.few.work), 256);  // never an empty buffer
+    return w;
+  }
+  // four blocks an SM are resident; no more than there are items or places for their scores
+  const uint64_t items = (uint64_t)b.rows * heads, line = 8ull * b.max_len;
+  w.rows_blocks = (uint32_t)std::min<uint64_t>(items, 4ull * f.sms);
+  if (w.tiles.use) {
+    w.rows_blocks = (uint32_t)std::min<uint64_t>(w.rows_blocks, (w.tiles.size - w.tiles.scores_off) / line);
+    w.work = align256(w.tiles.size);
+  } else {
+    w.work = align256(w.rows_blocks * line);
+  }
+  return w;
 }
 
 }  // namespace
@@ -552,9 +583,7 @@ int ck_paged_attention_work(const ck_paged_cache* cache, const ck_paged_batch* b
     return CK_INVALID_ARGUMENT;
   DeviceFacts f;
   CKP_CUDA(device_facts(&f));
-  const FewPlan few = plan_few(*cache, *batch, heads, f);
-  *out = align256(few.use ? few.work : 8ull * rows_blocks(*batch, heads, f.sms) * batch->max_len);
-  if (*out == 0) *out = 256;  // never an empty buffer
+  *out = attention_plan(*cache, *batch, heads, f).work;
   return CK_OK;
 }
 
@@ -570,29 +599,31 @@ int ck_paged_attention(const ck_paged_cache* cache, uint32_t layer, const ck_pag
     return CK_INVALID_ARGUMENT;
   if (overlaps(dev_out, 8 * batch->rows * q_dim, dev_q, 8 * ((batch->rows - 1) * (uint64_t)q_stride + q_dim)))
     return CK_INVALID_ARGUMENT;
-  size_t need;
-  if (const int rc = ck_paged_attention_work(cache, batch, heads, &need)) return rc;
-  if (work_len < need) return CK_BUFFER_TOO_SMALL;
   DeviceFacts f;
   CKP_CUDA(device_facts(&f));
-  PAttnParams p = {};
-  p.pool = pool_view(*cache, layer);
-  p.batch = batch_view(*batch);
-  p.q = dev_q;
-  p.q_stride = q_stride;
-  p.heads = heads;
-  p.inv_sqrt = inv_sqrt;
-  p.exp_tab = dev_exp;
-  p.out = dev_out;
-  p.scores = static_cast<long long*>(dev_work);
+  const AttentionPlan plan = attention_plan(*cache, *batch, heads, f);
+  if (work_len < plan.work) return CK_BUFFER_TOO_SMALL;
+  const PAttnParams p = {pool_view(*cache, layer), batch_view(*batch), dev_q, q_stride, heads, inv_sqrt, dev_exp, dev_out};
+  uint8_t* work = static_cast<uint8_t*>(dev_work);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const FewPlan few = plan_few(*cache, *batch, heads, f);
-  if (few.use) {
-    const FewParams fp = {p, few.cap, few.ids, few.sc_smem};
-    CKP_CUDA(few.NT == 256 ? launch_few_r<256>(fp, few, f, s) : launch_few_r<kNarrow>(fp, few, f, s));
+  if (plan.few.use) {
+    const FewParams fp = {p, reinterpret_cast<long long*>(work), plan.few.cap, plan.few.ids, plan.few.sc_smem};
+    CKP_CUDA(plan.few.NT == 256 ? launch_few_r<256>(fp, plan.few, f, s) : launch_few_r<kNarrow>(fp, plan.few, f, s));
     return CK_OK;
   }
-  k_pattn_rows<<<rows_blocks(*batch, heads, f.sms), kRowsThreads, 0, s>>>(p);
+  RowsParams rp = {p, reinterpret_cast<long long*>(work), nullptr, nullptr, 0};
+  if (plan.tiles.use) {
+    CKP_CUDA(cudaMemsetAsync(work + plan.tiles.any_off, 0, 4, s));
+    const TilesParams tp = {p, plan.tiles.tiles, plan.tiles.cap, reinterpret_cast<uint32_t*>(work + plan.tiles.any_off),
+                            reinterpret_cast<uint32_t*>(work + plan.tiles.away_off),
+                            reinterpret_cast<int32_t*>(work + plan.tiles.scores_off)};
+    CKP_CUDA(launch_tiles(tp, plan.tiles, f, s));
+    rp.scores = reinterpret_cast<long long*>(work + plan.tiles.scores_off);
+    rp.any = tp.any;
+    rp.away = tp.away;
+    rp.tiles = plan.tiles.tiles;
+  }
+  k_pattn_rows<<<plan.rows_blocks, kRowsThreads, 0, s>>>(rp);
   CKP_CUDA(cudaGetLastError());
   return CK_OK;
 }

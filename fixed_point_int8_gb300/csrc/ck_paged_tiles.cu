@@ -1,0 +1,635 @@
+// Attention of chunks of new tokens over a cache in pages, on the tensor cores ("Attention,
+// stage by stage"): 128 queries (rows x heads that share a key head) of one sequence at a time.
+//
+// Exactness.  Queries, keys and values that fit three balanced digits of 8 bits (x = d0 + 2^8 d1
+// + 2^16 d2, every d in -128 .. 127: |x| up to 127.5 with 16 fraction bits) are split into f16
+// planes, so a product is nine products of planes.  Products of digits are exact, and an f32
+// accumulator is exact while the sum of the magnitudes stays below 2^24:
+//   scores: products of equal weight share an accumulator, at most three pairs over at most 128
+//     elements: 3 * 128 * 2^14 < 2^23;
+//   values: a probability P (24 fraction bits) has the unsigned digits p0, p1, p2, and the P of
+//     a row add up to at most 2^24, so sum p1 <= 2^16 and sum p2 <= 2^8.  Over 256 positions the
+//     accumulator of weight 2^0 stays below 255 * 128 * 256, that of 2^8 below twice that (just
+//     under 2^24), that of 2^16 below 255 * 128 * 256 + 128 * 2^16 + 2^15 (under 2^24), and
+//     those of 2^24 and 2^32 together, in units of 2^24, below 2^23 + 2^15: they share one.  The
+//     planes carry powers of two (2^-12, 2^-4, 2^4) so that the products come out aligned.
+//     After 256 positions the four accumulators move into 64-bit integers.
+// The exponential depends on the row's maximum and the probability on its sum, and both are
+// floored table and quotient values that cannot be rescaled: scores go to a scratch as 32-bit
+// words (a score that does not fit, and any digit that does not, hands the tile to the kernel
+// for all values), then maximum, sum and weighted values follow in three passes.
+//
+// The vector units bound it: about 75 instructions a score against 18 tensor products of
+// 128 x N x 16.  A thread owns a row (its lane of tensor memory), so maxima and sums need no
+// exchange inside a warp.  A cluster splits a tile's positions, which fills the GPU when tiles
+// are few; it exchanges maxima, sums and the 64-bit sums of values through distributed shared
+// memory.
+#include "ck_paged_attention.cuh"
+#include "ck_tc.cuh"
+
+namespace ck {
+namespace {
+
+constexpr uint32_t kTileRows = 128, kTilePos = 32, kBlockPos = 64, kFlushBlocks = 4;
+constexpr uint32_t kDiags = 5;
+
+template <int HD>
+struct Tile {
+  static constexpr uint32_t kThreads = 4 * HD, kGroups = HD / 32;  // groups of 128 threads: a thread a row
+  static constexpr uint32_t kBufs = HD == 64 ? 1 : 2;              // score accumulators, operand buffers
+  static constexpr uint32_t kTmem = HD == 64 ? 256 : 512;          // two blocks an SM for head size 64
+  static constexpr uint32_t kScoreCol = 3 * HD / 2;                // behind the query digits
+  static constexpr uint32_t kKeyPlane = (HD / 64) * kTilePos * 128, kKeyBuf = 3 * kKeyPlane;
+  static constexpr uint32_t kProbPlane = kTileRows * 128, kValuePlane = HD * 128;
+  static constexpr uint32_t kValueBuf = 3 * (kProbPlane + kValuePlane);
+  static constexpr uint32_t kPitch = kTileRows + 1;  // of the 64-bit sums, [element][row]
+  static constexpr uint32_t max3(uint32_t a, uint32_t b, uint32_t c) {
+    return a > b ? (a > c ? a : c) : (b > c ? b : c);
+  }
+  static constexpr uint32_t kOperands = (max3(2 * kKeyBuf, kBufs * kValueBuf, HD * kPitch * 8) + 1023) & ~1023u;
+  static constexpr uint32_t kTableOff = kOperands, kTableBytes = 4097 * 4 + 12;
+  static constexpr uint32_t kRedOff = kTableOff + kTableBytes;   // [groups][128] u64
+  static constexpr uint32_t kMaxOff = kRedOff + kGroups * kTileRows * 8;  // [128] i32
+  static constexpr uint32_t kSumOff = kMaxOff + kTileRows * 4;   // [128] u64
+  static constexpr uint32_t kMiscOff = kSumOff + kTileRows * 8;  // barrier, tensor memory, flags
+  static constexpr uint32_t kSmem = kMiscOff + 64 + 1024;        // + alignment of the operands
+  static_assert(kScoreCol + kBufs * kDiags * kTilePos <= kTmem && 4 * HD <= kTmem, "tensor memory");
+};
+
+__device__ __forceinline__ uint32_t tile_idesc(uint32_t n) { return (1u << 4) | ((n >> 3) << 17) | ((kTileRows >> 4) << 24); }
+
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }"
+      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }"
+      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_operands() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_ld8(uint32_t addr, uint32_t* v) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "r"(addr));
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+      "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+// Balanced digits: the bytes of x + 0x808080 are the digits plus 128, when x fits them.
+__device__ __forceinline__ uint32_t biased(int32_t x) { return (uint32_t)x + 0x808080u; }
+// Two digit bytes at nibble selectors of w as f16: 0x64BB is 1024 + BB exactly.
+template <uint32_t SEL>
+__device__ __forceinline__ uint32_t lift(uint32_t w) {
+  return __byte_perm(w, 0x64646464u, SEL);
+}
+__device__ __forceinline__ uint32_t sub_1152(uint32_t h) {  // balanced digits, unscaled
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(0x64806480u));
+  return r;
+}
+__device__ __forceinline__ uint32_t fma_h2(uint32_t h, uint32_t scale, uint32_t bias) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(h), "r"(scale), "r"(bias));
+  return r;
+}
+// f16 pairs of the plane scales 2^-12, 2^-4, 2^4 and of the offsets they take away:
+// 1152 * scale for balanced digits, 1024 * scale for unsigned ones (all exact).
+constexpr uint32_t kScale0 = 0x0C000C00u, kScale1 = 0x2C002C00u, kScale2 = 0x4C004C00u;
+constexpr uint32_t kBal0 = 0xB480B480u, kBal1 = 0xD480D480u, kBal2 = 0xF480F480u;   // -0.28125, -72, -18432
+constexpr uint32_t kUns0 = 0xB400B400u, kUns1 = 0xD400D400u, kUns2 = 0xF400F400u;   // -0.25, -64, -16384
+
+__device__ __forceinline__ uint32_t peer32(const void* p, uint32_t rank) {
+  uint32_t a, v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ unsigned long long peer64(const void* p, uint32_t rank) {
+  uint32_t a;
+  unsigned long long v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void all_sync(uint32_t C) {  // the cluster's threads, or the block's
+  if (C > 1)
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  else
+    __syncthreads();
+}
+
+template <int HD>
+__global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_tiles(const TilesParams f) {
+  using T = Tile<HD>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* sm = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  const PAttnParams& p = f.a;
+  const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t cg = warp >> 2, r = 32 * (warp & 3) + lane;  // column group and row of this thread
+  const uint32_t lane_base = (32 * (warp & 3)) << 16;
+  uint32_t C, rank, clusters, cluster;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(C));
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  asm("mov.u32 %0, %%nclusterid.x;" : "=r"(clusters));
+  asm("mov.u32 %0, %%clusterid.x;" : "=r"(cluster));
+  uint32_t* table_s = reinterpret_cast<uint32_t*>(sm + T::kTableOff);
+  unsigned long long* red = reinterpret_cast<unsigned long long*>(sm + T::kRedOff);
+  int32_t* xmax = reinterpret_cast<int32_t*>(sm + T::kMaxOff);
+  unsigned long long* xsum = reinterpret_cast<unsigned long long*>(sm + T::kSumOff);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(sm + T::kMiscOff);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + T::kMiscOff + 8);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + T::kMiscOff + 12);
+  uint32_t* bad_s = reinterpret_cast<uint32_t*>(sm + T::kMiscOff + 16);  // this block's reason to give the tile away
+
+  for (uint32_t i = tid; i < 4097; i += T::kThreads) table_s[i] = min(__ldg(p.exp_tab + i), 1u << 30);
+  if (tid == 0) {
+    mb_init(bar, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                 ::"r"(smem_addr(tmem_slot)), "r"(T::kTmem) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = *tmem_slot;
+  uint32_t done = 0;  // tensor batches waited for: the barrier's parity
+  auto wait_mma = [&] {
+    mb_wait(bar, done & 1u, const_cast<volatile int*>(abort_flag));
+    ++done;
+    tc_after();
+  };
+
+  const uint32_t shift = p.pool.page_shift, pmask = (1u << shift) - 1;
+  const uint32_t group = p.heads / p.pool.kv_heads;
+  int32_t* scores = f.scores + (size_t)blockIdx.x * f.cap * kTileRows;  // [position][row]
+  const uint64_t per_seq = (uint64_t)p.pool.kv_heads * f.tiles;
+  const uint64_t items = (uint64_t)p.batch.seqs * per_seq;
+
+  for (uint64_t item = cluster; item < items; item += clusters) {
+    const uint32_t seq = (uint32_t)(item / per_seq), rest = (uint32_t)(item - seq * per_seq);
+    const uint32_t kvh = rest / f.tiles, v0 = (rest - kvh * f.tiles) * kTileRows;
+    const Sequence sq = load_sequence(p.batch, seq, shift);
+    if (!sq.ok) {
+      if (tid == 0 && rank == 0) note(p.batch, seq, err_key(0, p.pool.layer, CK_PAGED_BAD_SEQUENCE, 0));
+      continue;
+    }
+    const uint32_t queries = sq.count * group;
+    if (v0 >= queries) continue;
+    const uint32_t v = v0 + r, last = min(queries, v0 + kTileRows) - 1;
+    auto seen_by = [&](uint32_t q) {  // positions query q sees
+      const uint32_t up = q / group + sq.len;
+      return up >= sq.count ? up - sq.count + 1 : 0;
+    };
+    const uint32_t top = seen_by(last), np = v < queries ? seen_by(v) : 0;
+    const uint32_t per = ((top + C - 1) / C + kBlockPos - 1) & ~(kBlockPos - 1);
+    const uint32_t c0 = min(top, rank * per), n = min(top, c0 + per) - c0;
+    const uint32_t lim = np > c0 ? min(n, np - c0) : 0;  // positions of this block that the row sees
+    const uint32_t* table = p.batch.table + (size_t)seq * p.batch.stride;
+    if (tid == 0) *bad_s = 0;
+    uint32_t bad = 0;
+    __syncthreads();
+
+    // ---- query digits into tensor memory: a thread's row, 32 elements
+    {
+      uint32_t w[3][16];
+      const int64_t* q = p.q + (size_t)(sq.first + v / group) * p.q_stride +
+                         (size_t)(kvh * group + v % group) * HD + 32 * cg;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        longlong2 x = make_longlong2(0, 0);
+        if (v < queries) x = __ldg(reinterpret_cast<const longlong2*>(q) + i);
+        const uint64_t a = (uint64_t)x.x + 0x808080u, b = (uint64_t)x.y + 0x808080u;
+        bad |= (uint32_t)((a | b) >> 24 != 0);
+        const uint32_t u = __byte_perm((uint32_t)a, (uint32_t)b, 0x5410), t = __byte_perm((uint32_t)a, (uint32_t)b, 0x7632);
+        w[0][i] = sub_1152(lift<0x4240>(u));
+        w[1][i] = sub_1152(lift<0x4341>(u));
+        w[2][i] = sub_1152(lift<0x4240>(t));
+      }
+#pragma unroll
+      for (int k = 0; k < 3; ++k) tmem_st16(tmem + lane_base + k * (HD / 2) + 16 * cg, w[k]);
+      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+    }
+
+    // ---- scores: 32 positions at a time
+    const uint32_t nt = (n + kTilePos - 1) / kTilePos;
+    const uint32_t kpos = tid / (HD / 8), kchunk = tid % (HD / 8);
+    int4 raw[2];
+    auto load_keys = [&](uint32_t i) {
+      const uint32_t at = i * kTilePos + kpos;
+      raw[0] = raw[1] = make_int4(0, 0, 0, 0);
+      if (at < n) {
+        const uint32_t t = c0 + at, id = __ldg(table + (t >> shift));
+        if (id < p.pool.pages) {
+          const int4* src = reinterpret_cast<const int4*>(p.pool.k + page_word(p.pool, id, kvh) +
+                                                          (size_t)(t & pmask) * HD + 8 * kchunk);
+          raw[0] = __ldg(src);
+          raw[1] = __ldg(src + 1);
+        } else if ((t & pmask) == 0 || at == 0) {
+          note(p.batch, seq, err_key((t >> shift) << shift, p.pool.layer, CK_PAGED_BAD_PAGE, 0));
+        }
+      }
+    };
+    auto put_keys = [&](uint32_t buf) {
+      const uint32_t y[8] = {biased(raw[0].x), biased(raw[0].y), biased(raw[0].z), biased(raw[0].w),
+                             biased(raw[1].x), biased(raw[1].y), biased(raw[1].z), biased(raw[1].w)};
+      uint32_t d[3][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t a = y[2 * i], b = y[2 * i + 1];
+        bad |= (a | b) >> 24;
+        const uint32_t u = __byte_perm(a, b, 0x5410), t = __byte_perm(a, b, 0x7632);
+        d[0][i] = sub_1152(lift<0x4240>(u));
+        d[1][i] = sub_1152(lift<0x4341>(u));
+        d[2][i] = sub_1152(lift<0x4240>(t));
+      }
+      uint8_t* dst = sm + buf * T::kKeyBuf + (kchunk >> 3) * (kTilePos * 128) + kpos * 128 +
+                     (((kchunk & 7u) ^ (kpos & 7u)) << 4);
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        *reinterpret_cast<uint4*>(dst + k * T::kKeyPlane) = make_uint4(d[k][0], d[k][1], d[k][2], d[k][3]);
+      fence_operands();
+    };
+    auto issue_scores = [&](uint32_t i) {  // one thread
+      const uint32_t d0 = tmem + T::kScoreCol + (i % T::kBufs) * (kDiags * kTilePos);
+      const uint32_t b0 = smem_addr(sm) + (i & 1u) * T::kKeyBuf;
+#pragma unroll
+      for (uint32_t g = 0; g < kDiags; ++g) {
+        uint32_t acc = 0;
+#pragma unroll
+        for (uint32_t qp = g > 2 ? g - 2 : 0; qp <= (g < 2 ? g : 2); ++qp) {
+#pragma unroll
+          for (uint32_t kk = 0; kk < HD / 16; ++kk) {
+            mma_ts(d0 + g * kTilePos, tmem + qp * (HD / 2) + 8 * kk,
+                   smem_desc(b0 + (g - qp) * T::kKeyPlane + (kk >> 2) * (kTilePos * 128) + (kk & 3u) * 32),
+                   tile_idesc(kTilePos), acc);
+            acc = 1;
+          }
+        }
+      }
+      mma_commit(bar);
+    };
+    int32_t m = INT32_MIN;
+    constexpr uint32_t kCols = kTilePos / T::kGroups;  // columns a thread drains
+    auto drain_scores = [&](uint32_t i) {
+      const uint32_t base = tmem + lane_base + T::kScoreCol + (i % T::kBufs) * (kDiags * kTilePos) + cg * kCols;
+#pragma unroll
+      for (uint32_t h = 0; h < kCols; h += 8) {
+        uint32_t d[kDiags][8];
+#pragma unroll
+        for (uint32_t g = 0; g < kDiags; ++g) tmem_ld8(base + g * kTilePos + h, d[g]);
+        tmem_wait_ld();
+        const uint32_t at = i * kTilePos + cg * kCols + h;
+        int32_t* dst = scores + (size_t)at * kTileRows + r;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          // (sum of the accumulators by weight) >> 16, the low part in 32 bits
+          const int32_t lo = __float2int_rn(__uint_as_float(d[0][j])) + (__float2int_rn(__uint_as_float(d[1][j])) << 8);
+          const int32_t mid = (lo >> 16) + __float2int_rn(__uint_as_float(d[2][j])) +
+                              (__float2int_rn(__uint_as_float(d[3][j])) << 8);
+          const int64_t dot = (int64_t)mid + ((int64_t)__float2int_rn(__uint_as_float(d[4][j])) << 16);
+          const int64_t s = wmul(dot, (int64_t)p.inv_sqrt) >> 24;
+          int32_t c = (int32_t)s;
+          if (c != s) c = s < 0 ? INT32_MIN : INT32_MAX;
+          dst[j * kTileRows] = c;
+          if (at + j < lim) m = max(m, c);
+        }
+      }
+      tc_before();
+    };
+    if (nt) {
+      load_keys(0);
+      put_keys(0);
+      if (nt > 1) load_keys(1);
+    }
+    tc_before();
+    __syncthreads();
+    if (tid == 0 && nt) {
+      tc_after();
+      issue_scores(0);
+    }
+    for (uint32_t i = 0; i < nt; ++i) {
+      if (i + 1 < nt) {
+        put_keys((i + 1) & 1u);
+        if (i + 2 < nt) load_keys(i + 2);
+      }
+      if (T::kBufs == 2) {
+        wait_mma();
+        __syncthreads();  // the next tile's digits are in place, its accumulators drained
+        if (tid == 0 && i + 1 < nt) {
+          tc_after();
+          issue_scores(i + 1);
+        }
+        drain_scores(i);
+      } else {
+        wait_mma();
+        drain_scores(i);
+        __syncthreads();
+        if (tid == 0 && i + 1 < nt) {
+          tc_after();
+          issue_scores(i + 1);
+        }
+      }
+    }
+
+    // ---- the row's maximum, over the column groups and the cluster
+    int32_t* redm = reinterpret_cast<int32_t*>(red);
+    redm[cg * kTileRows + r] = m;
+    if (bad) *bad_s = 1;
+    __syncthreads();
+    if (tid < kTileRows) {
+      for (uint32_t g = 1; g < T::kGroups; ++g) m = max(m, redm[g * kTileRows + tid]);
+      xmax[tid] = m;
+    }
+    all_sync(C);
+    m = xmax[r];
+    uint32_t away = *bad_s;
+    for (uint32_t k = 0; C > 1 && k < C; ++k) {
+      m = max(m, (int32_t)peer32(xmax + r, k));
+      away |= peer32(bad_s, k);
+    }
+    // a maximum at either end of 32 bits: a score may have been cut that counts
+    away |= (uint32_t)(np != 0 && (m == INT32_MAX || m < INT32_MIN + (1 << 21)));
+    away = (uint32_t)__syncthreads_or((int)away);  // (the same rows, so the same in every block)
+
+    // ---- the sum of exponentials
+    unsigned long long z = 0;
+    if (!away) {
+      const int32_t* src = scores + r;
+#pragma unroll 8
+      for (uint32_t i = cg; i < lim; i += T::kGroups)
+        z += table_s[min(((uint32_t)m - (uint32_t)src[(size_t)i * kTileRows]) >> 8, 4096u)];
+    }
+    red[cg * kTileRows + r] = z;
+    __syncthreads();
+    if (tid < kTileRows) {
+      for (uint32_t g = 1; g < T::kGroups; ++g) z += red[g * kTileRows + tid];
+      xsum[tid] = z;
+    }
+    all_sync(C);
+    z = C > 1 ? 0 : xsum[r];
+    for (uint32_t k = 0; C > 1 && k < C; ++k) z += peer64(xsum + r, k);
+    if (z < (1ull << 30)) z = 1ull << 30;
+    const uint32_t rz = (uint32_t)((1ull << 61) / z);
+
+    // ---- weighted values: 64 positions at a time
+    unsigned long long acc[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) acc[j] = 0;
+    const uint32_t nb = away ? 0 : (n + kBlockPos - 1) / kBlockPos;
+    const uint32_t vchunk = tid & 7u, vpair = tid >> 3;  // eight positions, two elements
+    int2 vraw[8];
+    auto load_values = [&](uint32_t b) {
+      const uint32_t at = b * kBlockPos + vchunk * 8;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) vraw[j] = make_int2(0, 0);
+      if (at < n) {
+        const uint32_t t = c0 + at, id = __ldg(table + (t >> shift));  // a page holds whole chunks of eight
+        if (id < p.pool.pages) {
+          const int2* src = reinterpret_cast<const int2*>(p.pool.v + page_word(p.pool, id, kvh) +
+                                                          (size_t)(t & pmask) * HD + 2 * vpair);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (at + j < n) vraw[j] = __ldg(src + j * (HD / 2));
+        }
+      }
+    };
+    auto put_values = [&](uint8_t* planes) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        uint32_t d[3][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t a = biased(e ? vraw[2 * i].y : vraw[2 * i].x);
+          const uint32_t b = biased(e ? vraw[2 * i + 1].y : vraw[2 * i + 1].x);
+          bad |= (a | b) >> 24;
+          const uint32_t u = __byte_perm(a, b, 0x5410), t = __byte_perm(a, b, 0x7632);
+          d[0][i] = fma_h2(lift<0x4240>(u), kScale0, kBal0);
+          d[1][i] = fma_h2(lift<0x4341>(u), kScale1, kBal1);
+          d[2][i] = fma_h2(lift<0x4240>(t), kScale2, kBal2);
+        }
+        const uint32_t row = 2 * vpair + e;
+        uint8_t* dst = planes + row * 128 + ((vchunk ^ (row & 7u)) << 4);
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+          *reinterpret_cast<uint4*>(dst + k * T::kValuePlane) = make_uint4(d[k][0], d[k][1], d[k][2], d[k][3]);
+      }
+    };
+    auto put_probs = [&](uint32_t b, uint8_t* planes) {
+      constexpr uint32_t kChunks = 8 / T::kGroups;
+#pragma unroll
+      for (uint32_t c = 0; c < kChunks; ++c) {
+        const uint32_t chunk = cg * kChunks + c, at = b * kBlockPos + chunk * 8;
+        const int32_t* src = scores + (size_t)at * kTileRows + r;
+        uint32_t s[8], pr[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] = at + j < lim ? (uint32_t)src[j * kTileRows] : 0u;
+        uint32_t full = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t e = table_s[min(((uint32_t)m - s[j]) >> 8, 4096u)];
+          // floor((e << 24) / z): rz is below 2^61 / z by less than one, so the estimate is short
+          // by less than 2^-7 and wrong only when its fraction ends that close to the next integer
+          const unsigned long long w = (unsigned long long)e * rz;
+          uint32_t q = (uint32_t)(w >> 37);
+          if ((((uint32_t)(w >> 30)) & 0x7Fu) == 0x7Fu) {
+            const unsigned long long rem = ((unsigned long long)e << 24) - (unsigned long long)q * z;
+            q += rem >= z;
+          }
+          pr[j] = at + j < lim ? q : 0u;
+          full |= pr[j];
+        }
+        uint32_t d[3][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t a = pr[2 * i], bq = pr[2 * i + 1];
+          uint32_t extra = 0;
+          if (full >> 24) {  // P = 2^24 is 0xFFFFFF and one more in the lowest digit (2^-12 in its plane)
+            extra = (a >> 24 ? 0x0C00u : 0u) | (bq >> 24 ? 0x0C000000u : 0u);
+            a -= a >> 24;
+            bq -= bq >> 24;
+          }
+          const uint32_t u = __byte_perm(a, bq, 0x5410), t = __byte_perm(a, bq, 0x7632);
+          d[0][i] = fma_h2(lift<0x4240>(u), kScale0, kUns0);
+          d[1][i] = fma_h2(lift<0x4341>(u), kScale1, kUns1);
+          d[2][i] = fma_h2(lift<0x4240>(t), kScale2, kUns2);
+          if (full >> 24) asm("add.rn.f16x2 %0, %0, %1;" : "+r"(d[0][i]) : "r"(extra));
+        }
+        uint8_t* dst = planes + r * 128 + ((chunk ^ (r & 7u)) << 4);
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+          *reinterpret_cast<uint4*>(dst + k * T::kProbPlane) = make_uint4(d[k][0], d[k][1], d[k][2], d[k][3]);
+      }
+    };
+    auto issue_values = [&](uint32_t b, const uint8_t* planes) {
+      const uint32_t a0 = smem_addr(planes), b0 = a0 + 3 * T::kProbPlane;
+      const uint32_t fresh = b % kFlushBlocks == 0 ? 0u : 1u;
+#pragma unroll
+      for (uint32_t g = 0; g < 4; ++g) {
+        uint32_t accumulate = fresh;
+#pragma unroll
+        for (uint32_t pp = g > 2 ? g - 2 : 0; pp <= 2; ++pp) {
+          // planes of weight g; the last accumulator also takes weight 4
+#pragma unroll
+          for (uint32_t vp = 0; vp < 3; ++vp) {
+            if (pp + vp != g && !(g == 3 && pp + vp == 4)) continue;
+#pragma unroll
+            for (uint32_t kk = 0; kk < kBlockPos / 16; ++kk) {
+              mma_ss(tmem + g * HD, smem_desc(a0 + pp * T::kProbPlane + kk * 32),
+                     smem_desc(b0 + vp * T::kValuePlane + kk * 32), tile_idesc(HD), accumulate);
+              accumulate = 1;
+            }
+          }
+        }
+      }
+      mma_commit(bar);
+    };
+    auto flush = [&] {
+#pragma unroll
+      for (uint32_t h = 0; h < 32; h += 8) {
+        uint32_t d[4][8];
+#pragma unroll
+        for (uint32_t g = 0; g < 4; ++g) tmem_ld8(tmem + lane_base + g * HD + 32 * cg + h, d[g]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          long long t = (long long)acc[h + j];
+          t += __float2int_rn(__uint_as_float(d[0][j]) * 16777216.0f);
+          t += (long long)__float2int_rn(__uint_as_float(d[1][j]) * 65536.0f) * 256;
+          t += (long long)__float2int_rn(__uint_as_float(d[2][j]) * 256.0f) * 65536;
+          t += (long long)__float2int_rn(__uint_as_float(d[3][j])) * 16777216;
+          acc[h + j] = (unsigned long long)t;
+        }
+      }
+      tc_before();
+    };
+    if (nb) load_values(0);
+    for (uint32_t b = 0; b < nb; ++b) {
+      uint8_t* planes = sm + (b % T::kBufs) * T::kValueBuf;
+      if (T::kBufs == 1 && b > 0) {
+        // the one buffer is free once the block before is through
+        wait_mma();
+        if (b % kFlushBlocks == 0) flush();
+      }
+      put_values(planes + 3 * T::kProbPlane);
+      if (b + 1 < nb) load_values(b + 1);
+      put_probs(b, planes);
+      fence_operands();
+      if (T::kBufs == 2 && b > 0) {
+        wait_mma();
+        if (b % kFlushBlocks == 0) flush();
+      }
+      __syncthreads();
+      if (tid == 0) {
+        tc_after();
+        issue_values(b, planes);
+      }
+    }
+    if (nb) {
+      wait_mma();
+      flush();
+    }
+    if (bad) *bad_s = 1;
+    if (tid == 0 && *abort_flag) *bad_s = 1;
+    __syncthreads();  // the last products have read the operands' place
+
+    // ---- the cluster's sums, a slice of the rows each block
+    unsigned long long* sums = reinterpret_cast<unsigned long long*>(sm);
+    if (!away) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) sums[(size_t)(32 * cg + j) * T::kPitch + r] = acc[j];
+    }
+    all_sync(C);
+    away |= *bad_s;
+    for (uint32_t k = 0; C > 1 && k < C; ++k) away |= peer32(bad_s, k);
+    const uint32_t rows = kTileRows / C;
+    for (uint32_t i = tid; !away && i < rows * HD; i += T::kThreads) {
+      const uint32_t row = rank * rows + i / HD, e = i % HD, q = v0 + row;
+      if (q >= queries) break;
+      unsigned long long t = 0;
+      if (C > 1)
+        for (uint32_t k = 0; k < C; ++k) t += peer64(sums + (size_t)e * T::kPitch + row, k);
+      else
+        t = sums[(size_t)e * T::kPitch + row];
+      p.out[((size_t)(sq.first + q / group) * p.heads + kvh * group + q % group) * HD + e] = (long long)t >> 24;
+    }
+    if (rank == 0 && tid == 0) {
+      f.away[item] = away;
+      if (away) atomicAdd(f.any, 1u);
+    }
+    all_sync(C);  // no block goes on while another reads its sums or flags
+  }
+  tc_before();
+  __syncthreads();
+  if (warp == 0)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(T::kTmem) : "memory");
+}
+
+template <int HD>
+cudaError_t launch_tiles_hd(const TilesParams& p, const TilesPlan& w, const DeviceFacts& f, cudaStream_t s) {
+  static std::atomic<bool> ready[64];
+  if (!ready[f.dev].load(std::memory_order_relaxed)) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(k_pattn_tiles<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, Tile<HD>::kSmem);
+    if (e != cudaSuccess) return e;
+    ready[f.dev].store(true, std::memory_order_relaxed);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(w.clusters * w.C);
+  cfg.blockDim = dim3(Tile<HD>::kThreads);
+  cfg.dynamicSmemBytes = Tile<HD>::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = w.C;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_pattn_tiles<HD>, p);
+}
+
+}  // namespace
+
+TilesPlan plan_tiles(const ck_paged_cache& c, const ck_paged_batch& b, uint32_t heads, const DeviceFacts& f) {
+  TilesPlan w = {};
+  const uint64_t queries = (uint64_t)b.max_new * (heads / c.kv_heads);
+  if (c.head_dim != 64 && c.head_dim != 128) return w;
+  const uint32_t smem = c.head_dim == 64 ? Tile<64>::kSmem : Tile<128>::kSmem;
+  if (smem > (uint32_t)f.optin) return w;
+  const uint32_t slots = (uint32_t)f.sms * (c.head_dim == 64 ? 2 : 1);
+  w.tiles = (uint32_t)((queries + kTileRows - 1) / kTileRows);
+  const uint64_t items = (uint64_t)b.seqs * c.kv_heads * w.tiles;
+  // blocks of a cluster: until every place on the GPU has one, while each has 256 positions
+  w.C = 1;
+  while (w.C < 8 && items * w.C < slots && b.max_len / (2 * w.C) >= 256) w.C *= 2;
+  w.clusters = (uint32_t)std::min<uint64_t>(items, std::max(1u, slots / w.C));
+  w.cap = ((b.max_len + w.C - 1) / w.C + kBlockPos - 1) & ~(kBlockPos - 1);
+  w.any_off = 0;
+  w.away_off = 256;
+  w.scores_off = w.away_off + align256(4 * items);
+  w.size = w.scores_off + 4ull * kTileRows * w.cap * w.clusters * w.C;
+  w.use = true;
+  return w;
+}
+
+cudaError_t launch_tiles(const TilesParams& p, const TilesPlan& w, const DeviceFacts& f, cudaStream_t s) {
+  return p.a.pool.hd == 64 ? launch_tiles_hd<64>(p, w, f, s) : launch_tiles_hd<128>(p, w, f, s);
+}
+
+}  // namespace ck
