@@ -562,7 +562,7 @@ AttentionPlan attention_plan(const ck_paged_cache& c, const ck_paged_batch& b, u
   const uint64_t items = (uint64_t)b.rows * heads, line = 8ull * b.max_len;
   w.rows_blocks = (uint32_t)std::min<uint64_t>(items, 4ull * f.sms);
   if (w.tiles.use) {
-    w.rows_blocks = (uint32_t)std::min<uint64_t>(w.rows_blocks, (w.tiles.size - w.tiles.scores_off) / line);
+    w.rows_blocks = (uint32_t)std::min<uint64_t>(w.rows_blocks, (w.tiles.sums_off - w.tiles.scores_off) / line);
     w.work = align256(w.tiles.size);
   } else {
     w.work = align256(w.rows_blocks * line);
@@ -616,7 +616,8 @@ int ck_paged_attention(const ck_paged_cache* cache, uint32_t layer, const ck_pag
     CKP_CUDA(cudaMemsetAsync(work + plan.tiles.any_off, 0, 4, s));
     const TilesParams tp = {p, plan.tiles.tiles, plan.tiles.cap, reinterpret_cast<uint32_t*>(work + plan.tiles.any_off),
                             reinterpret_cast<uint32_t*>(work + plan.tiles.away_off),
-                            reinterpret_cast<int32_t*>(work + plan.tiles.scores_off)};
+                            reinterpret_cast<int32_t*>(work + plan.tiles.scores_off),
+                            reinterpret_cast<ulonglong2*>(work + plan.tiles.sums_off)};
     CKP_CUDA(launch_tiles(tp, plan.tiles, f, s));
     rp.scores = reinterpret_cast<long long*>(work + plan.tiles.scores_off);
     rp.any = tp.any;

@@ -16,11 +16,11 @@ struct PAttnParams {
 };
 
 // Tiles of 128 queries.  Scratch: a count of the tiles left to the kernel for all values and
-// a word a tile, then each block's scores.
+// a word a tile, then each block's scores and the sums it keeps between flushes.
 struct TilesPlan {
   bool use;
   uint32_t tiles, C, clusters, cap;
-  uint64_t any_off, away_off, scores_off, size;
+  uint64_t any_off, away_off, scores_off, sums_off, size;
 };
 struct TilesParams {
   PAttnParams a;
@@ -28,6 +28,7 @@ struct TilesParams {
   uint32_t* any;
   uint32_t* away;  // [sequence][key head][tile]
   int32_t* scores;
+  ulonglong2* sums;
 };
 TilesPlan plan_tiles(const ck_paged_cache& c, const ck_paged_batch& b, uint32_t heads, const DeviceFacts& f);
 cudaError_t launch_tiles(const TilesParams& p, const TilesPlan& w, const DeviceFacts& f, cudaStream_t s);

@@ -35,7 +35,8 @@ constexpr uint32_t kDiags = 5;
 
 template <int HD>
 struct Tile {
-  static constexpr uint32_t kThreads = 4 * HD, kGroups = HD / 32;  // groups of 128 threads: a thread a row
+  // groups of 128 threads, in each a thread a row
+  static constexpr uint32_t kThreads = 4 * HD, kGroups = HD / 32;
   static constexpr uint32_t kBufs = HD == 64 ? 1 : 2;              // score accumulators, operand buffers
   static constexpr uint32_t kTmem = HD == 64 ? 256 : 512;          // two blocks an SM for head size 64
   static constexpr uint32_t kScoreCol = 3 * HD / 2;                // behind the query digits
@@ -58,17 +59,34 @@ struct Tile {
 
 __device__ __forceinline__ uint32_t tile_idesc(uint32_t n) { return (1u << 4) | ((n >> 3) << 17) | ((kTileRows >> 4) << 24); }
 
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// One product, issued by the warp's elected lane: the whole warp computes the operands, so that
+// they stay in uniform registers (a branch of one lane would move each there by itself, which
+// measured 68 cycles a product against about 20).
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }"
-      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{ .reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }"
+      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(leader)
       : "memory");
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }"
-      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{ .reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }"
+      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(leader)
       : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t leader, uint64_t* bar) {
+  asm volatile(
+      "{ .reg .pred q; setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }"
+      ::"r"(smem_addr(bar)), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t elected() {
+  uint32_t e;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xFFFFFFFF; selp.u32 %0, 1, 0, p; }" : "=r"(e));
+  return e;
 }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -149,14 +167,22 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
   unsigned long long* red = reinterpret_cast<unsigned long long*>(sm + T::kRedOff);
   int32_t* xmax = reinterpret_cast<int32_t*>(sm + T::kMaxOff);
   unsigned long long* xsum = reinterpret_cast<unsigned long long*>(sm + T::kSumOff);
-  uint64_t* bar = reinterpret_cast<uint64_t*>(sm + T::kMiscOff);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + T::kMiscOff + 8);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + T::kMiscOff + 12);
-  uint32_t* bad_s = reinterpret_cast<uint32_t*>(sm + T::kMiscOff + 16);  // this block's reason to give the tile away
+  // Barriers, two of a kind used in turn: operands of a batch of products in place (and the
+  // accumulators free), the products done, a tile's accumulators drained.
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + T::kMiscOff);
+  uint64_t* done = full + 2;
+  uint64_t* drained = full + 4;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + T::kMiscOff + 48);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + T::kMiscOff + 52);
+  uint32_t* bad_s = reinterpret_cast<uint32_t*>(sm + T::kMiscOff + 56);  // this block's reason to give the tile away
 
   for (uint32_t i = tid; i < 4097; i += T::kThreads) table_s[i] = min(__ldg(p.exp_tab + i), 1u << 30);
   if (tid == 0) {
-    mb_init(bar, 1);
+    for (int i = 0; i < 2; ++i) {
+      mb_init(full + i, T::kThreads / 32);
+      mb_init(done + i, 1);
+      mb_init(drained + i, T::kThreads / 32);
+    }
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -168,17 +194,26 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
   tc_before();
   __syncthreads();
   tc_after();
-  const uint32_t tmem = *tmem_slot;
-  uint32_t done = 0;  // tensor batches waited for: the barrier's parity
-  auto wait_mma = [&] {
-    mb_wait(bar, done & 1u, const_cast<volatile int*>(abort_flag));
-    ++done;
-    tc_after();
+  const uint32_t tmem = *tmem_slot, tmem_u = __shfl_sync(0xffffffffu, tmem, 0);
+  const uint32_t warp_u = __shfl_sync(0xffffffffu, warp, 0);  // known to be the same in the warp
+  const uint64_t operands = smem_desc(smem_addr(sm));
+  constexpr uint32_t kWarps = T::kThreads / 32;
+  uint32_t batch = 0, tiles = 0;  // batches of products and tiles so far: the barriers' phases
+  auto wait_full = [&](uint32_t g) { mb_wait(full + (g & 1u), (g >> 1) & 1u, const_cast<volatile int*>(abort_flag)); tc_after(); };
+  auto wait_done = [&](uint32_t g) { mb_wait(done + (g & 1u), (g >> 1) & 1u, const_cast<volatile int*>(abort_flag)); tc_after(); };
+  auto wait_drained = [&](uint32_t g) { mb_wait(drained + (g & 1u), (g >> 1) & 1u, const_cast<volatile int*>(abort_flag)); tc_after(); };
+  auto arrive = [&](uint64_t* b) {  // this warp's accesses so far come before the phase
+    tc_before();
+    __syncwarp();
+    if (lane == 0) mb_arrive(b);
   };
 
   const uint32_t shift = p.pool.page_shift, pmask = (1u << shift) - 1;
   const uint32_t group = p.heads / p.pool.kv_heads;
-  int32_t* scores = f.scores + (size_t)blockIdx.x * f.cap * kTileRows;  // [position][row]
+  // [position / 4][row][4]: a thread writes and reads four positions of its row at once
+  int4* scores = reinterpret_cast<int4*>(f.scores) + (size_t)blockIdx.x * (f.cap / 4) * kTileRows;
+  // [pair of elements][thread]: the 64-bit sums between flushes
+  ulonglong2* kept = f.sums + (size_t)blockIdx.x * 16 * T::kThreads + tid;
   const uint64_t per_seq = (uint64_t)p.pool.kv_heads * f.tiles;
   const uint64_t items = (uint64_t)p.batch.seqs * per_seq;
 
@@ -201,21 +236,24 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
     const uint32_t per = ((top + C - 1) / C + kBlockPos - 1) & ~(kBlockPos - 1);
     const uint32_t c0 = min(top, rank * per), n = min(top, c0 + per) - c0;
     const uint32_t lim = np > c0 ? min(n, np - c0) : 0;  // positions of this block that the row sees
+    const uint32_t nt = (n + kTilePos - 1) / kTilePos, all_blocks = (n + kBlockPos - 1) / kBlockPos;
     const uint32_t* table = p.batch.table + (size_t)seq * p.batch.stride;
     if (tid == 0) *bad_s = 0;
-    uint32_t bad = 0;
+    uint32_t bad = 0, away = 0;
     __syncthreads();
 
     // ---- query digits into tensor memory: a thread's row, 32 elements
     {
-      uint32_t w[3][16];
       const int64_t* q = p.q + (size_t)(sq.first + v / group) * p.q_stride +
                          (size_t)(kvh * group + v % group) * HD + 32 * cg;
+      longlong2 x[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        x[i] = v < queries ? __ldg(reinterpret_cast<const longlong2*>(q) + i) : make_longlong2(0, 0);
+      uint32_t w[3][16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        longlong2 x = make_longlong2(0, 0);
-        if (v < queries) x = __ldg(reinterpret_cast<const longlong2*>(q) + i);
-        const uint64_t a = (uint64_t)x.x + 0x808080u, b = (uint64_t)x.y + 0x808080u;
+        const uint64_t a = (uint64_t)x[i].x + 0x808080u, b = (uint64_t)x[i].y + 0x808080u;
         bad |= (uint32_t)((a | b) >> 24 != 0);
         const uint32_t u = __byte_perm((uint32_t)a, (uint32_t)b, 0x5410), t = __byte_perm((uint32_t)a, (uint32_t)b, 0x7632);
         w[0][i] = sub_1152(lift<0x4240>(u));
@@ -228,23 +266,24 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
     }
 
     // ---- scores: 32 positions at a time
-    const uint32_t nt = (n + kTilePos - 1) / kTilePos;
     const uint32_t kpos = tid / (HD / 8), kchunk = tid % (HD / 8);
     int4 raw[2];
-    auto load_keys = [&](uint32_t i) {
-      const uint32_t at = i * kTilePos + kpos;
+    uint32_t next_id = 0;
+    auto page_of = [&](uint32_t at) {  // of position c0 + at
+      return at < n ? __ldg(table + ((c0 + at) >> shift)) : CK_NO_PAGE;
+    };
+    auto load_keys = [&](uint32_t i) {  // by the page looked up before, and looks the next one up
+      const uint32_t at = i * kTilePos + kpos, t = c0 + at, id = next_id;
       raw[0] = raw[1] = make_int4(0, 0, 0, 0);
-      if (at < n) {
-        const uint32_t t = c0 + at, id = __ldg(table + (t >> shift));
-        if (id < p.pool.pages) {
-          const int4* src = reinterpret_cast<const int4*>(p.pool.k + page_word(p.pool, id, kvh) +
-                                                          (size_t)(t & pmask) * HD + 8 * kchunk);
-          raw[0] = __ldg(src);
-          raw[1] = __ldg(src + 1);
-        } else if ((t & pmask) == 0 || at == 0) {
-          note(p.batch, seq, err_key((t >> shift) << shift, p.pool.layer, CK_PAGED_BAD_PAGE, 0));
-        }
+      if (id < p.pool.pages) {
+        const int4* src = reinterpret_cast<const int4*>(p.pool.k + page_word(p.pool, id, kvh) +
+                                                        (size_t)(t & pmask) * HD + 8 * kchunk);
+        raw[0] = __ldg(src);
+        raw[1] = __ldg(src + 1);
+      } else if (at < n && ((t & pmask) == 0 || at == 0)) {
+        note(p.batch, seq, err_key((t >> shift) << shift, p.pool.layer, CK_PAGED_BAD_PAGE, 0));
       }
+      next_id = page_of(at + kTilePos);
     };
     auto put_keys = [&](uint32_t buf) {
       const uint32_t y[8] = {biased(raw[0].x), biased(raw[0].y), biased(raw[0].z), biased(raw[0].w),
@@ -266,24 +305,28 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
         *reinterpret_cast<uint4*>(dst + k * T::kKeyPlane) = make_uint4(d[k][0], d[k][1], d[k][2], d[k][3]);
       fence_operands();
     };
-    auto issue_scores = [&](uint32_t i) {  // one thread
-      const uint32_t d0 = tmem + T::kScoreCol + (i % T::kBufs) * (kDiags * kTilePos);
-      const uint32_t b0 = smem_addr(sm) + (i & 1u) * T::kKeyBuf;
+    // A batch's products, by one thread of the warps in turn, once its operands are in place and
+    // its accumulators drained.
+    auto issue_scores = [&](uint32_t i) {
+      if (warp_u == i % kWarps) {
+        wait_full(batch + i);
+        if (i >= T::kBufs) wait_drained(tiles + i - T::kBufs);
+        const uint32_t leader = elected(), d0 = tmem_u + T::kScoreCol + (i % T::kBufs) * (kDiags * kTilePos);
+        const uint64_t b0 = operands + (i & 1u) * (T::kKeyBuf >> 4);
 #pragma unroll
-      for (uint32_t g = 0; g < kDiags; ++g) {
-        uint32_t acc = 0;
+        for (uint32_t g = 0; g < kDiags; ++g) {
 #pragma unroll
-        for (uint32_t qp = g > 2 ? g - 2 : 0; qp <= (g < 2 ? g : 2); ++qp) {
+          for (uint32_t qp = g > 2 ? g - 2 : 0; qp <= (g < 2 ? g : 2); ++qp) {
 #pragma unroll
-          for (uint32_t kk = 0; kk < HD / 16; ++kk) {
-            mma_ts(d0 + g * kTilePos, tmem + qp * (HD / 2) + 8 * kk,
-                   smem_desc(b0 + (g - qp) * T::kKeyPlane + (kk >> 2) * (kTilePos * 128) + (kk & 3u) * 32),
-                   tile_idesc(kTilePos), acc);
-            acc = 1;
+            for (uint32_t kk = 0; kk < HD / 16; ++kk)
+              mma_ts(leader, d0 + g * kTilePos, tmem_u + qp * (HD / 2) + 8 * kk,
+                     b0 + (((g - qp) * T::kKeyPlane + (kk >> 2) * (kTilePos * 128) + (kk & 3u) * 32) >> 4),
+                     tile_idesc(kTilePos), qp != (g > 2 ? g - 2 : 0) || kk != 0);
           }
         }
+        commit(leader, done + ((batch + i) & 1u));
       }
-      mma_commit(bar);
+      __syncwarp();
     };
     int32_t m = INT32_MIN;
     constexpr uint32_t kCols = kTilePos / T::kGroups;  // columns a thread drains
@@ -296,7 +339,7 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
         for (uint32_t g = 0; g < kDiags; ++g) tmem_ld8(base + g * kTilePos + h, d[g]);
         tmem_wait_ld();
         const uint32_t at = i * kTilePos + cg * kCols + h;
-        int32_t* dst = scores + (size_t)at * kTileRows + r;
+        int32_t c[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           // (sum of the accumulators by weight) >> 16, the low part in 32 bits
@@ -305,48 +348,37 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
                               (__float2int_rn(__uint_as_float(d[3][j])) << 8);
           const int64_t dot = (int64_t)mid + ((int64_t)__float2int_rn(__uint_as_float(d[4][j])) << 16);
           const int64_t s = wmul(dot, (int64_t)p.inv_sqrt) >> 24;
-          int32_t c = (int32_t)s;
-          if (c != s) c = s < 0 ? INT32_MIN : INT32_MAX;
-          dst[j * kTileRows] = c;
-          if (at + j < lim) m = max(m, c);
+          c[j] = (int32_t)s;
+          if (c[j] != s) c[j] = s < 0 ? INT32_MIN : INT32_MAX;
+          if (at + j < lim) m = max(m, c[j]);
         }
+        int4* dst = scores + (size_t)(at / 4) * kTileRows + r;
+        dst[0] = make_int4(c[0], c[1], c[2], c[3]);
+        dst[kTileRows] = make_int4(c[4], c[5], c[6], c[7]);
       }
-      tc_before();
     };
     if (nt) {
+      next_id = page_of(kpos);
       load_keys(0);
       put_keys(0);
-      if (nt > 1) load_keys(1);
-    }
-    tc_before();
-    __syncthreads();
-    if (tid == 0 && nt) {
-      tc_after();
+      arrive(full + (batch & 1u));
+      load_keys(1);
       issue_scores(0);
     }
     for (uint32_t i = 0; i < nt; ++i) {
       if (i + 1 < nt) {
-        put_keys((i + 1) & 1u);
-        if (i + 2 < nt) load_keys(i + 2);
+        put_keys((i + 1) & 1u);  // (the products that read the place before are done: tile i - 1's)
+        arrive(full + ((batch + i + 1) & 1u));
+        load_keys(i + 2);
+        if (T::kBufs == 2) issue_scores(i + 1);
       }
-      if (T::kBufs == 2) {
-        wait_mma();
-        __syncthreads();  // the next tile's digits are in place, its accumulators drained
-        if (tid == 0 && i + 1 < nt) {
-          tc_after();
-          issue_scores(i + 1);
-        }
-        drain_scores(i);
-      } else {
-        wait_mma();
-        drain_scores(i);
-        __syncthreads();
-        if (tid == 0 && i + 1 < nt) {
-          tc_after();
-          issue_scores(i + 1);
-        }
-      }
+      wait_done(batch + i);
+      drain_scores(i);
+      arrive(drained + ((tiles + i) & 1u));
+      if (T::kBufs == 1 && i + 1 < nt) issue_scores(i + 1);
     }
+    batch += nt;
+    tiles += nt;
 
     // ---- the row's maximum, over the column groups and the cluster
     int32_t* redm = reinterpret_cast<int32_t*>(red);
@@ -359,7 +391,7 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
     }
     all_sync(C);
     m = xmax[r];
-    uint32_t away = *bad_s;
+    away = *bad_s;
     for (uint32_t k = 0; C > 1 && k < C; ++k) {
       m = max(m, (int32_t)peer32(xmax + r, k));
       away |= peer32(bad_s, k);
@@ -371,10 +403,26 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
     // ---- the sum of exponentials
     unsigned long long z = 0;
     if (!away) {
-      const int32_t* src = scores + r;
-#pragma unroll 8
-      for (uint32_t i = cg; i < lim; i += T::kGroups)
-        z += table_s[min(((uint32_t)m - (uint32_t)src[(size_t)i * kTileRows]) >> 8, 4096u)];
+      const int4* src = scores + r;
+      constexpr uint32_t kAhead = 8;  // loads in flight
+      for (uint32_t i = 4 * cg; i < lim; i += 4 * T::kGroups * kAhead) {
+        int4 c[kAhead];
+#pragma unroll
+        for (uint32_t u = 0; u < kAhead; ++u) {
+          const uint32_t at = i + 4 * T::kGroups * u;
+          c[u] = at < lim ? src[(size_t)(at / 4) * kTileRows] : make_int4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (uint32_t u = 0; u < kAhead; ++u) {
+          const uint32_t at = i + 4 * T::kGroups * u;
+          const int32_t x[4] = {c[u].x, c[u].y, c[u].z, c[u].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t e = table_s[min(((uint32_t)m - (uint32_t)x[j]) >> 8, 4096u)];
+            z += at + j < lim ? e : 0u;
+          }
+        }
+      }
     }
     red[cg * kTileRows + r] = z;
     __syncthreads();
@@ -389,25 +437,31 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
     const uint32_t rz = (uint32_t)((1ull << 61) / z);
 
     // ---- weighted values: 64 positions at a time
-    unsigned long long acc[32];
-#pragma unroll
-    for (int j = 0; j < 32; ++j) acc[j] = 0;
-    const uint32_t nb = away ? 0 : (n + kBlockPos - 1) / kBlockPos;
+    const uint32_t nb = away ? 0 : all_blocks;
     const uint32_t vchunk = tid & 7u, vpair = tid >> 3;  // eight positions, two elements
+    constexpr uint32_t kChunks = 8 / T::kGroups;         // chunks of eight scores a thread takes
     int2 vraw[8];
+    int4 sraw[2 * kChunks];
     auto load_values = [&](uint32_t b) {
-      const uint32_t at = b * kBlockPos + vchunk * 8;
+      const uint32_t at = b * kBlockPos + vchunk * 8, t = c0 + at, id = next_id;
 #pragma unroll
       for (int j = 0; j < 8; ++j) vraw[j] = make_int2(0, 0);
-      if (at < n) {
-        const uint32_t t = c0 + at, id = __ldg(table + (t >> shift));  // a page holds whole chunks of eight
-        if (id < p.pool.pages) {
-          const int2* src = reinterpret_cast<const int2*>(p.pool.v + page_word(p.pool, id, kvh) +
-                                                          (size_t)(t & pmask) * HD + 2 * vpair);
+      if (id < p.pool.pages) {  // a page holds whole chunks of eight
+        const int2* src = reinterpret_cast<const int2*>(p.pool.v + page_word(p.pool, id, kvh) +
+                                                        (size_t)(t & pmask) * HD + 2 * vpair);
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (at + j < n) vraw[j] = __ldg(src + j * (HD / 2));
-        }
+        for (int j = 0; j < 8; ++j)
+          if (at + j < n) vraw[j] = __ldg(src + j * (HD / 2));
+      }
+      next_id = page_of(at + kBlockPos);
+    };
+    auto load_scores = [&](uint32_t b) {
+#pragma unroll
+      for (uint32_t c = 0; c < kChunks; ++c) {
+        const uint32_t at = b * kBlockPos + (cg * kChunks + c) * 8;
+        const int4* src = scores + (size_t)(at / 4) * kTileRows + r;
+        sraw[2 * c] = at < lim ? src[0] : make_int4(0, 0, 0, 0);
+        sraw[2 * c + 1] = at + 4 < lim ? src[kTileRows] : make_int4(0, 0, 0, 0);
       }
     };
     auto put_values = [&](uint8_t* planes) {
@@ -432,15 +486,13 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
       }
     };
     auto put_probs = [&](uint32_t b, uint8_t* planes) {
-      constexpr uint32_t kChunks = 8 / T::kGroups;
 #pragma unroll
       for (uint32_t c = 0; c < kChunks; ++c) {
         const uint32_t chunk = cg * kChunks + c, at = b * kBlockPos + chunk * 8;
-        const int32_t* src = scores + (size_t)at * kTileRows + r;
-        uint32_t s[8], pr[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s[j] = at + j < lim ? (uint32_t)src[j * kTileRows] : 0u;
-        uint32_t full = 0;
+        const int4 s0 = sraw[2 * c], s1 = sraw[2 * c + 1];
+        const uint32_t s[8] = {(uint32_t)s0.x, (uint32_t)s0.y, (uint32_t)s0.z, (uint32_t)s0.w,
+                               (uint32_t)s1.x, (uint32_t)s1.y, (uint32_t)s1.z, (uint32_t)s1.w};
+        uint32_t pr[8], full24 = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const uint32_t e = table_s[min(((uint32_t)m - s[j]) >> 8, 4096u)];
@@ -453,14 +505,14 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
             q += rem >= z;
           }
           pr[j] = at + j < lim ? q : 0u;
-          full |= pr[j];
+          full24 |= pr[j];
         }
         uint32_t d[3][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint32_t a = pr[2 * i], bq = pr[2 * i + 1];
           uint32_t extra = 0;
-          if (full >> 24) {  // P = 2^24 is 0xFFFFFF and one more in the lowest digit (2^-12 in its plane)
+          if (full24 >> 24) {  // P = 2^24 is 0xFFFFFF and one more in the lowest digit (2^-12 in its plane)
             extra = (a >> 24 ? 0x0C00u : 0u) | (bq >> 24 ? 0x0C000000u : 0u);
             a -= a >> 24;
             bq -= bq >> 24;
@@ -469,7 +521,7 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
           d[0][i] = fma_h2(lift<0x4240>(u), kScale0, kUns0);
           d[1][i] = fma_h2(lift<0x4341>(u), kScale1, kUns1);
           d[2][i] = fma_h2(lift<0x4240>(t), kScale2, kUns2);
-          if (full >> 24) asm("add.rn.f16x2 %0, %0, %1;" : "+r"(d[0][i]) : "r"(extra));
+          if (full24 >> 24) asm("add.rn.f16x2 %0, %0, %1;" : "+r"(d[0][i]) : "r"(extra));
         }
         uint8_t* dst = planes + r * 128 + ((chunk ^ (r & 7u)) << 4);
 #pragma unroll
@@ -477,83 +529,94 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
           *reinterpret_cast<uint4*>(dst + k * T::kProbPlane) = make_uint4(d[k][0], d[k][1], d[k][2], d[k][3]);
       }
     };
-    auto issue_values = [&](uint32_t b, const uint8_t* planes) {
-      const uint32_t a0 = smem_addr(planes), b0 = a0 + 3 * T::kProbPlane;
-      const uint32_t fresh = b % kFlushBlocks == 0 ? 0u : 1u;
-#pragma unroll
-      for (uint32_t g = 0; g < 4; ++g) {
-        uint32_t accumulate = fresh;
-#pragma unroll
-        for (uint32_t pp = g > 2 ? g - 2 : 0; pp <= 2; ++pp) {
-          // planes of weight g; the last accumulator also takes weight 4
-#pragma unroll
-          for (uint32_t vp = 0; vp < 3; ++vp) {
-            if (pp + vp != g && !(g == 3 && pp + vp == 4)) continue;
-#pragma unroll
-            for (uint32_t kk = 0; kk < kBlockPos / 16; ++kk) {
-              mma_ss(tmem + g * HD, smem_desc(a0 + pp * T::kProbPlane + kk * 32),
-                     smem_desc(b0 + vp * T::kValuePlane + kk * 32), tile_idesc(HD), accumulate);
-              accumulate = 1;
-            }
-          }
-        }
-      }
-      mma_commit(bar);
-    };
-    auto flush = [&] {
+    // Adds the accumulators to the 64-bit sums, which lie in the scratch between flushes; the
+    // last flush leaves them in shared memory, [element][row].
+    unsigned long long* sums = reinterpret_cast<unsigned long long*>(sm);
+    auto flush = [&](bool first, bool final) {
 #pragma unroll
       for (uint32_t h = 0; h < 32; h += 8) {
+        ulonglong2 old[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          old[j] = first ? make_ulonglong2(0, 0) : kept[(size_t)(h / 2 + j) * T::kThreads];
         uint32_t d[4][8];
 #pragma unroll
         for (uint32_t g = 0; g < 4; ++g) tmem_ld8(tmem + lane_base + g * HD + 32 * cg + h, d[g]);
         tmem_wait_ld();
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          long long t = (long long)acc[h + j];
+          long long t = (long long)(j & 1 ? old[j / 2].y : old[j / 2].x);
           t += __float2int_rn(__uint_as_float(d[0][j]) * 16777216.0f);
           t += (long long)__float2int_rn(__uint_as_float(d[1][j]) * 65536.0f) * 256;
           t += (long long)__float2int_rn(__uint_as_float(d[2][j]) * 256.0f) * 65536;
           t += (long long)__float2int_rn(__uint_as_float(d[3][j])) * 16777216;
-          acc[h + j] = (unsigned long long)t;
+          if (final) sums[(size_t)(32 * cg + h + j) * T::kPitch + r] = (unsigned long long)t;
+          (j & 1 ? old[j / 2].y : old[j / 2].x) = (unsigned long long)t;
+        }
+        if (!final) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) kept[(size_t)(h / 2 + j) * T::kThreads] = old[j];
         }
       }
-      tc_before();
     };
-    if (nb) load_values(0);
+    auto issue_values = [&](uint32_t b) {
+      if (warp_u == b % kWarps) {
+        wait_full(batch + b);
+        const uint32_t leader = elected();
+        const uint64_t a0 = operands + (b % T::kBufs) * (T::kValueBuf >> 4), b0 = a0 + (3 * T::kProbPlane >> 4);
+        const uint32_t go_on = b % kFlushBlocks != 0;
+#pragma unroll
+        for (uint32_t g = 0; g < 4; ++g) {
+          // planes of weight g; the last accumulator also takes weight 4
+#pragma unroll
+          for (uint32_t pp = g > 2 ? g - 2 : 0; pp < 3; ++pp) {
+#pragma unroll
+            for (uint32_t vp = 0; vp < 3; ++vp) {
+              if (pp + vp != g && !(g == 3 && pp + vp == 4)) continue;
+              const bool first = pp == (g > 2 ? g - 2 : 0) && vp == g - pp;
+#pragma unroll
+              for (uint32_t kk = 0; kk < kBlockPos / 16; ++kk)
+                mma_ss(leader, tmem_u + g * HD, a0 + ((pp * T::kProbPlane + kk * 32) >> 4),
+                       b0 + ((vp * T::kValuePlane + kk * 32) >> 4), tile_idesc(HD), first && kk == 0 ? go_on : 1u);
+            }
+          }
+        }
+        commit(leader, done + ((batch + b) & 1u));
+      }
+      __syncwarp();
+    };
+    if (nb) {
+      next_id = page_of(vchunk * 8);
+      load_values(0);
+      load_scores(0);
+    }
     for (uint32_t b = 0; b < nb; ++b) {
       uint8_t* planes = sm + (b % T::kBufs) * T::kValueBuf;
-      if (T::kBufs == 1 && b > 0) {
-        // the one buffer is free once the block before is through
-        wait_mma();
-        if (b % kFlushBlocks == 0) flush();
-      }
+      if (b >= T::kBufs) wait_done(batch + b - T::kBufs);  // the place is free
       put_values(planes + 3 * T::kProbPlane);
-      if (b + 1 < nb) load_values(b + 1);
+      load_values(b + 1);
       put_probs(b, planes);
+      if (b + 1 < nb) load_scores(b + 1);
       fence_operands();
-      if (T::kBufs == 2 && b > 0) {
-        wait_mma();
-        if (b % kFlushBlocks == 0) flush();
+      if (b > 0 && b % kFlushBlocks == 0) {
+        wait_done(batch + b - 1);
+        flush(b == kFlushBlocks, false);
       }
-      __syncthreads();
-      if (tid == 0) {
-        tc_after();
-        issue_values(b, planes);
-      }
+      arrive(full + ((batch + b) & 1u));
+      issue_values(b);
     }
-    if (nb) {
-      wait_mma();
-      flush();
-    }
+    if (nb) wait_done(batch + nb - 1);
+    batch += nb;
     if (bad) *bad_s = 1;
     if (tid == 0 && *abort_flag) *bad_s = 1;
-    __syncthreads();  // the last products have read the operands' place
+    __syncthreads();  // every warp has seen the last products done: they read the sums' place
 
     // ---- the cluster's sums, a slice of the rows each block
-    unsigned long long* sums = reinterpret_cast<unsigned long long*>(sm);
-    if (!away) {
+    if (nb) {
+      flush(nb <= kFlushBlocks, true);
+    } else {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) sums[(size_t)(32 * cg + j) * T::kPitch + r] = acc[j];
+      for (int j = 0; j < 32; ++j) sums[(size_t)(32 * cg + j) * T::kPitch + r] = 0;
     }
     all_sync(C);
     away |= *bad_s;
@@ -617,13 +680,14 @@ TilesPlan plan_tiles(const ck_paged_cache& c, const ck_paged_batch& b, uint32_t 
   const uint64_t items = (uint64_t)b.seqs * c.kv_heads * w.tiles;
   // blocks of a cluster: until every place on the GPU has one, while each has 256 positions
   w.C = 1;
-  while (w.C < 8 && items * w.C < slots && b.max_len / (2 * w.C) >= 256) w.C *= 2;
+  while (w.C < 8 && 2 * items * w.C <= slots && b.max_len / (2 * w.C) >= 256) w.C *= 2;
   w.clusters = (uint32_t)std::min<uint64_t>(items, std::max(1u, slots / w.C));
   w.cap = ((b.max_len + w.C - 1) / w.C + kBlockPos - 1) & ~(kBlockPos - 1);
   w.any_off = 0;
   w.away_off = 256;
   w.scores_off = w.away_off + align256(4 * items);
-  w.size = w.scores_off + 4ull * kTileRows * w.cap * w.clusters * w.C;
+  w.sums_off = w.scores_off + align256(4ull * kTileRows * w.cap * w.clusters * w.C);
+  w.size = w.sums_off + 8ull * kTileRows * c.head_dim * w.clusters * w.C;
   w.use = true;
   return w;
 }
