@@ -14,9 +14,6 @@ import os
 import numpy as np
 
 from . import build as _build
-from .paged import (BAD_PAGE, BAD_SEQUENCE, NO_PAGE, BeamPlan, PagedBatch, PagedCache, PagePlan,  # noqa: F401
-                    host_log_sum, paged_attention, paged_attention_work, paged_store)
-from .paged import SIGNATURES as _PAGED_SIGNATURES
 
 CK_FLAG_STOP_TOKENS = 1
 PATH_AUTO, PATH_STEP, PATH_KERNELS = 0, 1, 2
@@ -88,9 +85,20 @@ def lib() -> ctypes.CDLL:
             "ck_host_isqrt": ([u64], u64),
             "ck_host_div_trunc": ([i64, u32], i64),
             "ck_host_probability": ([u64, u64], u64),
+            # the paged cache and beam search (paged.py)
+            "ck_paged_store": ([vp, u32, vp, vp, sz, vp, sz, vp, sz, u32, vp, u32, u32, ctypes.c_int, vp, vp],
+                               ctypes.c_int),
+            "ck_paged_attention_work": ([vp, vp, u32, vp], ctypes.c_int),
+            "ck_paged_attention": ([vp, u32, vp, vp, sz, u32, vp, u32, vp, vp, sz, vp], ctypes.c_int),
+            "ck_pages_work": ([vp, u32, u32, vp], ctypes.c_int),
+            "ck_pages_fork": ([vp, u32, vp, vp, u32, vp, vp, u32, vp, vp, vp, vp, vp, sz, vp], ctypes.c_int),
+            "ck_pages_compact": ([vp, u32, vp, vp, u32, vp, vp, vp, vp, sz, vp], ctypes.c_int),
+            "ck_beam_work": ([u32, u32, u32, vp], ctypes.c_int),
+            "ck_beam_select": ([vp, sz, u32, u32, u32, vp, vp, vp, u32, u32, vp, vp, vp, vp, vp, sz, vp],
+                               ctypes.c_int),
+            "ck_host_log_sum": ([u64], i64),
             "ck_version": ([], ctypes.c_char_p),
         }
-        sig.update(_PAGED_SIGNATURES)
         for name, (args, res) in sig.items():
             f = getattr(L, name)
             f.argtypes = args
@@ -351,3 +359,17 @@ def host_probability(e: int, z: int) -> int:
 
 def version() -> str:
     return lib().ck_version().decode()
+
+
+# The paged cache and beam search, loaded at their first use (they import torch).
+_PAGED = ("NO_PAGE", "BAD_SEQUENCE", "BAD_PAGE", "PagedCache", "PagedBatch", "PagePlan", "BeamPlan", "paged_store",
+          "paged_attention_work", "paged_attention", "host_log_sum")
+
+
+def __getattr__(name):
+    if name == "paged" or name in _PAGED:
+        import importlib
+        paged = importlib.import_module(".paged", __name__)
+        globals().update({n: getattr(paged, n) for n in _PAGED}, paged=paged)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -160,9 +160,7 @@ __device__ __forceinline__ bool bit_of(const uint32_t* bits, uint32_t i) { retur
 
 // Forking, first step (a warp a row): checks the row, takes over the parent's whole pages and
 // marks them, and bids for its part-filled page.
-__global__ void __launch_bounds__(kTableThreads) k_fork_mark(const PagesParams p) {
-  const uint32_t r = blockIdx.x * (kTableThreads / 32) + threadIdx.x / 32, lane = threadIdx.x & 31;
-  if (r >= p.rows) return;
+__device__ __forceinline__ void fork_mark(const PagesParams& p, uint32_t r, uint32_t lane) {
   const uint32_t parent = p.parent[r];
   uint32_t status = 0, old = 0;
   if (parent != CK_NO_PAGE) {
@@ -194,6 +192,17 @@ __global__ void __launch_bounds__(kTableThreads) k_fork_mark(const PagesParams p
     if (live && part) atomicMax(p.owner + from[full], p.rows - r);
   }
 }
+__global__ void __launch_bounds__(kTableThreads) k_fork_mark(const PagesParams p) {
+  const uint32_t r = blockIdx.x * (kTableThreads / 32) + threadIdx.x / 32;
+  if (r < p.rows) fork_mark(p, r, threadIdx.x & 31);
+}
+
+// Small calls do the steps before the copies in one block: clears the marks.
+__device__ __forceinline__ void clear_marks(const PagesParams& p) {
+  for (uint32_t i = threadIdx.x; i < p.pages; i += kPlanThreads) p.owner[i] = 0;
+  for (uint32_t i = threadIdx.x; i < (p.pages + 31) / 32; i += kPlanThreads) p.bits[i] = 0;
+  __syncthreads();
+}
 
 // Inclusive sum over the block's warps of one value a thread; *total the block's sum.
 __device__ __forceinline__ unsigned long long block_scan(unsigned long long v, unsigned long long* warp_sum,
@@ -211,11 +220,18 @@ __device__ __forceinline__ unsigned long long block_scan(unsigned long long v, u
 }
 
 // Second step (one block): what each row needs, the free pages in ascending order, and the
-// rows' new pages and copies.
+// rows' new pages and copies.  ALONE: with the first step before it.
+template <bool ALONE>
 __global__ void __launch_bounds__(kPlanThreads) k_fork_plan(const PagesParams p) {
   __shared__ unsigned long long warp_sum[kPlanThreads / 32];
   __shared__ uint32_t n_copies;
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the copies wait for this grid's end)
+  if (ALONE) {
+    clear_marks(p);
+    for (uint32_t r = warp; r < p.rows; r += kPlanThreads / 32) fork_mark(p, r, lane);
+    __syncthreads();
+  }
   const uint32_t mask = (1u << p.page_shift) - 1;
   if (tid == 0) n_copies = 0;
   auto stays = [&](uint32_t r, uint32_t old, uint32_t* last) {
@@ -280,9 +296,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_fork_plan(const PagesParams p)
 }
 
 // Packing, first step (a warp a row): checks and marks the row's pages.
-__global__ void __launch_bounds__(kTableThreads) k_compact_mark(const PagesParams p) {
-  const uint32_t r = blockIdx.x * (kTableThreads / 32) + threadIdx.x / 32, lane = threadIdx.x & 31;
-  if (r >= p.rows) return;
+__device__ __forceinline__ void compact_mark(const PagesParams& p, uint32_t r, uint32_t lane) {
   const uint32_t len = p.len_in[r];
   uint32_t status = 0;
   if (len > kMaxPositions || len > ((uint64_t)p.stride << p.page_shift)) status = CK_CONTEXT_EXCEEDED;
@@ -295,12 +309,41 @@ __global__ void __launch_bounds__(kTableThreads) k_compact_mark(const PagesParam
     for (uint32_t i = lane; i < n; i += 32) atomicOr(p.bits + (from[i] >> 5), 1u << (from[i] & 31));
   if (lane == 0) p.status[r] = status;
 }
+__global__ void __launch_bounds__(kTableThreads) k_compact_mark(const PagesParams p) {
+  const uint32_t r = blockIdx.x * (kTableThreads / 32) + threadIdx.x / 32;
+  if (r < p.rows) compact_mark(p, r, threadIdx.x & 31);
+}
+
+// Third step (a warp a row): the row's pages by their new numbers.
+__device__ __forceinline__ void compact_table(const PagesParams& p, uint32_t r, uint32_t lane, uint32_t used) {
+  const uint32_t n = p.status[r] ? 0u : (p.len_in[r] + (1u << p.page_shift) - 1) >> p.page_shift;
+  for (uint32_t i = lane; i < p.stride; i += 32) {
+    uint32_t id = CK_NO_PAGE;
+    if (i < n) {
+      id = p.table_in[(size_t)r * p.stride + i];
+      if (id >= used) id = p.owner[id];
+    }
+    p.table_out[(size_t)r * p.stride + i] = id;
+  }
+}
+__global__ void __launch_bounds__(kTableThreads) k_compact_tables(const PagesParams p) {
+  const uint32_t r = blockIdx.x * (kTableThreads / 32) + threadIdx.x / 32;
+  if (r < p.rows) compact_table(p, r, threadIdx.x & 31, *p.used_out);
+}
 
 // Second step (one block): counts the pages in use, pairs those beyond the count with the
 // holes below it, and lists the moves; p.owner becomes each moved page's new number.
+// ALONE: with the first step before it and the third behind.
+template <bool ALONE>
 __global__ void __launch_bounds__(kPlanThreads) k_compact_plan(const PagesParams p) {
   __shared__ unsigned long long warp_sum[kPlanThreads / 32];
   const uint32_t tid = threadIdx.x;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (what follows waits for this grid's end)
+  if (ALONE) {
+    clear_marks(p);
+    for (uint32_t r = tid / 32; r < p.rows; r += kPlanThreads / 32) compact_mark(p, r, tid & 31);
+    __syncthreads();
+  }
   unsigned long long used = 0;
   const uint32_t words = (p.pages + 31) / 32;
   for (uint32_t base = 0; base < words; base += kPlanThreads) {
@@ -329,21 +372,9 @@ __global__ void __launch_bounds__(kPlanThreads) k_compact_plan(const PagesParams
     *p.copied = (uint32_t)movers;
     *p.used_out = (uint32_t)used;
   }
-}
-
-// Third step (a warp a row): the rows' pages by their new numbers.
-__global__ void __launch_bounds__(kTableThreads) k_compact_tables(const PagesParams p) {
-  const uint32_t r = blockIdx.x * (kTableThreads / 32) + threadIdx.x / 32, lane = threadIdx.x & 31;
-  if (r >= p.rows) return;
-  const uint32_t used = *p.used_out;
-  const uint32_t n = p.status[r] ? 0u : (p.len_in[r] + (1u << p.page_shift) - 1) >> p.page_shift;
-  for (uint32_t i = lane; i < p.stride; i += 32) {
-    uint32_t id = CK_NO_PAGE;
-    if (i < n) {
-      id = p.table_in[(size_t)r * p.stride + i];
-      if (id >= used) id = p.owner[id];
-    }
-    p.table_out[(size_t)r * p.stride + i] = id;
+  if (ALONE) {
+    __syncthreads();
+    for (uint32_t r = tid / 32; r < p.rows; r += kPlanThreads / 32) compact_table(p, r, tid & 31, (uint32_t)used);
   }
 }
 
@@ -353,6 +384,7 @@ constexpr int kCopyThreads = 256;
 __global__ void __launch_bounds__(kCopyThreads) k_copy_pages(int32_t* k, int32_t* v, uint32_t runs,
                                                               uint32_t page_shift, uint32_t hd,
                                                               const Copy* copies, const uint32_t* count) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const uint32_t lane = threadIdx.x & 31;
   const uint64_t tasks = 2ull * runs * *count;
   const uint32_t page4 = (hd << page_shift) / 4;  // 16-byte words of a head's page
@@ -380,10 +412,24 @@ int pages_args(const ck_paged_cache* cache, uint32_t rows, uint32_t stride, void
 int run_copies(const ck_paged_cache* c, const PagesParams& p, cudaStream_t s) {
   DeviceFacts f;
   CKP_CUDA(device_facts(&f));
-  k_copy_pages<<<f.sms * 8, kCopyThreads, 0, s>>>(c->dev_k, c->dev_v, c->layers * c->kv_heads, p.page_shift,
-                                                  c->head_dim, p.copies, p.copied);
-  CKP_CUDA(cudaGetLastError());
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(f.sms * 8);
+  cfg.blockDim = dim3(kCopyThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  CKP_CUDA(cudaLaunchKernelEx(&cfg, k_copy_pages, c->dev_k, c->dev_v, c->layers * c->kv_heads, p.page_shift,
+                              c->head_dim, static_cast<const Copy*>(p.copies), static_cast<const uint32_t*>(p.copied)));
   return CK_OK;
+}
+
+// One block does the table work of a call this small (a row is a warp's, 32 at a time, and a
+// thread clears every 1,024th page); larger ones spread it over the GPU.
+bool table_work_alone(uint32_t rows, uint32_t stride, uint32_t pages) {
+  return (uint64_t)rows * ((stride + 31) / 32) <= 1024 && pages <= 65536;
 }
 
 PagesParams pages_params(const ck_paged_cache* c, const PagesLayout& w, void* work) {
@@ -493,10 +539,14 @@ int ck_pages_fork(const ck_paged_cache* cache, uint32_t rows_in, const uint32_t*
   p.rows = rows;
   p.stride = stride;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  CKP_CUDA(cudaMemsetAsync(dev_work, 0, w.zero, s));
-  constexpr uint32_t per = kTableThreads / 32;
-  k_fork_mark<<<(rows + per - 1) / per, kTableThreads, 0, s>>>(p);
-  k_fork_plan<<<1, kPlanThreads, 0, s>>>(p);
+  if (table_work_alone(rows, stride, cache->pages)) {
+    k_fork_plan<true><<<1, kPlanThreads, 0, s>>>(p);
+  } else {
+    CKP_CUDA(cudaMemsetAsync(dev_work, 0, w.zero, s));
+    constexpr uint32_t per = kTableThreads / 32;
+    k_fork_mark<<<(rows + per - 1) / per, kTableThreads, 0, s>>>(p);
+    k_fork_plan<false><<<1, kPlanThreads, 0, s>>>(p);
+  }
   CKP_CUDA(cudaGetLastError());
   return run_copies(cache, p, s);
 }
@@ -528,11 +578,15 @@ int ck_pages_compact(const ck_paged_cache* cache, uint32_t rows, const uint32_t*
   p.rows = rows;
   p.stride = stride;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  CKP_CUDA(cudaMemsetAsync(dev_work, 0, w.zero, s));
-  constexpr uint32_t per = kTableThreads / 32;
-  k_compact_mark<<<(rows + per - 1) / per, kTableThreads, 0, s>>>(p);
-  k_compact_plan<<<1, kPlanThreads, 0, s>>>(p);
-  k_compact_tables<<<(rows + per - 1) / per, kTableThreads, 0, s>>>(p);
+  if (table_work_alone(rows, stride, cache->pages)) {
+    k_compact_plan<true><<<1, kPlanThreads, 0, s>>>(p);
+  } else {
+    CKP_CUDA(cudaMemsetAsync(dev_work, 0, w.zero, s));
+    constexpr uint32_t per = kTableThreads / 32;
+    k_compact_mark<<<(rows + per - 1) / per, kTableThreads, 0, s>>>(p);
+    k_compact_plan<false><<<1, kPlanThreads, 0, s>>>(p);
+    k_compact_tables<<<(rows + per - 1) / per, kTableThreads, 0, s>>>(p);
+  }
   CKP_CUDA(cudaGetLastError());
   return run_copies(cache, p, s);
 }

@@ -365,7 +365,12 @@ __global__ void __launch_bounds__(NT) k_pattn_few(const FewParams f) {
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     m[r] = (long long)xm[r];
-    for (uint32_t k = 0; k < C && C > 1; ++k) m[r] = max(m[r], (long long)peer_word(xm + r, k));
+    if (C > 1) {  // lane k asks block k
+      if (lane < C) m[r] = (long long)peer_word(xm + r, lane);
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) m[r] = max(m[r], __shfl_xor_sync(0xffffffffu, m[r], o));
+      m[r] = __shfl_sync(0xffffffffu, m[r], 0);
+    }
   }
   // exponentials and their sums
   unsigned long long z[R];
@@ -393,8 +398,13 @@ __global__ void __launch_bounds__(NT) k_pattn_few(const FewParams f) {
   else __syncthreads();
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    z[r] = C > 1 ? 0 : xz[r];
-    for (uint32_t k = 0; k < C && C > 1; ++k) z[r] += peer_word(xz + r, k);
+    z[r] = xz[r];
+    if (C > 1) {
+      z[r] = lane < C ? peer_word(xz + r, lane) : 0;
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) z[r] += __shfl_xor_sync(0xffffffffu, z[r], o);
+      z[r] = __shfl_sync(0xffffffffu, z[r], 0);
+    }
     if (z[r] < kOne) z[r] = kOne;
     const float rz = rcp_estimate((float)z[r]);
     long long* s = sc + (size_t)r * f.cap;
@@ -451,10 +461,15 @@ __global__ void __launch_bounds__(NT) k_pattn_few(const FewParams f) {
   // a slice of the outputs each block
   for (uint32_t i = rank * NT + tid; i < nv * hd; i += C * NT) {
     unsigned long long t = 0;
-    if (C > 1)
-      for (uint32_t k = 0; k < C; ++k) t += peer_word(part + i, k);
-    else
+    if (C > 1) {
+      unsigned long long w[8];
+#pragma unroll
+      for (uint32_t k = 0; k < 8; ++k) w[k] = k < C ? peer_word(part + i, k) : 0;
+#pragma unroll
+      for (uint32_t k = 0; k < 8; ++k) t += w[k];
+    } else {
       t = part[i];
+    }
     const uint32_t v = v0 + i / hd;
     p.out[((size_t)(sq.first + v / group) * p.heads + kvh * group + v % group) * hd + i % hd] = (long long)t >> 24;
   }

@@ -392,9 +392,19 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
     all_sync(C);
     m = xmax[r];
     away = *bad_s;
-    for (uint32_t k = 0; C > 1 && k < C; ++k) {
-      m = max(m, (int32_t)peer32(xmax + r, k));
-      away |= peer32(bad_s, k);
+    if (C > 1) {
+      int32_t peak[8];
+      uint32_t flag[8];
+#pragma unroll
+      for (uint32_t k = 0; k < 8; ++k) {
+        peak[k] = k < C ? (int32_t)peer32(xmax + r, k) : INT32_MIN;
+        flag[k] = k < C ? peer32(bad_s, k) : 0;
+      }
+#pragma unroll
+      for (uint32_t k = 0; k < 8; ++k) {
+        m = max(m, peak[k]);
+        away |= flag[k];
+      }
     }
     // a maximum at either end of 32 bits: a score may have been cut that counts
     away |= (uint32_t)(np != 0 && (m == INT32_MAX || m < INT32_MIN + (1 << 21)));
@@ -431,8 +441,15 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
       xsum[tid] = z;
     }
     all_sync(C);
-    z = C > 1 ? 0 : xsum[r];
-    for (uint32_t k = 0; C > 1 && k < C; ++k) z += peer64(xsum + r, k);
+    z = xsum[r];
+    if (C > 1) {
+      unsigned long long part[8];
+#pragma unroll
+      for (uint32_t k = 0; k < 8; ++k) part[k] = k < C ? peer64(xsum + r, k) : 0;
+      z = 0;
+#pragma unroll
+      for (uint32_t k = 0; k < 8; ++k) z += part[k];
+    }
     if (z < (1ull << 30)) z = 1ull << 30;
     const uint32_t rz = (uint32_t)((1ull << 61) / z);
 
@@ -626,10 +643,15 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
       const uint32_t row = rank * rows + i / HD, e = i % HD, q = v0 + row;
       if (q >= queries) break;
       unsigned long long t = 0;
-      if (C > 1)
-        for (uint32_t k = 0; k < C; ++k) t += peer64(sums + (size_t)e * T::kPitch + row, k);
-      else
+      if (C > 1) {
+        unsigned long long part[8];
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) part[k] = k < C ? peer64(sums + (size_t)e * T::kPitch + row, k) : 0;
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) t += part[k];
+      } else {
         t = sums[(size_t)e * T::kPitch + row];
+      }
       p.out[((size_t)(sq.first + q / group) * p.heads + kvh * group + q % group) * HD + e] = (long long)t >> 24;
     }
     if (rank == 0 && tid == 0) {

@@ -44,11 +44,11 @@ ADDR = 1 << 20  # stands for an aligned device address: nothing reads it
 
 
 def call(ck, name, good, **changed):
-    args = dict(good)
+    args = dict(good)  # (structures are passed by their addresses)
     for key, value in changed.items():
         assert key in args
         args[key] = value
-    return getattr(ck.lib(), name)(*args.values())
+    return getattr(ck.lib(), name)(*(ctypes.byref(a) if isinstance(a, ctypes.Structure) else a for a in args.values()))
 
 
 def cache(ck, **changed):
@@ -113,17 +113,17 @@ def test_work_sizes_are_refused_for_wrong_arguments(ck):
     n = ctypes.c_size_t()
     out = ctypes.byref(n)
     L = ck.lib()
-    assert L.ck_pages_work(cache(ck), 4, 4, None) == 10
+    assert L.ck_pages_work(ctypes.byref(cache(ck)), 4, 4, None) == 10
     for c, rows, stride in ((cache(ck, page=7), 4, 4), (cache(ck), 0, 4), (cache(ck), 65537, 4), (cache(ck), 4, 0),
                             (cache(ck), 4, 2**17 + 1), (None, 4, 4)):
-        assert L.ck_pages_work(c, rows, stride, out) == 10
-    assert L.ck_pages_work(cache(ck), 4, 4, out) == 0 and n.value > 0
+        assert L.ck_pages_work(c and ctypes.byref(c), rows, stride, out) == 10
+    assert L.ck_pages_work(ctypes.byref(cache(ck)), 4, 4, out) == 0 and n.value > 0
     for groups, beams, vocab in ((0, 1, 1), (1, 0, 1), (1, 65, 1), (1, 1, 0), (1, 1, 2**20 + 1), (1025, 64, 9)):
         assert L.ck_beam_work(groups, beams, vocab, out) == 10
     assert L.ck_beam_work(1, 1, 1, None) == 10
     assert L.ck_beam_work(1024, 64, 9, out) == 0 and n.value > 0
-    assert L.ck_paged_attention_work(cache(ck), batch(ck), 3, out) == 10
-    assert L.ck_paged_attention_work(cache(ck), batch(ck), 4, None) == 10
+    assert L.ck_paged_attention_work(ctypes.byref(cache(ck)), ctypes.byref(batch(ck)), 3, out) == 10
+    assert L.ck_paged_attention_work(ctypes.byref(cache(ck)), ctypes.byref(batch(ck)), 4, None) == 10
 
 
 def fork_args(ck):
@@ -182,6 +182,8 @@ def test_the_binding_checks_tensors(ck):
     pool = torch.zeros(3, 1, 2, 8, 4, dtype=torch.int32)
     with pytest.raises(ValueError):
         ck.PagedCache(pool, pool)                                   # not on a CUDA device
+    with pytest.raises(ValueError):
+        ck.PagedCache(pool[0], pool[0])
     with pytest.raises(ValueError):
         ck.PagedCache(pool.long(), pool.long())
     with pytest.raises(ValueError):
