@@ -147,10 +147,15 @@ __global__ void __launch_bounds__(kRowsThreads) k_pattn_rows(const RowsParams f)
 // and one key head, each block a range of positions, so that every key and value word is read
 // once: scores into the block's scratch, maximum and sum exchanged through distributed shared
 // memory, weighted values summed over the cluster.  HBM bounds it once the positions are many;
-// below, the chain of the two exchanges.  Lanes: hd / 4 a position, four elements each; kBatch
-// positions a lane group in flight.
-constexpr int kBatch = 8, kNarrow = 128;
-constexpr uint32_t kFewQueries = 16;
+// below, the instructions around the exchanges.  LPP lanes take a position, NCH chunks of four
+// elements each (eight lanes and two chunks for head size 64: adding up over few lanes is what
+// the scores cost, 11,000 instructions of a warp for 128 positions with sixteen lanes against
+// 4,000).  Keys and then values stream through a ring of asynchronous copies, kBatch positions a
+// lane group each; a lane copies the words that it uses itself, so nothing waits on another
+// lane, and the values are on their way while the exponentials are formed.
+constexpr uint32_t kMaxCluster = 16, kFewQueries = 16;
+constexpr int kNarrow = 64, kMiddle = 128, kBroad = 256;  // threads of a block
+constexpr unsigned long long kNowhere = ~0ull;
 
 struct FewParams {
   PAttnParams a;
@@ -158,19 +163,10 @@ struct FewParams {
   uint32_t cap;          // positions a block takes at most
   uint32_t ids;          // table entries a block holds
   uint32_t sc_smem;      // the scores lie in shared memory
+  uint32_t split;        // log2 of the cluster's blocks
 };
 
 __device__ __forceinline__ uint32_t smem_of(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -182,31 +178,37 @@ __device__ __forceinline__ unsigned long long peer_word(const void* p, uint32_t 
   return v;
 }
 
+// Batches in flight and the one at work: 16 KB a warp on their way where a block has the SM to
+// itself and another, 8 KB where seven share it.
+// Positions a lane group takes at once: fewer where four queries' sums fill the registers, and
+// where many small blocks share an SM.
+__host__ __device__ constexpr int few_batch(int nt, int r) { return r == 4 || nt == kNarrow ? 4 : 8; }
+__host__ __device__ constexpr int few_stages(int nt, int nch) { return nt == kMiddle ? 5 - nch : 4 - nch; }
 struct FewLayout {
-  uint32_t vpre, part, q, red, ids, sc, size;
+  uint32_t ring, part, q, red, ids, sc, size;
 };
 template <int NT, int R>
-__host__ __device__ inline FewLayout few_layout(uint32_t hd, uint32_t ids, uint32_t cap, bool sc_smem) {
+__host__ __device__ inline FewLayout few_layout(int nch, uint32_t hd, uint32_t ids, uint32_t cap, bool sc_smem) {
   FewLayout w;
   uint32_t off = 0;
-  w.vpre = off; off += kBatch * NT * 16;
+  w.ring = off; off += few_stages(NT, nch) * nch * few_batch(NT, R) * NT * 16;
   w.part = off; off += (NT / 32) * R * hd * 8;
   w.q = off; off += R * hd * 8;
-  w.red = off; off += ((NT / 32) + 2) * R * 8;
-  w.ids = off; off += (ids * 4 + 15) & ~15u;
+  w.red = off; off += (2 * (NT / 32) + 2) * R * 8;
+  w.ids = off; off += (ids * 8 + 15) & ~15u;
   w.sc = off; off += sc_smem ? R * cap * 8 : 0;
   w.size = off;
   return w;
 }
 
-// Sums d[0 .. kBatch) over the LPP lanes of a group; lane `sub` ends with the sum of batch
-// entry *which.  The first steps halve what a lane carries, so that 8 sums cost 8 exchanges.
-template <int LPP>
-__device__ __forceinline__ unsigned long long group_sums(unsigned long long (&d)[kBatch], uint32_t sub,
+// Sums d[0 .. N) over the LPP lanes of a group; lane `sub` ends with the sum of batch entry
+// *which.  The first steps halve what a lane carries, so that 8 sums cost 7 exchanges.
+template <int LPP, int N>
+__device__ __forceinline__ unsigned long long group_sums(unsigned long long (&d)[N], uint32_t sub,
                                                          uint32_t* which) {
   uint32_t w = 0;
 #pragma unroll
-  for (int n = kBatch / 2, o = LPP / 2; n > 0; n >>= 1, o >>= 1) {
+  for (int n = N / 2, o = LPP / 2; n > 0; n >>= 1, o >>= 1) {
     const bool up = sub & o;
     w = 2 * w + up;
 #pragma unroll
@@ -216,19 +218,33 @@ __device__ __forceinline__ unsigned long long group_sums(unsigned long long (&d)
     }
   }
 #pragma unroll
-  for (int o = LPP / kBatch / 2; o > 0; o >>= 1) d[0] += __shfl_xor_sync(0xffffffffu, d[0], o);
+  for (int o = LPP / N / 2; o > 0; o >>= 1) d[0] += __shfl_xor_sync(0xffffffffu, d[0], o);
   *which = w;
   return d[0];
 }
 
-// LPP: lanes a position (8, 16 or 32), 0 for fewer (head sizes below 32).
-template <int LPP, int R, int NT>
+// The largest of the warp's values, and the sum of its values below 2^55, by 32-bit reductions.
+__device__ __forceinline__ long long warp_max(long long v) {
+  const int32_t hi = __reduce_max_sync(0xffffffffu, (int32_t)(v >> 32));
+  const uint32_t lo = __reduce_max_sync(0xffffffffu, (int32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
+  return (long long)((unsigned long long)(uint32_t)hi << 32 | lo);
+}
+__device__ __forceinline__ unsigned long long warp_total(unsigned long long v) {
+  const uint32_t lo = __reduce_add_sync(0xffffffffu, (uint32_t)v & 0x7FFFFFFu);  // 27 bits of each
+  const uint32_t hi = __reduce_add_sync(0xffffffffu, (uint32_t)(v >> 27));
+  return ((unsigned long long)hi << 27) + lo;
+}
+
+// LPP = 0: hd / 4 lanes a position (head sizes below 32).
+template <int LPP, int NCH, int R, int NT>
 __global__ void __launch_bounds__(NT) k_pattn_few(const FewParams f) {
+  constexpr int kStages = few_stages(NT, NCH), kBatch = few_batch(NT, R), kWarps = NT / 32;
   extern __shared__ __align__(16) uint8_t smem[];
   const PAttnParams& p = f.a;
-  const uint32_t hd = p.pool.hd, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t C = cluster_size(), rank = cluster_rank();
-  const uint32_t seq = blockIdx.x / C, kvh = blockIdx.y, v0 = blockIdx.z * R;
+  const uint32_t hd = LPP ? 4 * LPP * NCH : p.pool.hd;
+  const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t C = 1u << f.split, rank = blockIdx.x & (C - 1);
+  const uint32_t seq = blockIdx.x >> f.split, kvh = blockIdx.y, v0 = blockIdx.z * R;
   const Sequence sq = load_sequence(p.batch, seq, p.pool.page_shift);
   if (!sq.ok) {  // (the whole cluster leaves)
     if (tid == 0 && rank == 0) note(p.batch, seq, err_key(0, p.pool.layer, CK_PAGED_BAD_SEQUENCE, 0));
@@ -236,65 +252,91 @@ __global__ void __launch_bounds__(NT) k_pattn_few(const FewParams f) {
   }
   const uint32_t group = p.heads / p.pool.kv_heads, queries = sq.count * group;
   if (v0 >= queries) return;
-  const uint32_t nv = min((uint32_t)R, queries - v0);
-  // positions each query sees: those up to its row's own
-  uint32_t np[R], top = 0;
+  // each query's row and head, and the positions it sees: those up to its row's own
+  uint32_t np[R], row[R], head[R], top = 0;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const uint32_t up = (v0 + r) / group + sq.len;  // position + count
-    np[r] = r < nv && up >= sq.count ? up - sq.count + 1 : 0;
+    const uint32_t token = group == 1 ? v0 + r : (v0 + r) / group, up = token + sq.len;  // position + count
+    const bool live = v0 + r < queries;
+    np[r] = live && up >= sq.count ? up - sq.count + 1 : 0;
+    row[r] = sq.first + token;
+    head[r] = kvh * group + (v0 + r - token * group);
     top = max(top, np[r]);
   }
-  const uint32_t per = (top + C - 1) / C, c0 = min(top, rank * per), n = min(top, c0 + per) - c0;
-  const FewLayout w = few_layout<NT, R>(hd, f.ids, f.cap, f.sc_smem);
-  int4* vpre = reinterpret_cast<int4*>(smem + w.vpre);
+  const uint32_t per = (top + C - 1) >> f.split, c0 = min(top, rank * per), n = min(top, c0 + per) - c0;
+  const FewLayout w = few_layout<NT, R>(NCH, hd, f.ids, f.cap, f.sc_smem);
+  int4* ring = reinterpret_cast<int4*>(smem + w.ring);
   unsigned long long* part = reinterpret_cast<unsigned long long*>(smem + w.part);
   int64_t* q_s = reinterpret_cast<int64_t*>(smem + w.q);
-  unsigned long long* red = reinterpret_cast<unsigned long long*>(smem + w.red);
-  unsigned long long* xm = red + (NT / 32) * R;
+  unsigned long long* redm = reinterpret_cast<unsigned long long*>(smem + w.red);  // [warp][R]
+  unsigned long long* redz = redm + kWarps * R;
+  unsigned long long* xm = redz + kWarps * R;
   unsigned long long* xz = xm + R;
-  uint32_t* ids = reinterpret_cast<uint32_t*>(smem + w.ids);
+  unsigned long long* pages = reinterpret_cast<unsigned long long*>(smem + w.ids);  // first bytes of the block's pages
   const size_t block = ((size_t)blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
   long long* sc = f.sc_smem ? reinterpret_cast<long long*>(smem + w.sc) : f.scores + block * R * f.cap;
 
   const uint32_t shift = p.pool.page_shift, mask = (1u << shift) - 1, page0 = c0 >> shift;
   const uint32_t* table = p.batch.table + (size_t)seq * p.batch.stride;
+  int holes = 0;  // a page outside the pool
   for (uint32_t i = tid; n != 0 && i <= ((c0 + n - 1) >> shift) - page0; i += NT) {
     const uint32_t id = table[page0 + i];
-    ids[i] = id;
-    if (id >= p.pool.pages) note(p.batch, seq, err_key((page0 + i) << shift, p.pool.layer, CK_PAGED_BAD_PAGE, 0));
+    pages[i] = id < p.pool.pages ? 4 * page_word(p.pool, id, kvh) : kNowhere;
+    if (id >= p.pool.pages) {
+      note(p.batch, seq, err_key((page0 + i) << shift, p.pool.layer, CK_PAGED_BAD_PAGE, 0));
+      holes = 1;
+    }
   }
   int wide = 0;
-  for (uint32_t i = tid; i < R * hd; i += NT) {
-    const uint32_t r = i / hd, v = v0 + r;
-    int64_t x = 0;
-    if (r < nv)
-      x = p.q[(size_t)(sq.first + v / group) * p.q_stride + (size_t)(kvh * group + v % group) * hd + i % hd];
-    q_s[i] = x;
-    wide |= x != (int32_t)x;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int64_t* q = p.q + row[r] * p.q_stride + head[r] * hd;
+    for (uint32_t i = tid; i < hd; i += NT) {
+      const int64_t x = v0 + r < queries ? q[i] : 0;
+      q_s[r * hd + i] = x;
+      wide |= x != (int32_t)x;
+    }
   }
   wide = __syncthreads_or(wide);
+  holes = __syncthreads_or(holes);
 
   const uint32_t lpp = LPP ? LPP : hd / 4, ppw = 32 / lpp, sub = lane % lpp, slot = lane / lpp, e0 = 4 * sub;
-  const uint32_t step = (NT / 32) * ppw, round = step * kBatch;
-  // position c0 + i of the pool, this lane's four words (zeros outside the range or the pool)
-  auto at = [&](const int32_t* pool, uint32_t i) -> const int4* {
-    if (i >= n) return nullptr;
-    const uint32_t t = c0 + i, id = ids[(t >> shift) - page0];
-    if (id >= p.pool.pages) return nullptr;
-    return reinterpret_cast<const int4*>(pool + page_word(p.pool, id, kvh) + (size_t)(t & mask) * hd + e0);
-  };
-  // the first values travel while the scores are formed
+  const uint32_t step = kWarps * ppw, round = step * kBatch;  // chunk c of a lane: elements e0 + 4 c lpp ..
+  // Batch g of the stream: keys of round g, then values of round g - rounds.  This lane's words of
+  // its kBatch positions go to its places of slot g % kStages: zeros of a page outside the pool,
+  // and those of the last position again behind it.
+  const uint32_t rounds = (n + round - 1) / round;
+  uint32_t sent = 0;
+  auto send = [&] {
+    if (sent < 2 * rounds) {
+      const bool keys = sent < rounds;
+      const char* pool = reinterpret_cast<const char*>((keys ? p.pool.k : p.pool.v) + e0);
+      const uint32_t first = (keys ? sent : sent - rounds) * round + warp * ppw + slot;
+      const uint32_t to = smem_of(ring + (sent % kStages) * NCH * kBatch * NT + tid);
 #pragma unroll
-  for (int b = 0; b < kBatch; ++b) {
-    const int4* src = at(p.pool.v, b * step + warp * ppw + slot);
-    if (src)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_of(vpre + b * NT + tid)), "l"(src)
-                   : "memory");
-    else
-      vpre[b * NT + tid] = make_int4(0, 0, 0, 0);
-  }
-  asm volatile("cp.async.commit_group;" ::: "memory");
+      for (int b = 0; b < kBatch; ++b) {
+        const uint32_t u = (c0 & mask) + min(first + b * step, n - 1);  // from the first page's start
+        unsigned long long at = pages[u >> shift];
+        uint32_t bytes = 16;
+        if (holes && at == kNowhere) at = bytes = 0;
+        const char* src = pool + (at + (u & mask) * (4 * hd));
+#pragma unroll
+        for (int c = 0; c < NCH; ++c)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + (c * kBatch + b) * NT * 16),
+                       "l"(src + 16 * c * lpp), "r"(bytes)
+                       : "memory");
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    ++sent;
+  };
+  uint32_t taken = 0;
+  auto take = [&]() -> const int4* {  // the next batch, arrived
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    return ring + (taken++ % kStages) * NCH * kBatch * NT + tid;
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) send();
 
   // scores
   long long m[R];
@@ -307,70 +349,84 @@ __global__ void __launch_bounds__(NT) k_pattn_few(const FewParams f) {
     if (c0 + i < np[r]) m[r] = max(m[r], v);
   };
   for (uint32_t base = 0; base < n; base += round) {
-    int4 k4[kBatch];
+    const int4* place = take();
+    send();  // (into the slot of the batch before, which this lane has used)
+    unsigned long long d[R][kBatch];
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const int4* src = at(p.pool.k, base + b * step + warp * ppw + slot);
-      k4[b] = src ? __ldg(src) : make_int4(0, 0, 0, 0);
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) d[r][b] = 0;
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+      int32_t q[R][4];  // the low words as signed 32-bit factors
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q[r][j] = (int32_t)q_s[r * hd + e0 + 4 * c * lpp + j];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int4 k4 = place[(c * kBatch + b) * NT];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          d[r][b] += (unsigned long long)((long long)q[r][0] * k4.x);
+          d[r][b] += (unsigned long long)((long long)q[r][1] * k4.y);
+          d[r][b] += (unsigned long long)((long long)q[r][2] * k4.z);
+          d[r][b] += (unsigned long long)((long long)q[r][3] * k4.w);
+        }
+      }
+    }
+    if (wide) {  // and what is left of the queries above them, times 2^32
+#pragma unroll 1
+      for (int c = 0; c < NCH; ++c)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const int64_t* q = q_s + r * hd + e0 + 4 * c * lpp;
+          const uint32_t h0 = (uint32_t)((q[0] - (int32_t)q[0]) >> 32), h1 = (uint32_t)((q[1] - (int32_t)q[1]) >> 32),
+                         h2 = (uint32_t)((q[2] - (int32_t)q[2]) >> 32), h3 = (uint32_t)((q[3] - (int32_t)q[3]) >> 32);
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b) {
+            const int4 k4 = place[(c * kBatch + b) * NT];
+            d[r][b] += (unsigned long long)(h0 * (uint32_t)k4.x + h1 * (uint32_t)k4.y + h2 * (uint32_t)k4.z +
+                                            h3 * (uint32_t)k4.w)
+                       << 32;
+          }
+        }
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int64_t q0 = q_s[r * hd + e0], q1 = q_s[r * hd + e0 + 1], q2 = q_s[r * hd + e0 + 2],
-                    q3 = q_s[r * hd + e0 + 3];
-      unsigned long long d[kBatch];
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b)  // the low words as signed 32-bit factors
-        d[b] = (unsigned long long)((long long)(int32_t)q0 * k4[b].x) +
-               (unsigned long long)((long long)(int32_t)q1 * k4[b].y) +
-               (unsigned long long)((long long)(int32_t)q2 * k4[b].z) +
-               (unsigned long long)((long long)(int32_t)q3 * k4[b].w);
-      if (wide) {  // and what is left of the queries above them, times 2^32
-        const uint32_t h0 = (uint32_t)((q0 - (int32_t)q0) >> 32), h1 = (uint32_t)((q1 - (int32_t)q1) >> 32),
-                       h2 = (uint32_t)((q2 - (int32_t)q2) >> 32), h3 = (uint32_t)((q3 - (int32_t)q3) >> 32);
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b)
-          d[b] += (unsigned long long)(h0 * (uint32_t)k4[b].x + h1 * (uint32_t)k4[b].y + h2 * (uint32_t)k4[b].z +
-                                       h3 * (uint32_t)k4[b].w)
-                  << 32;
-      }
       if constexpr (LPP >= kBatch) {
         uint32_t b;
-        const unsigned long long s = group_sums<LPP>(d, sub, &b);
+        const unsigned long long s = group_sums<LPP, kBatch>(d[r], sub, &b);
         if (sub % (LPP / kBatch) == 0) score(r, base + b * step + warp * ppw + slot, s);
       } else {
         for (uint32_t o = lpp >> 1; o > 0; o >>= 1) {
 #pragma unroll
-          for (int b = 0; b < kBatch; ++b) d[b] += __shfl_xor_sync(0xffffffffu, d[b], o);
+          for (int b = 0; b < kBatch; ++b) d[r][b] += __shfl_xor_sync(0xffffffffu, d[r][b], o);
         }
 #pragma unroll
         for (int b = 0; b < kBatch; ++b)
-          if (sub == 0) score(r, base + b * step + warp * ppw + slot, d[b]);
+          if (sub == 0) score(r, base + b * step + warp * ppw + slot, d[r][b]);
       }
     }
   }
+  // the maximum over the block and the cluster
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m[r] = max(m[r], __shfl_xor_sync(0xffffffffu, m[r], o));
-    if (lane == 0) red[warp * R + r] = (unsigned long long)m[r];
+    m[r] = warp_max(m[r]);
+    if (lane == 0) redm[warp * R + r] = (unsigned long long)m[r];
   }
   __syncthreads();
-  if (tid < R) {
-    long long v = LLONG_MIN;
-    for (int k = 0; k < (NT / 32); ++k) v = max(v, (long long)red[k * R + tid]);
-    xm[tid] = (unsigned long long)v;
-  }
-  if (C > 1) cluster_sync();
-  else __syncthreads();
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    m[r] = (long long)xm[r];
-    if (C > 1) {  // lane k asks block k
-      if (lane < C) m[r] = (long long)peer_word(xm + r, lane);
+  for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int o = 4; o > 0; o >>= 1) m[r] = max(m[r], __shfl_xor_sync(0xffffffffu, m[r], o));
-      m[r] = __shfl_sync(0xffffffffu, m[r], 0);
-    }
+    for (int k = 0; k < kWarps; ++k) m[r] = max(m[r], (long long)redm[k * R + r]);
+  if (C > 1) {  // lane k asks block k
+    if (tid == 0)
+#pragma unroll
+      for (int r = 0; r < R; ++r) xm[r] = (unsigned long long)m[r];
+    cluster_sync();
+#pragma unroll
+    for (int r = 0; r < R; ++r) m[r] = warp_max(lane < C ? (long long)peer_word(xm + r, lane) : LLONG_MIN);
   }
   // exponentials and their sums
   unsigned long long z[R];
@@ -384,96 +440,112 @@ __global__ void __launch_bounds__(NT) k_pattn_few(const FewParams f) {
       s[i] = e;
       z[r] += e;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) z[r] += __shfl_xor_sync(0xffffffffu, z[r], o);
-    if (lane == 0) red[warp * R + r] = z[r];
+    z[r] = warp_total(z[r]);
+    if (lane == 0) redz[warp * R + r] = z[r];
   }
   __syncthreads();
-  if (tid < R) {
-    unsigned long long v = 0;
-    for (int k = 0; k < (NT / 32); ++k) v += red[k * R + tid];
-    xz[tid] = v;
-  }
-  if (C > 1) cluster_sync();
-  else __syncthreads();
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    z[r] = xz[r];
-    if (C > 1) {
-      z[r] = lane < C ? peer_word(xz + r, lane) : 0;
+    z[r] = 0;
 #pragma unroll
-      for (int o = 4; o > 0; o >>= 1) z[r] += __shfl_xor_sync(0xffffffffu, z[r], o);
-      z[r] = __shfl_sync(0xffffffffu, z[r], 0);
-    }
-    if (z[r] < kOne) z[r] = kOne;
-    const float rz = rcp_estimate((float)z[r]);
-    long long* s = sc + (size_t)r * f.cap;
-    for (uint32_t i = tid; i < n; i += NT)
-      s[i] = (long long)div_by_estimate((unsigned long long)s[i] << 24, z[r], rz);
+    for (int k = 0; k < kWarps; ++k) z[r] += redz[k * R + r];
   }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  if (C > 1) {
+    if (tid == 0)
+#pragma unroll
+      for (int r = 0; r < R; ++r) xz[r] = z[r];
+    cluster_sync();
+#pragma unroll
+    for (int r = 0; r < R; ++r) z[r] = warp_total(lane < C ? peer_word(xz + r, lane) : 0);
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    if (z[r] < kOne) z[r] = kOne;
+    // floor((e << 24) / z) by the reciprocal floor(2^61 / z): short by less than e / 2^37 <= 2^-7,
+    // so wrong only when the estimate's fraction ends that close to the next integer
+    const uint32_t rz = (uint32_t)div_by_estimate(1ull << 61, z[r], rcp_estimate((float)z[r]));
+    long long* s = sc + (size_t)r * f.cap;
+    for (uint32_t i = tid; i < rounds * round; i += NT) {  // (zero behind the last position)
+      const uint32_t e = i < n ? (uint32_t)s[i] : 0;
+      const unsigned long long x = (unsigned long long)e * rz;
+      uint32_t q = (uint32_t)(x >> 37);
+      if (((uint32_t)(x >> 30) & 0x7Fu) == 0x7Fu) q += ((unsigned long long)e << 24) - (unsigned long long)q * z[r] >= z[r];
+      s[i] = q;
+    }
+  }
   __syncthreads();
   // weighted values
-  unsigned long long a[R][4];
+  unsigned long long a[R][NCH][4];
 #pragma unroll
-  for (int r = 0; r < R; ++r) a[r][0] = a[r][1] = a[r][2] = a[r][3] = 0;
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) a[r][c][0] = a[r][c][1] = a[r][c][2] = a[r][c][3] = 0;
   for (uint32_t base = 0; base < n; base += round) {
-    int4 v4[kBatch];
+    const int4* place = take();
+    send();
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      if (base == 0) {
-        v4[b] = vpre[b * NT + tid];
-      } else {
-        const int4* src = at(p.pool.v, base + b * step + warp * ppw + slot);
-        v4[b] = src ? __ldg(src) : make_int4(0, 0, 0, 0);
+      int4 v4[NCH];
+#pragma unroll
+      for (int c = 0; c < NCH; ++c) v4[c] = place[(c * kBatch + b) * NT];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        // P <= 2^24: the low word
+        const long long pb = reinterpret_cast<const int32_t*>(sc + (size_t)r * f.cap + base + b * step + warp * ppw + slot)[0];
+#pragma unroll
+        for (int c = 0; c < NCH; ++c) {
+          a[r][c][0] += (unsigned long long)(pb * v4[c].x);
+          a[r][c][1] += (unsigned long long)(pb * v4[c].y);
+          a[r][c][2] += (unsigned long long)(pb * v4[c].z);
+          a[r][c][3] += (unsigned long long)(pb * v4[c].w);
+        }
       }
     }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+      for (uint32_t o = 16; o >= lpp; o >>= 1) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a[r][c][j] += __shfl_xor_sync(0xffffffffu, a[r][c][j], o);
+      }
+      if (slot == 0) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) part[((size_t)warp * R + r) * hd + e0 + 4 * c * lpp + j] = a[r][c][j];
+      }
+    }
+  __syncthreads();
+  if (C == 1) {
 #pragma unroll
     for (int r = 0; r < R; ++r)
+      for (uint32_t i = tid; v0 + r < queries && i < hd; i += NT) {
+        unsigned long long t = 0;
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const uint32_t i = base + b * step + warp * ppw + slot;
-        const long long pb = i < n ? (int32_t)sc[(size_t)r * f.cap + i] : 0;  // P <= 2^24
-        a[r][0] += (unsigned long long)(pb * v4[b].x);
-        a[r][1] += (unsigned long long)(pb * v4[b].y);
-        a[r][2] += (unsigned long long)(pb * v4[b].z);
-        a[r][3] += (unsigned long long)(pb * v4[b].w);
+        for (int k = 0; k < kWarps; ++k) t += part[((size_t)k * R + r) * hd + i];
+        p.out[((size_t)row[r] * p.heads + head[r]) * hd + i] = (long long)t >> 24;
       }
+    return;
   }
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    for (uint32_t o = 16; o >= lpp; o >>= 1) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) a[r][j] += __shfl_xor_sync(0xffffffffu, a[r][j], o);
-    }
-    if (slot == 0) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) part[((size_t)warp * R + r) * hd + e0 + j] = a[r][j];
-    }
-  }
-  __syncthreads();
   for (uint32_t i = tid; i < R * hd; i += NT) {
     unsigned long long t = 0;
-    for (int k = 0; k < (NT / 32); ++k) t += part[(size_t)k * R * hd + i];
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) t += part[(size_t)k * R * hd + i];
     part[i] = t;  // (only this thread reads or writes entry i of any warp)
   }
-  if (C > 1) cluster_sync();
+  cluster_sync();
   // a slice of the outputs each block
-  for (uint32_t i = rank * NT + tid; i < nv * hd; i += C * NT) {
-    unsigned long long t = 0;
-    if (C > 1) {
-      unsigned long long w[8];
 #pragma unroll
-      for (uint32_t k = 0; k < 8; ++k) w[k] = k < C ? peer_word(part + i, k) : 0;
+  for (int r = 0; r < R; ++r)
+    for (uint32_t i = rank * NT + tid; v0 + r < queries && i < hd; i += C * NT) {
+      unsigned long long t = 0, word[kMaxCluster];
 #pragma unroll
-      for (uint32_t k = 0; k < 8; ++k) t += w[k];
-    } else {
-      t = part[i];
+      for (uint32_t k = 0; k < kMaxCluster; ++k) word[k] = k < C ? peer_word(part + r * hd + i, k) : 0;
+#pragma unroll
+      for (uint32_t k = 0; k < kMaxCluster; ++k) t += word[k];
+      p.out[((size_t)row[r] * p.heads + head[r]) * hd + i] = (long long)t >> 24;
     }
-    const uint32_t v = v0 + i / hd;
-    p.out[((size_t)(sq.first + v / group) * p.heads + kvh * group + v % group) * hd + i % hd] = (long long)t >> 24;
-  }
-  if (C > 1) cluster_sync();  // no block leaves while another reads its sums
+  cluster_sync();  // no block leaves while another reads its sums
 }
 
 struct FewPlan {
@@ -486,9 +558,10 @@ struct FewPlan {
 
 template <int NT>
 uint32_t few_smem(uint32_t R, uint32_t hd, uint32_t ids, uint32_t cap, bool sc_smem) {
-  return R == 1   ? few_layout<NT, 1>(hd, ids, cap, sc_smem).size
-         : R == 2 ? few_layout<NT, 2>(hd, ids, cap, sc_smem).size
-                  : few_layout<NT, 4>(hd, ids, cap, sc_smem).size;
+  const int nch = hd >= 64 ? 2 : 1;
+  return R == 1   ? few_layout<NT, 1>(nch, hd, ids, cap, sc_smem).size
+         : R == 2 ? few_layout<NT, 2>(nch, hd, ids, cap, sc_smem).size
+                  : few_layout<NT, 4>(nch, hd, ids, cap, sc_smem).size;
 }
 
 FewPlan plan_few(const ck_paged_cache& c, const ck_paged_batch& b, uint32_t heads, const DeviceFacts& f) {
@@ -496,31 +569,38 @@ FewPlan plan_few(const ck_paged_cache& c, const ck_paged_batch& b, uint32_t head
   const uint64_t queries = (uint64_t)b.max_new * (heads / c.kv_heads);
   w.R = queries == 1 ? 1 : queries == 2 ? 2 : 4;
   w.z = (uint32_t)((queries + w.R - 1) / w.R);
-  // blocks of a cluster: until two an SM are there, while each has 256 positions
+  // blocks of a cluster: until there are two an SM (one, for sixteen), while each has 256 positions
   const uint64_t items = (uint64_t)b.seqs * c.kv_heads * w.z;
   w.C = 1;
   while (w.C < 8 && items * w.C < 2ull * f.sms && b.max_len / (2 * w.C) >= 256) w.C *= 2;
-  w.NT = items * w.C >= 4ull * f.sms ? kNarrow : 256;
-  w.cap = (b.max_len + w.C - 1) / w.C;
+  if (w.C == 8 && items * w.C < (uint64_t)f.sms && b.max_len >= 16 * 256) w.C = kMaxCluster;
+  w.NT = items * w.C <= (uint64_t)f.sms ? kBroad : items * w.C >= 8ull * f.sms && b.max_len <= 512 ? kNarrow : kMiddle;
+  // (whole rounds: what a block's lanes cover at once)
+  const uint32_t lanes = c.head_dim == 128 ? 16 : c.head_dim == 64 ? 8 : c.head_dim / 4, round = w.NT / lanes * few_batch(w.NT, w.R);
+  w.cap = ((b.max_len + w.C - 1) / w.C + round - 1) / round * round;
   w.ids = w.cap / c.page + 2;
   auto smem = [&](bool sc) {
-    return w.NT == 256 ? few_smem<256>(w.R, c.head_dim, w.ids, w.cap, sc)
-                       : few_smem<kNarrow>(w.R, c.head_dim, w.ids, w.cap, sc);
+    return w.NT == kBroad    ? few_smem<kBroad>(w.R, c.head_dim, w.ids, w.cap, sc)
+           : w.NT == kMiddle ? few_smem<kMiddle>(w.R, c.head_dim, w.ids, w.cap, sc)
+                             : few_smem<kNarrow>(w.R, c.head_dim, w.ids, w.cap, sc);
   };
-  w.sc_smem = smem(true) <= (uint32_t)f.optin / 2 - 2048;
+  w.sc_smem = smem(true) <= (w.NT == kBroad ? (uint32_t)f.optin : (uint32_t)f.optin / 2 - 2048);
   w.smem = smem(w.sc_smem);
   w.work = w.sc_smem ? 0 : 8ull * w.cap * w.R * items * w.C;
   w.use = w.smem <= (uint32_t)f.optin && w.z <= 65535;
   return w;
 }
 
-template <int LPP, int R, int NT>
+template <int LPP, int NCH, int R, int NT>
 cudaError_t launch_few(const FewParams& p, const FewPlan& w, const DeviceFacts& f, cudaStream_t s) {
   static std::atomic<bool> ready[64];
   if (!ready[f.dev].load(std::memory_order_relaxed)) {
     const cudaError_t e =
-        cudaFuncSetAttribute(k_pattn_few<LPP, R, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, f.optin);
+        cudaFuncSetAttribute(k_pattn_few<LPP, NCH, R, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, f.optin);
     if (e != cudaSuccess) return e;
+    const cudaError_t e16 =  // clusters of sixteen
+        cudaFuncSetAttribute(k_pattn_few<LPP, NCH, R, NT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e16 != cudaSuccess) return e16;
     ready[f.dev].store(true, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t cfg = {};
@@ -534,16 +614,16 @@ cudaError_t launch_few(const FewParams& p, const FewPlan& w, const DeviceFacts& 
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_pattn_few<LPP, R, NT>, p);
+  return cudaLaunchKernelEx(&cfg, k_pattn_few<LPP, NCH, R, NT>, p);
 }
 
 template <int R, int NT>
 cudaError_t launch_few_lpp(const FewParams& p, const FewPlan& w, const DeviceFacts& f, cudaStream_t s) {
   switch (p.a.pool.hd) {
-    case 128: return launch_few<32, R, NT>(p, w, f, s);
-    case 64: return launch_few<16, R, NT>(p, w, f, s);
-    case 32: return launch_few<8, R, NT>(p, w, f, s);
-    default: return launch_few<0, R, NT>(p, w, f, s);
+    case 128: return launch_few<16, 2, R, NT>(p, w, f, s);
+    case 64: return launch_few<8, 2, R, NT>(p, w, f, s);
+    case 32: return launch_few<8, 1, R, NT>(p, w, f, s);
+    default: return launch_few<0, 1, R, NT>(p, w, f, s);
   }
 }
 
@@ -622,8 +702,11 @@ int ck_paged_attention(const ck_paged_cache* cache, uint32_t layer, const ck_pag
   uint8_t* work = static_cast<uint8_t*>(dev_work);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (plan.few.use) {
-    const FewParams fp = {p, reinterpret_cast<long long*>(work), plan.few.cap, plan.few.ids, plan.few.sc_smem};
-    CKP_CUDA(plan.few.NT == 256 ? launch_few_r<256>(fp, plan.few, f, s) : launch_few_r<kNarrow>(fp, plan.few, f, s));
+    const FewParams fp = {p, reinterpret_cast<long long*>(work), plan.few.cap, plan.few.ids, plan.few.sc_smem,
+                          log2_of(plan.few.C)};
+    CKP_CUDA(plan.few.NT == kBroad    ? launch_few_r<kBroad>(fp, plan.few, f, s)
+             : plan.few.NT == kMiddle ? launch_few_r<kMiddle>(fp, plan.few, f, s)
+                                      : launch_few_r<kNarrow>(fp, plan.few, f, s));
     return CK_OK;
   }
   RowsParams rp = {p, reinterpret_cast<long long*>(work), nullptr, nullptr, 0};
