@@ -33,6 +33,24 @@ __device__ __forceinline__ void load2(const int64_t* p, int64_t& a, int64_t& b) 
 // rot / 2), otherwise four in a row.
 __global__ void __launch_bounds__(kStoreThreads) k_paged_store(const StoreParams p) {
   const uint32_t row = blockIdx.x, hd = p.pool.hd;
+  const uint32_t per = hd / 4, kvh = p.pool.kv_heads;
+  const uint32_t unit = blockIdx.y * kStoreThreads + threadIdx.x;
+  const bool in = unit < (p.heads + 2 * kvh) * per;
+  uint32_t head = unit / per;
+  const uint32_t u = unit % per;
+  const bool is_q = head < p.heads, is_v = head >= p.heads + kvh;
+  head -= is_q ? 0u : is_v ? p.heads + kvh : p.heads;
+  // the unit's elements: e0, e0 + 1 and e1, e1 + 1, asked for before the sequence is looked up
+  const bool turned = !is_v && 4 * u < p.rot;
+  const bool halves = turned && p.half;
+  const uint32_t e0 = halves ? 2 * u : 4 * u, e1 = halves ? 2 * u + p.rot / 2 : 4 * u + 2;
+  int64_t x[4] = {0, 0, 0, 0};
+  if (in) {
+    const int64_t* src = (is_q ? p.q + row * p.q_stride : is_v ? p.v + row * p.v_stride : p.k + row * p.k_stride) +
+                         (size_t)head * hd;
+    load2(src + e0, x[0], x[1]);
+    load2(src + e1, x[2], x[3]);
+  }
   const uint32_t s = block_find_seq(p.batch, row);
   if (s >= p.batch.seqs) return;
   const Sequence sq = load_sequence(p.batch, s, p.pool.page_shift);
@@ -49,25 +67,13 @@ __global__ void __launch_bounds__(kStoreThreads) k_paged_store(const StoreParams
     if (lead) note(p.batch, s, err_key(pos, p.pool.layer, CK_PAGED_BAD_SEQUENCE, 0));
     return;
   }
+  if (!in) return;
+  // pair j of the table row: 2u and 2u + 1 in both layouts
+  int4 cs = make_int4(0, 0, 0, 0);
+  if (turned) cs = __ldg(reinterpret_cast<const int4*>(p.rope + (size_t)pos * p.rot + 4 * u));
   const uint32_t id = p.batch.table[(size_t)s * p.batch.stride + (pos >> p.pool.page_shift)];
   const bool paged = id < p.pool.pages;
   if (!paged && lead) note(p.batch, s, err_key(pos, p.pool.layer, CK_PAGED_BAD_PAGE, 0));
-  const uint32_t per = hd / 4, kvh = p.pool.kv_heads;
-  const uint32_t unit = blockIdx.y * kStoreThreads + threadIdx.x;
-  if (unit >= (p.heads + 2 * kvh) * per) return;
-  uint32_t head = unit / per;
-  const uint32_t u = unit % per;
-  const bool is_q = head < p.heads, is_v = head >= p.heads + kvh;
-  head -= is_q ? 0u : is_v ? p.heads + kvh : p.heads;
-  const int64_t* src = (is_q ? p.q + row * p.q_stride : is_v ? p.v + row * p.v_stride : p.k + row * p.k_stride) +
-                       (size_t)head * hd;
-  // the unit's elements: e0, e0 + 1 and e1, e1 + 1
-  const bool turned = !is_v && 4 * u < p.rot;
-  const bool halves = turned && p.half;
-  const uint32_t e0 = halves ? 2 * u : 4 * u, e1 = halves ? 2 * u + p.rot / 2 : 4 * u + 2;
-  int64_t x[4];
-  load2(src + e0, x[0], x[1]);
-  load2(src + e1, x[2], x[3]);
   const int phase = is_v ? 7 : 6;
   if (!is_q) {
 #pragma unroll
@@ -78,8 +84,6 @@ __global__ void __launch_bounds__(kStoreThreads) k_paged_store(const StoreParams
     }
   }
   if (turned) {
-    // pair j of the table row: 2u and 2u + 1 in both layouts
-    const int4 cs = __ldg(reinterpret_cast<const int4*>(p.rope + (size_t)pos * p.rot + 4 * u));
     if (halves) {
       rotate_pair(x[0], x[2], cs.x, cs.y, x[0], x[2]);
       rotate_pair(x[1], x[3], cs.z, cs.w, x[1], x[3]);
@@ -131,6 +135,45 @@ PagesLayout pages_layout(uint32_t pages, uint32_t rows) {
   w.copies = take(sizeof(Copy) * (uint64_t)std::max(pages, rows));
   w.size = off;
   return w;
+}
+
+// The listed copies of pages, keys and values: warp `first` of `warps`, then every one `warps`
+// on, takes one head's filled positions of one layer, count * head_dim words in a row.
+constexpr uint32_t kCopyAhead = 8;
+struct CopyJob {
+  int32_t* k;
+  int32_t* v;
+  uint32_t runs, page_shift, hd;
+};
+__device__ __forceinline__ void copy_pages(const CopyJob& c, const Copy* copies, uint32_t count, uint64_t first,
+                                           uint64_t warps) {
+  const uint32_t lane = threadIdx.x & 31;
+  const uint64_t tasks = 2ull * c.runs * count;
+  const uint32_t page4 = (c.hd << c.page_shift) / 4;  // 16-byte words of a head's page
+  for (uint64_t t = first; t < tasks; t += warps) {
+    const uint64_t i = t / (2 * c.runs);
+    const uint32_t rest = (uint32_t)(t - i * 2 * c.runs), run = rest >> 1;
+    const Copy one = copies[i];
+    int4* pool = reinterpret_cast<int4*>(rest & 1 ? c.v : c.k);
+    const int4* src = pool + ((size_t)one.src * c.runs + run) * page4;
+    int4* dst = pool + ((size_t)one.dst * c.runs + run) * page4;
+    const uint32_t n = one.count * (c.hd / 4);
+    for (uint32_t j0 = lane; j0 < n; j0 += 32 * kCopyAhead) {  // loads in flight before the stores
+      int4 w[kCopyAhead];
+#pragma unroll
+      for (uint32_t u = 0; u < kCopyAhead; ++u)
+        if (j0 + 32 * u < n) w[u] = __ldcs(src + j0 + 32 * u);
+#pragma unroll
+      for (uint32_t u = 0; u < kCopyAhead; ++u)
+        if (j0 + 32 * u < n) __stcs(dst + j0 + 32 * u, w[u]);
+    }
+  }
+}
+constexpr int kCopyThreads = 256;
+__global__ void __launch_bounds__(kCopyThreads) k_copy_pages(const CopyJob c, const Copy* copies, const uint32_t* count) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  copy_pages(c, copies, *count, (uint64_t)blockIdx.x * (kCopyThreads / 32) + threadIdx.x / 32,
+             (uint64_t)gridDim.x * (kCopyThreads / 32));
 }
 
 struct PagesParams {
@@ -222,7 +265,7 @@ __device__ __forceinline__ unsigned long long block_scan(unsigned long long v, u
 // Second step (one block): what each row needs, the free pages in ascending order, and the
 // rows' new pages and copies.  ALONE: with the first step before it.
 template <bool ALONE>
-__global__ void __launch_bounds__(kPlanThreads) k_fork_plan(const PagesParams p) {
+__global__ void __launch_bounds__(kPlanThreads) k_fork_plan(const PagesParams p, const CopyJob job) {
   __shared__ unsigned long long warp_sum[kPlanThreads / 32];
   __shared__ uint32_t n_copies;
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -293,6 +336,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_fork_plan(const PagesParams p)
   }
   __syncthreads();
   if (tid == 0) *p.copied = n_copies;
+  if (job.k) copy_pages(job, p.copies, n_copies, warp, kPlanThreads / 32);  // few enough for one block
 }
 
 // Packing, first step (a warp a row): checks and marks the row's pages.
@@ -335,7 +379,7 @@ __global__ void __launch_bounds__(kTableThreads) k_compact_tables(const PagesPar
 // holes below it, and lists the moves; p.owner becomes each moved page's new number.
 // ALONE: with the first step before it and the third behind.
 template <bool ALONE>
-__global__ void __launch_bounds__(kPlanThreads) k_compact_plan(const PagesParams p) {
+__global__ void __launch_bounds__(kPlanThreads) k_compact_plan(const PagesParams p, const CopyJob job) {
   __shared__ unsigned long long warp_sum[kPlanThreads / 32];
   const uint32_t tid = threadIdx.x;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (what follows waits for this grid's end)
@@ -376,28 +420,9 @@ __global__ void __launch_bounds__(kPlanThreads) k_compact_plan(const PagesParams
     __syncthreads();
     for (uint32_t r = tid / 32; r < p.rows; r += kPlanThreads / 32) compact_table(p, r, tid & 31, (uint32_t)used);
   }
-}
-
-// The listed copies of pages, keys and values: a warp takes one head's filled positions of one
-// layer, count * head_dim words in a row.
-constexpr int kCopyThreads = 256;
-__global__ void __launch_bounds__(kCopyThreads) k_copy_pages(int32_t* k, int32_t* v, uint32_t runs,
-                                                              uint32_t page_shift, uint32_t hd,
-                                                              const Copy* copies, const uint32_t* count) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const uint32_t lane = threadIdx.x & 31;
-  const uint64_t tasks = 2ull * runs * *count;
-  const uint32_t page4 = (hd << page_shift) / 4;  // 16-byte words of a head's page
-  for (uint64_t t = (uint64_t)blockIdx.x * (kCopyThreads / 32) + threadIdx.x / 32; t < tasks;
-       t += (uint64_t)gridDim.x * (kCopyThreads / 32)) {
-    const uint64_t i = t / (2 * runs);
-    const uint32_t rest = (uint32_t)(t - i * 2 * runs), run = rest >> 1;
-    const Copy c = copies[i];
-    int4* pool = reinterpret_cast<int4*>(rest & 1 ? v : k);
-    const int4* src = pool + ((size_t)c.src * runs + run) * page4;
-    int4* dst = pool + ((size_t)c.dst * runs + run) * page4;
-    const uint32_t n = c.count * (hd / 4);
-    for (uint32_t j = lane; j < n; j += 32) dst[j] = src[j];
+  if (job.k) {  // few enough for one block
+    __syncthreads();
+    copy_pages(job, p.copies, (uint32_t)movers, tid / 32, kPlanThreads / 32);
   }
 }
 
@@ -407,6 +432,10 @@ int pages_args(const ck_paged_cache* cache, uint32_t rows, uint32_t stride, void
   if (rows < 1 || rows > 65536 || stride < 1 || stride > (1u << 17)) return CK_INVALID_ARGUMENT;
   *w = pages_layout(cache->pages, rows);
   return work_len < w->size ? CK_BUFFER_TOO_SMALL : CK_OK;
+}
+
+CopyJob copy_job(const ck_paged_cache* c) {
+  return {c->dev_k, c->dev_v, c->layers * c->kv_heads, log2_of(c->page), c->head_dim};
 }
 
 int run_copies(const ck_paged_cache* c, const PagesParams& p, cudaStream_t s) {
@@ -421,9 +450,15 @@ int run_copies(const ck_paged_cache* c, const PagesParams& p, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  CKP_CUDA(cudaLaunchKernelEx(&cfg, k_copy_pages, c->dev_k, c->dev_v, c->layers * c->kv_heads, p.page_shift,
-                              c->head_dim, static_cast<const Copy*>(p.copies), static_cast<const uint32_t*>(p.copied)));
+  CKP_CUDA(cudaLaunchKernelEx(&cfg, k_copy_pages, copy_job(c), static_cast<const Copy*>(p.copies),
+                              static_cast<const uint32_t*>(p.copied)));
   return CK_OK;
+}
+
+// The copies too, where they move at most 256 KB: of a page a row (a fork) or of as many as lie
+// outside the packed range (packing, at most half the pool).
+bool copies_alone(const ck_paged_cache* c, uint64_t pages) {
+  return 8 * pages * c->layers * c->kv_heads * c->page * c->head_dim <= 256 * 1024;
 }
 
 // One block does the table work of a call this small (a row is a warp's, 32 at a time, and a
@@ -540,12 +575,17 @@ int ck_pages_fork(const ck_paged_cache* cache, uint32_t rows_in, const uint32_t*
   p.stride = stride;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (table_work_alone(rows, stride, cache->pages)) {
-    k_fork_plan<true><<<1, kPlanThreads, 0, s>>>(p);
+    const bool all = copies_alone(cache, rows);
+    k_fork_plan<true><<<1, kPlanThreads, 0, s>>>(p, all ? copy_job(cache) : CopyJob{});
+    if (all) {
+      CKP_CUDA(cudaGetLastError());
+      return CK_OK;
+    }
   } else {
     CKP_CUDA(cudaMemsetAsync(dev_work, 0, w.zero, s));
     constexpr uint32_t per = kTableThreads / 32;
     k_fork_mark<<<(rows + per - 1) / per, kTableThreads, 0, s>>>(p);
-    k_fork_plan<false><<<1, kPlanThreads, 0, s>>>(p);
+    k_fork_plan<false><<<1, kPlanThreads, 0, s>>>(p, CopyJob{});
   }
   CKP_CUDA(cudaGetLastError());
   return run_copies(cache, p, s);
@@ -579,12 +619,17 @@ int ck_pages_compact(const ck_paged_cache* cache, uint32_t rows, const uint32_t*
   p.stride = stride;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (table_work_alone(rows, stride, cache->pages)) {
-    k_compact_plan<true><<<1, kPlanThreads, 0, s>>>(p);
+    const bool all = copies_alone(cache, cache->pages / 2);
+    k_compact_plan<true><<<1, kPlanThreads, 0, s>>>(p, all ? copy_job(cache) : CopyJob{});
+    if (all) {
+      CKP_CUDA(cudaGetLastError());
+      return CK_OK;
+    }
   } else {
     CKP_CUDA(cudaMemsetAsync(dev_work, 0, w.zero, s));
     constexpr uint32_t per = kTableThreads / 32;
     k_compact_mark<<<(rows + per - 1) / per, kTableThreads, 0, s>>>(p);
-    k_compact_plan<false><<<1, kPlanThreads, 0, s>>>(p);
+    k_compact_plan<false><<<1, kPlanThreads, 0, s>>>(p, CopyJob{});
     k_compact_tables<<<(rows + per - 1) / per, kTableThreads, 0, s>>>(p);
   }
   CKP_CUDA(cudaGetLastError());

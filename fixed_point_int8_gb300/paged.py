@@ -142,7 +142,7 @@ def paged_store(cache, layer, batch, q, k, v, rope, half=False, out=None, stream
     if cols % hd or k.shape[1] != kv_cols or v.shape[1] != kv_cols:
         raise ValueError("q, k and v: columns do not match the cache's heads")
     if out is None:
-        out = _empty(stream, (rows, cols), torch.int64, q.device)
+        out = _empty(stream, (rows, cols), torch.int64, device)
     else:
         _check("out", out, torch.int64, (rows, cols), device)
     rc = lib().ck_paged_store(cache._c, layer, batch._c, q.data_ptr(), q_step, k.data_ptr(), k_step, v.data_ptr(),
@@ -153,7 +153,7 @@ def paged_store(cache, layer, batch, q, k, v, rope, half=False, out=None, stream
 
 def paged_attention_work(cache, batch, heads, stream=None):
     """Scratch for paged_attention on the stream, as large as the batch's bounds need."""
-    return _empty(stream, _size("ck_paged_attention_work", cache._c, batch._c, heads), torch.uint8, cache.k.device)
+    return _empty(stream, _size("ck_paged_attention_work", cache._c, batch._c, heads), torch.uint8, cache.device)
 
 
 def paged_attention(cache, layer, batch, q, exp_table, inv_sqrt, out=None, work=None, stream=None):
@@ -166,7 +166,7 @@ def paged_attention(cache, layer, batch, q, exp_table, inv_sqrt, out=None, work=
     if cols == 0 or cols % (hd * cache.kv_heads):
         raise ValueError("q: columns are no multiple of the cache's heads")
     if out is None:
-        out = _empty(stream, (rows, cols), torch.int64, q.device)
+        out = _empty(stream, (rows, cols), torch.int64, device)
     else:
         _check("out", out, torch.int64, (rows, cols), device)
     if work is None:
@@ -219,8 +219,8 @@ class PagePlan:
         _check("grow", grow, torch.int32, (rows,), device)
         if held is not None:
             _check("held", held, torch.uint8, (self.cache.pages,), device)
-        out = _empty(stream, (rows, self.stride), torch.int32, table.device)
-        new_lens, status = _empty(stream, (2, rows), torch.int32, table.device).unbind()
+        out = _empty(stream, (rows, self.stride), torch.int32, device)
+        new_lens, status = _empty(stream, (rows,), torch.int32, device), _empty(stream, (rows,), torch.int32, device)
         rc = lib().ck_pages_fork(self.cache._c, rows_in, lens.data_ptr(), table.data_ptr(), rows, parent.data_ptr(),
                                  grow.data_ptr(), self.stride, None if held is None else held.data_ptr(),
                                  new_lens.data_ptr(), out.data_ptr(), status.data_ptr(), *self._args,
@@ -232,9 +232,9 @@ class PagePlan:
         device, rows = self._begin(lens, table)
         if rows > self.rows:
             raise ValueError(f"table: {rows} rows, the plan has room for {self.rows}")
-        out = _empty(stream, (rows, self.stride), torch.int32, table.device)
-        status = _empty(stream, (rows,), torch.int32, table.device)
-        used = _empty(stream, (), torch.int32, table.device)
+        out = _empty(stream, (rows, self.stride), torch.int32, device)
+        status = _empty(stream, (rows,), torch.int32, device)
+        used = _empty(stream, (), torch.int32, device)
         rc = lib().ck_pages_compact(self.cache._c, rows, lens.data_ptr(), table.data_ptr(), self.stride,
                                     out.data_ptr(), used.data_ptr(), status.data_ptr(), *self._args,
                                     _raw(stream, device))
@@ -270,9 +270,9 @@ class BeamPlan:
         _check("scores", scores, torch.int64, (rows,), device)
         _check("done", done, torch.uint8, (rows,), device)
         _check("exp_table", exp_table, torch.int32, (4097,), device)
-        new_scores = _empty(stream, (rows,), torch.int64, logits.device)
-        parent, token = _empty(stream, (2, rows), torch.int32, logits.device).unbind()
-        new_done = _empty(stream, (rows,), torch.uint8, logits.device)
+        new_scores = _empty(stream, (rows,), torch.int64, device)
+        parent, token = _empty(stream, (rows,), torch.int32, device), _empty(stream, (rows,), torch.int32, device)
+        new_done = _empty(stream, (rows,), torch.uint8, device)
         rc = lib().ck_beam_select(logits.data_ptr(), step, self.groups, self.beams, self.vocab, scores.data_ptr(),
                                   done.data_ptr(), exp_table.data_ptr(), stop_tokens, done_token,
                                   new_scores.data_ptr(), parent.data_ptr(), token.data_ptr(), new_done.data_ptr(),
