@@ -711,7 +711,7 @@ int ck_paged_attention(const ck_paged_cache* cache, uint32_t layer, const ck_pag
   }
   RowsParams rp = {p, reinterpret_cast<long long*>(work), nullptr, nullptr, 0};
   if (plan.tiles.use) {
-    CKP_CUDA(cudaMemsetAsync(work + plan.tiles.any_off, 0, 4, s));
+    CKP_CUDA(cudaMemsetAsync(work + plan.tiles.any_off, 0, 8, s));
     const TilesParams tp = {p, plan.tiles.tiles, plan.tiles.cap, reinterpret_cast<uint32_t*>(work + plan.tiles.any_off),
                             reinterpret_cast<uint32_t*>(work + plan.tiles.away_off),
                             reinterpret_cast<int32_t*>(work + plan.tiles.scores_off),

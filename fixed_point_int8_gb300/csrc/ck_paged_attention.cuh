@@ -25,7 +25,7 @@ struct TilesPlan {
 struct TilesParams {
   PAttnParams a;
   uint32_t tiles, cap;
-  uint32_t* any;
+  uint32_t* any;   // the count, and that of the tiles drawn beyond the first of each cluster
   uint32_t* away;  // [sequence][key head][tile]
   int32_t* scores;
   ulonglong2* sums;

@@ -47,7 +47,9 @@ struct Tile {
   static constexpr uint32_t max3(uint32_t a, uint32_t b, uint32_t c) {
     return a > b ? (a > c ? a : c) : (b > c ? b : c);
   }
-  static constexpr uint32_t kOperands = (max3(2 * kKeyBuf, kBufs * kValueBuf, HD * kPitch * 8) + 1023) & ~1023u;
+  static constexpr uint32_t kTurn = (kThreads / 32) * 48 * 33 * 4;  // query digits on their way to tensor memory
+  static constexpr uint32_t kOperands =
+      (max3(2 * kKeyBuf, kBufs * kValueBuf, max3(HD * kPitch * 8, kTurn, 0)) + 1023) & ~1023u;
   static constexpr uint32_t kTableOff = kOperands, kTableBytes = 4097 * 4 + 12;
   static constexpr uint32_t kRedOff = kTableOff + kTableBytes;   // [groups][128] u64
   static constexpr uint32_t kMaxOff = kRedOff + kGroups * kTileRows * 8;  // [128] i32
@@ -174,6 +176,7 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
   uint64_t* drained = full + 4;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + T::kMiscOff + 48);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + T::kMiscOff + 52);
+  uint32_t* next_s = reinterpret_cast<uint32_t*>(sm + T::kMiscOff + 60);
   uint32_t* bad_s = reinterpret_cast<uint32_t*>(sm + T::kMiscOff + 56);  // this block's reason to give the tile away
 
   for (uint32_t i = tid; i < 4097; i += T::kThreads) table_s[i] = min(__ldg(p.exp_tab + i), 1u << 30);
@@ -217,16 +220,24 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
   const uint64_t per_seq = (uint64_t)p.pool.kv_heads * f.tiles;
   const uint64_t items = (uint64_t)p.batch.seqs * per_seq;
 
-  for (uint64_t item = cluster; item < items; item += clusters) {
+  // a cluster's first tile is its number's, the next ones come from a count that all draw from
+  uint64_t item = cluster;
+  while (item < items) {
     const uint32_t seq = (uint32_t)(item / per_seq), rest = (uint32_t)(item - seq * per_seq);
     const uint32_t kvh = rest / f.tiles, v0 = (rest - kvh * f.tiles) * kTileRows;
     const Sequence sq = load_sequence(p.batch, seq, shift);
     if (!sq.ok) {
       if (tid == 0 && rank == 0) note(p.batch, seq, err_key(0, p.pool.layer, CK_PAGED_BAD_SEQUENCE, 0));
+    }
+    const uint32_t queries = sq.ok ? sq.count * group : 0;
+    if (tid == 0 && rank == 0) *next_s = clusters + atomicAdd(f.any + 1, 1u);
+    if (v0 >= queries) {  // (for every block of the cluster)
+      all_sync(C);
+      const uint32_t then = C > 1 ? peer32(next_s, 0) : *next_s;
+      all_sync(C);
+      item = then;
       continue;
     }
-    const uint32_t queries = sq.count * group;
-    if (v0 >= queries) continue;
     const uint32_t v = v0 + r, last = min(queries, v0 + kTileRows) - 1;
     auto seen_by = [&](uint32_t q) {  // positions query q sees
       const uint32_t up = q / group + sq.len;
@@ -242,27 +253,44 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
     uint32_t bad = 0, away = 0;
     __syncthreads();
 
-    // ---- query digits into tensor memory: a thread's row, 32 elements
+    // ---- query digits into tensor memory: a thread's row, 32 elements.  A warp loads two rows at a
+    // time, sixteen lanes along each, and turns them around in shared memory ([plane][pair][row]).
     {
-      const int64_t* q = p.q + (size_t)(sq.first + v / group) * p.q_stride +
-                         (size_t)(kvh * group + v % group) * HD + 32 * cg;
-      longlong2 x[16];
+      uint32_t* turn = reinterpret_cast<uint32_t*>(sm) + warp * (48 * 33);
+      const uint32_t pair = lane & 15u;
+      longlong2 words[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        x[i] = v < queries ? __ldg(reinterpret_cast<const longlong2*>(q) + i) : make_longlong2(0, 0);
-      uint32_t w[3][16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const uint64_t a = (uint64_t)x[i].x + 0x808080u, b = (uint64_t)x[i].y + 0x808080u;
-        bad |= (uint32_t)((a | b) >> 24 != 0);
-        const uint32_t u = __byte_perm((uint32_t)a, (uint32_t)b, 0x5410), t = __byte_perm((uint32_t)a, (uint32_t)b, 0x7632);
-        w[0][i] = sub_1152(lift<0x4240>(u));
-        w[1][i] = sub_1152(lift<0x4341>(u));
-        w[2][i] = sub_1152(lift<0x4240>(t));
+      for (uint32_t i = 0; i < 16; ++i) {
+        const uint32_t q = v0 + 32 * (warp & 3) + 2 * i + (lane >> 4);
+        words[i] = make_longlong2(0, 0);
+        if (q < queries) {
+          const uint32_t token = group == 1 ? q : q / group;
+          words[i] = __ldg(reinterpret_cast<const longlong2*>(p.q + (size_t)(sq.first + token) * p.q_stride +
+                                                              (size_t)(kvh * group + q - token * group) * HD + 32 * cg) +
+                           pair);
+        }
       }
 #pragma unroll
-      for (int k = 0; k < 3; ++k) tmem_st16(tmem + lane_base + k * (HD / 2) + 16 * cg, w[k]);
+      for (uint32_t i = 0; i < 16; ++i) {
+        const uint32_t row = 2 * i + (lane >> 4);
+        const longlong2 x = words[i];
+        const uint64_t a = (uint64_t)x.x + 0x808080u, b = (uint64_t)x.y + 0x808080u;
+        bad |= (uint32_t)((a | b) >> 24 != 0);
+        const uint32_t u = __byte_perm((uint32_t)a, (uint32_t)b, 0x5410), t = __byte_perm((uint32_t)a, (uint32_t)b, 0x7632);
+        turn[pair * 33 + row] = sub_1152(lift<0x4240>(u));
+        turn[(16 + pair) * 33 + row] = sub_1152(lift<0x4341>(u));
+        turn[(32 + pair) * 33 + row] = sub_1152(lift<0x4240>(t));
+      }
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = turn[(16 * k + i) * 33 + lane];
+        tmem_st16(tmem + lane_base + k * (HD / 2) + 16 * cg, w);
+      }
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      __syncthreads();  // the keys' operands go to the same place
     }
 
     // ---- scores: 32 positions at a time
@@ -340,17 +368,38 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
         tmem_wait_ld();
         const uint32_t at = i * kTilePos + cg * kCols + h;
         int32_t c[8];
+        float peak = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          // (sum of the accumulators by weight) >> 16, the low part in 32 bits
-          const int32_t lo = __float2int_rn(__uint_as_float(d[0][j])) + (__float2int_rn(__uint_as_float(d[1][j])) << 8);
-          const int32_t mid = (lo >> 16) + __float2int_rn(__uint_as_float(d[2][j])) +
-                              (__float2int_rn(__uint_as_float(d[3][j])) << 8);
-          const int64_t dot = (int64_t)mid + ((int64_t)__float2int_rn(__uint_as_float(d[4][j])) << 16);
-          const int64_t s = wmul(dot, (int64_t)p.inv_sqrt) >> 24;
-          c[j] = (int32_t)s;
-          if (c[j] != s) c[j] = s < 0 ? INT32_MIN : INT32_MAX;
-          if (at + j < lim) m = max(m, c[j]);
+        for (int j = 0; j < 8; ++j) peak = fmaxf(peak, fabsf(__uint_as_float(d[4][j])));
+        if (peak < 8192.0f && p.inv_sqrt <= 1u << 24) {
+          // the highest accumulator is small (the usual case): it joins the next exactly (below
+          // 2^23), and (the sum of the accumulators by weight) >> 16 fits 32 bits, and so the score
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int32_t lo = __float2int_rn(__uint_as_float(d[0][j])) + (__float2int_rn(__uint_as_float(d[1][j])) << 8);
+            const int32_t dot = (lo >> 16) + __float2int_rn(__uint_as_float(d[2][j])) +
+                                (__float2int_rn(fmaf(__uint_as_float(d[4][j]), 256.0f, __uint_as_float(d[3][j]))) << 8);
+            c[j] = (int32_t)(((int64_t)dot * (int32_t)p.inv_sqrt) >> 24);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int32_t lo = __float2int_rn(__uint_as_float(d[0][j])) + (__float2int_rn(__uint_as_float(d[1][j])) << 8);
+            const int32_t mid = (lo >> 16) + __float2int_rn(__uint_as_float(d[2][j])) +
+                                (__float2int_rn(__uint_as_float(d[3][j])) << 8);
+            const int64_t dot = (int64_t)mid + ((int64_t)__float2int_rn(__uint_as_float(d[4][j])) << 16);
+            const int64_t s = wmul(dot, (int64_t)p.inv_sqrt) >> 24;
+            c[j] = (int32_t)s;
+            if (c[j] != s) c[j] = s < 0 ? INT32_MIN : INT32_MAX;
+          }
+        }
+        if (at + 8 <= lim) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) m = max(m, c[j]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (at + j < lim) m = max(m, c[j]);
         }
         int4* dst = scores + (size_t)(at / 4) * kTileRows + r;
         dst[0] = make_int4(c[0], c[1], c[2], c[3]);
@@ -451,7 +500,8 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
       for (uint32_t k = 0; k < 8; ++k) z += part[k];
     }
     if (z < (1ull << 30)) z = 1ull << 30;
-    const uint32_t rz = (uint32_t)((1ull << 61) / z);
+    const bool alone = z <= 1ull << 30;  // one score counts: P = e >> 6, and it may be 2^24
+    const uint32_t rz = alone ? 0u : (uint32_t)div_by_estimate(1ull << 62, z, rcp_estimate((float)z));
 
     // ---- weighted values: 64 positions at a time
     const uint32_t nb = away ? 0 : all_blocks;
@@ -509,27 +559,33 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
         const int4 s0 = sraw[2 * c], s1 = sraw[2 * c + 1];
         const uint32_t s[8] = {(uint32_t)s0.x, (uint32_t)s0.y, (uint32_t)s0.z, (uint32_t)s0.w,
                                (uint32_t)s1.x, (uint32_t)s1.y, (uint32_t)s1.z, (uint32_t)s1.w};
-        uint32_t pr[8], full24 = 0;
+        uint32_t pr[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const uint32_t e = table_s[min(((uint32_t)m - s[j]) >> 8, 4096u)];
-          // floor((e << 24) / z): rz is below 2^61 / z by less than one, so the estimate is short
-          // by less than 2^-7 and wrong only when its fraction ends that close to the next integer
-          const unsigned long long w = (unsigned long long)e * rz;
-          uint32_t q = (uint32_t)(w >> 37);
-          if ((((uint32_t)(w >> 30)) & 0x7Fu) == 0x7Fu) {
-            const unsigned long long rem = ((unsigned long long)e << 24) - (unsigned long long)q * z;
-            q += rem >= z;
+          // floor((e << 24) / z): with rz = floor(2^62 / z) it lies between the products of e with
+          // rz and rz + 1, >> 38; where those differ (less than one in 2^8) the remainder decides
+          const uint32_t low = __umulhi(e, rz), high = __umulhi(e, rz + 1);
+          pr[j] = low >> 6;
+          if ((low ^ high) >> 6) {
+            const unsigned long long rem = ((unsigned long long)e << 24) - (unsigned long long)pr[j] * z;
+            pr[j] += rem >= z;
           }
-          pr[j] = at + j < lim ? q : 0u;
-          full24 |= pr[j];
+        }
+        if (alone) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) pr[j] = table_s[min(((uint32_t)m - s[j]) >> 8, 4096u)] >> 6;
+        }
+        if (at + 8 > lim) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (at + j >= lim) pr[j] = 0;
         }
         uint32_t d[3][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          uint32_t a = pr[2 * i], bq = pr[2 * i + 1];
-          uint32_t extra = 0;
-          if (full24 >> 24) {  // P = 2^24 is 0xFFFFFF and one more in the lowest digit (2^-12 in its plane)
+          uint32_t a = pr[2 * i], bq = pr[2 * i + 1], extra = 0;
+          if (alone) {  // P = 2^24 is 0xFFFFFF and one more in the lowest digit (2^-12 in its plane)
             extra = (a >> 24 ? 0x0C00u : 0u) | (bq >> 24 ? 0x0C000000u : 0u);
             a -= a >> 24;
             bq -= bq >> 24;
@@ -538,7 +594,7 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
           d[0][i] = fma_h2(lift<0x4240>(u), kScale0, kUns0);
           d[1][i] = fma_h2(lift<0x4341>(u), kScale1, kUns1);
           d[2][i] = fma_h2(lift<0x4240>(t), kScale2, kUns2);
-          if (full24 >> 24) asm("add.rn.f16x2 %0, %0, %1;" : "+r"(d[0][i]) : "r"(extra));
+          if (alone) asm("add.rn.f16x2 %0, %0, %1;" : "+r"(d[0][i]) : "r"(extra));
         }
         uint8_t* dst = planes + r * 128 + ((chunk ^ (r & 7u)) << 4);
 #pragma unroll
@@ -638,6 +694,7 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
     all_sync(C);
     away |= *bad_s;
     for (uint32_t k = 0; C > 1 && k < C; ++k) away |= peer32(bad_s, k);
+    const uint32_t then = C > 1 ? peer32(next_s, 0) : *next_s;
     const uint32_t rows = kTileRows / C;
     for (uint32_t i = tid; !away && i < rows * HD; i += T::kThreads) {
       const uint32_t row = rank * rows + i / HD, e = i % HD, q = v0 + row;
@@ -659,6 +716,7 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
       if (away) atomicAdd(f.any, 1u);
     }
     all_sync(C);  // no block goes on while another reads its sums or flags
+    item = then;
   }
   tc_before();
   __syncthreads();
@@ -667,25 +725,56 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
 }
 
 template <int HD>
-cudaError_t launch_tiles_hd(const TilesParams& p, const TilesPlan& w, const DeviceFacts& f, cudaStream_t s) {
+cudaError_t configure_tiles(const DeviceFacts& f) {
   static std::atomic<bool> ready[64];
-  if (!ready[f.dev].load(std::memory_order_relaxed)) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(k_pattn_tiles<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, Tile<HD>::kSmem);
+  if (ready[f.dev].load(std::memory_order_relaxed)) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(k_pattn_tiles<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, Tile<HD>::kSmem);
+  if (e == cudaSuccess) ready[f.dev].store(true, std::memory_order_relaxed);
+  return e;
+}
+
+template <int HD>
+void tiles_config(uint32_t blocks, uint32_t C, cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr) {
+  *cfg = {};
+  cfg->gridDim = dim3(blocks);
+  cfg->blockDim = dim3(Tile<HD>::kThreads);
+  cfg->dynamicSmemBytes = Tile<HD>::kSmem;
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = C;
+  attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+  cfg->attrs = attr;
+  cfg->numAttrs = 1;
+}
+
+// Clusters of C blocks that are resident at once, looked up once for each C (the runtime counts one
+// block an SM; of head size 64 two run).
+template <int HD>
+cudaError_t resident_tiles(uint32_t C, const DeviceFacts& f, uint32_t* out) {
+  static std::atomic<int> known[64][9];  // the number and one more, zero before
+  int n = known[f.dev][C].load(std::memory_order_relaxed) - 1;
+  if (n < 0) {
+    cudaError_t e = configure_tiles<HD>(f);
     if (e != cudaSuccess) return e;
-    ready[f.dev].store(true, std::memory_order_relaxed);
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[1];
+    tiles_config<HD>(C, C, &cfg, attr);
+    if ((e = cudaOccupancyMaxActiveClusters(&n, k_pattn_tiles<HD>, &cfg)) != cudaSuccess) return e;
+    n *= HD == 64 ? 2 : 1;
+    known[f.dev][C].store(n + 1, std::memory_order_relaxed);
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(w.clusters * w.C);
-  cfg.blockDim = dim3(Tile<HD>::kThreads);
-  cfg.dynamicSmemBytes = Tile<HD>::kSmem;
-  cfg.stream = s;
+  *out = (uint32_t)n;
+  return cudaSuccess;
+}
+
+template <int HD>
+cudaError_t launch_tiles_hd(const TilesParams& p, const TilesPlan& w, const DeviceFacts& f, cudaStream_t s) {
+  const cudaError_t e = configure_tiles<HD>(f);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = w.C;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  tiles_config<HD>(w.clusters * w.C, w.C, &cfg, attr);
+  cfg.stream = s;
   return cudaLaunchKernelEx(&cfg, k_pattn_tiles<HD>, p);
 }
 
@@ -697,20 +786,35 @@ TilesPlan plan_tiles(const ck_paged_cache& c, const ck_paged_batch& b, uint32_t 
   if (c.head_dim != 64 && c.head_dim != 128) return w;
   const uint32_t smem = c.head_dim == 64 ? Tile<64>::kSmem : Tile<128>::kSmem;
   if (smem > (uint32_t)f.optin) return w;
-  const uint32_t slots = (uint32_t)f.sms * (c.head_dim == 64 ? 2 : 1);
   w.tiles = (uint32_t)((queries + kTileRows - 1) / kTileRows);
   const uint64_t items = (uint64_t)b.seqs * c.kv_heads * w.tiles;
-  // blocks of a cluster: until every place on the GPU has one, while each has 256 positions
-  w.C = 1;
-  while (w.C < 8 && 2 * items * w.C <= slots && b.max_len / (2 * w.C) >= 256) w.C *= 2;
-  w.clusters = (uint32_t)std::min<uint64_t>(items, std::max(1u, slots / w.C));
+  if (items > 0xFFFFFFFFull - 65536) return w;  // (the count of tiles is 32 bits)
+  // Blocks of a cluster, by what each choice takes, in positions a block goes through: rounds of
+  // equal tiles for one sequence; for several, whose lengths differ, three quarters of the bound
+  // on average, but never less than the longest.  What surrounds a tile (queries, exchanges,
+  // sums) measured as about 200 positions.
+  double best = 0;
+  for (uint32_t C = 1; C <= 8; C *= 2) {
+    uint32_t n = 0;
+    if ((c.head_dim == 64 ? resident_tiles<64>(C, f, &n) : resident_tiles<128>(C, f, &n)) != cudaSuccess) return w;
+    if (n == 0) continue;
+    const double each = (double)b.max_len / C + 200, clusters = (double)std::min<uint64_t>(items, n);
+    const double cost = b.seqs == 1 ? std::ceil(items / clusters) * each
+                                    : std::max(each, items / clusters * (0.75 * b.max_len / C + 200));
+    if (!w.use || cost < 0.95 * best) {
+      w.use = true;
+      best = cost;
+      w.C = C;
+      w.clusters = (uint32_t)clusters;
+    }
+  }
+  if (!w.use) return w;
   w.cap = ((b.max_len + w.C - 1) / w.C + kBlockPos - 1) & ~(kBlockPos - 1);
   w.any_off = 0;
   w.away_off = 256;
   w.scores_off = w.away_off + align256(4 * items);
   w.sums_off = w.scores_off + align256(4ull * kTileRows * w.cap * w.clusters * w.C);
   w.size = w.sums_off + 8ull * kTileRows * c.head_dim * w.clusters * w.C;
-  w.use = true;
   return w;
 }
 
