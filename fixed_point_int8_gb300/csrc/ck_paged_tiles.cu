@@ -326,11 +326,11 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
         d[1][i] = sub_1152(lift<0x4341>(u));
         d[2][i] = sub_1152(lift<0x4240>(t));
       }
-      uint8_t* dst = sm + buf * T::kKeyBuf + (kchunk >> 3) * (kTilePos * 128) + kpos * 128 +
-                     (((kchunk & 7u) ^ (kpos & 7u)) << 4);
+      uint8_t* dst = sm + buf * T::kKeyBuf + (kchunk >> 3) * (3 * kTilePos * 128) + kpos * 128 +
+                     (((kchunk & 7u) ^ (kpos & 7u)) << 4);  // [64 elements][plane][position]
 #pragma unroll
       for (int k = 0; k < 3; ++k)
-        *reinterpret_cast<uint4*>(dst + k * T::kKeyPlane) = make_uint4(d[k][0], d[k][1], d[k][2], d[k][3]);
+        *reinterpret_cast<uint4*>(dst + k * (kTilePos * 128)) = make_uint4(d[k][0], d[k][1], d[k][2], d[k][3]);
       fence_operands();
     };
     // A batch's products, by one thread of the warps in turn, once its operands are in place and
@@ -341,16 +341,24 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
         if (i >= T::kBufs) wait_drained(tiles + i - T::kBufs);
         const uint32_t leader = elected(), d0 = tmem_u + T::kScoreCol + (i % T::kBufs) * (kDiags * kTilePos);
         const uint64_t b0 = operands + (i & 1u) * (T::kKeyBuf >> 4);
+        // A query plane times the three key planes side by side goes to the accumulators of weights
+        // qp, qp + 1, qp + 2, which lie side by side too; the first products of the two highest
+        // weights go ahead of the others, as they start their accumulators.
+        auto product = [&](uint32_t qp, uint32_t kp, uint32_t planes, uint32_t kk, uint32_t acc) {
+          mma_ts(leader, d0 + (qp + kp) * kTilePos, tmem_u + qp * (HD / 2) + 8 * kk,
+                 b0 + (((kk >> 2) * (3 * kTilePos * 128) + kp * (kTilePos * 128) + (kk & 3u) * 32) >> 4),
+                 tile_idesc(planes * kTilePos), acc);
+        };
+        product(0, 0, 3, 0, 0);
+        product(1, 2, 1, 0, 0);
+        product(2, 2, 1, 0, 0);
+        product(1, 0, 2, 0, 1);
+        product(2, 0, 2, 0, 1);
 #pragma unroll
-        for (uint32_t g = 0; g < kDiags; ++g) {
-#pragma unroll
-          for (uint32_t qp = g > 2 ? g - 2 : 0; qp <= (g < 2 ? g : 2); ++qp) {
-#pragma unroll
-            for (uint32_t kk = 0; kk < HD / 16; ++kk)
-              mma_ts(leader, d0 + g * kTilePos, tmem_u + qp * (HD / 2) + 8 * kk,
-                     b0 + (((g - qp) * T::kKeyPlane + (kk >> 2) * (kTilePos * 128) + (kk & 3u) * 32) >> 4),
-                     tile_idesc(kTilePos), qp != (g > 2 ? g - 2 : 0) || kk != 0);
-          }
+        for (uint32_t kk = 1; kk < HD / 16; ++kk) {
+          product(0, 0, 3, kk, 1);
+          product(1, 0, 3, kk, 1);
+          product(2, 0, 3, kk, 1);
         }
         commit(leader, done + ((batch + i) & 1u));
       }
@@ -459,26 +467,34 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
     away |= (uint32_t)(np != 0 && (m == INT32_MAX || m < INT32_MIN + (1 << 21)));
     away = (uint32_t)__syncthreads_or((int)away);  // (the same rows, so the same in every block)
 
-    // ---- the sum of exponentials
+    // ---- the exponentials, in the place of the scores, and their sum
     unsigned long long z = 0;
     if (!away) {
-      const int4* src = scores + r;
+      int4* src = scores + r;
       constexpr uint32_t kAhead = 8;  // loads in flight
-      for (uint32_t i = 4 * cg; i < lim; i += 4 * T::kGroups * kAhead) {
+      const uint32_t quads = (lim + 3) / 4;
+      for (uint32_t i = cg; i < quads; i += T::kGroups * kAhead) {
         int4 c[kAhead];
 #pragma unroll
         for (uint32_t u = 0; u < kAhead; ++u) {
-          const uint32_t at = i + 4 * T::kGroups * u;
-          c[u] = at < lim ? src[(size_t)(at / 4) * kTileRows] : make_int4(0, 0, 0, 0);
+          const uint32_t k = i + T::kGroups * u;
+          c[u] = k < quads ? src[(size_t)k * kTileRows] : make_int4(0, 0, 0, 0);
         }
 #pragma unroll
         for (uint32_t u = 0; u < kAhead; ++u) {
-          const uint32_t at = i + 4 * T::kGroups * u;
+          const uint32_t k = i + T::kGroups * u;
           const int32_t x[4] = {c[u].x, c[u].y, c[u].z, c[u].w};
+          uint32_t e[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t e = table_s[min(((uint32_t)m - (uint32_t)x[j]) >> 8, 4096u)];
-            z += at + j < lim ? e : 0u;
+          for (int j = 0; j < 4; ++j) e[j] = table_s[min(((uint32_t)m - (uint32_t)x[j]) >> 8, 4096u)];
+          if (4 * k + 4 > lim) {  // the last quad may be cut
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (4 * k + j >= lim) e[j] = 0;
+          }
+          if (k < quads) {
+            z += (unsigned long long)(e[0] + e[1]) + (e[2] + e[3]);
+            src[(size_t)k * kTileRows] = make_int4(e[0], e[1], e[2], e[3]);
           }
         }
       }
@@ -562,7 +578,7 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
         uint32_t pr[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const uint32_t e = table_s[min(((uint32_t)m - s[j]) >> 8, 4096u)];
+          const uint32_t e = s[j];
           // floor((e << 24) / z): with rz = floor(2^62 / z) it lies between the products of e with
           // rz and rz + 1, >> 38; where those differ (less than one in 2^8) the remainder decides
           const uint32_t low = __umulhi(e, rz), high = __umulhi(e, rz + 1);
@@ -574,12 +590,7 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
         }
         if (alone) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) pr[j] = table_s[min(((uint32_t)m - s[j]) >> 8, 4096u)] >> 6;
-        }
-        if (at + 8 > lim) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (at + j >= lim) pr[j] = 0;
+          for (int j = 0; j < 8; ++j) pr[j] = s[j] >> 6;
         }
         uint32_t d[3][4];
 #pragma unroll
@@ -638,21 +649,25 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
         const uint32_t leader = elected();
         const uint64_t a0 = operands + (b % T::kBufs) * (T::kValueBuf >> 4), b0 = a0 + (3 * T::kProbPlane >> 4);
         const uint32_t go_on = b % kFlushBlocks != 0;
+        // As for the scores; the product of the highest weight shares the last accumulator (and
+        // starts it, where a flush went before).
+        auto product = [&](uint32_t pp, uint32_t vp, uint32_t planes, uint32_t g, uint32_t kk, uint32_t acc) {
+          mma_ss(leader, tmem_u + g * HD, a0 + ((pp * T::kProbPlane + kk * 32) >> 4),
+                 b0 + ((vp * T::kValuePlane + kk * 32) >> 4), tile_idesc(planes * HD), acc);
+        };
 #pragma unroll
-        for (uint32_t g = 0; g < 4; ++g) {
-          // planes of weight g; the last accumulator also takes weight 4
-#pragma unroll
-          for (uint32_t pp = g > 2 ? g - 2 : 0; pp < 3; ++pp) {
-#pragma unroll
-            for (uint32_t vp = 0; vp < 3; ++vp) {
-              if (pp + vp != g && !(g == 3 && pp + vp == 4)) continue;
-              const bool first = pp == (g > 2 ? g - 2 : 0) && vp == g - pp;
-#pragma unroll
-              for (uint32_t kk = 0; kk < kBlockPos / 16; ++kk)
-                mma_ss(leader, tmem_u + g * HD, a0 + ((pp * T::kProbPlane + kk * 32) >> 4),
-                       b0 + ((vp * T::kValuePlane + kk * 32) >> 4), tile_idesc(HD), first && kk == 0 ? go_on : 1u);
-            }
+        for (uint32_t kk = 0; kk < kBlockPos / 16; ++kk) {
+          product(2, 2, 1, 3, kk, kk == 0 ? go_on : 1u);
+          if (HD == 64) {
+            product(0, 0, 3, 0, kk, kk == 0 ? go_on : 1u);
+            product(1, 0, 3, 1, kk, 1);
+          } else {  // (256 columns at most)
+            product(0, 0, 2, 0, kk, kk == 0 ? go_on : 1u);
+            product(0, 2, 1, 2, kk, kk == 0 ? go_on : 1u);
+            product(1, 0, 2, 1, kk, 1);
+            product(1, 2, 1, 3, kk, 1);
           }
+          product(2, 0, 2, 2, kk, 1);
         }
         commit(leader, done + ((batch + b) & 1u));
       }
