@@ -97,6 +97,9 @@ def lib() -> ctypes.CDLL:
             "ck_beam_select": ([vp, sz, u32, u32, u32, vp, vp, vp, u32, u32, vp, vp, vp, vp, vp, sz, vp],
                                ctypes.c_int),
             "ck_host_log_sum": ([u64], i64),
+            "ck_turn_paged_work": ([vp, vp, vp, vp], ctypes.c_int),
+            "ck_turn_paged": ([vp, vp, vp, vp, vp, sz, vp, sz, vp], ctypes.c_int),
+            "ck_model_tables": ([vp, vp, vp, vp], ctypes.c_int),
             "ck_version": ([], ctypes.c_char_p),
         }
         for name, (args, res) in sig.items():
@@ -256,6 +259,27 @@ class Model:
         res = TurnResult()
         rc = lib().ck_turn_noalloc(self._h, _ptr(state), state.numel(), _stream(stream), ctypes.byref(res))
         return rc, res.as_dict()
+
+    def turn_paged(self, cache, batch, tokens, logits=None, work=None, stream=None):
+        """A paged batch's new rows through the layers (ck_turn_paged): tokens int32 [rows].
+        Returns (rc, logits int64 [seqs][vocab] of each sequence's last row)."""
+        from . import paged
+        return paged.turn_paged(self, cache, batch, tokens, logits, work, stream)
+
+    def turn_paged_work(self, cache, batch, stream=None):
+        """Scratch for turn_paged, as large as the batch's bounds need."""
+        from . import paged
+        return paged.turn_paged_work(self, cache, batch, stream)
+
+    def exp_table(self):
+        """The exponential table in device memory, int32 [4097] (a view of the model's memory)."""
+        import torch
+        exp, rope, inv = ctypes.c_void_p(), ctypes.c_void_p(), ctypes.c_uint32()
+        rc = lib().ck_model_tables(self._h, ctypes.byref(exp), ctypes.byref(rope), ctypes.byref(inv))
+        if rc:
+            raise CkError(rc, "ck_model_tables")
+        at = exp.value - self.mem.data_ptr()
+        return self.mem[at:at + 4 * 4097].view(torch.int32)
 
     def logits(self, state, stream=None):
         out = np.zeros(self.config["vocab"], dtype=np.int64)

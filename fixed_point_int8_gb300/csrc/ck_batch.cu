@@ -26,6 +26,7 @@
 #include <cuda_fp16.h>
 
 #include "ck_internal.cuh"
+#include "ck_paged.cuh"
 #include "ck_tc.cuh"
 
 namespace ck {
@@ -38,7 +39,7 @@ constexpr uint32_t kBTile = kBN * kBK * 2;   // f16 planes: one 64 x 128 tile
 constexpr uint32_t kFlushGroups = 4;         // column groups between f32 -> i32 moves
 constexpr int kRowThreads = 256;
 
-enum BEpi : int { kBEpiQKV = 0, kBEpiResid = 1, kBEpiSiLU = 2, kBEpiLogits = 3 };
+enum BEpi : int { kBEpiQKV = 0, kBEpiResid = 1, kBEpiSiLU = 2, kBEpiLogits = 3, kBEpiStore = 4 };
 
 // A chunk of one run is gated by that run's state: a position earlier in the same turn
 // that failed it stops the chunk.  A batch of runs has no gate (nullptr).
@@ -566,6 +567,11 @@ struct BEpiParams {
   // residual followed by the next RMS normalization (k_bresnorm): its weights and output
   int64_t* XB;
   const int32_t* norm_w;
+  // store: Y[n][r] = y (y_stride words from row to row), for the rows n whose sequence has a new
+  // token, or all of them (start null)
+  int64_t* Y;
+  size_t y_stride;
+  const uint32_t* start;
 };
 
 // y[n][r] = ((sum_k S_k[n][r] << 8k) * scale[r]) >> 24, wrapping, for rows r and r + 1 (r
@@ -615,8 +621,15 @@ __global__ void __launch_bounds__(kRowThreads) k_bepi(const BEpiParams p) {
       if (r + 1 < p.rows) lg[r + 1] = y1;
       continue;
     }
+    if (p.mode == kBEpiStore && p.start && p.start[n + 1] <= p.start[n]) continue;
     int64_t y0, y1;
     combine_pair(p, L, n, r, y0, y1);
+    if (p.mode == kBEpiStore) {
+      int64_t* y = p.Y + n * p.y_stride + r;
+      y[0] = y0;
+      if (r + 1 < p.rows) y[1] = y1;
+      continue;
+    }
     if (p.mode == kBEpiResid) {
       int64_t* x = p.X + (size_t)n * p.rows + r;
       x[0] = wadd(x[0], y0);
@@ -929,6 +942,50 @@ __global__ void __launch_bounds__(kRowThreads) k_battn(const BAttnParams p) {
   block_or_to(orv, p.or_out, reinterpret_cast<unsigned long long*>(red));
 }
 
+// ------------------------------------------------------------------ rows over a cache in pages
+
+// Phase 3 for the rows of a paged batch (one block each): x of the row's token.  A token outside
+// the vocabulary gives zeros and is the sequence's failure there.
+__global__ void __launch_bounds__(kRowThreads) k_pembed(const BatchView b, const uint32_t* tokens, int64_t* X,
+                                                        uint32_t d, const uint8_t* E, const uint32_t* Es,
+                                                        uint32_t vocab) {
+  const uint32_t n = blockIdx.x, tok = tokens[n];
+  int64_t* x = X + (size_t)n * d;
+  const uint32_t s = block_find_seq(b, n);
+  if (tok >= vocab || s >= b.seqs || n < b.start[s]) {  // (a row of no sequence: zeros go through the layers)
+    if (threadIdx.x == 0 && s < b.seqs && n >= b.start[s]) {
+      const uint32_t count = b.start[s + 1] - b.start[s], up = n - b.start[s] + b.len[s];
+      if (up >= count) note(b, s, err_key(min(up - count, kMaxPositions), 0, 3, 0));
+    }
+    for (uint32_t i = threadIdx.x; i < d; i += blockDim.x) x[i] = 0;
+    return;
+  }
+  const int64_t scale = (int64_t)__ldg(Es + tok);
+  for (uint32_t i = threadIdx.x; i < d; i += blockDim.x)
+    x[i] = ((int64_t)E[grouped_offset(vocab, tok, i)] - 128) * scale >> 8;
+}
+
+// ORs the magnitudes of V's words into *orw, for the plane count.
+__global__ void __launch_bounds__(kRowThreads) k_magnitudes(const int64_t* V, uint64_t words, unsigned long long* orw) {
+  __shared__ unsigned long long red[kRowThreads / 32];
+  unsigned long long o = 0;
+  for (uint64_t i = (uint64_t)blockIdx.x * kRowThreads + threadIdx.x; i < words; i += (uint64_t)gridDim.x * kRowThreads)
+    o |= (unsigned long long)(V[i] ^ (V[i] >> 63));
+  block_or_to(o, orw, red);
+}
+
+// The last row of each sequence (one block each), zeros where it has none.
+__global__ void __launch_bounds__(kRowThreads) k_last_rows(const BatchView b, const int64_t* X, int64_t* G, uint32_t d) {
+  const uint32_t s = blockIdx.x, end = b.start[s + 1];
+  const bool some = end > b.start[s] && end <= b.rows;
+  for (uint32_t i = threadIdx.x; i < d; i += blockDim.x) G[(size_t)s * d + i] = some ? X[(size_t)(end - 1) * d + i] : 0;
+}
+
+// A contraction's wait ran out: nothing of the pass is trusted, every sequence fails.
+__global__ void __launch_bounds__(kRowThreads) k_pfinish(const BatchView b, const int* fault) {
+  for (uint32_t s = threadIdx.x; *fault && s < b.seqs; s += kRowThreads) note(b, s, 0);
+}
+
 // ------------------------------------------------------------------ end of a pass
 
 // Rows pos0 .. pos0+P-1 of one run.
@@ -1144,13 +1201,28 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// A pass over a cache in pages: the batch and its tokens, where its stacked matrix rows and its
+// attention's scratch lie, and the sequences' logits.
+struct PagedPass {
+  const ck_paged_cache* cache;
+  const ck_paged_batch* batch;
+  const uint32_t* tokens;
+  int64_t* qkv;
+  uint8_t* attn_work;
+  size_t attn_len;
+  uint32_t rope_rows;
+  int64_t* logits;
+  size_t logits_stride;
+};
+
 // The layers for P rows (phases 3 to 16), then, with `classify`, the final norm and the
-// classifier rows into the logits of the rows that generate.
+// classifier rows into the logits of the rows that generate.  With `paged`, the rows' tokens,
+// keys and values are the batch's, and the logits those of each sequence's last row.
 cudaError_t enqueue_rows(const PrefillModel& m, const uint8_t* gate, const WorkLayout& w,
                          uint8_t* work, uint32_t P, uint32_t max_positions, bool classify,
-                         cudaStream_t s) {
+                         cudaStream_t s, const PagedPass* paged = nullptr) {
   const ck_config& c = m.cfg;
-  const uint32_t Npad = pad64(P);
+  uint32_t Npad = pad64(P);
   const uint32_t KGd = m.pitch_d / kBK, KGh = m.pitch_h / kBK;
   int64_t* X = reinterpret_cast<int64_t*>(work + w.X);
   int64_t* XB = reinterpret_cast<int64_t*>(work + w.XB);
@@ -1213,7 +1285,11 @@ cudaError_t enqueue_rows(const PrefillModel& m, const uint8_t* gate, const WorkL
     launch_pdl(k_bepi, dim3(blocks), dim3(kRowThreads), 0, s, p);
   };
 
-  k_bembed<<<P, kRowThreads, 0, s>>>(gate, rows, X, c.dim, m.embed, m.embed_scale, c.vocab, rstat);
+  if (paged)
+    k_pembed<<<P, kRowThreads, 0, s>>>(batch_view(*paged->batch), paged->tokens, X, c.dim, m.embed, m.embed_scale,
+                                       c.vocab);
+  else
+    k_bembed<<<P, kRowThreads, 0, s>>>(gate, rows, X, c.dim, m.embed, m.embed_scale, c.vocab, rstat);
   for (uint32_t l = 0; l < c.layers; ++l) {
     const DevLayer& Wl = m.layers[l];
     unsigned long long* o4 = orw + 4 * l;
@@ -1234,23 +1310,40 @@ cudaError_t enqueue_rows(const PrefillModel& m, const uint8_t* gate, const WorkL
     pq.kv_dim = m.kv_dim;
     pq.head_dim = m.head_dim;
     pq.layer = l;
-    epi(pq);
-    // phase 9
-    BAttnParams pa = {};
-    pa.gate = gate;
-    pa.rdesc = rows;
-    pa.Q = Q;
-    pa.O = O;
-    pa.exp_tab = m.exp_tab;
-    pa.layer = l;
-    pa.dim = c.dim;
-    pa.heads = c.heads;
-    pa.kv_heads = c.kv_heads;
-    pa.head_dim = m.head_dim;
-    pa.kv_dim = m.kv_dim;
-    pa.inv_sqrt = m.inv_sqrt;
-    pa.or_out = o4 + 1;
-    launch_pdl(k_battn, dim3(c.heads, P), dim3(kRowThreads), battn_smem(m.head_dim, max_positions), s, pa);
+    if (paged) {  // the stacked rows first, then rotary and the stores into pages, and phase 9
+      const uint32_t q_dim = c.dim, kv_dim = m.kv_dim;
+      pq.mode = kBEpiStore;
+      pq.Y = paged->qkv;
+      pq.y_stride = pq.rows;
+      epi(pq);
+      int rc = ck_paged_store(paged->cache, l, paged->batch, paged->qkv, pq.rows, paged->qkv + q_dim, pq.rows,
+                              paged->qkv + q_dim + kv_dim, pq.rows, c.heads, m.rope, paged->rope_rows, m.head_dim, 0, Q, s);
+      if (rc == CK_OK)
+        rc = ck_paged_attention(paged->cache, l, paged->batch, Q, c.dim, c.heads, m.exp_tab, m.inv_sqrt, O,
+                                paged->attn_work, paged->attn_len, s);
+      if (rc != CK_OK) return cudaErrorUnknown;
+      const uint64_t words = (uint64_t)P * c.dim;
+      k_magnitudes<<<(uint32_t)std::min<uint64_t>((words + 4 * kRowThreads - 1) / (4 * kRowThreads), 1024), kRowThreads, 0, s>>>(
+          O, words, o4 + 1);
+    } else {
+      epi(pq);
+      // phase 9
+      BAttnParams pa = {};
+      pa.gate = gate;
+      pa.rdesc = rows;
+      pa.Q = Q;
+      pa.O = O;
+      pa.exp_tab = m.exp_tab;
+      pa.layer = l;
+      pa.dim = c.dim;
+      pa.heads = c.heads;
+      pa.kv_heads = c.kv_heads;
+      pa.head_dim = m.head_dim;
+      pa.kv_dim = m.kv_dim;
+      pa.inv_sqrt = m.inv_sqrt;
+      pa.or_out = o4 + 1;
+      launch_pdl(k_battn, dim3(c.heads, P), dim3(kRowThreads), battn_smem(m.head_dim, max_positions), s, pa);
+    }
     // phases 10-11: output rows and the residual
     planes(O, c.dim, c.dim, KGd, o4 + 1, c.dim, KGd);
     gemm(Wl.wo, c.dim, KGd, o4 + 1);
@@ -1285,7 +1378,7 @@ cudaError_t enqueue_rows(const PrefillModel& m, const uint8_t* gate, const WorkL
     pd.X = X;
     if (l + 1 < c.layers)  // with the next layer's attention norm
       resnorm(pd, m.layers[l + 1].attn_norm, orw + 4 * (l + 1));
-    else if (classify)     // with the final norm
+    else if (classify && !paged)  // with the final norm
       resnorm(pd, m.final_norm, orw + 4 * c.layers);
     else
       epi(pd);
@@ -1293,6 +1386,13 @@ cudaError_t enqueue_rows(const PrefillModel& m, const uint8_t* gate, const WorkL
   if (classify) {
     // phases 17-18: final norm and classifier rows (written only for generating rows)
     unsigned long long* of = orw + 4 * c.layers;  // the final norm ran with the last residual
+    if (paged) {  // only the last row of each sequence goes on
+      const BatchView b = batch_view(*paged->batch);
+      k_last_rows<<<b.seqs, kRowThreads, 0, s>>>(b, X, Q, c.dim);
+      P = b.seqs;
+      Npad = pad64(P);
+      launch_pdl(k_bnorm, dim3(P), dim3(kNormThreads), 0, s, gate, (const int64_t*)Q, XB, m.final_norm, c.dim, of);
+    }
     planes(XB, c.dim, c.dim, KGd, of, c.vocab, KGd);
     gemm(m.cls, c.vocab, KGd, of);
     BEpiParams pc = {};
@@ -1300,9 +1400,31 @@ cudaError_t enqueue_rows(const PrefillModel& m, const uint8_t* gate, const WorkL
     pc.orw = of;
     pc.scale = m.cls_scale;
     pc.mode = kBEpiLogits;
+    if (paged) {
+      pc.mode = kBEpiStore;
+      pc.Y = paged->logits;
+      pc.y_stride = paged->logits_stride;
+      pc.start = paged->batch->dev_start;
+    }
     epi(pc);
+    if (paged) k_pfinish<<<1, kRowThreads, 0, s>>>(batch_view(*paged->batch), fault);
   }
   return cudaGetLastError();
+}
+
+// Scratch of a pass over pages: the batched kernels' for `cap` rows, the stacked rows, the
+// attention's.
+struct PagedLayout {
+  WorkLayout w;
+  uint64_t qkv, attn, size;
+};
+PagedLayout paged_layout(const PrefillModel& m, uint32_t cap, size_t attn_bytes) {
+  PagedLayout l;
+  l.w = work_layout(m, cap);
+  l.qkv = l.w.size;
+  l.attn = l.qkv + align256(8ull * pad64(cap) * (m.cfg.dim + 2ull * m.kv_dim));
+  l.size = l.attn + align256(attn_bytes);
+  return l;
 }
 
 // The attention kernel's dynamic shared memory may use what its static variables leave.
@@ -1315,6 +1437,23 @@ size_t battn_dynamic_max(size_t smem_optin) {
 }  // namespace
 
 size_t prefill_work_bytes(const PrefillModel& m, uint32_t cap) { return work_layout(m, cap).size; }
+
+size_t paged_pass_bytes(const PrefillModel& m, uint32_t cap, size_t attn_bytes) {
+  return paged_layout(m, cap, attn_bytes).size;
+}
+
+cudaError_t enqueue_paged_pass(const PrefillModel& m, const ck_paged_cache* cache, const ck_paged_batch* batch,
+                               const uint32_t* tokens, int64_t* logits, size_t logits_stride, size_t attn_bytes,
+                               uint8_t* work, cudaStream_t s) {
+  const PagedLayout l = paged_layout(m, std::max(batch->rows, batch->seqs), attn_bytes);
+  const PagedPass pass = {cache, batch, tokens, reinterpret_cast<int64_t*>(work + l.qkv), work + l.attn, attn_bytes,
+                          m.cfg.context, logits, logits_stride};
+  // rows of no sequence are not written by the attention
+  cudaError_t e = cudaMemsetAsync(work + l.w.O, 0, 8ull * batch->rows * m.cfg.dim, s);
+  if (e != cudaSuccess) return e;
+  if ((e = cudaMemsetAsync(work + l.w.Q, 0, 8ull * batch->rows * m.cfg.dim, s)) != cudaSuccess) return e;
+  return enqueue_rows(m, nullptr, l.w, work, batch->rows, 0, true, s, &pass);
+}
 
 bool prefill_supported(const PrefillModel& m, uint32_t cache, size_t smem_optin) {
   const uint32_t hd = m.head_dim;

@@ -65,6 +65,12 @@ inline cudaError_t device_facts(DeviceFacts* f) {
   return cudaSuccess;
 }
 
+// A pass of a paged batch through a model's layers (ck_batch.cu): its scratch, and its kernels.
+size_t paged_pass_bytes(const PrefillModel& m, uint32_t cap, size_t attn_bytes);
+cudaError_t enqueue_paged_pass(const PrefillModel& m, const ck_paged_cache* cache, const ck_paged_batch* batch,
+                               const uint32_t* tokens, int64_t* logits, size_t logits_stride, size_t attn_bytes,
+                               uint8_t* work, cudaStream_t s);
+
 // The pool and the batch as kernels take them.
 struct PoolView {
   int32_t* k;

@@ -178,6 +178,29 @@ def paged_attention(cache, layer, batch, q, exp_table, inv_sqrt, out=None, work=
     return rc, out
 
 
+def turn_paged_work(model, cache, batch, stream=None):
+    return _empty(stream, _size("ck_turn_paged_work", model._h, cache._c, batch._c), torch.uint8, cache.device)
+
+
+def turn_paged(model, cache, batch, tokens, logits=None, work=None, stream=None):
+    device, seqs, vocab = _devices(cache, batch), batch.lens.shape[0], model.config["vocab"]
+    if model.mem.get_device() != device:
+        raise ValueError("the model is not on the current CUDA device")
+    _check("tokens", tokens, torch.int32, (batch.rows,), device)
+    if logits is None:
+        logits = _empty(stream, (seqs, vocab), torch.int64, device)
+    step = _check_rows("logits", logits, seqs, device)
+    if logits.shape[1] != vocab:
+        raise ValueError(f"logits: {logits.shape[1]} columns, the vocabulary is {vocab}")
+    if work is None:
+        work = turn_paged_work(model, cache, batch, stream)
+    else:
+        _check("work", work, torch.uint8, (work.numel(),), device)
+    rc = lib().ck_turn_paged(model._h, cache._c, batch._c, tokens.data_ptr(), logits.data_ptr(), step,
+                             work.data_ptr(), work.numel(), _raw(stream, device))
+    return rc, logits
+
+
 class Fork(NamedTuple):
     table: object   # int32 [rows][stride]
     lens: object    # int32 [rows], grown

@@ -414,6 +414,23 @@ int ck_paged_attention(const ck_paged_cache* cache, uint32_t layer, const ck_pag
                        const int64_t* dev_q, size_t q_stride, uint32_t heads, const uint32_t* dev_exp,
                        uint32_t inv_sqrt, int64_t* dev_out, void* dev_work, size_t work_len, void* stream);
 
+/* The new rows of a batch through the model's layers (phases 3 to 18, "The forward pass, in
+ * order"): dev_tokens u32 [rows] the rows' tokens; every layer's keys and values go into the
+ * cache (the model's layers, key heads and head size), and dev_logits i64 [seqs][logits_stride]
+ * receives the logits of each sequence's last new row (sequences without one are left as they
+ * were).  The same bits as ck_turn and ck_turn_batch at the same tokens and positions: matrix
+ * rows as in the batched pass, rotary, stores and attention by the two operators above.  A token
+ * outside the vocabulary is phase 3 in dev_status and counts as zeros; all zeros there: a wait of
+ * a contraction ran out.  The logits of a sequence with a failure are unspecified.  Nothing
+ * synchronizes; the call may be captured.  Limits: rows and seqs <= 4096, max_len <= the model's
+ * context.  Errors: 4 (work_len), 9, 10. */
+int ck_turn_paged_work(ck_model* m, const ck_paged_cache* cache, const ck_paged_batch* batch, size_t* out);
+int ck_turn_paged(ck_model* m, const ck_paged_cache* cache, const ck_paged_batch* batch, const uint32_t* dev_tokens,
+                  int64_t* dev_logits, size_t logits_stride, void* dev_work, size_t work_len, void* stream);
+/* The model's exponential and rotary tables in device memory and its one over the square root
+ * of the head size, for the single operators.  Errors: 10. */
+int ck_model_tables(const ck_model* m, const uint32_t** dev_exp, const int32_t** dev_rope, uint32_t* inv_sqrt);
+
 /* Reorders, forks, frees and grows sequences.  Output row r takes over the sequence of input
  * row dev_parent[r] (CK_NO_PAGE: the row is empty), dev_len_in positions long, and receives
  * pages for dev_grow[r] more; several rows may name one parent, and an input row that none
