@@ -58,6 +58,12 @@ def _empty(stream, shape, dtype, device):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _keep(t, stream):
+    """A plan's scratch stays in use on the stream, whatever becomes of the plan."""
+    if stream is not None:
+        t.record_stream(stream)
+
+
 def _raw(stream, device):
     return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
@@ -242,6 +248,7 @@ class PagePlan:
         _check("grow", grow, torch.int32, (rows,), device)
         if held is not None:
             _check("held", held, torch.uint8, (self.cache.pages,), device)
+        _keep(self._work, stream)
         out = _empty(stream, (rows, self.stride), torch.int32, device)
         new_lens, status = _empty(stream, (rows,), torch.int32, device), _empty(stream, (rows,), torch.int32, device)
         rc = lib().ck_pages_fork(self.cache._c, rows_in, lens.data_ptr(), table.data_ptr(), rows, parent.data_ptr(),
@@ -255,6 +262,7 @@ class PagePlan:
         device, rows = self._begin(lens, table)
         if rows > self.rows:
             raise ValueError(f"table: {rows} rows, the plan has room for {self.rows}")
+        _keep(self._work, stream)
         out = _empty(stream, (rows, self.stride), torch.int32, device)
         status = _empty(stream, (rows,), torch.int32, device)
         used = _empty(stream, (), torch.int32, device)
@@ -293,6 +301,7 @@ class BeamPlan:
         _check("scores", scores, torch.int64, (rows,), device)
         _check("done", done, torch.uint8, (rows,), device)
         _check("exp_table", exp_table, torch.int32, (4097,), device)
+        _keep(self._work, stream)
         new_scores = _empty(stream, (rows,), torch.int64, device)
         parent, token = _empty(stream, (rows,), torch.int32, device), _empty(stream, (rows,), torch.int32, device)
         new_done = _empty(stream, (rows,), torch.uint8, device)

@@ -164,6 +164,120 @@ def test_attention_with_equal_and_with_single_scores(ck, new):
         assert np.array_equal(out.cpu().numpy(), s.attention(0, q, inv, exp))
 
 
+@pytest.mark.parametrize("hd,new,length", [(64, 70, 600), (128, 33, 777), (64, 1, 300)])
+def test_attention_at_the_ends_of_three_digits(ck, hd, new, length):
+    """Words at both ends of what three balanced 8-bit digits hold, in every combination of signs:
+    the largest sums that the tensor cores' f32 accumulators see."""
+    lo, hi = -128 * 65793, 127 * 65793
+    s = Setup(ck, [length], [new], 2, 1, hd, 16, seed=hd)
+    inv = synth.inv_sqrt_head(hd)
+    for kind in ("all low", "all high", "mixed", "equal scores"):
+        pick = {"all low": [lo], "all high": [hi], "mixed": [lo, hi], "equal scores": [lo]}[kind]
+        s.k[:] = s.rng.choice(pick, s.k.shape)
+        s.v[:] = s.rng.choice([lo, hi] if kind == "equal scores" else pick, s.v.shape)
+        s.cache.k.copy_(cuda(s.k))
+        s.cache.v.copy_(cuda(s.v))
+        q = s.rng.choice(pick, (s.rows, 2 * hd)).astype(np.int64)
+        rc, out = ck.paged_attention(s.cache, 0, s.batch, cuda(q), cuda(EXP.view(np.int32)), inv)
+        assert rc == 0
+        assert np.array_equal(out.cpu().numpy(), s.attention(0, q, inv)), kind
+
+
+@pytest.mark.parametrize("inv", [1, 1 << 21, (1 << 24) + 1, 2**32 - 1])
+@pytest.mark.parametrize("new", [1, 40])
+def test_attention_with_other_scales(ck, inv, new):
+    """One over the square root may be any u32: products and scores that pass 32 bits."""
+    s = Setup(ck, [300], [new], 2, 2, 64, 16, seed=3)
+    q = (s.rng.standard_normal((s.rows, 128)) * 65536 * 8).astype(np.int64)
+    rc, out = ck.paged_attention(s.cache, 1, s.batch, cuda(q), cuda(EXP.view(np.int32)), inv)
+    assert rc == 0
+    assert np.array_equal(out.cpu().numpy(), s.attention(1, q, inv))
+
+
+def test_attention_of_a_long_sequence_of_few_heads(ck):
+    """Clusters of sixteen blocks, scores in the scratch, and a bound far above the length."""
+    for lens, max_len in (([9001], 9001), ([40, 7], 200000)):
+        s = Setup(ck, lens, [1] * len(lens), 4, 1, 64, 32, seed=4, max_len=max_len)
+        s.table = np.concatenate([s.table, np.full((len(lens), max_len // 32 + 2), -1, np.int32)], 1)
+        s.batch = ck.PagedBatch(cuda(s.table), cuda(np.array(lens, np.int32)), cuda(s.starts), None, s.rows, 1, max_len)
+        q = (s.rng.standard_normal((s.rows, 256)) * 65536).astype(np.int64)
+        rc, out = ck.paged_attention(s.cache, 0, s.batch, cuda(q), cuda(EXP.view(np.int32)), 1 << 21)
+        assert rc == 0
+        assert np.array_equal(out.cpu().numpy(), s.attention(0, q, 1 << 21))
+
+
+def test_pools_beyond_32_bits_of_words(ck):
+    """Stores, attention (both forms), a fork and packing at the far end of pools of over 2^32
+    words each."""
+    import torch
+    page, hd, pages = 256, 128, 131072 + 64
+    if torch.cuda.mem_get_info()[0] < 60e9:
+        pytest.skip("needs 36 GB of device memory")
+    cache = ck.PagedCache.empty(pages, 1, 1, page, hd)
+    rng = np.random.default_rng(8)
+    n, top = 300, pages - 1
+    table = np.full((1, 4), -1, np.int32)
+    table[0, :2] = [top, top - 40]
+    k, v = ((rng.standard_normal((n, hd)) * 65536).astype(np.int64) for _ in range(2))
+    q = (rng.standard_normal((n, 2 * hd)) * 65536).astype(np.int64)
+    batch = ck.PagedBatch(cuda(table), cuda(np.array([n], np.int32)), cuda(np.array([0, n], np.int32)), None, n, n, n)
+    rc, rotated = ck.paged_store(cache, 0, batch, cuda(q), cuda(k), cuda(v), cuda(rope_of(n, 0)))
+    assert rc == 0 and batch.errors() == [None] and np.array_equal(rotated.cpu().numpy(), q)
+    inv = synth.inv_sqrt_head(hd)
+    rc, out = ck.paged_attention(cache, 0, batch, rotated, cuda(EXP.view(np.int32)), inv)
+    assert rc == 0
+    for row in (0, 130, 299):
+        for h in range(2):
+            want = plain_attention(q[row, h * hd:(h + 1) * hd], k[:row + 1], v[:row + 1], inv)
+            assert np.array_equal(out[row, h * hd:(h + 1) * hd].cpu().numpy(), want)
+    plan = ck.PagePlan(cache, 2, 4)
+    held = torch.ones(pages, dtype=torch.uint8, device="cuda")
+    held[top - 7] = 0
+    rc, fork = plan.fork(cuda(np.array([0, 0], np.int32)), batch.lens, batch.table, cuda(np.array([0, 0], np.int32)), held=held)
+    assert rc == 0 and fork.status.tolist() == [0, 0]
+    assert fork.table.tolist() == [[top, top - 40, -1, -1], [top, top - 7, -1, -1]]
+    rc, packed = plan.compact(fork.lens, fork.table)
+    assert rc == 0 and int(packed.used) == 3 and packed.table.tolist() == [[2, 0, -1, -1], [2, 1, -1, -1]]
+    one = ck.PagedBatch(packed.table, fork.lens, cuda(np.array([0, 1, 2], np.int32)), None, 2, 1, n)
+    rc, last = ck.paged_attention(cache, 0, one, rotated[[299, 299]].contiguous(), cuda(EXP.view(np.int32)), inv)
+    assert rc == 0
+    assert torch.equal(last[0], out[299]) and torch.equal(last[1], out[299])
+
+
+def test_calls_on_two_streams_and_captured_ones_repeat(ck):
+    """Attention, both forms, on two streams at once with scratch of their own; and captured, then
+    replayed over other inputs in the same places."""
+    import torch
+    jobs = []
+    for new in (1, 60):
+        s = Setup(ck, [500, 420], [new, new], 4, 2, 64, 16, seed=new)
+        q = [(s.rng.standard_normal((s.rows, 256)) * 65536).astype(np.int64) for _ in range(2)]
+        jobs.append((s, q, [s.attention(0, x, 1 << 21) for x in q]))
+    exp = cuda(EXP.view(np.int32))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    dev = [[cuda(x) for x in q] for _, q, _ in jobs]
+    torch.cuda.synchronize()
+    outs = []
+    for turn in range(20):
+        for (s, _, _), d, stream in zip(jobs, dev, streams):
+            outs.append(ck.paged_attention(s.cache, 0, s.batch, d[turn % 2], exp, 1 << 21, stream=stream))
+    torch.cuda.synchronize()
+    for i, (rc, out) in enumerate(outs):
+        assert rc == 0 and np.array_equal(out.cpu().numpy(), jobs[i % 2][2][i // 2 % 2])
+    for (s, q, want), d in zip(jobs, dev):
+        place, out = d[0].clone(), torch.zeros_like(d[0])
+        work = ck.paged_attention_work(s.cache, s.batch, 4)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            rc, _ = ck.paged_attention(s.cache, 0, s.batch, place, exp, 1 << 21, out=out, work=work)
+        assert rc == 0
+        for turn in (1, 0, 1):
+            place.copy_(d[turn])
+            out.zero_()
+            graph.replay()
+            assert np.array_equal(out.cpu().numpy(), want[turn])
+
+
 def test_attention_leaves_rows_of_no_sequence_and_strided_queries(ck):
     """Rows before the first sequence and behind the last stay as they were; queries are a
     column range of wider rows."""
@@ -423,7 +537,8 @@ def test_fork_step_after_step(ck, seed):
 def test_compact_packs_the_pages_in_use(ck):
     rng = np.random.default_rng(6)
     page = 8
-    for pages, rows, share in ((40, 5, True), (5000, 300, False), (1, 1, False), (64, 2, False)):
+    for pages, rows, share in ((40, 5, True), (5000, 300, False), (1, 1, False), (64, 2, False), (6000, 1100, True),
+                               (70000, 40, False)):
         k, v = pools(rng, pages, 2, 1, page, 8)
         stride = 6
         lens = [int(rng.integers(0, page * stride + 1)) for _ in range(rows)]
