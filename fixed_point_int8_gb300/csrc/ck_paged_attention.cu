@@ -178,12 +178,11 @@ __device__ __forceinline__ unsigned long long peer_word(const void* p, uint32_t 
   return v;
 }
 
-// Batches in flight and the one at work: 16 KB a warp on their way where a block has the SM to
-// itself and another, 8 KB where seven share it.
+// Batches in flight and the one at work.
 // Positions a lane group takes at once: fewer where four queries' sums fill the registers, and
 // where many small blocks share an SM.
 __host__ __device__ constexpr int few_batch(int nt, int r) { return r == 4 || nt == kNarrow ? 4 : 8; }
-__host__ __device__ constexpr int few_stages(int nt, int nch) { return nt == kMiddle ? 5 - nch : 4 - nch; }
+__host__ __device__ constexpr int few_stages(int nt, int nch) { return nt == kBroad ? 4 - nch : 5 - nch; }
 struct FewLayout {
   uint32_t ring, part, q, red, ids, sc, size;
 };
