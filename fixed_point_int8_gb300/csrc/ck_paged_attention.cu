@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kRowsThreads) k_pattn_rows(const RowsParams f)
 // 4,000).  Keys and then values stream through a ring of asynchronous copies, kBatch positions a
 // lane group each; a lane copies the words that it uses itself, so nothing waits on another
 // lane, and the values are on their way while the exponentials are formed.
-constexpr uint32_t kMaxCluster = 16, kFewQueries = 16;
+constexpr uint32_t kMaxCluster = 16;
 constexpr int kNarrow = 64, kMiddle = 128, kBroad = 256;  // threads of a block
 constexpr unsigned long long kNowhere = ~0ull;
 
@@ -633,10 +633,14 @@ cudaError_t launch_few_r(const FewParams& p, const FewPlan& w, const DeviceFacts
                     : launch_few_lpp<4, NT>(p, w, f, s);
 }
 
-// Which kernel a call takes, by the queries a key head has at most (rows x heads that share it):
-// a few go to k_pattn_few, more of head size 64 or 128 to the tensor cores, with k_pattn_rows
-// behind them for tiles with values beyond their digits; small heads in any number to
-// k_pattn_few as long as its grid holds them.
+// Which kernel a call takes.  Head sizes 64 and 128 compare what k_pattn_few and the tensor-core
+// tiles would take, by the launch's bounds: 8 us and 0.9 us a million products of a query's and a
+// key's element, against 35 us and 0.65 or 1.05 ns a tile and position.  (Measured, few against
+// tiles: head size 64, 32 heads: 32 rows over 200 positions 21 and 35 us, over 1,000 69 and 53,
+// four sequences of 16 rows over 1,500 144 and 141, of 8 rows 89 and 135; head size 128: 16 rows
+// over 2,000 117 and 94, 128 rows over 128 45 and 53, 32 sequences of one row and four heads a
+// key head over 2,000 179 and 458.)  k_pattn_rows follows the tiles for those with values beyond
+// their digits, and takes calls that k_pattn_few's grid or shared memory does not hold.
 struct AttentionPlan {
   FewPlan few;
   TilesPlan tiles;
@@ -645,9 +649,14 @@ struct AttentionPlan {
 };
 AttentionPlan attention_plan(const ck_paged_cache& c, const ck_paged_batch& b, uint32_t heads, const DeviceFacts& f) {
   AttentionPlan w = {};
-  const uint64_t queries = (uint64_t)b.max_new * (heads / c.kv_heads);
-  if (queries > kFewQueries) w.tiles = plan_tiles(c, b, heads, f);
-  if (!w.tiles.use) w.few = plan_few(c, b, heads, f);
+  w.few = plan_few(c, b, heads, f);
+  if (c.head_dim >= 64) {
+    const double tiles = std::ceil((double)b.max_new * (heads / c.kv_heads) / 128) * b.seqs * c.kv_heads;
+    const double few_us = 8 + 0.9e-6 * b.seqs * heads * b.max_new * b.max_len * c.head_dim;
+    const double tiles_us = 35 + (c.head_dim == 64 ? 0.65e-3 : 1.05e-3) * tiles * b.max_len;
+    if (!w.few.use || tiles_us < few_us) w.tiles = plan_tiles(c, b, heads, f);
+    if (w.tiles.use) w.few.use = false;
+  }
   if (w.few.use) {
     w.work = std::max<uint64_t>(align256(w.few.work), 256);  // never an empty buffer
     return w;
