@@ -115,11 +115,28 @@ ATTENTION = [
     ([700], [40], 6, 2, 16, 8),
     ([260], [129], 2, 2, 4, 16),
 ]
+# work enough for the tensor-core tiles: shared key heads, ragged, a last tile of few queries, pages
+# that end inside a block, rows without a position
+TILES = [
+    ([900, 333], [70, 129], 32, 8, 64, 16),
+    ([640], [200], 16, 16, 128, 32),
+    ([1030, 40], [129, 40], 8, 1, 64, 8),
+    ([2100], [20], 32, 4, 128, 64),
+    ([77, 130], [90, 2], 48, 3, 64, 32),
+    ([300, 1000, 5], [0, 65, 5], 32, 32, 64, 256),
+]
 
 
-@pytest.mark.parametrize("lens,news,heads,kv,hd,page", ATTENTION)
+def on_tiles(ck, s):
+    """The call takes the tensor-core tiles (their scores need scratch; short ones of a few queries
+    need none)."""
+    return ck.paged_attention_work(s.cache, s.batch, s.heads).numel() > 1 << 20
+
+
+@pytest.mark.parametrize("lens,news,heads,kv,hd,page", ATTENTION + TILES)
 def test_attention_against_the_plain_form(ck, lens, news, heads, kv, hd, page):
     s = Setup(ck, lens, news, heads, kv, hd, page, seed=hd + len(lens))
+    assert on_tiles(ck, s) == ((lens, news, heads, kv, hd, page) in TILES)
     q = (s.rng.standard_normal((s.rows, heads * hd)) * 65536).astype(np.int64)
     inv = synth.inv_sqrt_head(hd)
     for layer in (0, 1):
@@ -134,12 +151,13 @@ def test_attention_against_the_plain_form(ck, lens, news, heads, kv, hd, page):
                                                 (2**22, 2**23), (2**23 + 5, 2**23 + 5), (1, 1), (0, 65536)])
 def test_attention_over_the_whole_range_of_values(ck, new, q_spread, kv_spread):
     """Queries to 63 bits and cached words to 32, wrapping products among them."""
-    s = Setup(ck, [150], [new], 4, 2, 64, 16, seed=1)
+    s = Setup(ck, [150], [new], 4, 2, 64, 16, seed=1) if new == 1 else Setup(ck, [600], [new], 32, 4, 64, 16, seed=1)
+    assert on_tiles(ck, s) == (new == 70)
     s.k[:] = s.rng.integers(-kv_spread - 1, kv_spread + 1, s.k.shape)
     s.v[:] = s.rng.integers(-kv_spread - 1, kv_spread + 1, s.v.shape)
     s.cache.k.copy_(cuda(s.k))
     s.cache.v.copy_(cuda(s.v))
-    q = s.rng.integers(-q_spread, q_spread + 1, (s.rows, 256))
+    q = s.rng.integers(-q_spread, q_spread + 1, (s.rows, s.heads * 64))
     inv = synth.inv_sqrt_head(64)
     rc, out = ck.paged_attention(s.cache, 1, s.batch, cuda(q), cuda(EXP.view(np.int32)), inv)
     assert rc == 0
@@ -149,7 +167,8 @@ def test_attention_over_the_whole_range_of_values(ck, new, q_spread, kv_spread):
 @pytest.mark.parametrize("new", [1, 130])
 def test_attention_with_equal_and_with_single_scores(ck, new):
     """Every score the same, and one score far above all others (its probability is 2^24)."""
-    s = Setup(ck, [200], [new], 2, 2, 64, 16, seed=2)
+    s = Setup(ck, [200], [new], 2, 2, 64, 16, seed=2) if new == 1 else Setup(ck, [400], [new], 32, 4, 64, 16, seed=2)
+    assert on_tiles(ck, s) == (new == 130)
     inv = synth.inv_sqrt_head(64)
     exp = EXP.copy()
     exp[4096] = 0
@@ -158,18 +177,19 @@ def test_attention_with_equal_and_with_single_scores(ck, new):
         if kind == "single":
             s.k[s.table[0, 0], :, :, 3] = 1 << 20
         s.cache.k.copy_(cuda(s.k))
-        q = np.full((s.rows, 128), 1 << 18, np.int64)
+        q = np.full((s.rows, s.heads * 64), 1 << 18, np.int64)
         rc, out = ck.paged_attention(s.cache, 0, s.batch, cuda(q), cuda(exp.view(np.int32)), inv)
         assert rc == 0
         assert np.array_equal(out.cpu().numpy(), s.attention(0, q, inv, exp))
 
 
-@pytest.mark.parametrize("hd,new,length", [(64, 70, 600), (128, 33, 777), (64, 1, 300)])
-def test_attention_at_the_ends_of_three_digits(ck, hd, new, length):
+@pytest.mark.parametrize("hd,new,length,heads,kv", [(64, 70, 600, 32, 4), (128, 33, 777, 32, 8), (64, 1, 300, 2, 1)])
+def test_attention_at_the_ends_of_three_digits(ck, hd, new, length, heads, kv):
     """Words at both ends of what three balanced 8-bit digits hold, in every combination of signs:
     the largest sums that the tensor cores' f32 accumulators see."""
     lo, hi = -128 * 65793, 127 * 65793
-    s = Setup(ck, [length], [new], 2, 1, hd, 16, seed=hd)
+    s = Setup(ck, [length], [new], heads, kv, hd, 16, seed=hd)
+    assert on_tiles(ck, s) == (new > 1)
     inv = synth.inv_sqrt_head(hd)
     for kind in ("all low", "all high", "mixed", "equal scores"):
         pick = {"all low": [lo], "all high": [hi], "mixed": [lo, hi], "equal scores": [lo]}[kind]
@@ -177,7 +197,7 @@ def test_attention_at_the_ends_of_three_digits(ck, hd, new, length):
         s.v[:] = s.rng.choice([lo, hi] if kind == "equal scores" else pick, s.v.shape)
         s.cache.k.copy_(cuda(s.k))
         s.cache.v.copy_(cuda(s.v))
-        q = s.rng.choice(pick, (s.rows, 2 * hd)).astype(np.int64)
+        q = s.rng.choice(pick, (s.rows, heads * hd)).astype(np.int64)
         rc, out = ck.paged_attention(s.cache, 0, s.batch, cuda(q), cuda(EXP.view(np.int32)), inv)
         assert rc == 0
         assert np.array_equal(out.cpu().numpy(), s.attention(0, q, inv)), kind
@@ -187,8 +207,9 @@ def test_attention_at_the_ends_of_three_digits(ck, hd, new, length):
 @pytest.mark.parametrize("new", [1, 40])
 def test_attention_with_other_scales(ck, inv, new):
     """One over the square root may be any u32: products and scores that pass 32 bits."""
-    s = Setup(ck, [300], [new], 2, 2, 64, 16, seed=3)
-    q = (s.rng.standard_normal((s.rows, 128)) * 65536 * 8).astype(np.int64)
+    s = Setup(ck, [300], [new], 2, 2, 64, 16, seed=3) if new == 1 else Setup(ck, [600], [new], 32, 4, 64, 16, seed=3)
+    assert on_tiles(ck, s) == (new == 40)
+    q = (s.rng.standard_normal((s.rows, s.heads * 64)) * 65536 * 8).astype(np.int64)
     rc, out = ck.paged_attention(s.cache, 1, s.batch, cuda(q), cuda(EXP.view(np.int32)), inv)
     assert rc == 0
     assert np.array_equal(out.cpu().numpy(), s.attention(1, q, inv))
@@ -219,15 +240,16 @@ def test_pools_beyond_32_bits_of_words(ck):
     table = np.full((1, 4), -1, np.int32)
     table[0, :2] = [top, top - 40]
     k, v = ((rng.standard_normal((n, hd)) * 65536).astype(np.int64) for _ in range(2))
-    q = (rng.standard_normal((n, 2 * hd)) * 65536).astype(np.int64)
+    q = (rng.standard_normal((n, 32 * hd)) * 65536).astype(np.int64)
     batch = ck.PagedBatch(cuda(table), cuda(np.array([n], np.int32)), cuda(np.array([0, n], np.int32)), None, n, n, n)
     rc, rotated = ck.paged_store(cache, 0, batch, cuda(q), cuda(k), cuda(v), cuda(rope_of(n, 0)))
     assert rc == 0 and batch.errors() == [None] and np.array_equal(rotated.cpu().numpy(), q)
     inv = synth.inv_sqrt_head(hd)
+    assert ck.paged_attention_work(cache, batch, 32).numel() > 1 << 20       # the tiles
     rc, out = ck.paged_attention(cache, 0, batch, rotated, cuda(EXP.view(np.int32)), inv)
     assert rc == 0
     for row in (0, 130, 299):
-        for h in range(2):
+        for h in (0, 17, 31):
             want = plain_attention(q[row, h * hd:(h + 1) * hd], k[:row + 1], v[:row + 1], inv)
             assert np.array_equal(out[row, h * hd:(h + 1) * hd].cpu().numpy(), want)
     plan = ck.PagePlan(cache, 2, 4)
@@ -250,8 +272,9 @@ def test_calls_on_two_streams_and_captured_ones_repeat(ck):
     import torch
     jobs = []
     for new in (1, 60):
-        s = Setup(ck, [500, 420], [new, new], 4, 2, 64, 16, seed=new)
-        q = [(s.rng.standard_normal((s.rows, 256)) * 65536).astype(np.int64) for _ in range(2)]
+        s = Setup(ck, [500, 420], [new, new], 32, 4, 64, 16, seed=new)
+        assert on_tiles(ck, s) == (new == 60)
+        q = [(s.rng.standard_normal((s.rows, 32 * 64)) * 65536).astype(np.int64) for _ in range(2)]
         jobs.append((s, q, [s.attention(0, x, 1 << 21) for x in q]))
     exp = cuda(EXP.view(np.int32))
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]
@@ -266,7 +289,7 @@ def test_calls_on_two_streams_and_captured_ones_repeat(ck):
         assert rc == 0 and np.array_equal(out.cpu().numpy(), jobs[i % 2][2][i // 2 % 2])
     for (s, q, want), d in zip(jobs, dev):
         place, out = d[0].clone(), torch.zeros_like(d[0])
-        work = ck.paged_attention_work(s.cache, s.batch, 4)
+        work = ck.paged_attention_work(s.cache, s.batch, 32)
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
             rc, _ = ck.paged_attention(s.cache, 0, s.batch, place, exp, 1 << 21, out=out, work=work)
@@ -387,6 +410,30 @@ def test_store_reports_the_first_word_that_does_not_fit(ck, half):
 
 
 # ---------------------------------------------------------------- sequences and pages that do not fit
+
+def test_bad_pages_and_sequences_on_tiles(ck):
+    """As below for the tensor-core tiles: a bad page reads as zeros, a sequence beyond the bounds is
+    left as it was, one with words beyond the digits beside others is done all the same."""
+    import torch
+    s = Setup(ck, [500, 480, 450, 470], [40, 40, 30, 40], 32, 4, 64, 16, seed=7)
+    assert on_tiles(ck, s)
+    s.v[s.table[2, 3]] = 2**31 - 1                       # beyond the digits
+    s.k[s.table[3, 1]] = 2**30
+    s.cache.k.copy_(cuda(s.k))
+    s.cache.v.copy_(cuda(s.v))
+    q = (s.rng.standard_normal((s.rows, 2048)) * 65536).astype(np.int64)
+    s.batch.lens.copy_(cuda(np.array([500, 501, 450, 470], np.int32)))   # the second is past max_len
+    s.batch.table[0, 5] = s.pages + 3                    # positions 80 .. 95 of the first
+    out = torch.full((s.rows, 2048), 5, dtype=torch.int64, device="cuda")
+    rc, _ = ck.paged_attention(s.cache, 1, s.batch, cuda(q), cuda(EXP.view(np.int32)), 1 << 21, out=out)
+    assert rc == 0
+    assert s.batch.errors() == [(80, 1, 2, 0), (0, 1, 1, 0), None, None]
+    for pool in (s.k, s.v):
+        pool[s.table[0, 5]] = 0
+    want, got = s.attention(1, q, 1 << 21), out.cpu().numpy()
+    keep = np.r_[0:40, 80:150]
+    assert np.array_equal(got[keep], want[keep]) and (got[40:80] == 5).all()
+
 
 def test_bad_sequences_and_pages_are_reported_and_the_others_done(ck):
     """A length beyond the launch's bound, a table entry outside the pool, a position past the

@@ -86,16 +86,17 @@ def test_prompts_in_chunks_then_single_tokens(ck, gqa, page, sizes):
 def test_a_larger_model_over_pages_agrees_with_the_batched_turn(ck):
     """Head size 64 and a chunk that goes to the tensor-core attention: the logits of the last
     prompt position are those of a run's own state after ck_turn."""
-    spec = synth.ModelSpec("hd64", 256, 352, 2, 4, 2, 512, 512, tied=False, seed=0x5EED0077)
-    both = Both(ck, spec)
-    ids = [int(t) for t in synth.prompt_ids(spec, 200)]
-    state = both.gpu.new_state(200, 1)
+    spec = synth.ModelSpec("hd64", 512, 352, 2, 8, 2, 512, 512, tied=False, seed=0x5EED0077)
+    both, n = Both(ck, spec), 400
+    ids = [int(t) for t in synth.prompt_ids(spec, n)]
+    state = both.gpu.new_state(n, 1)
     assert both.gpu.init_state(state, ids, 1) == 0
-    assert both.gpu.turn(state, 200)[0] == 0
+    assert both.gpu.turn(state, n)[0] == 0
     rc, want = both.gpu.logits(state)
     assert rc == 0
-    cache = both.cache(ck, 16, 16)
-    batch = ck.PagedBatch(i32([list(range(15, 2, -1))]), i32([200]), i32([0, 200]), None, 200, 200, 200)
+    cache = both.cache(ck, 28, 16)
+    batch = ck.PagedBatch(i32([list(range(27, 2, -1))]), i32([n]), i32([0, n]), None, n, n, n)
+    assert ck.paged_attention_work(cache, batch, 8).numel() > 1 << 20   # the tiles
     rc, logits = both.gpu.turn_paged(cache, batch, i32(ids))
     assert rc == 0 and batch.errors() == [None]
     assert np.array_equal(logits[0].cpu().numpy(), want)
