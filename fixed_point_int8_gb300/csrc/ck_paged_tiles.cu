@@ -376,17 +376,27 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
         tmem_wait_ld();
         const uint32_t at = i * kTilePos + cg * kCols + h;
         int32_t c[8];
-        float peak = 0;
+        float high[8], peak = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) peak = fmaxf(peak, fabsf(__uint_as_float(d[4][j])));
-        if (peak < 8192.0f && p.inv_sqrt <= 1u << 24) {
-          // the highest accumulator is small (the usual case): it joins the next exactly (below
-          // 2^23), and (the sum of the accumulators by weight) >> 16 fits 32 bits, and so the score
+        for (int j = 0; j < 8; ++j) {
+          high[j] = fmaf(__uint_as_float(d[4][j]), 256.0f, __uint_as_float(d[3][j]));
+          peak = fmaxf(peak, fabsf(high[j]));
+          if (HD > 64) peak = fmaxf(peak, fabsf(__uint_as_float(d[2][j])));  // (3 * 64 * 2^14 < 2^22)
+        }
+        if (peak <= 4194304.0f && p.inv_sqrt <= 1u << 24) {
+          // the usual case: the two highest accumulators join exactly, every number lies within
+          // 2^22 and turns into an integer by an addition, (the sum of the accumulators by
+          // weight) >> 16 fits 32 bits, and so the score
+          constexpr uint32_t kOne = 0x4B400000u;  // the bits of kWhole; those of kWhole + x are x more
+          constexpr float kWhole = 12582912.0f;   // 3 * 2^22
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const int32_t lo = __float2int_rn(__uint_as_float(d[0][j])) + (__float2int_rn(__uint_as_float(d[1][j])) << 8);
-            const int32_t dot = (lo >> 16) + __float2int_rn(__uint_as_float(d[2][j])) +
-                                (__float2int_rn(fmaf(__uint_as_float(d[4][j]), 256.0f, __uint_as_float(d[3][j]))) << 8);
+            const uint32_t x0 = __float_as_uint(__uint_as_float(d[0][j]) + kWhole);
+            const uint32_t x1 = __float_as_uint(__uint_as_float(d[1][j]) + kWhole);
+            const uint32_t x2 = __float_as_uint(__uint_as_float(d[2][j]) + kWhole);
+            const uint32_t x3 = __float_as_uint(high[j] + kWhole);
+            const int32_t lo = (int32_t)(x0 + (x1 << 8) - (kOne + (kOne << 8)));
+            const int32_t dot = (int32_t)((uint32_t)(lo >> 16) + x2 + (x3 << 8) - (kOne + (kOne << 8)));
             c[j] = (int32_t)(((int64_t)dot * (int32_t)p.inv_sqrt) >> 24);
           }
         } else {
@@ -575,7 +585,7 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
         const int4 s0 = sraw[2 * c], s1 = sraw[2 * c + 1];
         const uint32_t s[8] = {(uint32_t)s0.x, (uint32_t)s0.y, (uint32_t)s0.z, (uint32_t)s0.w,
                                (uint32_t)s1.x, (uint32_t)s1.y, (uint32_t)s1.z, (uint32_t)s1.w};
-        uint32_t pr[8];
+        uint32_t pr[8], differ = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const uint32_t e = s[j];
@@ -583,8 +593,12 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
           // rz and rz + 1, >> 38; where those differ (less than one in 2^8) the remainder decides
           const uint32_t low = __umulhi(e, rz), high = __umulhi(e, rz + 1);
           pr[j] = low >> 6;
-          if ((low ^ high) >> 6) {
-            const unsigned long long rem = ((unsigned long long)e << 24) - (unsigned long long)pr[j] * z;
+          differ |= low ^ high;
+        }
+        if (differ >> 6) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const unsigned long long rem = ((unsigned long long)s[j] << 24) - (unsigned long long)pr[j] * z;
             pr[j] += rem >= z;
           }
         }
