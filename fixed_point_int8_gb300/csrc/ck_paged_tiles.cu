@@ -32,6 +32,8 @@ namespace {
 
 constexpr uint32_t kTileRows = 128, kTilePos = 32, kBlockPos = 64, kFlushBlocks = 4;
 constexpr uint32_t kDiags = 5;
+// scores on their way back: four stages of 32 positions, [position / 4][row][4] as in the scratch
+constexpr uint32_t kRing = 4, kStage = kTilePos * kTileRows * 4;
 
 template <int HD>
 struct Tile {
@@ -55,7 +57,9 @@ struct Tile {
   static constexpr uint32_t kMaxOff = kRedOff + kGroups * kTileRows * 8;  // [128] i32
   static constexpr uint32_t kSumOff = kMaxOff + kTileRows * 4;   // [128] u64
   static constexpr uint32_t kMiscOff = kSumOff + kTileRows * 8;  // barrier, tensor memory, flags
-  static constexpr uint32_t kSmem = kMiscOff + 64 + 1024;        // + alignment of the operands
+  static constexpr uint32_t kRingOff = kMiscOff + 64;            // the scores' barriers
+  static constexpr uint32_t kSmem = kRingOff + kRing * 8 + 1024; // + alignment of the operands
+  static_assert(kRing * kStage <= kOperands, "the scores' ring");
   static_assert(kScoreCol + kBufs * kDiags * kTilePos <= kTmem && 4 * HD <= kTmem, "tensor memory");
 };
 
@@ -174,6 +178,7 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + T::kMiscOff);
   uint64_t* done = full + 2;
   uint64_t* drained = full + 4;
+  uint64_t* ring = reinterpret_cast<uint64_t*>(sm + T::kRingOff);  // a stage of scores has come
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + T::kMiscOff + 48);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + T::kMiscOff + 52);
   uint32_t* next_s = reinterpret_cast<uint32_t*>(sm + T::kMiscOff + 60);
@@ -186,6 +191,7 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
       mb_init(done + i, 1);
       mb_init(drained + i, T::kThreads / 32);
     }
+    for (uint32_t i = 0; i < kRing; ++i) mb_init(ring + i, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -201,10 +207,15 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
   const uint32_t warp_u = __shfl_sync(0xffffffffu, warp, 0);  // known to be the same in the warp
   const uint64_t operands = smem_desc(smem_addr(sm));
   constexpr uint32_t kWarps = T::kThreads / 32;
-  uint32_t batch = 0, tiles = 0;  // batches of products and tiles so far: the barriers' phases
+  uint32_t batch = 0, tiles = 0, staged = 0;  // batches, tiles and stages so far: the barriers' phases
   auto wait_full = [&](uint32_t g) { mb_wait(full + (g & 1u), (g >> 1) & 1u, const_cast<volatile int*>(abort_flag)); tc_after(); };
   auto wait_done = [&](uint32_t g) { mb_wait(done + (g & 1u), (g >> 1) & 1u, const_cast<volatile int*>(abort_flag)); tc_after(); };
   auto wait_drained = [&](uint32_t g) { mb_wait(drained + (g & 1u), (g >> 1) & 1u, const_cast<volatile int*>(abort_flag)); tc_after(); };
+  auto wait_copy = [&](uint64_t* b, uint32_t parity) {  // also when giving up: no block ends before its copies
+    for (uint32_t it = 0; it < kTcPoll; ++it)
+      if (mb_try(b, parity)) return;
+    *abort_flag = 1;
+  };
   auto arrive = [&](uint64_t* b) {  // this warp's accesses so far come before the phase
     tc_before();
     __syncwarp();
@@ -261,14 +272,11 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
       longlong2 words[16];
 #pragma unroll
       for (uint32_t i = 0; i < 16; ++i) {
-        const uint32_t q = v0 + 32 * (warp & 3) + 2 * i + (lane >> 4);
-        words[i] = make_longlong2(0, 0);
-        if (q < queries) {
-          const uint32_t token = group == 1 ? q : q / group;
-          words[i] = __ldg(reinterpret_cast<const longlong2*>(p.q + (size_t)(sq.first + token) * p.q_stride +
-                                                              (size_t)(kvh * group + q - token * group) * HD + 32 * cg) +
-                           pair);
-        }
+        // (rows behind the last repeat it, so that no branch comes between the loads)
+        const uint32_t q = min(v0 + 32 * (warp & 3) + 2 * i + (lane >> 4), queries - 1), token = q / group;
+        words[i] = __ldg(reinterpret_cast<const longlong2*>(p.q + (size_t)(sq.first + token) * p.q_stride +
+                                                            (size_t)(kvh * group + q - token * group) * HD + 32 * cg) +
+                         pair);
       }
 #pragma unroll
       for (uint32_t i = 0; i < 16; ++i) {
@@ -446,6 +454,7 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
     }
     batch += nt;
     tiles += nt;
+    asm volatile("fence.proxy.async.global;" ::: "memory");  // the scores come back by bulk copies
 
     // ---- the row's maximum, over the column groups and the cluster
     int32_t* redm = reinterpret_cast<int32_t*>(red);
@@ -480,19 +489,26 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
     // ---- the exponentials, in the place of the scores, and their sum
     unsigned long long z = 0;
     if (!away) {
-      int4* src = scores + r;
-      constexpr uint32_t kAhead = 8;  // loads in flight
-      const uint32_t quads = (lim + 3) / 4;
-      for (uint32_t i = cg; i < quads; i += T::kGroups * kAhead) {
-        int4 c[kAhead];
+      constexpr uint32_t kMine = kTilePos / 4 / T::kGroups;  // quads of a stage a thread takes
+      auto fetch = [&](uint32_t i) {  // by one thread
+        const uint32_t at = (staged + i) % kRing;
+        mb_expect_tx(ring + at, kStage);
+        bulk_copy(sm + at * kStage, scores + (size_t)i * (kStage / 16), kStage, ring + at);
+      };
+      if (tid == 0)
+        for (uint32_t i = 0; i < min(nt, kRing); ++i) fetch(i);
+      for (uint32_t i = 0; i < nt; ++i) {
+        const uint32_t at = staged + i;
+        wait_copy(ring + at % kRing, (at / kRing) & 1u);
+        const int4* stage = reinterpret_cast<const int4*>(sm + (at % kRing) * kStage) + r;
+        int4 c[kMine];
 #pragma unroll
-        for (uint32_t u = 0; u < kAhead; ++u) {
-          const uint32_t k = i + T::kGroups * u;
-          c[u] = k < quads ? src[(size_t)k * kTileRows] : make_int4(0, 0, 0, 0);
-        }
+        for (uint32_t u = 0; u < kMine; ++u) c[u] = stage[(cg + T::kGroups * u) * kTileRows];
+        __syncthreads();  // the place is free
+        if (tid == 0 && i + kRing < nt) fetch(i + kRing);
 #pragma unroll
-        for (uint32_t u = 0; u < kAhead; ++u) {
-          const uint32_t k = i + T::kGroups * u;
+        for (uint32_t u = 0; u < kMine; ++u) {
+          const uint32_t k = i * (kTilePos / 4) + cg + T::kGroups * u;
           const int32_t x[4] = {c[u].x, c[u].y, c[u].z, c[u].w};
           uint32_t e[4];
 #pragma unroll
@@ -502,12 +518,13 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
             for (int j = 0; j < 4; ++j)
               if (4 * k + j >= lim) e[j] = 0;
           }
-          if (k < quads) {
+          if (4 * k < lim) {
             z += (unsigned long long)(e[0] + e[1]) + (e[2] + e[3]);
-            src[(size_t)k * kTileRows] = make_int4(e[0], e[1], e[2], e[3]);
+            scores[(size_t)k * kTileRows + r] = make_int4(e[0], e[1], e[2], e[3]);
           }
         }
       }
+      staged += nt;
     }
     red[cg * kTileRows + r] = z;
     __syncthreads();
