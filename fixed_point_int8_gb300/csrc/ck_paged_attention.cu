@@ -723,7 +723,7 @@ int ck_paged_attention(const ck_paged_cache* cache, uint32_t layer, const ck_pag
     const TilesParams tp = {p, plan.tiles.tiles, plan.tiles.cap, reinterpret_cast<uint32_t*>(work + plan.tiles.any_off),
                             reinterpret_cast<uint32_t*>(work + plan.tiles.away_off),
                             reinterpret_cast<int32_t*>(work + plan.tiles.scores_off),
-                            reinterpret_cast<ulonglong2*>(work + plan.tiles.sums_off)};
+                            reinterpret_cast<unsigned long long*>(work + plan.tiles.sums_off)};
     CKP_CUDA(launch_tiles(tp, plan.tiles, f, s));
     rp.scores = reinterpret_cast<long long*>(work + plan.tiles.scores_off);
     rp.any = tp.any;

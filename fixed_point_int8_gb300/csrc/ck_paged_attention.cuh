@@ -28,7 +28,7 @@ struct TilesParams {
   uint32_t* any;   // the count, and that of the tiles drawn beyond the first of each cluster
   uint32_t* away;  // [sequence][key head][tile]
   int32_t* scores;
-  ulonglong2* sums;
+  unsigned long long* sums;
 };
 TilesPlan plan_tiles(const ck_paged_cache& c, const ck_paged_batch& b, uint32_t heads, const DeviceFacts& f);
 cudaError_t launch_tiles(const TilesParams& p, const TilesPlan& w, const DeviceFacts& f, cudaStream_t s);

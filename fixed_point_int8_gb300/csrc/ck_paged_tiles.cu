@@ -226,8 +226,8 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
   const uint32_t group = p.heads / p.pool.kv_heads;
   // [position / 4][row][4]: a thread writes and reads four positions of its row at once
   int4* scores = reinterpret_cast<int4*>(f.scores) + (size_t)blockIdx.x * (f.cap / 4) * kTileRows;
-  // [pair of elements][thread]: the 64-bit sums between flushes
-  ulonglong2* kept = f.sums + (size_t)blockIdx.x * 16 * T::kThreads + tid;
+  // [element][thread]: the 64-bit sums between flushes
+  unsigned long long* kept = f.sums + (size_t)blockIdx.x * 32 * T::kThreads + tid;
   const uint64_t per_seq = (uint64_t)p.pool.kv_heads * f.tiles;
   const uint64_t items = (uint64_t)p.batch.seqs * per_seq;
 
@@ -650,27 +650,25 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
     auto flush = [&](bool first, bool final) {
 #pragma unroll
       for (uint32_t h = 0; h < 32; h += 8) {
-        ulonglong2 old[4];
+        unsigned long long old[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          old[j] = first ? make_ulonglong2(0, 0) : kept[(size_t)(h / 2 + j) * T::kThreads];
+        for (int j = 0; j < 8; ++j) old[j] = final && !first ? __ldcg(kept + (h + j) * T::kThreads) : 0;
         uint32_t d[4][8];
 #pragma unroll
         for (uint32_t g = 0; g < 4; ++g) tmem_ld8(tmem + lane_base + g * HD + 32 * cg + h, d[g]);
         tmem_wait_ld();
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          long long t = (long long)(j & 1 ? old[j / 2].y : old[j / 2].x);
-          t += __float2int_rn(__uint_as_float(d[0][j]) * 16777216.0f);
+          long long t = __float2int_rn(__uint_as_float(d[0][j]) * 16777216.0f);
           t += (long long)__float2int_rn(__uint_as_float(d[1][j]) * 65536.0f) * 256;
           t += (long long)__float2int_rn(__uint_as_float(d[2][j]) * 256.0f) * 65536;
           t += (long long)__float2int_rn(__uint_as_float(d[3][j])) * 16777216;
-          if (final) sums[(size_t)(32 * cg + h + j) * T::kPitch + r] = (unsigned long long)t;
-          (j & 1 ? old[j / 2].y : old[j / 2].x) = (unsigned long long)t;
-        }
-        if (!final) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) kept[(size_t)(h / 2 + j) * T::kThreads] = old[j];
+          if (final)
+            sums[(size_t)(32 * cg + h + j) * T::kPitch + r] = (unsigned long long)t + old[j];
+          else if (first)
+            __stcg(kept + (h + j) * T::kThreads, (unsigned long long)t);
+          else
+            atomicAdd(kept + (h + j) * T::kThreads, (unsigned long long)t);  // nothing to wait for
         }
       }
     };
