@@ -58,7 +58,7 @@ struct Tile {
   static constexpr uint32_t kSumOff = kMaxOff + kTileRows * 4;   // [128] u64
   static constexpr uint32_t kMiscOff = kSumOff + kTileRows * 8;  // barrier, tensor memory, flags
   static constexpr uint32_t kRingOff = kMiscOff + 64;            // the scores' barriers
-  static constexpr uint32_t kSmem = kRingOff + kRing * 8 + 1024; // + alignment of the operands
+  static constexpr uint32_t kSmem = kRingOff + kRing * 16 + 1024; // + alignment of the operands
   static_assert(kRing * kStage <= kOperands, "the scores' ring");
   static_assert(kScoreCol + kBufs * kDiags * kTilePos <= kTmem && 4 * HD <= kTmem, "tensor memory");
 };
@@ -179,6 +179,7 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
   uint64_t* done = full + 2;
   uint64_t* drained = full + 4;
   uint64_t* ring = reinterpret_cast<uint64_t*>(sm + T::kRingOff);  // a stage of scores has come
+  uint64_t* freed = ring + kRing;                                   // and has been read
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + T::kMiscOff + 48);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + T::kMiscOff + 52);
   uint32_t* next_s = reinterpret_cast<uint32_t*>(sm + T::kMiscOff + 60);
@@ -191,7 +192,10 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
       mb_init(done + i, 1);
       mb_init(drained + i, T::kThreads / 32);
     }
-    for (uint32_t i = 0; i < kRing; ++i) mb_init(ring + i, 1);
+    for (uint32_t i = 0; i < kRing; ++i) {
+      mb_init(ring + i, 1);
+      mb_init(freed + i, T::kThreads / 32);
+    }
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -499,13 +503,19 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
         for (uint32_t i = 0; i < min(nt, kRing); ++i) fetch(i);
       for (uint32_t i = 0; i < nt; ++i) {
         const uint32_t at = staged + i;
+        if (tid == 0 && i > 0 && i - 1 + kRing < nt) {
+          wait_copy(freed + (at - 1) % kRing, ((at - 1) / kRing) & 1u);
+          fetch(i - 1 + kRing);
+        }
         wait_copy(ring + at % kRing, (at / kRing) & 1u);
         const int4* stage = reinterpret_cast<const int4*>(sm + (at % kRing) * kStage) + r;
         int4 c[kMine];
 #pragma unroll
         for (uint32_t u = 0; u < kMine; ++u) c[u] = stage[(cg + T::kGroups * u) * kTileRows];
-        __syncthreads();  // the place is free
-        if (tid == 0 && i + kRing < nt) fetch(i + kRing);
+        // An arrival comes after the reads before it; a block barrier would let reads on their way
+        // meet the next copy.
+        __syncwarp();
+        if (lane == 0) mb_arrive(freed + at % kRing);
 #pragma unroll
         for (uint32_t u = 0; u < kMine; ++u) {
           const uint32_t k = i * (kTilePos / 4) + cg + T::kGroups * u;

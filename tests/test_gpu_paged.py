@@ -146,6 +146,19 @@ def test_attention_against_the_plain_form(ck, lens, news, heads, kv, hd, page):
     assert s.batch.errors() == [None] * len(lens)
 
 
+@pytest.mark.parametrize("lens,news,heads,kv,hd,page", TILES)
+def test_tiles_give_the_same_bits_every_time(ck, lens, news, heads, kv, hd, page):
+    s = Setup(ck, lens, news, heads, kv, hd, page, seed=hd + len(lens))
+    assert on_tiles(ck, s)
+    q, exp = cuda((s.rng.standard_normal((s.rows, heads * hd)) * 65536).astype(np.int64)), cuda(EXP.view(np.int32))
+    inv = synth.inv_sqrt_head(hd)
+    rc, first = ck.paged_attention(s.cache, 0, s.batch, q, exp, inv)
+    assert rc == 0
+    for _ in range(100):
+        rc, out = ck.paged_attention(s.cache, 0, s.batch, q, exp, inv)
+        assert rc == 0 and torch.equal(out, first)
+
+
 @pytest.mark.parametrize("new", [1, 70])
 @pytest.mark.parametrize("q_spread,kv_spread", [(2**62, 65536), (65536, 2**31 - 1), (2**31, 2**31 - 1),
                                                 (2**22, 2**23), (2**23 + 5, 2**23 + 5), (1, 1), (0, 65536)])
