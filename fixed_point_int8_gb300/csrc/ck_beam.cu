@@ -79,12 +79,13 @@ __device__ __forceinline__ unsigned long long distance(long long m, long long l)
 // clusters), whose blocks split the vocabulary.  A block reads its logits once into registers
 // (once a pass where they are more): the maximum, pushed to the other blocks; the distances, cut
 // to 32 bits, and the sum of their exponentials, from a table in shared memory (gathered through
-// L1 it bounds the kernel: 63 against 29 us for 512 rows of 32,000); then a bound that at least
+// L1 the kernel takes 63 us for 512 rows of 32,000, against 41 to 46); then a bound that at least
 // `beams` threads' least distances meet, by their bit length and the three bits below it, so that
 // what meets it (a few more than `beams`, unless there are many ties) contains the block's
 // nearest, which are ranked by counting.  More than kFound at the bound, or a bound past 32
-// bits: one after the other, by index.  HBM bounds it where rows are many, the chain of these
-// steps where they are few.
+// bits: one after the other, by index.  Where rows are many the instructions bound it (512 rows of
+// 32,000: 131 MB in 46 us, 2.9 TB/s, half of the issue slots), where they are few the chain of
+// these steps.
 template <bool ONE>
 __global__ void __launch_bounds__(kBeamThreads, kBeamBlocks) k_beam_row(const BeamParams p) {
   __shared__ uint32_t table[4097], found_d[kFound], found_i[kFound], bits[33], below[8], red_i[kBeamWarps], n_found;
@@ -306,6 +307,7 @@ __global__ void __launch_bounds__(kBeamThreads, kBeamBlocks) k_beam_row(const Be
 // bounds what can be chosen: the entries that meet it (those of equal scores among them) are
 // ranked by counting.  More than kChosen of them: one warp walks the lists, taking the best
 // head each time.  Lists come in the order of beam and token, so the lower list wins a tie.
+// The latency of its steps bounds it: 10.6 us for 64 searches of 8 beams.
 constexpr int kMergeThreads = 256;
 constexpr uint32_t kChosen = 512;
 __global__ void __launch_bounds__(kMergeThreads) k_beam_merge(const BeamParams p) {

@@ -19,11 +19,15 @@
 // words (a score that does not fit, and any digit that does not, hands the tile to the kernel
 // for all values), then maximum, sum and weighted values follow in three passes.
 //
-// The vector units bound it: about 75 instructions a score against 18 tensor products of
-// 128 x N x 16.  A thread owns a row (its lane of tensor memory), so maxima and sums need no
-// exchange inside a warp.  A cluster splits a tile's positions, which fills the GPU when tiles
-// are few; it exchanges maxima, sums and the 64-bit sums of values through distributed shared
-// memory.
+// The instructions around the products bound it (about 70 a score, a third of the issue slots in
+// phases that wait for one another; the tensor pipe is busy for a fifth): 256 rows over 7,936
+// positions of 32 heads of 64 take 338 us, chunks of 201 and 151 rows over 2,047 and 777 of 32 heads
+// of 128 take 234.  Twice the warps with 64 registers a thread were slower (447 against 388 us, 276
+// against 255), and so were 16-bit places in the table in the scratch for the exponentials (346
+// against 338, 243 against 234).  A thread owns a row (its lane of tensor memory), so maxima and
+// sums need no exchange inside a warp.  A cluster splits a tile's positions, which fills the GPU
+// when tiles are few; it exchanges maxima, sums and the 64-bit sums of values through distributed
+// shared memory.
 #include "ck_paged_attention.cuh"
 #include "ck_tc.cuh"
 

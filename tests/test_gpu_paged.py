@@ -148,6 +148,7 @@ def test_attention_against_the_plain_form(ck, lens, news, heads, kv, hd, page):
 
 @pytest.mark.parametrize("lens,news,heads,kv,hd,page", TILES)
 def test_tiles_give_the_same_bits_every_time(ck, lens, news, heads, kv, hd, page):
+    import torch
     s = Setup(ck, lens, news, heads, kv, hd, page, seed=hd + len(lens))
     assert on_tiles(ck, s)
     q, exp = cuda((s.rng.standard_normal((s.rows, heads * hd)) * 65536).astype(np.int64)), cuda(EXP.view(np.int32))
