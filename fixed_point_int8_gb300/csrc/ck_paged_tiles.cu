@@ -46,7 +46,8 @@ struct Tile {
   static constexpr uint32_t kBufs = HD == 64 ? 1 : 2;              // score accumulators, operand buffers
   static constexpr uint32_t kTmem = HD == 64 ? 256 : 512;          // two blocks an SM for head size 64
   static constexpr uint32_t kScoreCol = 3 * HD / 2;                // behind the query digits
-  static constexpr uint32_t kKeyPlane = (HD / 64) * kTilePos * 128, kKeyBuf = 3 * kKeyPlane;
+  // [64 elements][place][position]: two buffers of three key planes, two places of zeros around each
+  static constexpr uint32_t kKeyPlane = kTilePos * 128, kKeyHalf = 12 * kKeyPlane, kKeys = (HD / 64) * kKeyHalf;
   static constexpr uint32_t kProbPlane = kTileRows * 128, kValuePlane = HD * 128;
   static constexpr uint32_t kValueBuf = 3 * (kProbPlane + kValuePlane);
   static constexpr uint32_t kPitch = kTileRows + 1;  // of the 64-bit sums, [element][row]
@@ -55,7 +56,7 @@ struct Tile {
   }
   static constexpr uint32_t kTurn = (kThreads / 32) * 48 * 33 * 4;  // query digits on their way to tensor memory
   static constexpr uint32_t kOperands =
-      (max3(2 * kKeyBuf, kBufs * kValueBuf, max3(HD * kPitch * 8, kTurn, 0)) + 1023) & ~1023u;
+      (max3(kKeys, kBufs * kValueBuf, max3(HD * kPitch * 8, kTurn, 0)) + 1023) & ~1023u;
   static constexpr uint32_t kTableOff = kOperands, kTableBytes = 4097 * 4 + 12;
   static constexpr uint32_t kRedOff = kTableOff + kTableBytes;   // [groups][128] u64
   static constexpr uint32_t kMaxOff = kRedOff + kGroups * kTileRows * 8;  // [128] i32
@@ -307,6 +308,11 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
       }
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       __syncthreads();  // the keys' operands go to the same place
+      for (uint32_t i = tid; i < T::kKeys / 2 / 16; i += T::kThreads) {  // places 0, 1, 5, 6, 10 and 11
+        const uint32_t half = i / (T::kKeyHalf / 2 / 16), in = i % (T::kKeyHalf / 2 / 16), at = in / (T::kKeyPlane / 16);
+        *reinterpret_cast<uint4*>(sm + half * T::kKeyHalf + (at / 2 * 5 + at % 2) * T::kKeyPlane +
+                                  in % (T::kKeyPlane / 16) * 16) = make_uint4(0, 0, 0, 0);
+      }
     }
 
     // ---- scores: 32 positions at a time
@@ -342,11 +348,11 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
         d[1][i] = sub_1152(lift<0x4341>(u));
         d[2][i] = sub_1152(lift<0x4240>(t));
       }
-      uint8_t* dst = sm + buf * T::kKeyBuf + (kchunk >> 3) * (3 * kTilePos * 128) + kpos * 128 +
-                     (((kchunk & 7u) ^ (kpos & 7u)) << 4);  // [64 elements][plane][position]
+      uint8_t* dst = sm + (kchunk >> 3) * T::kKeyHalf + (2 + 5 * buf) * T::kKeyPlane + kpos * 128 +
+                     (((kchunk & 7u) ^ (kpos & 7u)) << 4);
 #pragma unroll
       for (int k = 0; k < 3; ++k)
-        *reinterpret_cast<uint4*>(dst + k * (kTilePos * 128)) = make_uint4(d[k][0], d[k][1], d[k][2], d[k][3]);
+        *reinterpret_cast<uint4*>(dst + k * T::kKeyPlane) = make_uint4(d[k][0], d[k][1], d[k][2], d[k][3]);
       fence_operands();
     };
     // A batch's products, by one thread of the warps in turn, once its operands are in place and
@@ -356,26 +362,18 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
         wait_full(batch + i);
         if (i >= T::kBufs) wait_drained(tiles + i - T::kBufs);
         const uint32_t leader = elected(), d0 = tmem_u + T::kScoreCol + (i % T::kBufs) * (kDiags * kTilePos);
-        const uint64_t b0 = operands + (i & 1u) * (T::kKeyBuf >> 4);
-        // A query plane times the three key planes side by side goes to the accumulators of weights
-        // qp, qp + 1, qp + 2, which lie side by side too; the first products of the two highest
-        // weights go ahead of the others, as they start their accumulators.
-        auto product = [&](uint32_t qp, uint32_t kp, uint32_t planes, uint32_t kk, uint32_t acc) {
-          mma_ts(leader, d0 + (qp + kp) * kTilePos, tmem_u + qp * (HD / 2) + 8 * kk,
-                 b0 + (((kk >> 2) * (3 * kTilePos * 128) + kp * (kTilePos * 128) + (kk & 3u) * 32) >> 4),
-                 tile_idesc(planes * kTilePos), acc);
-        };
-        product(0, 0, 3, 0, 0);
-        product(1, 2, 1, 0, 0);
-        product(2, 2, 1, 0, 0);
-        product(1, 0, 2, 0, 1);
-        product(2, 0, 2, 0, 1);
+        const uint64_t b0 = operands + ((2 + 5 * (i & 1u)) * T::kKeyPlane >> 4);
+        // A query plane times five places side by side, the three key planes and zeros, adds to the
+        // five accumulators at once: plane qp's begin qp places before the keys.  Products of one
+        // shape into the same accumulators are done in order; of several shapes into parts of
+        // them, which saved a fifth of the products' time, they need not be, and were not always.
 #pragma unroll
-        for (uint32_t kk = 1; kk < HD / 16; ++kk) {
-          product(0, 0, 3, kk, 1);
-          product(1, 0, 3, kk, 1);
-          product(2, 0, 3, kk, 1);
-        }
+        for (uint32_t kk = 0; kk < HD / 16; ++kk)
+#pragma unroll
+          for (uint32_t qp = 0; qp < 3; ++qp)
+            mma_ts(leader, d0, tmem_u + qp * (HD / 2) + 8 * kk,
+                   b0 + ((kk >> 2) * T::kKeyHalf >> 4) - (qp * T::kKeyPlane >> 4) + 2 * (kk & 3u),
+                   tile_idesc(kDiags * kTilePos), kk + qp != 0);
         commit(leader, done + ((batch + i) & 1u));
       }
       __syncwarp();
@@ -516,10 +514,6 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
         int4 c[kMine];
 #pragma unroll
         for (uint32_t u = 0; u < kMine; ++u) c[u] = stage[(cg + T::kGroups * u) * kTileRows];
-        // An arrival comes after the reads before it; a block barrier would let reads on their way
-        // meet the next copy.
-        __syncwarp();
-        if (lane == 0) mb_arrive(freed + at % kRing);
 #pragma unroll
         for (uint32_t u = 0; u < kMine; ++u) {
           const uint32_t k = i * (kTilePos / 4) + cg + T::kGroups * u;
@@ -537,6 +531,10 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
             scores[(size_t)k * kTileRows + r] = make_int4(e[0], e[1], e[2], e[3]);
           }
         }
+        // Only now, as the lookups above needed the words: neither a barrier of the block nor an
+        // arrival holds back the next copy until reads on their way have come.
+        __syncwarp();
+        if (lane == 0) mb_arrive(freed + at % kRing);
       }
       staged += nt;
     }
@@ -692,26 +690,19 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
         const uint32_t leader = elected();
         const uint64_t a0 = operands + (b % T::kBufs) * (T::kValueBuf >> 4), b0 = a0 + (3 * T::kProbPlane >> 4);
         const uint32_t go_on = b % kFlushBlocks != 0;
-        // As for the scores; the product of the highest weight shares the last accumulator (and
-        // starts it, where a flush went before).
-        auto product = [&](uint32_t pp, uint32_t vp, uint32_t planes, uint32_t g, uint32_t kk, uint32_t acc) {
-          mma_ss(leader, tmem_u + g * HD, a0 + ((pp * T::kProbPlane + kk * 32) >> 4),
-                 b0 + ((vp * T::kValuePlane + kk * 32) >> 4), tile_idesc(planes * HD), acc);
-        };
+        // The products of a weight have one shape and their accumulator to themselves; that of the
+        // highest weight shares the last.
 #pragma unroll
-        for (uint32_t kk = 0; kk < kBlockPos / 16; ++kk) {
-          product(2, 2, 1, 3, kk, kk == 0 ? go_on : 1u);
-          if (HD == 64) {
-            product(0, 0, 3, 0, kk, kk == 0 ? go_on : 1u);
-            product(1, 0, 3, 1, kk, 1);
-          } else {  // (256 columns at most)
-            product(0, 0, 2, 0, kk, kk == 0 ? go_on : 1u);
-            product(0, 2, 1, 2, kk, kk == 0 ? go_on : 1u);
-            product(1, 0, 2, 1, kk, 1);
-            product(1, 2, 1, 3, kk, 1);
-          }
-          product(2, 0, 2, 2, kk, 1);
-        }
+        for (uint32_t kk = 0; kk < kBlockPos / 16; ++kk)
+#pragma unroll
+          for (uint32_t pp = 0; pp < 3; ++pp)
+#pragma unroll
+            for (uint32_t vp = 0; vp < 3; ++vp) {
+              const uint32_t g = min(pp + vp, 3u);
+              const bool begins = kk == 0 && (pp == 0 || (pp == 1 && vp == 2));
+              mma_ss(leader, tmem_u + g * HD, a0 + ((pp * T::kProbPlane + kk * 32) >> 4),
+                     b0 + ((vp * T::kValuePlane + kk * 32) >> 4), tile_idesc(HD), begins ? go_on : 1u);
+            }
         commit(leader, done + ((batch + b) & 1u));
       }
       __syncwarp();
