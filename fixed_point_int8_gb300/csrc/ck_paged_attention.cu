@@ -30,7 +30,7 @@ __device__ __forceinline__ uint32_t exponential(const uint32_t* tab, unsigned lo
 // One (row, head) at a time a block, whatever the values and the lengths: the products are
 // 64-bit, the scores of the row lie in the block's part of the scratch.  Every row reads its
 // keys and values again, and 64-bit products bound it: one token over 8,191 positions of 32 heads
-// takes 883 us, 256 rows over 7,936 take 12.9 ms (the other kernels: 28.8 and 338 us).
+// takes 883 us, 256 rows over 7,936 take 12.9 ms (the other kernels: 28.8 and 357 us).
 __global__ void __launch_bounds__(kRowsThreads) k_pattn_rows(const RowsParams f) {
   const PAttnParams& p = f.a;
   if (f.away && *f.any == 0) return;
@@ -639,11 +639,11 @@ cudaError_t launch_few_r(const FewParams& p, const FewPlan& w, const DeviceFacts
 
 // Which kernel a call takes.  Head sizes 64 and 128 compare what k_pattn_few and the tensor-core
 // tiles would take, by the launch's bounds: 8 us and 0.9 us a million products of a query's and a
-// key's element, against 30 us and 0.62 ns a tile and position (head size 64) or 34 us and 1 ns.
-// (Measured, few against tiles: head size 64, 32 heads: 32 rows over 200 positions 21 and 31 us,
-// over 1,000 68 and 47, four sequences of 16 rows over 1,500 144 and 134, of 8 rows 89 and 131;
-// head size 128: 16 rows over 2,000 117 and 93, 128 rows over 128 44 and 49, 32 sequences of one
-// row and four heads a key head over 2,000 179 and 462.)  k_pattn_rows follows the tiles for those
+// key's element, against 30 us and 0.66 ns a tile and position (head size 64) or 34 us and
+// 1.06 ns.  (Measured, few against tiles: head size 64, 32 heads: 32 rows over 200 positions 21 and
+// 31 us, over 1,000 68 and 51, four sequences of 16 rows over 1,500 144 and 146, of 8 rows 89 and
+// 142; head size 128: 16 rows over 2,000 117 and 98, 128 rows over 128 44 and 49, 32 sequences of
+// one row and four heads a key head over 2,000 179 and 494.)  k_pattn_rows follows the tiles for those
 // with values beyond their digits, and takes calls that k_pattn_few's grid or shared memory does
 // not hold.
 struct AttentionPlan {
@@ -658,7 +658,7 @@ AttentionPlan attention_plan(const ck_paged_cache& c, const ck_paged_batch& b, u
   if (c.head_dim >= 64) {
     const double tiles = std::ceil((double)b.max_new * (heads / c.kv_heads) / 128) * b.seqs * c.kv_heads;
     const double few_us = 8 + 0.9e-6 * b.seqs * heads * b.max_new * b.max_len * c.head_dim;
-    const double at = tiles * b.max_len, tiles_us = c.head_dim == 64 ? 30 + 0.62e-3 * at : 34 + 1e-3 * at;
+    const double at = tiles * b.max_len, tiles_us = c.head_dim == 64 ? 30 + 0.66e-3 * at : 34 + 1.06e-3 * at;
     if (!w.few.use || tiles_us < few_us) w.tiles = plan_tiles(c, b, heads, f);
     if (w.tiles.use) w.few.use = false;
   }

@@ -20,14 +20,14 @@
 // for all values), then maximum, sum and weighted values follow in three passes.
 //
 // The instructions around the products bound it (about 70 a score, a third of the issue slots in
-// phases that wait for one another; the tensor pipe is busy for a fifth): 256 rows over 7,936
-// positions of 32 heads of 64 take 338 us, chunks of 201 and 151 rows over 2,047 and 777 of 32 heads
-// of 128 take 234.  Twice the warps with 64 registers a thread were slower (447 against 388 us, 276
-// against 255), and so were 16-bit places in the table in the scratch for the exponentials (346
-// against 338, 243 against 234).  A thread owns a row (its lane of tensor memory), so maxima and
-// sums need no exchange inside a warp.  A cluster splits a tile's positions, which fills the GPU
-// when tiles are few; it exchanges maxima, sums and the 64-bit sums of values through distributed
-// shared memory.
+// phases that wait for one another), and the scratch's traffic where it is larger than L2: 256 rows
+// over 7,936 positions of 32 heads of 64 take 357 us, chunks of 201 and 151 rows over 2,047 and 777
+// of 32 heads of 128 take 249.  Twice the warps with 64 registers a thread were slower (447 against
+// 388 us, 276 against 255 then), and so were 16-bit places in the table in the scratch for the
+// exponentials (346 against 338, 243 against 234 then).  A thread owns a row (its lane of tensor
+// memory), so maxima and sums need no exchange inside a warp.  A cluster splits a tile's positions,
+// which fills the GPU when tiles are few; it exchanges maxima, sums and the 64-bit sums of values
+// through distributed shared memory.
 #include "ck_paged_attention.cuh"
 #include "ck_tc.cuh"
 
@@ -108,7 +108,16 @@ __device__ __forceinline__ void tmem_ld8(uint32_t addr, uint32_t* v) {
                : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
                : "r"(addr));
 }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// The words are there after the wait; the second statement reads and writes each of them, so that
+// the compiler moves nothing that uses them before it.
+template <int N>
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&v)[N][8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    asm volatile("" : "+r"(v[i][0]), "+r"(v[i][1]), "+r"(v[i][2]), "+r"(v[i][3]), "+r"(v[i][4]), "+r"(v[i][5]),
+                      "+r"(v[i][6]), "+r"(v[i][7]));
+}
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* v) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
@@ -366,7 +375,7 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
         // A query plane times five places side by side, the three key planes and zeros, adds to the
         // five accumulators at once: plane qp's begin qp places before the keys.  Products of one
         // shape into the same accumulators are done in order; of several shapes into parts of
-        // them, which saved a fifth of the products' time, they need not be, and were not always.
+        // them, which measured 234 against 249 us and 337 against 357, they need not be.
 #pragma unroll
         for (uint32_t kk = 0; kk < HD / 16; ++kk)
 #pragma unroll
@@ -387,7 +396,7 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
         uint32_t d[kDiags][8];
 #pragma unroll
         for (uint32_t g = 0; g < kDiags; ++g) tmem_ld8(base + g * kTilePos + h, d[g]);
-        tmem_wait_ld();
+        tmem_wait_ld(d);
         const uint32_t at = i * kTilePos + cg * kCols + h;
         int32_t c[8];
         float high[8], peak = 0;
@@ -668,7 +677,7 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
         uint32_t d[4][8];
 #pragma unroll
         for (uint32_t g = 0; g < 4; ++g) tmem_ld8(tmem + lane_base + g * HD + 32 * cg + h, d[g]);
-        tmem_wait_ld();
+        tmem_wait_ld(d);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           long long t = __float2int_rn(__uint_as_float(d[0][j]) * 16777216.0f);
