@@ -58,10 +58,11 @@ def _empty(stream, shape, dtype, device):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _keep(t, stream):
-    """A plan's scratch stays in use on the stream, whatever becomes of the plan."""
+def _keep(stream, *tensors):
+    """The tensors stay in use on the stream, whatever becomes of them after the call."""
     if stream is not None:
-        t.record_stream(stream)
+        for t in tensors:
+            t.record_stream(stream)
 
 
 def _raw(stream, device):
@@ -89,6 +90,7 @@ class PagedCache:
         self.pages, self.layers, self.kv_heads, self.page, self.head_dim = k.shape
         self._struct = _Cache(k.data_ptr(), v.data_ptr(), *k.shape)
         self._c = ctypes.addressof(self._struct)
+        self._tensors = k, v
 
     @classmethod
     def empty(cls, pages, layers, kv_heads, page, head_dim):
@@ -118,6 +120,7 @@ class PagedBatch:
         self._struct = _Batch(starts.data_ptr(), lens.data_ptr(), table.data_ptr(), status.data_ptr(), seqs, rows,
                               table.shape[1], max_new, max_len)
         self._c = ctypes.addressof(self._struct)
+        self._tensors = table, lens, starts, status
 
     def errors(self):
         """The status words on the host as (position, layer, phase, element), None where there is
@@ -151,6 +154,7 @@ def paged_store(cache, layer, batch, q, k, v, rope, half=False, out=None, stream
         out = _empty(stream, (rows, cols), torch.int64, device)
     else:
         _check("out", out, torch.int64, (rows, cols), device)
+    _keep(stream, q, k, v, rope, out, *cache._tensors, *batch._tensors)
     rc = lib().ck_paged_store(cache._c, layer, batch._c, q.data_ptr(), q_step, k.data_ptr(), k_step, v.data_ptr(),
                               v_step, cols // hd, rope.data_ptr(), rope.shape[0], 2 * rope.shape[1], half,
                               out.data_ptr(), _raw(stream, device))
@@ -179,6 +183,7 @@ def paged_attention(cache, layer, batch, q, exp_table, inv_sqrt, out=None, work=
         work = paged_attention_work(cache, batch, cols // hd, stream)
     else:
         _check("work", work, torch.uint8, (work.numel(),), device)
+    _keep(stream, q, exp_table, out, work, *cache._tensors, *batch._tensors)
     rc = lib().ck_paged_attention(cache._c, layer, batch._c, q.data_ptr(), step, cols // hd, exp_table.data_ptr(),
                                   inv_sqrt, out.data_ptr(), work.data_ptr(), work.numel(), _raw(stream, device))
     return rc, out
@@ -202,6 +207,7 @@ def turn_paged(model, cache, batch, tokens, logits=None, work=None, stream=None)
         work = turn_paged_work(model, cache, batch, stream)
     else:
         _check("work", work, torch.uint8, (work.numel(),), device)
+    _keep(stream, model.mem, tokens, logits, work, *cache._tensors, *batch._tensors)
     rc = lib().ck_turn_paged(model._h, cache._c, batch._c, tokens.data_ptr(), logits.data_ptr(), step,
                              work.data_ptr(), work.numel(), _raw(stream, device))
     return rc, logits
@@ -248,7 +254,7 @@ class PagePlan:
         _check("grow", grow, torch.int32, (rows,), device)
         if held is not None:
             _check("held", held, torch.uint8, (self.cache.pages,), device)
-        _keep(self._work, stream)
+        _keep(stream, self._work, parent, lens, table, grow, *(() if held is None else (held,)), *self.cache._tensors)
         out = _empty(stream, (rows, self.stride), torch.int32, device)
         new_lens, status = _empty(stream, (rows,), torch.int32, device), _empty(stream, (rows,), torch.int32, device)
         rc = lib().ck_pages_fork(self.cache._c, rows_in, lens.data_ptr(), table.data_ptr(), rows, parent.data_ptr(),
@@ -262,7 +268,7 @@ class PagePlan:
         device, rows = self._begin(lens, table)
         if rows > self.rows:
             raise ValueError(f"table: {rows} rows, the plan has room for {self.rows}")
-        _keep(self._work, stream)
+        _keep(stream, self._work, lens, table, *self.cache._tensors)
         out = _empty(stream, (rows, self.stride), torch.int32, device)
         status = _empty(stream, (rows,), torch.int32, device)
         used = _empty(stream, (), torch.int32, device)
@@ -301,7 +307,7 @@ class BeamPlan:
         _check("scores", scores, torch.int64, (rows,), device)
         _check("done", done, torch.uint8, (rows,), device)
         _check("exp_table", exp_table, torch.int32, (4097,), device)
-        _keep(self._work, stream)
+        _keep(stream, self._work, logits, scores, done, exp_table)
         new_scores = _empty(stream, (rows,), torch.int64, device)
         parent, token = _empty(stream, (rows,), torch.int32, device), _empty(stream, (rows,), torch.int32, device)
         new_done = _empty(stream, (rows,), torch.uint8, device)

@@ -315,6 +315,30 @@ def test_calls_on_two_streams_and_captured_ones_repeat(ck):
             assert np.array_equal(out.cpu().numpy(), want[turn])
 
 
+def test_inputs_freed_after_a_call_on_another_stream_stay_in_use(ck):
+    """The stream is busy when the call is enqueued; its inputs are dropped and their memory asked
+    for again on the current stream before the kernels run."""
+    import torch
+    s = Setup(ck, [70], [1], 4, 2, 64, 16)
+    q = (s.rng.standard_normal((1, 256)) * 65536).astype(np.int64)
+    want = s.attention(0, q, 1 << 21)
+    side = torch.cuda.Stream()
+    place, exp = cuda(q), cuda(EXP.view(np.int32))
+    for t in (place, exp):  # (every kernel below is loaded before the stream is busy)
+        torch.full_like(t, 3)
+    ck.paged_attention(s.cache, 0, s.batch, place, exp, 1 << 21, stream=side)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+    rc, out = ck.paged_attention(s.cache, 0, s.batch, place, exp, 1 << 21, stream=side)
+    assert rc == 0
+    del place, exp
+    other = [torch.full((1, 256), 3, dtype=torch.int64, device="cuda") for _ in range(500)]
+    other += [torch.full((4097,), 3, dtype=torch.int32, device="cuda") for _ in range(100)]
+    torch.cuda.synchronize()
+    assert np.array_equal(out.cpu().numpy(), want) and len(other) == 600
+
+
 def test_attention_leaves_rows_of_no_sequence_and_strided_queries(ck):
     """Rows before the first sequence and behind the last stay as they were; queries are a
     column range of wider rows."""

@@ -176,6 +176,14 @@ def test_wrong_selections_are_refused(ck, bad):
     assert call(ck, "ck_beam_select", beam_args(ck), **bad) == 10
 
 
+def test_paged_turns_and_tables_without_a_model_are_refused(ck):
+    L, n, p = ck.lib(), ctypes.c_size_t(), ctypes.c_void_p()
+    c, b = ctypes.byref(cache(ck)), ctypes.byref(batch(ck))
+    assert L.ck_turn_paged_work(None, c, b, ctypes.byref(n)) == 10
+    assert L.ck_turn_paged(None, c, b, ADDR, ADDR, 64, ADDR, 1 << 30, None) == 10
+    assert L.ck_model_tables(None, ctypes.byref(p), ctypes.byref(p), ctypes.byref(ctypes.c_uint32())) == 10
+
+
 def test_the_binding_checks_tensors(ck):
     """Types, shapes, strides and devices that the library cannot see."""
     import torch
