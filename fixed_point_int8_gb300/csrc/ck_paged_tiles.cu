@@ -736,6 +736,7 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
       arrive(full + ((batch + b) & 1u));
       issue_values(b);
     }
+    if (T::kBufs == 2 && nb > 1) wait_done(batch + nb - 2);  // (another thread's products)
     if (nb) wait_done(batch + nb - 1);
     batch += nb;
     if (bad) *bad_s = 1;
