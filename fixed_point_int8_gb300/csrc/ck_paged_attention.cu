@@ -652,14 +652,21 @@ struct AttentionPlan {
   uint32_t rows_blocks;
   uint64_t work;
 };
-AttentionPlan attention_plan(const ck_paged_cache& c, const ck_paged_batch& b, uint32_t heads, const DeviceFacts& f) {
+// `resident` fills in the resident clusters of the tiles, where they are asked for.
+template <class Resident>
+AttentionPlan attention_plan(const ck_paged_cache& c, const ck_paged_batch& b, uint32_t heads, const DeviceFacts& f,
+                             Resident resident) {
   AttentionPlan w = {};
   w.few = plan_few(c, b, heads, f);
   if (c.head_dim >= 64) {
     const double tiles = std::ceil((double)b.max_new * (heads / c.kv_heads) / 128) * b.seqs * c.kv_heads;
     const double few_us = 8 + 0.9e-6 * b.seqs * heads * b.max_new * b.max_len * c.head_dim;
     const double at = tiles * b.max_len, tiles_us = c.head_dim == 64 ? 30 + 0.66e-3 * at : 34 + 1.06e-3 * at;
-    if (!w.few.use || tiles_us < few_us) w.tiles = plan_tiles(c, b, heads, f);
+    if (!w.few.use || tiles_us < few_us) {
+      int32_t clusters[kTileClusters] = {};
+      resident(clusters);
+      w.tiles = plan_tiles(c, b, heads, f, clusters);
+    }
     if (w.tiles.use) w.few.use = false;
   }
   if (w.few.use) {
@@ -677,6 +684,14 @@ AttentionPlan attention_plan(const ck_paged_cache& c, const ck_paged_batch& b, u
   }
   return w;
 }
+AttentionPlan attention_plan(const ck_paged_cache& c, const ck_paged_batch& b, uint32_t heads, const DeviceFacts& f) {
+  return attention_plan(c, b, heads, f, [&](int32_t* out) { resident_tiles(c, f, out); });
+}
+
+// Whether the arguments that size the scratch are within the limits.
+bool work_args_ok(const ck_paged_cache* cache, const ck_paged_batch* batch, uint32_t heads) {
+  return cache_ok(cache) && batch_sizes_ok(batch) && heads >= 1 && heads <= 65536 && heads % cache->kv_heads == 0;
+}
 
 }  // namespace
 }  // namespace ck
@@ -687,11 +702,22 @@ extern "C" {
 
 int ck_paged_attention_work(const ck_paged_cache* cache, const ck_paged_batch* batch, uint32_t heads,
                             size_t* out) {
-  if (!out || !cache_ok(cache) || !batch_sizes_ok(batch) || heads < 1 || heads > 65536 || heads % cache->kv_heads)
-    return CK_INVALID_ARGUMENT;
+  if (!out || !work_args_ok(cache, batch, heads)) return CK_INVALID_ARGUMENT;
   DeviceFacts f;
   CKP_CUDA(device_facts(&f));
   *out = attention_plan(*cache, *batch, heads, f).work;
+  return CK_OK;
+}
+
+int ck_host_attention_plan(const ck_paged_cache* cache, const ck_paged_batch* batch, uint32_t heads, uint32_t sms,
+                           uint32_t smem, const int32_t* clusters, uint32_t* kernel, size_t* work) {
+  if (!clusters || !kernel || !work || sms < 1 || sms > 65536 || smem > (1u << 20) || !work_args_ok(cache, batch, heads))
+    return CK_INVALID_ARGUMENT;
+  const DeviceFacts f = {0, (int)sms, (int)smem};
+  const AttentionPlan plan =
+      attention_plan(*cache, *batch, heads, f, [&](int32_t* out) { std::copy(clusters, clusters + kTileClusters, out); });
+  *kernel = plan.few.use ? 0 : plan.tiles.use ? 1 : 2;
+  *work = plan.work;
   return CK_OK;
 }
 

@@ -30,7 +30,12 @@ struct TilesParams {
   int32_t* scores;
   unsigned long long* sums;
 };
-TilesPlan plan_tiles(const ck_paged_cache& c, const ck_paged_batch& b, uint32_t heads, const DeviceFacts& f);
+// Clusters of 1, 2, 4 and 8 blocks of the tiles that are resident at once, 0 where none is or the
+// device could not say; and the plan by them, of host values alone.
+constexpr int kTileClusters = 4;
+void resident_tiles(const ck_paged_cache& c, const DeviceFacts& f, int32_t* out);
+TilesPlan plan_tiles(const ck_paged_cache& c, const ck_paged_batch& b, uint32_t heads, const DeviceFacts& f,
+                     const int32_t* resident);
 cudaError_t launch_tiles(const TilesParams& p, const TilesPlan& w, const DeviceFacts& f, cudaStream_t s);
 
 }  // namespace ck

@@ -807,23 +807,28 @@ void tiles_config(uint32_t blocks, uint32_t C, cudaLaunchConfig_t* cfg, cudaLaun
 }
 
 // Clusters of C blocks that are resident at once, looked up once for each C (the runtime counts one
-// block an SM; of head size 64 two run).
+// block an SM; of head size 64 two run).  0 where the lookup fails: no plan then uses that C, and the
+// failure is not left for a later call to report.
 template <int HD>
-cudaError_t resident_tiles(uint32_t C, const DeviceFacts& f, uint32_t* out) {
+int32_t resident_clusters(uint32_t C, const DeviceFacts& f) {
   static std::atomic<int> known[64][9];  // the number and one more, zero before
   int n = known[f.dev][C].load(std::memory_order_relaxed) - 1;
   if (n < 0) {
     cudaError_t e = configure_tiles<HD>(f);
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg;
-    cudaLaunchAttribute attr[1];
-    tiles_config<HD>(C, C, &cfg, attr);
-    if ((e = cudaOccupancyMaxActiveClusters(&n, k_pattn_tiles<HD>, &cfg)) != cudaSuccess) return e;
+    if (e == cudaSuccess) {
+      cudaLaunchConfig_t cfg;
+      cudaLaunchAttribute attr[1];
+      tiles_config<HD>(C, C, &cfg, attr);
+      e = cudaOccupancyMaxActiveClusters(&n, k_pattn_tiles<HD>, &cfg);
+    }
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
     n *= HD == 64 ? 2 : 1;
     known[f.dev][C].store(n + 1, std::memory_order_relaxed);
   }
-  *out = (uint32_t)n;
-  return cudaSuccess;
+  return n;
 }
 
 template <int HD>
@@ -839,12 +844,21 @@ cudaError_t launch_tiles_hd(const TilesParams& p, const TilesPlan& w, const Devi
 
 }  // namespace
 
-TilesPlan plan_tiles(const ck_paged_cache& c, const ck_paged_batch& b, uint32_t heads, const DeviceFacts& f) {
+bool tiles_fit(const ck_paged_cache& c, const DeviceFacts& f) {
+  return (c.head_dim == 64 && Tile<64>::kSmem <= (uint32_t)f.optin) ||
+         (c.head_dim == 128 && Tile<128>::kSmem <= (uint32_t)f.optin);
+}
+
+void resident_tiles(const ck_paged_cache& c, const DeviceFacts& f, int32_t* out) {
+  for (int i = 0; i < kTileClusters; ++i)
+    out[i] = !tiles_fit(c, f) ? 0 : c.head_dim == 64 ? resident_clusters<64>(1u << i, f) : resident_clusters<128>(1u << i, f);
+}
+
+TilesPlan plan_tiles(const ck_paged_cache& c, const ck_paged_batch& b, uint32_t heads, const DeviceFacts& f,
+                     const int32_t* resident) {
   TilesPlan w = {};
   const uint64_t queries = (uint64_t)b.max_new * (heads / c.kv_heads);
-  if (c.head_dim != 64 && c.head_dim != 128) return w;
-  const uint32_t smem = c.head_dim == 64 ? Tile<64>::kSmem : Tile<128>::kSmem;
-  if (smem > (uint32_t)f.optin) return w;
+  if (!tiles_fit(c, f)) return w;
   w.tiles = (uint32_t)((queries + kTileRows - 1) / kTileRows);
   const uint64_t items = (uint64_t)b.seqs * c.kv_heads * w.tiles;
   if (items > 0xFFFFFFFFull - 65536) return w;  // (the count of tiles is 32 bits)
@@ -853,11 +867,10 @@ TilesPlan plan_tiles(const ck_paged_cache& c, const ck_paged_batch& b, uint32_t 
   // on average, but never less than the longest.  What surrounds a tile (queries, exchanges,
   // sums) measured as about 200 positions.
   double best = 0;
-  for (uint32_t C = 1; C <= 8; C *= 2) {
-    uint32_t n = 0;
-    if ((c.head_dim == 64 ? resident_tiles<64>(C, f, &n) : resident_tiles<128>(C, f, &n)) != cudaSuccess) return w;
-    if (n == 0) continue;
-    const double each = (double)b.max_len / C + 200, clusters = (double)std::min<uint64_t>(items, n);
+  for (int i = 0; i < kTileClusters; ++i) {
+    if (resident[i] <= 0) continue;
+    const uint32_t C = 1u << i;
+    const double each = (double)b.max_len / C + 200, clusters = (double)std::min<uint64_t>(items, resident[i]);
     const double cost = b.seqs == 1 ? std::ceil(items / clusters) * each
                                     : std::max(each, items / clusters * (0.75 * b.max_len / C + 200));
     if (!w.use || cost < 0.95 * best) {

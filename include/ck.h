@@ -501,6 +501,12 @@ int64_t ck_host_div_trunc(int64_t n, uint32_t d);
  * stage", stage 2) as the attention kernels form it from an estimate of 1 / z, for an
  * exponential 0 <= e <= min(z, 2^30) and a sum 2^30 <= z < 2^46. */
 uint64_t ck_host_probability(uint64_t e, uint64_t z);
+/* What ck_paged_attention would choose on a device of `sms` multiprocessors with `smem` bytes of
+ * shared memory a block, of whose tensor-core kernel clusters[i] clusters of 2^i blocks (i = 0 to 3)
+ * are resident at once, 0 or less where the device does not say: *kernel is 0 for a few queries, 1
+ * for tiles, 2 for single rows, *work the scratch in bytes.  Errors: 10. */
+int ck_host_attention_plan(const ck_paged_cache* cache, const ck_paged_batch* batch, uint32_t heads, uint32_t sms,
+                           uint32_t smem, const int32_t* clusters, uint32_t* kernel, size_t* work);
 
 /* Library version string. */
 const char* ck_version(void);

@@ -200,3 +200,43 @@ def test_the_binding_checks_tensors(ck):
                     (torch.zeros(3, 2, dtype=torch.int64).t(), 2)):
         with pytest.raises(ValueError):
             ck.paged._check_rows("q", t, rows, 0)
+
+
+def attention_plan(ck, seqs, new, length, heads, kv_heads, hd, clusters, page=16, sms=152, smem=232448, rows=None):
+    """The kernel (0 a few queries, 1 tiles, 2 single rows) and the scratch of a call on a device."""
+    kernel, work = ctypes.c_uint32(), ctypes.c_size_t()
+    c = cache(ck, kv_heads=kv_heads, page=page, head_dim=hd)
+    b = batch(ck, seqs=seqs, rows=rows or seqs * new, stride=2**17, max_new=new, max_len=length)
+    rc = ck.lib().ck_host_attention_plan(ctypes.byref(c), ctypes.byref(b), heads, sms, smem, (ctypes.c_int32 * 4)(*clusters),
+                                         ctypes.byref(kernel), ctypes.byref(work))
+    assert rc == 0
+    return kernel.value, work.value
+
+
+@pytest.mark.parametrize("hd,new,length,heads,kv", [(64, 256, 7936, 32, 32), (128, 201, 2047, 32, 32), (64, 70, 600, 32, 4)])
+@pytest.mark.parametrize("clusters", [(304, 152, 76, 38), (304, -1, -1, -1), (304, 152, -1, 38), (-1, -1, 76, 38),
+                                      (304, 0, 0, 0), (-1, 152, 0, -1), (0, 0, 0, 0), (-1, -1, -1, -1)], ids=str)
+def test_a_plan_is_whole_whatever_the_device_answers(ck, hd, new, length, heads, kv, clusters):
+    """A lookup of resident clusters that fails takes that cluster size out of the choice and no more:
+    tiles always come with the scratch of every block that runs."""
+    kernel, work = attention_plan(ck, 1, new, length, heads, kv, hd, clusters)
+    assert (kernel, work) == attention_plan(ck, 1, new, length, heads, kv, hd, [max(n, 0) for n in clusters])
+    tiles = kv * -(-new * (heads // kv) // 128)
+    if max(clusters) <= 0:
+        assert kernel != 1 and work >= 256
+    else:
+        # of one cluster size: 128 rows' scores of all positions a cluster (the positions split over its
+        # blocks), and 128 rows' sums of 64 bits a block
+        sizes = [min(tiles, n) * (4 * 128 * length + 8 * 128 * hd * 2**i) for i, n in enumerate(clusters) if n > 0]
+        assert kernel == 1 and work >= min(sizes)
+
+
+def test_wrong_arguments_of_a_plan_are_refused(ck):
+    kernel, work, n = ctypes.c_uint32(), ctypes.c_size_t(), (ctypes.c_int32 * 4)(1, 1, 1, 1)
+    good = dict(cache=cache(ck), batch=batch(ck), heads=4, sms=152, smem=232448, clusters=n, kernel=ctypes.byref(kernel),
+                work=ctypes.byref(work))
+    assert call(ck, "ck_host_attention_plan", good) == 0
+    for bad in (dict(cache=None), dict(batch=None), dict(heads=3), dict(heads=0), dict(sms=0), dict(smem=2**21),
+                dict(clusters=None), dict(kernel=None), dict(work=None), dict(cache=cache(ck, page=7)),
+                dict(batch=batch(ck, seqs=0))):
+        assert call(ck, "ck_host_attention_plan", good, **bad) == 10
