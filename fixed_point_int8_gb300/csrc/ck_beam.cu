@@ -98,6 +98,7 @@ __global__ void __launch_bounds__(kBeamThreads, kBeamBlocks) k_beam_row(const Be
   const uint32_t per = (p.vocab + S - 1) / S, v0 = min(p.vocab, rank * per), n = min(p.vocab, v0 + per) - v0;
   const uint32_t want = min(k, n);  // (at most 64: each thread has one)
   constexpr uint32_t kWord = 8;
+  if (tid < 33) bits[tid] = 0;
   if (tid == 0) {
     gave_up = 0;
     for (int i = 0; i < 2; ++i) {
@@ -142,8 +143,7 @@ __global__ void __launch_bounds__(kBeamThreads, kBeamBlocks) k_beam_row(const Be
     }
     m = warp_max(m);
     __syncthreads();  // the row before is done with shared memory
-    if (tid < 33) bits[tid] = 0;
-    if (tid < 8) below[tid] = 0;
+    if (tid < 8) below[tid] = 0;  // (the block's next barriers come before their use)
     if (tid == 0) n_found = 0;
     const uint32_t turn = pushed & 1u;
     if (lane < S) {  // each warp's maximum to block `lane`, completing on that block's barrier
@@ -208,6 +208,9 @@ __global__ void __launch_bounds__(kBeamThreads, kBeamBlocks) k_beam_row(const Be
     z = warp_sum48(z);
     if (lane == 0) red[warp] = z;
     __syncthreads();
+    // The counts have been read, and this row's last barrier and the next one's first come before
+    // they are added to again: the wait for the maxima in between orders the pushed words alone.
+    if (tid < 33) bits[tid] = 0;
     uint32_t bound = at >= 32 ? kFar : (1u << at) - 1;
     if (at >= 4 && at < 32) {
       uint32_t sum = lane < 8 ? below[lane] : 0;

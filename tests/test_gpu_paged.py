@@ -744,3 +744,27 @@ def test_beam_selection_at_the_edges(ck):
         ramp = np.arange(vocab)[None, :] * np.array([1, -1, 300, -300])[:, None]
         check_beam(ck, ramp.astype(np.int64), [0, 0, 0, 0], [0] * 4, 1, 4)
         check_beam(ck, ramp.astype(np.int64), [0, 0, 0, 0], [0] * 4, 4, 1)
+
+
+@pytest.mark.parametrize("groups,beams,vocab", [(256, 8, 5000), (700, 3, 4096), (64, 8, 32000)])
+def test_rows_that_follow_one_another_in_a_cluster(ck, groups, beams, vocab):
+    """More rows than clusters are resident, rows of far apart and of close logits in turn: a block's
+    counts of one row are not another's.  The same bits every time, and the plain form's in some."""
+    import torch
+    rng = np.random.default_rng(vocab)
+    rows = groups * beams
+    logits = (rng.standard_normal((rows, vocab)) * np.array([1, 65536, 2.0**40])[np.arange(rows) % 3, None]).astype(np.int64)
+    scores, done = -rng.integers(0, 10 << 16, rows), np.zeros(rows, np.uint8)
+    done[::7] = 1
+    plan = ck.BeamPlan(groups, beams, vocab)
+    dev = cuda(logits), cuda(scores), cuda(done), cuda(EXP.view(np.int32))
+    rc, first = plan.select(*dev)
+    assert rc == 0
+    for _ in range(100):
+        rc, again = plan.select(*dev)
+        assert rc == 0 and all(torch.equal(a, b) for a, b in zip(first, again))
+    for g in (0, groups // 2, groups - 1):
+        at = slice(g * beams, (g + 1) * beams)
+        want = plain_beam(logits[at], scores[at], done[at], 1, beams, 0, False)
+        got = [t[at].tolist() for t in first]
+        assert list(zip(*got)) == [(s, r + g * beams if r >= 0 else r, t, d) for s, r, t, d in want]
