@@ -96,6 +96,7 @@ def lib() -> ctypes.CDLL:
             "ck_beam_work": ([u32, u32, u32, vp], ctypes.c_int),
             "ck_beam_select": ([vp, sz, u32, u32, u32, vp, vp, vp, u32, u32, vp, vp, vp, vp, vp, sz, vp],
                                ctypes.c_int),
+            "ck_set_beam_wait_limit": ([u32], ctypes.c_int),
             "ck_host_log_sum": ([u64], i64),
             "ck_host_attention_plan": ([vp, vp, u32, u32, u32, vp, vp, vp], ctypes.c_int),
             "ck_turn_paged_work": ([vp, vp, vp, vp], ctypes.c_int),
@@ -387,7 +388,7 @@ def version() -> str:
 
 
 # The paged cache and beam search, loaded at their first use (they import torch).
-_PAGED = ("NO_PAGE", "BAD_SEQUENCE", "BAD_PAGE", "PagedCache", "PagedBatch", "PagePlan", "BeamPlan", "paged_store",
+_PAGED = ("NO_PAGE", "BAD_SEQUENCE", "BAD_PAGE", "BEAM_FAILED", "set_beam_wait_limit", "PagedCache", "PagedBatch", "PagePlan", "BeamPlan", "paged_store",
           "paged_attention_work", "paged_attention", "host_log_sum")
 
 

@@ -9,6 +9,8 @@ namespace {
 
 constexpr long long kDeadScore = -(1ll << 61);
 constexpr unsigned long long kMaxDistance = 1ull << 62;
+constexpr unsigned long long kLost = ~0ull;  // a sum of exponentials (below 2^51) that is none
+std::atomic<uint32_t> g_wait_limit{0};       // ck_set_beam_wait_limit
 
 // ln(z / 2^30), 16 fraction bits (0 below 2^30): z = 2^n y with y in [1, 2), ln y = 2 atanh t
 // of t = (y - 1) / (y + 1) <= 1/3, its series to t^15 (the next term is below 2^-28).
@@ -46,7 +48,8 @@ struct BeamParams {
   // of every row and block of its cluster: the sum of exponentials, and the block's nearest
   // continuations, nearest first (distance all ones: none; token `vocab`: an ended beam)
   uint32_t split;
-  unsigned long long* part_z;     // [rows][split]
+  uint32_t polls;                 // of a row's wait for the cluster's maxima, before it is given up
+  unsigned long long* part_z;     // [rows][split]; kLost: the block gave the row up
   unsigned long long* list_d;     // [rows][split][beams]
   uint32_t* list_token;           // [rows][split][beams]
 };
@@ -75,6 +78,13 @@ __device__ __forceinline__ unsigned long long distance(long long m, long long l)
   return d < kMaxDistance ? d : kMaxDistance;
 }
 
+// Polls for the phase with the given parity; whether it came.
+__device__ __forceinline__ bool came(uint64_t* bar, uint32_t parity, uint32_t polls) {
+  for (uint32_t i = 0; i < polls; ++i)
+    if (mb_try(bar, parity)) return true;
+  return false;
+}
+
 // The rows' nearest continuations, a cluster a row (and then the next but as many as there are
 // clusters), whose blocks split the vocabulary.  A block reads its logits once into registers
 // (once a pass where they are more): the maximum, pushed to the other blocks; the distances, cut
@@ -83,7 +93,9 @@ __device__ __forceinline__ unsigned long long distance(long long m, long long l)
 // `beams` threads' least distances meet, by their bit length and the three bits below it, so that
 // what meets it (a few more than `beams`, unless there are many ties) contains the block's
 // nearest, which are ranked by counting.  More than kFound at the bound, or a bound past 32
-// bits: one after the other, by index.  Where rows are many the instructions bound it (512 rows of
+// bits: one after the other, by index.  A block whose wait for the maxima runs out gives the row up:
+// it marks its sum as lost, so that the merge fails the row's search, and waits once more for what
+// is on its way to it, so that it neither leaves before nor takes it for the next row's.  Where rows are many the instructions bound it (512 rows of
 // 32,000: 131 MB in 46 us, 2.9 TB/s, half of the issue slots), where they are few the chain of
 // these steps.
 template <bool ONE>
@@ -91,7 +103,7 @@ __global__ void __launch_bounds__(kBeamThreads, kBeamBlocks) k_beam_row(const Be
   __shared__ uint32_t table[4097], found_d[kFound], found_i[kFound], bits[33], below[8], red_i[kBeamWarps], n_found;
   __shared__ unsigned long long red[kBeamWarps], peaks[2][8 * kBeamWarps];
   __shared__ uint64_t arrived[2];  // the cluster's maxima of a row, in turn
-  __shared__ int gave_up;
+  __shared__ int gave_up;          // a warp's wait for this row's maxima ran out
   const uint32_t S = p.split, rank = blockIdx.x % S, clusters = gridDim.x / S;
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = p.beams, rows = p.groups * k;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the merge waits for this grid's end)
@@ -156,7 +168,10 @@ __global__ void __launch_bounds__(kBeamThreads, kBeamBlocks) k_beam_row(const Be
     }
     // A block sends its next row's maxima once it has read this one's, and waits for all: so
     // those of the row after next find this turn's words read.
-    mb_wait(arrived + turn, (pushed >> 1) & 1u, &gave_up);
+    if (!came(arrived + turn, (pushed >> 1) & 1u, p.polls)) {
+      gave_up = 1;
+      came(arrived + turn, (pushed >> 1) & 1u, kTcPoll);
+    }
     ++pushed;
     if (tid == 0) mb_expect_tx(arrived + turn, S * kBeamWarps * kWord);
 #pragma unroll
@@ -193,6 +208,7 @@ __global__ void __launch_bounds__(kBeamThreads, kBeamBlocks) k_beam_row(const Be
     const uint32_t length = 32 - __clz((int)least), three = length >= 4 ? least >> (length - 4) & 7u : 0;
     if (mine) atomicAdd(bits + length, 1u);
     __syncthreads();
+    const bool lost = gave_up != 0;
     // each warp scans the counts: bit lengths 0 .. 31 (at = 32: none of them)
     const uint32_t count = bits[lane];
     uint32_t upto = count;
@@ -211,6 +227,7 @@ __global__ void __launch_bounds__(kBeamThreads, kBeamBlocks) k_beam_row(const Be
     // The counts have been read, and this row's last barrier and the next one's first come before
     // they are added to again: the wait for the maxima in between orders the pushed words alone.
     if (tid < 33) bits[tid] = 0;
+    if (tid == 0) gave_up = 0;
     uint32_t bound = at >= 32 ? kFar : (1u << at) - 1;
     if (at >= 4 && at < 32) {
       uint32_t sum = lane < 8 ? below[lane] : 0;
@@ -225,7 +242,7 @@ __global__ void __launch_bounds__(kBeamThreads, kBeamBlocks) k_beam_row(const Be
     if (tid == 0) {
       z = 0;
       for (int w = 0; w < kBeamWarps; ++w) z += red[w];
-      p.part_z[(size_t)row * S + rank] = z;
+      p.part_z[(size_t)row * S + rank] = lost ? kLost : z;
     }
     for (uint32_t base = 0; base < (ONE ? 1 : n) && least <= bound; base += kRound) {
       if (!ONE) {
@@ -245,7 +262,7 @@ __global__ void __launch_bounds__(kBeamThreads, kBeamBlocks) k_beam_row(const Be
     }
     __syncthreads();
     const uint32_t nf = n_found;
-    const uint32_t some = gave_up ? 0 : want;  // (a wait that ran out: no continuations)
+    const uint32_t some = lost ? 0 : want;
     for (uint32_t i = some + tid; i < k; i += kBeamThreads) {
       ld[i] = ~0ull;
       lt[i] = p.vocab;
@@ -326,10 +343,15 @@ __global__ void __launch_bounds__(kMergeThreads) k_beam_merge(const BeamParams p
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const unsigned long long* ld = p.list_d + (size_t)first * lists;
   const uint32_t* lt = p.list_token + (size_t)first * lists;
+  int lost = 0;
   for (uint32_t b = tid; b < k; b += kMergeThreads) {
     unsigned long long z = 0;
 #pragma unroll
-    for (uint32_t r = 0; r < 8; ++r) z += r < S ? __ldcg(p.part_z + (size_t)(first + b) * S + r) : 0;
+    for (uint32_t r = 0; r < 8; ++r) {
+      const unsigned long long part = r < S ? __ldcg(p.part_z + (size_t)(first + b) * S + r) : 0;
+      lost |= part == kLost;
+      z += part;
+    }
     base[b] = p.scores[first + b] - log_sum(z);  // (an ended beam's z is zero, and so its logarithm)
   }
   // outcome n: entry e (list * beams + place) with token t
@@ -339,11 +361,11 @@ __global__ void __launch_bounds__(kMergeThreads) k_beam_merge(const BeamParams p
     p.token[first + n] = t < p.vocab ? t : p.done_token;
     p.done_out[first + n] = t == p.vocab || ((p.flags & CK_FLAG_STOP_TOKENS) && (t == 1 || t == 2));
   };
-  auto put_none = [&](uint32_t n) {
+  auto put_none = [&](uint32_t n, uint8_t done) {
     p.scores_out[first + n] = LLONG_MIN;
     p.parent[first + n] = CK_NO_PAGE;
     p.token[first + n] = p.done_token;
-    p.done_out[first + n] = 0;
+    p.done_out[first + n] = done;
   };
   // heads, and the first entries (all of them, where beams are few), asked for at once
   const uint32_t all = lists * k;
@@ -356,7 +378,10 @@ __global__ void __launch_bounds__(kMergeThreads) k_beam_merge(const BeamParams p
     early_d[u] = i < all ? __ldcg(ld + i) : ~0ull;
     early_t[u] = i < all ? __ldcg(lt + i) : 0;
   }
-  __syncthreads();
+  if (__syncthreads_or(lost)) {  // what is left of the search is not its selection
+    for (uint32_t n = tid; n < k; n += kMergeThreads) put_none(n, CK_BEAM_FAILED);
+    return;
+  }
 #pragma unroll
   for (uint32_t u = 0; u < 2; ++u) {
     const uint32_t i = tid + u * kMergeThreads;
@@ -400,7 +425,7 @@ __global__ void __launch_bounds__(kMergeThreads) k_beam_merge(const BeamParams p
       for (uint32_t j = 0; j < nc; ++j) rank_of += chosen[j] > v || (chosen[j] == v && entry[j] < e);
       if (rank_of < k) put(rank_of, v, e, token[i]);
     }
-    for (uint32_t n = nc + tid; n < k; n += kMergeThreads) put_none(n);
+    for (uint32_t n = nc + tid; n < k; n += kMergeThreads) put_none(n, 0);
     return;
   }
   if (tid >= 32) return;
@@ -430,7 +455,7 @@ __global__ void __launch_bounds__(kMergeThreads) k_beam_merge(const BeamParams p
         const unsigned long long d = c < k ? __ldcg(ld + (size_t)from * k + c) : ~0ull;
         head[from] = d == ~0ull ? LLONG_MIN : base[from / S] - (long long)d;
       } else {
-        put_none(n);
+        put_none(n, 0);
       }
     }
     __syncwarp();
@@ -513,6 +538,11 @@ extern "C" {
 
 int64_t ck_host_log_sum(uint64_t z) { return log_sum(z); }
 
+int ck_set_beam_wait_limit(uint32_t polls) {
+  g_wait_limit.store(polls, std::memory_order_relaxed);
+  return CK_OK;
+}
+
 int ck_beam_work(uint32_t groups, uint32_t beams, uint32_t vocab, size_t* out) {
   if (!out || !beam_sizes_ok(groups, beams, vocab)) return CK_INVALID_ARGUMENT;
   *out = beam_layout((uint64_t)groups * beams, beams, vocab).size;
@@ -564,6 +594,8 @@ int ck_beam_select(const int64_t* dev_logits, size_t logits_stride, uint32_t gro
   const BeamLayout w = beam_layout(rows, beams, vocab);
   uint8_t* work = static_cast<uint8_t*>(dev_work);
   p.split = beam_split(vocab);
+  const uint32_t limit = g_wait_limit.load(std::memory_order_relaxed);
+  p.polls = limit ? limit - 1 : kTcPoll;
   p.part_z = reinterpret_cast<unsigned long long*>(work + w.z);
   p.list_d = reinterpret_cast<unsigned long long*>(work + w.d);
   p.list_token = reinterpret_cast<uint32_t*>(work + w.token);

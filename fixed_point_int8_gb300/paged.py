@@ -16,6 +16,8 @@ from . import CkError, lib
 NO_PAGE = -1
 # phase bytes of a batch's status words besides the cache stores' 6, 7 and 8
 BAD_SEQUENCE, BAD_PAGE = 1, 2
+# Beams.done of a search that failed (a wait of its kernel ran out)
+BEAM_FAILED = 255
 
 _vp, _sz, _u32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_uint32
 _device = torch.cuda.current_device
@@ -282,7 +284,7 @@ class Beams(NamedTuple):
     scores: object  # int64 [groups * beams]
     parent: object  # int32: the row extended, -1 for none
     token: object   # int32
-    done: object    # uint8
+    done: object    # uint8: 1 ended, BEAM_FAILED everywhere in a search that failed
 
 
 class BeamPlan:
@@ -316,6 +318,11 @@ class BeamPlan:
                                   new_scores.data_ptr(), parent.data_ptr(), token.data_ptr(), new_done.data_ptr(),
                                   *self._args, _raw(stream, device))
         return rc, Beams(new_scores, parent, token, new_done)
+
+
+def set_beam_wait_limit(polls: int) -> int:
+    """The process's limit on a row's wait for its cluster's maxima (ck_set_beam_wait_limit)."""
+    return lib().ck_set_beam_wait_limit(polls)
 
 
 def host_log_sum(z: int) -> int:

@@ -479,15 +479,24 @@ int ck_pages_compact(const ck_paged_cache* cache, uint32_t rows, const uint32_t*
  * 2^61) is dead and gives none.  Outputs, per search in order: dev_scores_out, dev_parent
  * (the row the continuation extends, 0 .. groups * beams - 1, as ck_pages_fork takes it),
  * dev_token, dev_done_out (ended before, or, with CK_FLAG_STOP_TOKENS in flags, its token is
- * 1 or 2).  Where a search has fewer candidates: the lowest int64, CK_NO_PAGE, done_token, 0.
+ * 1 or 2).  Where a search has fewer candidates: the lowest int64, CK_NO_PAGE, done_token, 0.  Every
+ * output of a search is the lowest int64, CK_NO_PAGE, done_token and CK_BEAM_FAILED where a wait of
+ * its rows' kernel ran out (the blocks that share a row wait for each other's maxima): nothing of
+ * such a search is chosen, and its beams are dead to the next call.
  * The outputs may not overlap the inputs.  Limits: beams 1 to 64, vocab 1 to 2^20, groups *
  * beams <= 65536, done_token < vocab.  Errors: 4 (work_len), 9, 10. */
+#define CK_BEAM_FAILED 255u /* dev_done_out of a search that a wait's end has failed */
 int ck_beam_work(uint32_t groups, uint32_t beams, uint32_t vocab, size_t* out);
 int ck_beam_select(const int64_t* dev_logits, size_t logits_stride, uint32_t groups, uint32_t beams,
                    uint32_t vocab, const int64_t* dev_scores, const uint8_t* dev_done,
                    const uint32_t* dev_exp, uint32_t flags, uint32_t done_token, int64_t* dev_scores_out,
                    uint32_t* dev_parent, uint32_t* dev_token, uint8_t* dev_done_out, void* dev_work,
                    size_t work_len, void* stream);
+/* A testing control, of the whole process: a row's wait for its cluster's maxima gives up after
+ * `polls` - 1 polls (0, the default: about four million, far beyond any wait that ends), so 1 makes
+ * every one run out.  The kernel then waits for them with the default limit before it goes on.  A
+ * captured call keeps the limit that it was captured with. */
+int ck_set_beam_wait_limit(uint32_t polls);
 /* A host build of lnZ above, for tests without a GPU. */
 int64_t ck_host_log_sum(uint64_t z);
 

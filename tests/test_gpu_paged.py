@@ -768,3 +768,33 @@ def test_rows_that_follow_one_another_in_a_cluster(ck, groups, beams, vocab):
         want = plain_beam(logits[at], scores[at], done[at], 1, beams, 0, False)
         got = [t[at].tolist() for t in first]
         assert list(zip(*got)) == [(s, r + g * beams if r >= 0 else r, t, d) for s, r, t, d in want]
+
+
+@pytest.mark.parametrize("groups,beams,vocab", [(1, 1, 5), (3, 4, 1000), (2, 2, 4099), (40, 8, 32000), (1, 3, 40000)])
+def test_a_wait_that_runs_out_fails_its_searches(ck, groups, beams, vocab):
+    """Every wait given up at once: no search comes with a candidate, all of them say so, and the next
+    call is whole again.  A search of ended and dead beams alone has nothing to wait for."""
+    import torch
+    rng = np.random.default_rng(vocab)
+    rows = groups * beams
+    logits = cuda((rng.standard_normal((rows, vocab)) * 65536).astype(np.int64))
+    scores, done = cuda(-rng.integers(0, 10 << 16, rows)), cuda(np.zeros(rows, np.uint8))
+    exp, plan = cuda(EXP.view(np.int32)), ck.BeamPlan(groups, beams, vocab)
+    rc, want = plan.select(logits, scores, done, exp, done_token=vocab - 1)
+    assert rc == 0 and (want.done <= 1).all()
+    try:
+        assert ck.set_beam_wait_limit(1) == 0
+        rc, got = plan.select(logits, scores, done, exp, done_token=vocab - 1)
+        assert rc == 0
+        assert got.scores.tolist() == [MIN] * rows and got.parent.tolist() == [-1] * rows
+        assert got.token.tolist() == [vocab - 1] * rows and got.done.tolist() == [ck.BEAM_FAILED] * rows
+        rc, ended = plan.select(logits, scores, torch.ones_like(done), exp)
+        assert rc == 0 and ended.done.tolist() == [1] * rows
+        assert ended.parent.tolist() == [r for g in range(groups) for r in sorted(
+            range(g * beams, (g + 1) * beams), key=lambda r: (-int(scores[r]), r))]
+    finally:
+        ck.set_beam_wait_limit(0)
+    rc, again = plan.select(logits, scores, done, exp, done_token=vocab - 1)
+    assert rc == 0 and all(torch.equal(a, b) for a, b in zip(want, again))
+    rc, after = plan.select(logits, got.scores, got.done, exp)
+    assert rc == 0 and after.scores.tolist() == [MIN] * rows and after.done.tolist() == [0] * rows
