@@ -798,3 +798,45 @@ def test_a_wait_that_runs_out_fails_its_searches(ck, groups, beams, vocab):
     assert rc == 0 and all(torch.equal(a, b) for a, b in zip(want, again))
     rc, after = plan.select(logits, got.scores, got.done, exp)
     assert rc == 0 and after.scores.tolist() == [MIN] * rows and after.done.tolist() == [0] * rows
+
+
+def near_of(logits, scores, done, beams, done_token):
+    """One search over many logits: the plain form with numpy's sums and sorts (distances below 2^63)."""
+    found, vocab = [], logits.shape[1]
+    for r in range(beams):
+        old = int(scores[r])
+        if not -2**61 < old < 2**61:
+            continue
+        if done[r]:
+            found.append((-old, r, vocab))
+            continue
+        d = np.minimum(logits[r].max() - logits[r], 2**62)
+        z = int(EXP.astype(np.int64)[np.minimum(d >> 8, 4096)].sum())
+        found += [(int(d[i]) + plain_log_sum(z) - old, r, int(i)) for i in np.argsort(d, kind="stable")[:beams]]
+    found = sorted(found)[:beams]
+    return [(-c, r, done_token if i == vocab else i, int(i == vocab)) for c, r, i in found] + \
+        [(MIN, -1, done_token, 0)] * (beams - len(found))
+
+
+@pytest.mark.parametrize("vocab", [32768, 32769, 50257, 65536, 151936, 2**20 - 1, 2**20])
+@pytest.mark.parametrize("beams", [1, 4, 64])
+def test_beam_selection_over_large_vocabularies(ck, vocab, beams):
+    """More logits than a cluster of eight holds in registers: they are gone through once a pass.  Rows
+    of ordinary logits, of many ties, of distances past 32 bits, of one value, and rising ones; the
+    largest logits at the ends of the blocks' parts."""
+    rng = np.random.default_rng(vocab + beams)
+    logits = (rng.standard_normal((max(beams, 4), vocab)) * 3 * 65536).astype(np.int64)
+    logits[1] = rng.integers(-3, 3, vocab)
+    logits[2] = rng.integers(-2**61, 2**61, vocab)
+    logits[3] = np.arange(vocab) if vocab % 2 else 5
+    per = -(-vocab // 8)
+    logits[0, [vocab - 1, 0, per - 1, min(per, vocab - 1)]] = 2**20
+    for shift in range(1 if beams == 64 else 4):
+        rows = np.roll(logits, shift, axis=0)[:beams]
+        scores, done = -rng.integers(0, 10 << 16, beams), np.zeros(beams, np.uint8)
+        if beams == 64:
+            scores[5], done[7] = MIN, 1
+        rc, got = ck.BeamPlan(1, beams, vocab).select(cuda(rows), cuda(scores), cuda(done), cuda(EXP.view(np.int32)),
+                                                      done_token=9)
+        assert rc == 0
+        assert list(zip(*(t.tolist() for t in got))) == near_of(rows, scores, done, beams, 9)
