@@ -73,6 +73,7 @@ __global__ void __launch_bounds__(kStoreThreads) k_paged_store(const StoreParams
     if (lead) note(p.batch, s, err_key(0, p.pool.layer, CK_PAGED_BAD_SEQUENCE, 0));
     return;
   }
+  if (!sq.holds(row)) return;
   const uint32_t up = row - sq.first + sq.len;  // position + count
   if (up < sq.count) return;
   const uint32_t pos = up - sq.count;

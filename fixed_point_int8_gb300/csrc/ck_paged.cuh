@@ -111,6 +111,9 @@ __device__ __forceinline__ uint32_t block_find_seq(const BatchView& b, uint32_t 
 struct Sequence {
   uint32_t s, first, count, len;
   bool ok;  // within the bounds the launch was sized by
+  // Whether the row, at or behind the first, is one of the sequence's: where the starts do not ascend
+  // it may not be, and its position would lie behind the sequence's pages.
+  __device__ __forceinline__ bool holds(uint32_t row) const { return row - first < count; }
 };
 __device__ __forceinline__ Sequence load_sequence(const BatchView& b, uint32_t s, uint32_t page_shift) {
   Sequence q;

@@ -54,6 +54,7 @@ __global__ void __launch_bounds__(kRowsThreads) k_pattn_rows(const RowsParams f)
       if (tid == 0) note(p.batch, s, err_key(0, p.pool.layer, CK_PAGED_BAD_SEQUENCE, 0));
       continue;
     }
+    if (!sq.holds(row)) continue;
     if (f.away) {
       const uint32_t group = p.heads / p.pool.kv_heads, query = (row - sq.first) * group + h % group;
       if (!f.away[((size_t)s * p.pool.kv_heads + h / group) * f.tiles + query / 128]) continue;

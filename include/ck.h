@@ -364,7 +364,8 @@ typedef struct ck_paged_cache {
 #define CK_NO_PAGE 0xFFFFFFFFu /* a table entry without a page; a parent of no row */
 
 /* New tokens of several sequences.  Sequence s owns rows dev_start[s] .. dev_start[s+1] - 1
- * (ascending, dev_start[0] .. dev_start[seqs], none above `rows`); its cache holds dev_len[s]
+ * (ascending, dev_start[0] .. dev_start[seqs], none above `rows`; where they do not ascend, which
+ * sequence has a row is unspecified, and no buffer's end is passed); its cache holds dev_len[s]
  * positions, those of its new rows included, so that the last row is at position dev_len[s]
  * - 1.  A row whose position would be negative holds nothing: no store, zero attention.  Rows
  * that no sequence owns are left as they were.  dev_table: u32 [seqs][stride], the pages of

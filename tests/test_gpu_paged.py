@@ -840,3 +840,60 @@ def test_beam_selection_over_large_vocabularies(ck, vocab, beams):
                                                       done_token=9)
         assert rc == 0
         assert list(zip(*(t.tolist() for t in got))) == near_of(rows, scores, done, beams, 9)
+
+
+def single_rows(ck, lens, news, hd, bound, seed=0, **more):
+    """A batch whose bounds send it to the kernel of single rows: blocks of the kernel for a few queries
+    could not hold the page list of so long a sequence."""
+    s = Setup(ck, lens, news, 4, 2, hd, 8, seed=seed, **more)
+    s.table = np.concatenate([s.table, np.full((len(lens), bound // 8 + 2), -1, np.int32)], 1)
+    s.batch = ck.PagedBatch(cuda(s.table), cuda(np.array(lens, np.int32)), cuda(s.starts), None, s.rows, 320, bound)
+    return s
+
+
+@pytest.mark.parametrize("hd", [4, 16, 32])
+def test_single_rows_alone(ck, hd):
+    """The kernel for all values on its own, with sequences without rows, without positions, and
+    words of 32 and queries of 63 bits."""
+    s = single_rows(ck, [400, 33, 8, 0, 2], [320, 5, 0, 1, 4], hd, 300_000, seed=hd, lead=1, tail=2)
+    assert ck.paged_attention_work(s.cache, s.batch, 4).numel() == 608 * 300_000 * 8
+    wide = s.rng.integers(-2**62, 2**62, (s.rows, 4 * hd))
+    q = np.where(np.arange(s.rows)[:, None] % 3 == 0, wide, wide >> 45)
+    s.k[s.table[1, 2]] = s.rng.integers(-2**31, 2**31, s.k[0].shape)
+    s.v[s.table[1, 2]] = s.rng.integers(-2**31, 2**31, s.k[0].shape)
+    s.cache.k.copy_(cuda(s.k))
+    s.cache.v.copy_(cuda(s.v))
+    import torch
+    out = torch.full((s.rows, 4 * hd), 7, dtype=torch.int64, device="cuda")
+    rc, _ = ck.paged_attention(s.cache, 1, s.batch, cuda(q), cuda(EXP.view(np.int32)), 1 << 22, out=out)
+    assert rc == 0 and s.batch.errors() == [None] * 5
+    assert np.array_equal(out.cpu().numpy(), s.attention(1, q, 1 << 22, fill=7))
+
+
+def test_starts_that_do_not_ascend_stay_within_the_tables(ck):
+    """Rows 2 to 8 lie behind the last sequence's end: they have no position, and the last sequence's
+    table ends with its length."""
+    import torch
+    hd = 16
+    rng = np.random.default_rng(1)
+    cache = ck.PagedCache.empty(4, 1, 1, 8, hd)
+    # the table is a view whose last row is followed by other words
+    words = cuda(np.array([[0], [1], [2], [3], [3], [3]], np.int32))
+    q, k, v = (cuda((rng.standard_normal((9, hd)) * 65536).astype(np.int64)) for _ in range(3))
+    batch = ck.PagedBatch(words[:3], cuda(np.array([8, 8, 8], np.int32)), cuda(np.array([0, 9, 1, 2], np.int32)), None,
+                          9, 9, 8)
+    out = torch.full((9, hd), 5, dtype=torch.int64, device="cuda")
+    rc, _ = ck.paged_store(cache, 0, batch, q, k, v, cuda(rope_of(8, 0)), out=out)
+    assert rc == 0
+    assert (out[2:] == 5).all() and (cache.k[3] == 0).all() and (cache.v[3] == 0).all()
+    long = torch.full((3, 300_000 // 8 + 1), 3, dtype=torch.int32, device="cuda")
+    long[:, :1] = words[:3]
+    many = cuda(np.concatenate([[0, 900, 1], np.arange(2, 321)]).astype(np.int32))
+    wide = ck.PagedBatch(long[:1].expand(321, -1).contiguous(), cuda(np.full(321, 8, np.int32)), many, None, 900, 320, 300_000)
+    out = torch.full((900, hd), 5, dtype=torch.int64, device="cuda")
+    rows = cuda((rng.standard_normal((900, hd)) * 65536).astype(np.int64))
+    assert ck.paged_attention_work(cache, wide, 1).numel() == 608 * 300_000 * 8      # the kernel of single rows
+    rc, _ = ck.paged_attention(cache, 0, wide, rows, cuda(EXP.view(np.int32)), 1 << 22, out=out)
+    assert rc == 0
+    assert (out[320:] == 5).all()
+    assert wide.errors()[2:] == [None] * 319
