@@ -897,3 +897,28 @@ def test_starts_that_do_not_ascend_stay_within_the_tables(ck):
     assert rc == 0
     assert (out[320:] == 5).all()
     assert wide.errors()[2:] == [None] * 319
+
+
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("heads,kv,hd,rot", [(15, 3, 64, 48), (5, 5, 128, 128), (33, 1, 32, 0)])
+def test_store_of_rows_that_fill_the_gpu(ck, heads, kv, hd, rot, half):
+    """A block a row whose threads take several units, the last ones not all of them: words that do not
+    fit, rows of no sequence, and rows without a position among them."""
+    import torch
+    lens, news = [411, 90, 300, 3], [411, 0, 290, 6]
+    s = Setup(ck, lens, news, heads, kv, hd, 16, seed=heads, lead=1, tail=2)
+    units = (heads + 2 * kv) * hd // 4
+    assert s.rows >= 4 * torch.cuda.get_device_properties(0).multi_processor_count and 256 < units and units % 256
+    qkv = (s.rng.standard_normal((s.rows, (heads + 2 * kv) * hd)) * 65536).astype(np.int64)
+    parts = np.split(qkv, [heads * hd, (heads + kv) * hd], axis=1)
+    parts[1][7, kv * hd - 1], parts[2][500, kv * hd - 2], parts[0][3, 5] = 2**31, -2**40, 2**62
+    qkv = np.concatenate(parts, axis=1)
+    rope = rope_of(max(lens), rot)
+    out = torch.zeros(s.rows, heads * hd, dtype=torch.int64, device="cuda")
+    dev = cuda(qkv).split((heads * hd, kv * hd, kv * hd), -1)
+    rc, q = ck.paged_store(s.cache, 1, s.batch, *dev, cuda(rope), half=half, out=out)
+    assert rc == 0
+    qo, pk, pv, status = plain_store(s, 1, *parts, rope, half)
+    assert np.array_equal(q.cpu().numpy(), qo)
+    assert np.array_equal(s.cache.k.cpu().numpy(), pk) and np.array_equal(s.cache.v.cpu().numpy(), pv)
+    assert status[0] is not None and status[2] is not None and s.batch.errors() == status
