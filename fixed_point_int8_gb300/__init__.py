@@ -388,8 +388,9 @@ def version() -> str:
 
 
 # The paged cache and beam search, loaded at their first use (they import torch).
-_PAGED = ("NO_PAGE", "BAD_SEQUENCE", "BAD_PAGE", "BEAM_FAILED", "set_beam_wait_limit", "PagedCache", "PagedBatch", "PagePlan", "BeamPlan", "paged_store",
-          "paged_attention_work", "paged_attention", "host_log_sum")
+_PAGED = ("NO_PAGE", "BAD_SEQUENCE", "BAD_PAGE", "PAGE_RESERVED", "PAGE_SHARED", "BEAM_FAILED", "PagedCache", "PagedBatch",
+          "PagePlan", "BeamPlan", "paged_store", "paged_attention_work", "paged_attention", "set_beam_wait_limit",
+          "host_log_sum")
 
 
 def __getattr__(name):

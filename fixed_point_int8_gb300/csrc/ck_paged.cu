@@ -299,9 +299,11 @@ __global__ void __launch_bounds__(kPlanThreads) k_fork_plan(const PagesParams p,
   }
   const uint32_t mask = (1u << p.page_shift) - 1;
   if (tid == 0) n_copies = 0;
+  // whether the row keeps its parent's part-filled page: as the lowest row that holds it, and where
+  // no row holds it whole and no sequence outside the call has it
   auto stays = [&](uint32_t r, uint32_t old, uint32_t* last) {
     *last = p.table_in[(size_t)p.parent[r] * p.stride + (old >> p.page_shift)];
-    return p.owner[*last] == p.rows - r && !bit_of(p.bits, *last);
+    return p.owner[*last] == p.rows - r && !bit_of(p.bits, *last) && !(p.held && (p.held[*last] & CK_PAGE_SHARED));
   };
   unsigned long long asked = 0;
   for (uint32_t base = 0; base < p.rows; base += kPlanThreads) {

@@ -16,6 +16,8 @@ from . import CkError, lib
 NO_PAGE = -1
 # phase bytes of a batch's status words besides the cache stores' 6, 7 and 8
 BAD_SEQUENCE, BAD_PAGE = 1, 2
+# marks of PagePlan.fork's held: not handed out; and of a sequence that lives on outside the call
+PAGE_RESERVED, PAGE_SHARED = 1, 2
 # Beams.done of a search that failed (a wait of its kernel ran out)
 BEAM_FAILED = 255
 
@@ -247,7 +249,9 @@ class PagePlan:
 
     def fork(self, parent, lens, table, grow, held=None, stream=None):
         """ck_pages_fork: output row r takes over input row parent[r] (-1: none) and gets pages for
-        grow[r] more positions; held (uint8 [pages]) marks pages of others.  Returns (rc, Fork)."""
+        grow[r] more positions; held (uint8 [pages]): PAGE_RESERVED pages are not handed out,
+        PAGE_SHARED ones, of sequences that live on outside the call, are also copied where a row
+        has them part-filled.  Returns (rc, Fork)."""
         device, rows_in = self._begin(lens, table)
         rows = parent.numel()
         if rows > self.rows:

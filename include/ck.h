@@ -439,14 +439,20 @@ int ck_model_tables(const ck_model* m, const uint32_t** dev_exp, const int32_t**
  * position goes, belongs to one sequence: it stays with the lowest output row that holds it
  * (with none if another row holds it whole), and every other row gets a page of its own with
  * the filled positions of all layers copied.  Free are the pages in no output row and not
- * marked in dev_held (u8 [pages], nonzero: held by others; may be null); they are handed out
- * in ascending order, row after row.  The call keeps no counts: the tables say what is in use.
+ * marked in dev_held (u8 [pages]; may be null); they are handed out in ascending order, row after
+ * row.  A page marked CK_PAGE_RESERVED is not handed out, and that is all: a row of the call that
+ * has it part-filled keeps it as above, and the next call that names the same parent would keep it
+ * too.  So the pages of sequences that live on outside the call (those of the batch that goes on, those
+ * of a prompt that is kept and forked again) are marked CK_PAGE_SHARED: not handed out either, and a
+ * part-filled one stays with no row, every row gets a copy.  The call keeps no counts: the tables say what is in use.
  * Outputs: dev_table_out u32 [rows][stride] (CK_NO_PAGE behind a row's pages), dev_len_out u32
  * [rows] (the length grown), dev_status u32 [rows]: 0, or the row is empty: 3 (a parent
  * outside the input rows, a table entry outside the pool), 7 (longer than stride * page), 4
  * (the free pages ran out before this row: its request and those of the rows before it exceed
  * them).  The outputs may not overlap the inputs.  Limits: rows_in, rows <= 65536, stride <=
  * 2^17.  Errors: 4 (work_len), 9, 10. */
+#define CK_PAGE_RESERVED 1u /* dev_held: not handed out */
+#define CK_PAGE_SHARED 2u   /* dev_held (the bit): not handed out, and written by nobody else */
 int ck_pages_work(const ck_paged_cache* cache, uint32_t rows, uint32_t stride, size_t* out);
 int ck_pages_fork(const ck_paged_cache* cache, uint32_t rows_in, const uint32_t* dev_len_in,
                   const uint32_t* dev_table_in, uint32_t rows, const uint32_t* dev_parent,

@@ -922,3 +922,83 @@ def test_store_of_rows_that_fill_the_gpu(ck, heads, kv, hd, rot, half):
     assert np.array_equal(q.cpu().numpy(), qo)
     assert np.array_equal(s.cache.k.cpu().numpy(), pk) and np.array_equal(s.cache.v.cpu().numpy(), pv)
     assert status[0] is not None and status[2] is not None and s.batch.errors() == status
+
+
+def fork_beside(lens, table, parent, grow, pages, page, shared):
+    """The plain fork where `shared` pages are another sequence's: as if one more output row had each
+    of them whole."""
+    stride = max(table.shape[1], len(shared))
+    wide = np.full((len(lens) + 1, stride), -1)
+    wide[:-1, :table.shape[1]], wide[-1, :len(shared)] = table, shared
+    out, out_lens, status, copies = plain_fork(list(lens) + [len(shared) * page], wide, list(parent) + [len(lens)],
+                                               list(grow) + [0], pages, page)
+    return out[:-1, :table.shape[1]], out_lens[:-1], status[:-1], copies
+
+
+@pytest.mark.parametrize("page,hd,rows,n", [(8, 16, 3, 21), (16, 4, 1, 5), (8, 8, 40, 63), (32, 64, 2, 64)])
+def test_a_kept_prompt_forked_again_and_again(ck, page, hd, rows, n):
+    """Each fork extends every row by a position and writes it.  The prompt's pages and those of the
+    rows of the forks before are shared: nothing that a live sequence wrote is written again."""
+    rng = np.random.default_rng(n)
+    stride = -(-(n + 1) // page) + 1
+    pages = 4 * rows * stride
+    k, v = pools(rng, pages, 2, 1, page, hd)
+    cache = ck.PagedCache(cuda(k), cuda(v))
+    plan = ck.PagePlan(cache, rows, stride)
+    prompt = np.full((1, stride), -1, np.int32)
+    prompt[0, :-(-n // page)] = rng.permutation(pages)[:-(-n // page)]
+    live, words = [], {}
+    for turn in range(3):
+        shared = sorted({int(w) for t in [prompt] + live for w in t.flatten() if w >= 0})
+        held = np.where(np.isin(np.arange(pages), shared), ck.PAGE_SHARED, 0).astype(np.uint8)
+        parent, grow = np.zeros(rows, np.int32), np.ones(rows, np.int32)
+        rc, got = plan.fork(cuda(parent), cuda(np.array([n], np.int32)), cuda(prompt), cuda(grow), held=cuda(held))
+        assert rc == 0
+        want, want_lens, status, copies = fork_beside([n], prompt, parent, grow, pages, page, shared)
+        assert got.status.tolist() == status == [0] * rows and got.lens.tolist() == want_lens
+        table = got.table.cpu().numpy()
+        assert np.array_equal(table, want) and len(copies) == (rows if n % page else 0)
+        for src, dst, m in copies:
+            k[dst, :, :, :m], v[dst, :, :, :m] = k[src, :, :, :m], v[src, :, :, :m]
+        assert np.array_equal(cache.k.cpu().numpy(), k) and np.array_equal(cache.v.cpu().numpy(), v)
+        for r in range(rows):                         # position n of the row
+            at = int(table[r, n // page]), n % page
+            assert at not in words
+            words[at] = 1000 * turn + r
+            k[at[0], :, :, at[1]] = words[at]
+        cache.k.copy_(cuda(k))
+        live.append(table)
+    pool = cache.k.cpu().numpy()
+    for at, word in words.items():
+        assert (pool[at[0], :, :, at[1]] == word).all()
+
+
+def test_marks_of_held_pages(ck):
+    """A reserved page stays with its first row, a shared one (and one marked with both) with none; a
+    row whose copy finds no page is empty, and the rows behind it too."""
+    rng = np.random.default_rng(11)
+    page, pages = 8, 12
+    k, v = pools(rng, pages, 1, 2, page, 8)
+    table, lens = np.array([[3, 5, -1, -1], [9, -1, -1, -1]]), [13, 4]
+    for mark, full in ((1, False), (2, False), (3, False), (2, True)):
+        cache = ck.PagedCache(cuda(k), cuda(v))
+        held = np.zeros(pages, np.uint8)
+        held[5], held[9] = mark, 1
+        if full:
+            held[[w for w in range(pages) if w not in (3, 5, 9, 11)]] = 1
+        rc, got = ck.PagePlan(cache, 3, 4).fork(cuda(np.array([0, 0, 1], np.int32)), cuda(np.array(lens, np.int32)),
+                                                cuda(table.astype(np.int32)), cuda(np.array([1, 1, 1], np.int32)),
+                                                held=cuda(held))
+        assert rc == 0
+        if full:
+            assert got.status.tolist() == [0, 4, 4] and got.lens.tolist() == [14, 0, 0]
+            assert got.table.tolist() == [[3, 11, -1, -1], [-1] * 4, [-1] * 4]
+        else:
+            assert got.status.tolist() == [0] * 3 and got.lens.tolist() == [14, 14, 5]
+            first = [3, 5, -1, -1] if mark == 1 else [3, 0, -1, -1]
+            assert got.table.tolist() == [first, [3, 0 if mark == 1 else 1, -1, -1], [9, -1, -1, -1]]
+        pool = cache.k.cpu().numpy()
+        for row in got.table.tolist():
+            if row[1] >= 0:
+                assert np.array_equal(pool[row[1], :, :, :5], k[5, :, :, :5])
+        assert np.array_equal(pool[5], k[5])
