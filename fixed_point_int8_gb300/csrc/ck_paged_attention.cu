@@ -169,6 +169,7 @@ struct FewParams {
   uint32_t ids;          // table entries a block holds
   uint32_t sc_smem;      // the scores lie in shared memory
   uint32_t split;        // log2 of the cluster's blocks
+  uint32_t seq0, z0;     // first sequence and first group of R queries of this launch
 };
 
 __device__ __forceinline__ uint32_t smem_of(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -248,7 +249,7 @@ __global__ void __launch_bounds__(NT) k_pattn_few(const FewParams f) {
   const uint32_t hd = LPP ? 4 * LPP * NCH : p.pool.hd;
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t C = 1u << f.split, rank = blockIdx.x & (C - 1);
-  const uint32_t seq = blockIdx.x >> f.split, kvh = blockIdx.y, v0 = blockIdx.z * R;
+  const uint32_t seq = f.seq0 + (blockIdx.x >> f.split), kvh = blockIdx.y, v0 = (f.z0 + blockIdx.z) * R;
   const Sequence sq = load_sequence(p.batch, seq, p.pool.page_shift);
   if (!sq.ok) {  // (the whole cluster leaves)
     if (tid == 0 && rank == 0) note(p.batch, seq, err_key(0, p.pool.layer, CK_PAGED_BAD_SEQUENCE, 0));
@@ -552,9 +553,17 @@ __global__ void __launch_bounds__(NT) k_pattn_few(const FewParams f) {
   cluster_sync();  // no block leaves while another reads its sums
 }
 
+// Scores that do not fit shared memory take R * cap words of the scratch a block; those of every group
+// of queries at once would be gigabytes (4 GB for a chunk of 2,048 rows over 8,192 positions of 32 key
+// heads of 32).  Past kFewScratch, launches that follow one another share it, each of whole sequences
+// or, of one sequence, of some groups of queries.  Each ends with SMs idle: that chunk takes 11.8 ms in
+// two launches, 11.6 in one and 13.0 in eight of 512 MB; fewer blocks that loop took 16.6.
+constexpr uint64_t kFewScratch = 2ull << 30;
+constexpr uint64_t kFewLaunches = 64;
 struct FewPlan {
   bool use;
   uint32_t NT, R, C, z, cap, ids;
+  uint32_t seqs_each, z_each;  // sequences and groups of queries of one launch
   bool sc_smem;
   uint32_t smem;
   uint64_t work;
@@ -590,13 +599,22 @@ FewPlan plan_few(const ck_paged_cache& c, const ck_paged_batch& b, uint32_t head
   };
   w.sc_smem = smem(true) <= (w.NT == kBroad ? (uint32_t)f.optin : (uint32_t)f.optin / 2 - 2048);
   w.smem = smem(w.sc_smem);
-  w.work = w.sc_smem ? 0 : 8ull * w.cap * w.R * items * w.C;
-  w.use = w.smem <= (uint32_t)f.optin && w.z <= 65535;
+  w.seqs_each = b.seqs;
+  w.z_each = w.z;
+  if (!w.sc_smem) {
+    const uint64_t group = 8ull * w.cap * w.R * w.C * c.kv_heads;  // one sequence's R queries of every key head
+    const uint64_t groups = std::max<uint64_t>(1, kFewScratch / group);
+    w.z_each = (uint32_t)std::min<uint64_t>(w.z, groups);
+    w.seqs_each = (uint32_t)std::min<uint64_t>(b.seqs, std::max<uint64_t>(1, groups / w.z));
+    w.work = group * w.z_each * w.seqs_each;
+  }
+  const uint64_t launches = (uint64_t)((b.seqs + w.seqs_each - 1) / w.seqs_each) * ((w.z + w.z_each - 1) / w.z_each);
+  w.use = w.smem <= (uint32_t)f.optin && w.z <= 65535 && launches <= kFewLaunches;
   return w;
 }
 
 template <int LPP, int NCH, int R, int NT>
-cudaError_t launch_few(const FewParams& p, const FewPlan& w, const DeviceFacts& f, cudaStream_t s) {
+cudaError_t launch_few(FewParams p, const FewPlan& w, const DeviceFacts& f, cudaStream_t s) {
   static std::atomic<bool> ready[64];
   if (!ready[f.dev].load(std::memory_order_relaxed)) {
     const cudaError_t e =
@@ -608,7 +626,6 @@ cudaError_t launch_few(const FewParams& p, const FewPlan& w, const DeviceFacts& 
     ready[f.dev].store(true, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.a.batch.seqs * w.C, p.a.pool.kv_heads, w.z);
   cfg.blockDim = dim3(NT);
   cfg.dynamicSmemBytes = w.smem;
   cfg.stream = s;
@@ -618,7 +635,13 @@ cudaError_t launch_few(const FewParams& p, const FewPlan& w, const DeviceFacts& 
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_pattn_few<LPP, NCH, R, NT>, p);
+  for (p.seq0 = 0; p.seq0 < p.a.batch.seqs; p.seq0 += w.seqs_each)
+    for (p.z0 = 0; p.z0 < w.z; p.z0 += w.z_each) {
+      cfg.gridDim = dim3(std::min(w.seqs_each, p.a.batch.seqs - p.seq0) * w.C, p.a.pool.kv_heads, std::min(w.z_each, w.z - p.z0));
+      const cudaError_t e = cudaLaunchKernelEx(&cfg, k_pattn_few<LPP, NCH, R, NT>, p);
+      if (e != cudaSuccess) return e;
+    }
+  return cudaSuccess;
 }
 
 template <int R, int NT>
@@ -743,7 +766,7 @@ int ck_paged_attention(const ck_paged_cache* cache, uint32_t layer, const ck_pag
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (plan.few.use) {
     const FewParams fp = {p, reinterpret_cast<long long*>(work), plan.few.cap, plan.few.ids, plan.few.sc_smem,
-                          log2_of(plan.few.C)};
+                          log2_of(plan.few.C), 0, 0};
     CKP_CUDA(plan.few.NT == kBroad    ? launch_few_r<kBroad>(fp, plan.few, f, s)
              : plan.few.NT == kMiddle ? launch_few_r<kMiddle>(fp, plan.few, f, s)
                                       : launch_few_r<kNarrow>(fp, plan.few, f, s));

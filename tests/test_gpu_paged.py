@@ -1002,3 +1002,24 @@ def test_marks_of_held_pages(ck):
             if row[1] >= 0:
                 assert np.array_equal(pool[row[1], :, :, :5], k[5, :, :, :5])
         assert np.array_equal(pool[5], k[5])
+
+
+@pytest.mark.parametrize("lens,news,heads,kv,hd,page,bound", [
+    ([700], [300], 32, 8, 32, 16, 60_000),                           # groups of queries of one sequence
+    ([300, 0, 41, 555], [160, 3, 0, 161], 8, 8, 4, 8, 100_000),      # of several, ragged
+    ([int(n) for n in np.arange(200) * 7 % 45], [1] * 200, 4, 4, 16, 256, 500_000),  # whole sequences
+])
+def test_attention_in_launches_that_share_the_scratch(ck, lens, news, heads, kv, hd, page, bound):
+    """Bounds so large that the scores of all queries at once would pass two gigabytes."""
+    import torch
+    s = Setup(ck, lens, news, heads, kv, hd, page, seed=hd, lead=2, tail=1)
+    s.table = np.concatenate([s.table, np.full((len(lens), bound // page + 2), -1, np.int32)], 1)
+    s.batch = ck.PagedBatch(cuda(s.table), cuda(np.array(lens, np.int32)), cuda(s.starts), None, s.rows, max(news), bound)
+    queries = max(news) * heads // kv
+    assert 8 * bound * kv * len(lens) * (queries if queries > 1 else 1) > 2**31
+    assert 2**30 < ck.paged_attention_work(s.cache, s.batch, heads).numel() <= 2**31
+    q = (s.rng.standard_normal((s.rows, heads * hd)) * 65536).astype(np.int64)
+    out = torch.full((s.rows, heads * hd), 7, dtype=torch.int64, device="cuda")
+    rc, _ = ck.paged_attention(s.cache, 1, s.batch, cuda(q), cuda(EXP.view(np.int32)), 1 << 22, out=out)
+    assert rc == 0 and s.batch.errors() == [None] * len(lens)
+    assert np.array_equal(out.cpu().numpy(), s.attention(1, q, 1 << 22, fill=7))

@@ -240,3 +240,18 @@ def test_wrong_arguments_of_a_plan_are_refused(ck):
                 dict(clusters=None), dict(kernel=None), dict(work=None), dict(cache=cache(ck, page=7)),
                 dict(batch=batch(ck, seqs=0))):
         assert call(ck, "ck_host_attention_plan", good, **bad) == 10
+
+
+@pytest.mark.parametrize("seqs,new,length,heads,kv,hd", [(1, 2048, 8192, 32, 32, 32), (1, 4096, 8192, 32, 32, 32),
+                                                         (8, 512, 32768, 32, 8, 16), (256, 1, 32768, 32, 32, 64),
+                                                         (4096, 1, 32768, 32, 32, 32), (1, 2, 8192, 4, 4, 4)])
+def test_the_scratch_of_a_few_queries_is_bounded(ck, seqs, new, length, heads, kv, hd):
+    """Scores that do not fit shared memory: no more than 2 GB of them at once, whatever the batch."""
+    kernel, work = attention_plan(ck, seqs, new, length, heads, kv, hd, (304, 152, 76, 38))
+    assert kernel == 0 and 256 <= work <= 2**31
+
+
+def test_bounds_that_would_take_very_many_launches_go_to_single_rows(ck):
+    """2^16 sequences of up to 2^20 positions by their bounds, 70,000 rows in all."""
+    kernel, work = attention_plan(ck, 65535, 1000, 2**20 - 1, 32, 32, 32, (304, 152, 76, 38), page=256, rows=70000)
+    assert kernel == 2 and work <= 4 * 152 * 8 * 2**20
