@@ -3,10 +3,11 @@ search").  As the rest of the binding this module only marshals arguments; what 
 cannot see (a tensor's type, shape, strides and device) is checked here, and a wrong one raises
 ValueError.  Every call returns the library's error number first and enqueues its work on
 `stream` (the current one by default) without synchronising.  Arrays of u32 are int32 tensors;
-CK_NO_PAGE is -1 in them."""
+CK_NO_PAGE is -1 in them.  A number that is no u32 raises ValueError too."""
 from __future__ import annotations
 
 import ctypes
+import operator
 from typing import NamedTuple
 
 import torch
@@ -33,6 +34,14 @@ class _Cache(ctypes.Structure):
 class _Batch(ctypes.Structure):
     _fields_ = [(n, _vp) for n in ("dev_start", "dev_len", "dev_table", "dev_status")] + [
         (n, _u32) for n in ("seqs", "rows", "stride", "max_new", "max_len")]
+
+
+def _u32_of(name, value):
+    """The number as the library takes it (ctypes would cut it to its low 32 bits)."""
+    value = operator.index(value)
+    if not 0 <= value <= 0xFFFFFFFF:
+        raise ValueError(f"{name}: want a number from 0 to 2^32 - 1, got {value}")
+    return value
 
 
 def _check(name, t, dtype, shape, device):
@@ -120,6 +129,7 @@ class PagedBatch:
         if status is None:
             status = torch.full((seqs,), -1, dtype=torch.int64, device=table.device)
         _check("status", status, torch.int64, (seqs,), self.device)
+        rows, max_new, max_len = _u32_of("rows", rows), _u32_of("max_new", max_new), _u32_of("max_len", max_len)
         self.table, self.lens, self.starts, self.status, self.rows = table, lens, starts, status, rows
         self._struct = _Batch(starts.data_ptr(), lens.data_ptr(), table.data_ptr(), status.data_ptr(), seqs, rows,
                               table.shape[1], max_new, max_len)
@@ -159,7 +169,7 @@ def paged_store(cache, layer, batch, q, k, v, rope, half=False, out=None, stream
     else:
         _check("out", out, torch.int64, (rows, cols), device)
     _keep(stream, q, k, v, rope, out, *cache._tensors, *batch._tensors)
-    rc = lib().ck_paged_store(cache._c, layer, batch._c, q.data_ptr(), q_step, k.data_ptr(), k_step, v.data_ptr(),
+    rc = lib().ck_paged_store(cache._c, _u32_of("layer", layer), batch._c, q.data_ptr(), q_step, k.data_ptr(), k_step, v.data_ptr(),
                               v_step, cols // hd, rope.data_ptr(), rope.shape[0], 2 * rope.shape[1], half,
                               out.data_ptr(), _raw(stream, device))
     return rc, out
@@ -188,8 +198,8 @@ def paged_attention(cache, layer, batch, q, exp_table, inv_sqrt, out=None, work=
     else:
         _check("work", work, torch.uint8, (work.numel(),), device)
     _keep(stream, q, exp_table, out, work, *cache._tensors, *batch._tensors)
-    rc = lib().ck_paged_attention(cache._c, layer, batch._c, q.data_ptr(), step, cols // hd, exp_table.data_ptr(),
-                                  inv_sqrt, out.data_ptr(), work.data_ptr(), work.numel(), _raw(stream, device))
+    rc = lib().ck_paged_attention(cache._c, _u32_of("layer", layer), batch._c, q.data_ptr(), step, cols // hd,
+                                  exp_table.data_ptr(), _u32_of("inv_sqrt", inv_sqrt), out.data_ptr(), work.data_ptr(), work.numel(), _raw(stream, device))
     return rc, out
 
 
@@ -234,7 +244,7 @@ class PagePlan:
     Calls on one plan must follow one another on one stream (or be ordered by the caller)."""
 
     def __init__(self, cache, rows, stride):
-        self.cache, self.rows, self.stride = cache, rows, stride
+        self.cache, self.rows, self.stride = cache, _u32_of("rows", rows), _u32_of("stride", stride)
         self._work = torch.empty(_size("ck_pages_work", cache._c, rows, stride), dtype=torch.uint8,
                                  device=cache.k.device)
         self._args = self._work.data_ptr(), self._work.numel()
@@ -296,7 +306,8 @@ class BeamPlan:
     follow one another on one stream (or be ordered by the caller)."""
 
     def __init__(self, groups, beams, vocab):
-        self.groups, self.beams, self.vocab = groups, beams, vocab
+        self.groups, self.beams = _u32_of("groups", groups), _u32_of("beams", beams)
+        self.vocab = _u32_of("vocab", vocab)
         self._work = torch.empty(_size("ck_beam_work", groups, beams, vocab), dtype=torch.uint8, device="cuda")
         self._args = self._work.data_ptr(), self._work.numel()
         self._on = self._work.get_device()
@@ -318,7 +329,8 @@ class BeamPlan:
         parent, token = _empty(stream, (rows,), torch.int32, device), _empty(stream, (rows,), torch.int32, device)
         new_done = _empty(stream, (rows,), torch.uint8, device)
         rc = lib().ck_beam_select(logits.data_ptr(), step, self.groups, self.beams, self.vocab, scores.data_ptr(),
-                                  done.data_ptr(), exp_table.data_ptr(), stop_tokens, done_token,
+                                  done.data_ptr(), exp_table.data_ptr(), stop_tokens,
+                                  _u32_of("done_token", done_token),
                                   new_scores.data_ptr(), parent.data_ptr(), token.data_ptr(), new_done.data_ptr(),
                                   *self._args, _raw(stream, device))
         return rc, Beams(new_scores, parent, token, new_done)
@@ -326,7 +338,7 @@ class BeamPlan:
 
 def set_beam_wait_limit(polls: int) -> int:
     """The process's limit on a row's wait for its cluster's maxima (ck_set_beam_wait_limit)."""
-    return lib().ck_set_beam_wait_limit(polls)
+    return lib().ck_set_beam_wait_limit(_u32_of("polls", polls))
 
 
 def host_log_sum(z: int) -> int:

@@ -1023,3 +1023,21 @@ def test_attention_in_launches_that_share_the_scratch(ck, lens, news, heads, kv,
     rc, _ = ck.paged_attention(s.cache, 1, s.batch, cuda(q), cuda(EXP.view(np.int32)), 1 << 22, out=out)
     assert rc == 0 and s.batch.errors() == [None] * len(lens)
     assert np.array_equal(out.cpu().numpy(), s.attention(1, q, 1 << 22, fill=7))
+
+
+def test_numbers_that_are_no_u32_are_refused(ck):
+    s = Setup(ck, [20], [2], 2, 2, 16, 8)
+    b, exp = s.batch, cuda(EXP.view(np.int32))
+    q = cuda(np.zeros((2, 32), np.int64))
+    for rows, max_new, max_len in ((2**32 + 2, 2, 20), (2, 2**32 + 2, 20), (2, 2, 2**32 + 20), (2, 2, -1)):
+        with pytest.raises(ValueError):
+            ck.PagedBatch(b.table, b.lens, b.starts, b.status, rows, max_new, max_len)
+    for layer, inv in ((2**32, 1), (-1, 1), (0, 2**32), (0, -1)):
+        with pytest.raises(ValueError):
+            ck.paged_attention(s.cache, layer, b, q, exp, inv)
+    with pytest.raises(ValueError):
+        ck.paged_store(s.cache, 2**32, b, q, q, q, cuda(rope_of(20, 16)))
+    plan = ck.BeamPlan(1, 1, 9)
+    with pytest.raises(ValueError):
+        plan.select(cuda(np.zeros((1, 9), np.int64)), cuda(np.zeros(1, np.int64)), cuda(np.zeros(1, np.uint8)), exp,
+                    done_token=2**32)

@@ -255,3 +255,26 @@ def test_bounds_that_would_take_very_many_launches_go_to_single_rows(ck):
     """2^16 sequences of up to 2^20 positions by their bounds, 70,000 rows in all."""
     kernel, work = attention_plan(ck, 65535, 1000, 2**20 - 1, 32, 32, 32, (304, 152, 76, 38), page=256, rows=70000)
     assert kernel == 2 and work <= 4 * 152 * 8 * 2**20
+
+
+def test_numbers_past_32_bits_are_refused(ck):
+    """A number that ctypes would cut to 32 bits (here: to a good one) is an error."""
+    import torch
+
+    class Pool:
+        k = torch.zeros(1)
+        _struct = cache(ck)
+        _c = ctypes.addressof(_struct)
+
+    assert ck.PagePlan(Pool, 4, 4).rows == 4
+    for rows, stride in ((2**32 + 4, 4), (4, 2**32 + 4), (-2**32 + 4, 4), (4, -1)):
+        with pytest.raises(ValueError):
+            ck.PagePlan(Pool, rows, stride)
+    for sizes in ((2**32 + 1, 1, 5), (1, 2**32 + 1, 5), (1, 1, 2**32 + 5), (-1, 1, 5)):
+        with pytest.raises(ValueError):
+            ck.BeamPlan(*sizes)
+    with pytest.raises(ValueError):
+        ck.set_beam_wait_limit(2**32)
+    with pytest.raises(TypeError):
+        ck.PagePlan(Pool, 4.0, 4)
+    assert ck.PagePlan(Pool, np.int64(4), np.uint8(4)).stride == 4
