@@ -139,6 +139,7 @@ class Model:
     def __init__(self, handle, mem, config):
         self._h = handle
         self.mem = mem            # the torch tensor holding the device copy
+        self._home, self._made = None, ()  # the stream that load allocated it on
         self.config = config
 
     @classmethod
@@ -157,7 +158,9 @@ class Model:
             return rc, None
         cfg = Config()
         lib().ck_model_config(h, ctypes.byref(cfg))
-        return 0, cls(h, mem, {n: getattr(cfg, n) for n, _ in Config._fields_})
+        model = cls(h, mem, {n: getattr(cfg, n) for n, _ in Config._fields_})
+        model._home, model._made = torch.cuda.current_stream().cuda_stream, (mem,)
+        return 0, model
 
     def close(self):
         if self._h:

@@ -78,8 +78,26 @@ def _keep(stream, *tensors):
             t.record_stream(stream)
 
 
-def _raw(stream, device):
-    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+def _raw(device):
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
+def _allocated(*tensors):
+    """What an object allocated itself: the stream it did so on (None: not on a GPU), and the tensors."""
+    return _raw(tensors[0].get_device()) if tensors[0].is_cuda else None, tensors
+
+
+def _on(stream, device, *owners):
+    """The stream a call runs on, as the library takes it.  What the owners allocated themselves stays
+    in use there, as on a `stream` given (_keep): their caller has no tensor to record."""
+    if stream is not None:
+        return stream.cuda_stream
+    raw = _raw(device)
+    for o in owners:
+        if o._home is not None and o._home != raw:
+            for t in o._made:
+                t.record_stream(torch.cuda.current_stream(device))
+    return raw
 
 
 def _size(name, *args):
@@ -104,12 +122,15 @@ class PagedCache:
         self._struct = _Cache(k.data_ptr(), v.data_ptr(), *k.shape)
         self._c = ctypes.addressof(self._struct)
         self._tensors = k, v
+        self._home, self._made = None, ()  # (the caller's own)
 
     @classmethod
     def empty(cls, pages, layers, kv_heads, page, head_dim):
         """Pools of zeros on the current device."""
         shape = (pages, layers, kv_heads, page, head_dim)
-        return cls(*(torch.zeros(shape, dtype=torch.int32, device="cuda") for _ in range(2)))
+        cache = cls(*(torch.zeros(shape, dtype=torch.int32, device="cuda") for _ in range(2)))
+        cache._home, cache._made = _allocated(*cache._tensors)
+        return cache
 
 
 class PagedBatch:
@@ -126,8 +147,10 @@ class PagedBatch:
         seqs = table.shape[0]
         _check("lens", lens, torch.int32, (seqs,), self.device)
         _check("starts", starts, torch.int32, (seqs + 1,), self.device)
+        self._home, self._made = None, ()
         if status is None:
             status = torch.full((seqs,), -1, dtype=torch.int64, device=table.device)
+            self._home, self._made = _allocated(status)
         _check("status", status, torch.int64, (seqs,), self.device)
         rows, max_new, max_len = _u32_of("rows", rows), _u32_of("max_new", max_new), _u32_of("max_len", max_len)
         self.table, self.lens, self.starts, self.status, self.rows = table, lens, starts, status, rows
@@ -171,7 +194,7 @@ def paged_store(cache, layer, batch, q, k, v, rope, half=False, out=None, stream
     _keep(stream, q, k, v, rope, out, *cache._tensors, *batch._tensors)
     rc = lib().ck_paged_store(cache._c, _u32_of("layer", layer), batch._c, q.data_ptr(), q_step, k.data_ptr(), k_step, v.data_ptr(),
                               v_step, cols // hd, rope.data_ptr(), rope.shape[0], 2 * rope.shape[1], half,
-                              out.data_ptr(), _raw(stream, device))
+                              out.data_ptr(), _on(stream, device, cache, batch))
     return rc, out
 
 
@@ -199,7 +222,8 @@ def paged_attention(cache, layer, batch, q, exp_table, inv_sqrt, out=None, work=
         _check("work", work, torch.uint8, (work.numel(),), device)
     _keep(stream, q, exp_table, out, work, *cache._tensors, *batch._tensors)
     rc = lib().ck_paged_attention(cache._c, _u32_of("layer", layer), batch._c, q.data_ptr(), step, cols // hd,
-                                  exp_table.data_ptr(), _u32_of("inv_sqrt", inv_sqrt), out.data_ptr(), work.data_ptr(), work.numel(), _raw(stream, device))
+                                  exp_table.data_ptr(), _u32_of("inv_sqrt", inv_sqrt), out.data_ptr(), work.data_ptr(), work.numel(),
+                                  _on(stream, device, cache, batch))
     return rc, out
 
 
@@ -223,7 +247,7 @@ def turn_paged(model, cache, batch, tokens, logits=None, work=None, stream=None)
         _check("work", work, torch.uint8, (work.numel(),), device)
     _keep(stream, model.mem, tokens, logits, work, *cache._tensors, *batch._tensors)
     rc = lib().ck_turn_paged(model._h, cache._c, batch._c, tokens.data_ptr(), logits.data_ptr(), step,
-                             work.data_ptr(), work.numel(), _raw(stream, device))
+                             work.data_ptr(), work.numel(), _on(stream, device, model, cache, batch))
     return rc, logits
 
 
@@ -248,6 +272,7 @@ class PagePlan:
         self._work = torch.empty(_size("ck_pages_work", cache._c, rows, stride), dtype=torch.uint8,
                                  device=cache.k.device)
         self._args = self._work.data_ptr(), self._work.numel()
+        self._home, self._made = _allocated(self._work)
 
     def _begin(self, lens, table):
         device, rows = _device(), table.shape[0]
@@ -276,7 +301,7 @@ class PagePlan:
         rc = lib().ck_pages_fork(self.cache._c, rows_in, lens.data_ptr(), table.data_ptr(), rows, parent.data_ptr(),
                                  grow.data_ptr(), self.stride, None if held is None else held.data_ptr(),
                                  new_lens.data_ptr(), out.data_ptr(), status.data_ptr(), *self._args,
-                                 _raw(stream, device))
+                                 _on(stream, device, self, self.cache))
         return rc, Fork(out, new_lens, status)
 
     def compact(self, lens, table, stream=None):
@@ -290,7 +315,7 @@ class PagePlan:
         used = _empty(stream, (), torch.int32, device)
         rc = lib().ck_pages_compact(self.cache._c, rows, lens.data_ptr(), table.data_ptr(), self.stride,
                                     out.data_ptr(), used.data_ptr(), status.data_ptr(), *self._args,
-                                    _raw(stream, device))
+                                    _on(stream, device, self, self.cache))
         return rc, Compact(out, used, status)
 
 
@@ -310,13 +335,14 @@ class BeamPlan:
         self.vocab = _u32_of("vocab", vocab)
         self._work = torch.empty(_size("ck_beam_work", groups, beams, vocab), dtype=torch.uint8, device="cuda")
         self._args = self._work.data_ptr(), self._work.numel()
-        self._on = self._work.get_device()
+        self._device = self._work.get_device()
+        self._home, self._made = _allocated(self._work)
 
     def select(self, logits, scores, done, exp_table, stop_tokens=False, done_token=0, stream=None):
         """ck_beam_select: the next beams of every search from logits int64 [groups * beams][vocab]
         (rows may be further apart), scores int64 and done uint8.  Returns (rc, Beams)."""
         device, rows = _device(), self.groups * self.beams
-        if self._on != device:
+        if self._device != device:
             raise ValueError("the plan is not on the current CUDA device")
         step = _check_rows("logits", logits, rows, device)
         if logits.shape[1] != self.vocab:
@@ -332,7 +358,7 @@ class BeamPlan:
                                   done.data_ptr(), exp_table.data_ptr(), stop_tokens,
                                   _u32_of("done_token", done_token),
                                   new_scores.data_ptr(), parent.data_ptr(), token.data_ptr(), new_done.data_ptr(),
-                                  *self._args, _raw(stream, device))
+                                  *self._args, _on(stream, device, self))
         return rc, Beams(new_scores, parent, token, new_done)
 
 

@@ -1041,3 +1041,49 @@ def test_numbers_that_are_no_u32_are_refused(ck):
     with pytest.raises(ValueError):
         plan.select(cuda(np.zeros((1, 9), np.int64)), cuda(np.zeros(1, np.int64)), cuda(np.zeros(1, np.uint8)), exp,
                     done_token=2**32)
+
+
+def test_what_plans_and_caches_allocated_stays_in_use_on_another_current_stream(ck):
+    """The current stream is busy when the calls are enqueued; then the plan, the cache and the batch
+    (its status words too) are dropped and their memory is asked for again on the stream that they
+    were made on, before the kernels run."""
+    import torch
+    rng = np.random.default_rng(4)
+    logits, scores = rng.integers(0, 2**20, (4, 900)), np.zeros(4, np.int64)
+    dev = cuda(logits), cuda(scores), cuda(np.zeros(4, np.uint8)), cuda(EXP.view(np.int32))
+    parent, lens, grow = cuda(np.zeros(4, np.int32)), cuda(np.array([9], np.int32)), cuda(np.ones(4, np.int32))
+    table, starts = cuda(np.array([[5, 2, -1]], np.int32)), cuda(np.array([0, 1], np.int32))
+    q = cuda((rng.standard_normal((1, 16)) * 65536).astype(np.int64))
+    side = torch.cuda.Stream()
+
+    def calls():
+        plan, cache = ck.BeamPlan(1, 4, 900), ck.PagedCache.empty(12, 1, 1, 8, 16)
+        move, batch = ck.PagePlan(cache, 4, 3), ck.PagedBatch(table, lens, starts, None, 1, 1, 9)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000_000)
+            rc, beams = plan.select(*dev)
+            assert rc == 0
+            rc, fork = move.fork(parent, lens, table, grow)
+            assert rc == 0
+            rc, _ = ck.paged_store(cache, 0, batch, q, q, q, cuda(rope_of(9, 0)))
+            assert rc == 0
+            rc, out = ck.paged_attention(cache, 0, batch, q, dev[3], 1 << 22)
+            assert rc == 0
+        return beams, fork, out
+
+    for t in (torch.int32, torch.int64, torch.uint8):  # (every kernel below is loaded before the stream is busy)
+        torch.full((3,), 3, dtype=t, device="cuda")
+    calls()
+    torch.cuda.synchronize()
+    beams, fork, out = calls()
+    sizes = [1 << n for n in range(8, 18)]
+    other = [torch.full((n,), 3, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(100)]
+    torch.cuda.synchronize()
+    assert list(zip(*(t.tolist() for t in beams))) == plain_beam(logits, scores, np.zeros(4), 1, 4, 0, False)
+    assert fork.table.tolist() == [[5, 2, -1], [5, 0, -1], [5, 1, -1], [5, 3, -1]] and fork.status.tolist() == [0] * 4
+    # position 8 of nine: the positions before it hold zeros, so the value is a part of its word
+    k = np.zeros((9, 16), np.int64)
+    k[8] = q.cpu().numpy()
+    assert np.array_equal(out.cpu().numpy()[0], plain_attention(k[8], k, k, 1 << 22))
+    assert all((t == 3).all() for t in other)
