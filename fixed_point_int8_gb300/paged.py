@@ -166,8 +166,16 @@ class PagedBatch:
                 for w in self.status.tolist()]
 
 
-def _devices(cache, batch):
+def _call_device(stream):
+    """The current device, which a stream given has to be on as well."""
     device = _device()
+    if stream is not None and stream.device.index != device:
+        raise ValueError(f"stream: want one on the current CUDA device {device}, got {stream.device}")
+    return device
+
+
+def _devices(cache, batch, stream):
+    device = _call_device(stream)
     if cache.device != device or batch.device != device:
         raise ValueError("the cache and the batch are not both on the current CUDA device")
     return device
@@ -177,7 +185,7 @@ def paged_store(cache, layer, batch, q, k, v, rope, half=False, out=None, stream
     """Rotary and the checked stores of a batch's new rows (ck_paged_store).  q, k, v: int64 rows,
     which may be column ranges of one tensor; rope: int32 [positions][rot / 2][2].  Returns (rc,
     rotated queries)."""
-    device, rows, hd = _devices(cache, batch), batch.rows, cache.head_dim
+    device, rows, hd = _devices(cache, batch, stream), batch.rows, cache.head_dim
     q_step = _check_rows("q", q, rows, device)
     k_step = _check_rows("k", k, rows, device)
     v_step = _check_rows("v", v, rows, device)
@@ -200,13 +208,14 @@ def paged_store(cache, layer, batch, q, k, v, rope, half=False, out=None, stream
 
 def paged_attention_work(cache, batch, heads, stream=None):
     """Scratch for paged_attention on the stream, as large as the batch's bounds need."""
-    return _empty(stream, _size("ck_paged_attention_work", cache._c, batch._c, heads), torch.uint8, cache.device)
+    device = _devices(cache, batch, stream)
+    return _empty(stream, _size("ck_paged_attention_work", cache._c, batch._c, heads), torch.uint8, device)
 
 
 def paged_attention(cache, layer, batch, q, exp_table, inv_sqrt, out=None, work=None, stream=None):
     """Attention of a batch's new rows over their sequences' pages (ck_paged_attention).  q: int64
     rows of rotated queries; exp_table: int32 [4097].  Returns (rc, outputs)."""
-    device, rows, hd = _devices(cache, batch), batch.rows, cache.head_dim
+    device, rows, hd = _devices(cache, batch, stream), batch.rows, cache.head_dim
     step = _check_rows("q", q, rows, device)
     _check("exp_table", exp_table, torch.int32, (4097,), device)
     cols = q.shape[1]
@@ -228,11 +237,12 @@ def paged_attention(cache, layer, batch, q, exp_table, inv_sqrt, out=None, work=
 
 
 def turn_paged_work(model, cache, batch, stream=None):
-    return _empty(stream, _size("ck_turn_paged_work", model._h, cache._c, batch._c), torch.uint8, cache.device)
+    device = _devices(cache, batch, stream)
+    return _empty(stream, _size("ck_turn_paged_work", model._h, cache._c, batch._c), torch.uint8, device)
 
 
 def turn_paged(model, cache, batch, tokens, logits=None, work=None, stream=None):
-    device, seqs, vocab = _devices(cache, batch), batch.lens.shape[0], model.config["vocab"]
+    device, seqs, vocab = _devices(cache, batch, stream), batch.lens.shape[0], model.config["vocab"]
     if model.mem.get_device() != device:
         raise ValueError("the model is not on the current CUDA device")
     _check("tokens", tokens, torch.int32, (batch.rows,), device)
@@ -274,8 +284,8 @@ class PagePlan:
         self._args = self._work.data_ptr(), self._work.numel()
         self._home, self._made = _allocated(self._work)
 
-    def _begin(self, lens, table):
-        device, rows = _device(), table.shape[0]
+    def _begin(self, lens, table, stream):
+        device, rows = _call_device(stream), table.shape[0]
         if self.cache.device != device:
             raise ValueError("the cache is not on the current CUDA device")
         _check("table", table, torch.int32, (rows, self.stride), device)
@@ -287,7 +297,7 @@ class PagePlan:
         grow[r] more positions; held (uint8 [pages]): PAGE_RESERVED pages are not handed out,
         PAGE_SHARED ones, of sequences that live on outside the call, are also copied where a row
         has them part-filled.  Returns (rc, Fork)."""
-        device, rows_in = self._begin(lens, table)
+        device, rows_in = self._begin(lens, table, stream)
         rows = parent.numel()
         if rows > self.rows:
             raise ValueError(f"parent: {rows} rows, the plan has room for {self.rows}")
@@ -306,7 +316,7 @@ class PagePlan:
 
     def compact(self, lens, table, stream=None):
         """ck_pages_compact: the rows' pages move to the lowest page numbers.  Returns (rc, Compact)."""
-        device, rows = self._begin(lens, table)
+        device, rows = self._begin(lens, table, stream)
         if rows > self.rows:
             raise ValueError(f"table: {rows} rows, the plan has room for {self.rows}")
         _keep(stream, self._work, lens, table, *self.cache._tensors)
@@ -341,7 +351,7 @@ class BeamPlan:
     def select(self, logits, scores, done, exp_table, stop_tokens=False, done_token=0, stream=None):
         """ck_beam_select: the next beams of every search from logits int64 [groups * beams][vocab]
         (rows may be further apart), scores int64 and done uint8.  Returns (rc, Beams)."""
-        device, rows = _device(), self.groups * self.beams
+        device, rows = _call_device(stream), self.groups * self.beams
         if self._device != device:
             raise ValueError("the plan is not on the current CUDA device")
         step = _check_rows("logits", logits, rows, device)

@@ -278,3 +278,31 @@ def test_numbers_past_32_bits_are_refused(ck):
     with pytest.raises(TypeError):
         ck.PagePlan(Pool, 4.0, 4)
     assert ck.PagePlan(Pool, np.int64(4), np.uint8(4)).stride == 4
+
+
+def test_a_stream_of_another_device_is_refused(ck, monkeypatch):
+    """Its number on the current device could be any stream's, the default one's among them."""
+    import torch
+
+    class On:
+        cuda_stream = 0
+
+        def __init__(self, index):
+            self.device = torch.device("cuda", index)
+
+    class Here:
+        device, _c = 0, None
+
+    monkeypatch.setattr(ck.paged, "_device", lambda: 0)
+    assert ck.paged._devices(Here, Here, None) == ck.paged._devices(Here, Here, On(0)) == 0
+    for call_it in (lambda: ck.paged._devices(Here, Here, On(1)), lambda: ck.paged_attention_work(Here, Here, 1, stream=On(1)),
+                    lambda: ck.paged_attention(Here, 0, Here, None, None, 1, stream=On(1)),
+                    lambda: ck.paged_store(Here, 0, Here, None, None, None, None, stream=On(1)),
+                    lambda: ck.paged.turn_paged(None, Here, Here, None, stream=On(1)),
+                    lambda: ck.paged.turn_paged_work(None, Here, Here, stream=On(1))):
+        with pytest.raises(ValueError, match="stream"):
+            call_it()
+    there = Here()
+    there.device = 1
+    with pytest.raises(ValueError, match="current CUDA device"):
+        ck.paged_attention_work(there, Here, 1)
