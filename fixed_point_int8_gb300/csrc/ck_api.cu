@@ -1280,6 +1280,11 @@ int ck_turn_paged(ck_model* m, const ck_paged_cache* cache, const ck_paged_batch
   if (!aligned_to(dev_tokens, 4) || !aligned_to(dev_logits, 8) || !aligned_to(dev_work, 256) ||
       logits_stride < m->cfg.vocab || logits_stride >> 40)
     return CK_INVALID_ARGUMENT;
+  const uint64_t logits_bytes = 8 * ((uint64_t)(batch->seqs - 1) * logits_stride + m->cfg.vocab);
+  if (overlaps(dev_logits, logits_bytes, dev_work, work_len) || overlaps(dev_logits, logits_bytes, dev_tokens, 4ull * batch->rows) ||
+      overlaps(dev_work, work_len, dev_tokens, 4ull * batch->rows) || on_batch(dev_logits, logits_bytes, *cache, *batch) ||
+      on_batch(dev_work, work_len, *cache, *batch))
+    return CK_INVALID_ARGUMENT;
   const PrefillModel pm = prefill_model(m);
   if (work_len < paged_pass_bytes(pm, std::max(batch->rows, batch->seqs), attn)) return CK_BUFFER_TOO_SMALL;
   if (!m->pf_configured) {

@@ -530,7 +530,8 @@ int ck_paged_store(const ck_paged_cache* cache, uint32_t layer, const ck_paged_b
   const uint64_t last = batch->rows - 1, out_bytes = 8 * batch->rows * q_dim;
   if (overlaps(dev_q_out, out_bytes, dev_q, 8 * (last * q_stride + q_dim)) ||
       overlaps(dev_q_out, out_bytes, dev_k, 8 * (last * k_stride + kv_dim)) ||
-      overlaps(dev_q_out, out_bytes, dev_v, 8 * (last * v_stride + kv_dim)))
+      overlaps(dev_q_out, out_bytes, dev_v, 8 * (last * v_stride + kv_dim)) ||
+      overlaps(dev_q_out, out_bytes, dev_rope, 4ull * rope_rows * rot) || on_batch(dev_q_out, out_bytes, *cache, *batch))
     return CK_INVALID_ARGUMENT;
   StoreParams p = {};
   p.pool = pool_view(*cache, layer);

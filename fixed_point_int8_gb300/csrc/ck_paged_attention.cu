@@ -755,8 +755,12 @@ int ck_paged_attention(const ck_paged_cache* cache, uint32_t layer, const ck_pag
   if (!aligned_to(dev_q, 16) || !aligned_to(dev_out, 16) || !aligned_to(dev_exp, 4) || !aligned_to(dev_work, 256) ||
       q_stride < q_dim || (q_stride & 1) || q_stride >> 40)
     return CK_INVALID_ARGUMENT;
-  if (overlaps(dev_out, 8 * batch->rows * q_dim, dev_q, 8 * ((batch->rows - 1) * (uint64_t)q_stride + q_dim)))
-    return CK_INVALID_ARGUMENT;
+  const uint64_t q_bytes = 8 * ((batch->rows - 1) * (uint64_t)q_stride + q_dim), out_bytes = 8 * batch->rows * q_dim;
+  if (overlaps(dev_out, out_bytes, dev_work, work_len)) return CK_INVALID_ARGUMENT;
+  for (const auto& to : {std::make_pair((const void*)dev_out, out_bytes), std::make_pair((const void*)dev_work, (uint64_t)work_len)})
+    if (overlaps(to.first, to.second, dev_q, q_bytes) || overlaps(to.first, to.second, dev_exp, 4 * 4097) ||
+        on_batch(to.first, to.second, *cache, *batch))
+      return CK_INVALID_ARGUMENT;
   DeviceFacts f;
   CKP_CUDA(device_facts(&f));
   const AttentionPlan plan = attention_plan(*cache, *batch, heads, f);

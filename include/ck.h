@@ -393,7 +393,7 @@ typedef struct ck_paged_batch {
  * `layer`, the rotated queries to dev_q_out.  dev_q, dev_k, dev_v: i64 rows of heads *
  * head_dim and kv_heads * head_dim words, `stride` words from row to row (so the three parts
  * of a stacked matrix row can be given), 16-byte aligned with even strides; dev_q_out i64
- * [rows][heads * head_dim], which may not overlap the inputs.  The first `rot` elements of
+ * [rows][heads * head_dim], which may not overlap the inputs, the batch's arrays or the pools.  The first `rot` elements of
  * each head are rotated (a multiple of 4 up to head_dim, 0 for none): pairs (2j, 2j + 1), or
  * (j, j + rot / 2) with `half` set.  dev_rope: i32 [rope_rows][rot / 2][2] (cos, sin) with 24
  * fraction bits; a scaled or lengthened context is a table of scaled angles.  A position past
@@ -408,7 +408,8 @@ int ck_paged_store(const ck_paged_cache* cache, uint32_t layer, const ck_paged_b
  * (q_stride words from row to row), dev_out i64 [rows][heads * head_dim], both 16-byte
  * aligned; heads a multiple of kv_heads, head h reading key head h / (heads / kv_heads).
  * dev_exp: the exponential table u32 [4097], entry 0 = 2^30 and none larger; inv_sqrt: one
- * over the square root of the head size, 24 fraction bits.  Errors: 4 (work_len), 9, 10. */
+ * over the square root of the head size, 24 fraction bits.  dev_out and dev_work may overlap neither
+ * each other nor anything that the call reads.  Errors: 4 (work_len), 9, 10. */
 int ck_paged_attention_work(const ck_paged_cache* cache, const ck_paged_batch* batch, uint32_t heads,
                             size_t* out);
 int ck_paged_attention(const ck_paged_cache* cache, uint32_t layer, const ck_paged_batch* batch,
@@ -423,7 +424,8 @@ int ck_paged_attention(const ck_paged_cache* cache, uint32_t layer, const ck_pag
  * rows as in the batched pass, rotary, stores and attention by the two operators above.  A token
  * outside the vocabulary is phase 3 in dev_status and counts as zeros; all zeros there: a wait of
  * a contraction ran out.  The logits of a sequence with a failure are unspecified.  Nothing
- * synchronizes; the call may be captured.  Limits: rows and seqs <= 4096, max_len <= the model's
+ * synchronizes; the call may be captured.  dev_logits and dev_work may overlap neither each other
+ * nor the tokens, the batch's arrays or the pools.  Limits: rows and seqs <= 4096, max_len <= the model's
  * context.  Errors: 4 (work_len), 9, 10. */
 int ck_turn_paged_work(ck_model* m, const ck_paged_cache* cache, const ck_paged_batch* batch, size_t* out);
 int ck_turn_paged(ck_model* m, const ck_paged_cache* cache, const ck_paged_batch* batch, const uint32_t* dev_tokens,

@@ -306,3 +306,34 @@ def test_a_stream_of_another_device_is_refused(ck, monkeypatch):
     there.device = 1
     with pytest.raises(ValueError, match="current CUDA device"):
         ck.paged_attention_work(there, Here, 1)
+
+
+POOL = 8 * 2 * 2 * 16 * 32 * 4     # bytes of either pool of cache()
+
+
+def apart(ck):
+    """The batch's arrays at places of their own: 16 bytes of starts, 12 of lengths, 48 of the table, 24 of
+    status words."""
+    return batch(ck, dev_start=20 * ADDR, dev_len=21 * ADDR, dev_table=22 * ADDR, dev_status=23 * ADDR)
+
+
+@pytest.mark.parametrize("at,size", [(ADDR, POOL), (2 * ADDR, POOL), (20 * ADDR, 16), (21 * ADDR, 12), (22 * ADDR, 48),
+                                     (23 * ADDR, 24), (4 * ADDR, 6 * 128 * 8)])
+def test_outputs_on_inputs_are_refused(ck, at, size):
+    """Outputs and scratch that begin on an input's last bytes or end on its first ones."""
+    last = (at + size - 1) // 16 * 16
+    rows = 6 * 128 * 8
+    assert call(ck, "ck_paged_store", store_args(ck), batch=apart(ck), out=last) == 10
+    assert call(ck, "ck_paged_store", store_args(ck), batch=apart(ck), out=at - rows + 16) == 10
+    good = dict(batch=apart(ck), exp=24 * ADDR, work=16 * ADDR, work_len=ADDR)
+    for bad in (dict(out=last), dict(out=at - rows + 16), dict(work=(at + size - 1) // 256 * 256),
+                dict(work=at - 512, work_len=513)):
+        assert call(ck, "ck_paged_attention", attention_args(ck), **{**good, **bad}) == 10
+
+
+def test_outputs_on_tables_and_scratch_are_refused(ck):
+    assert call(ck, "ck_paged_store", store_args(ck), batch=apart(ck), out=7 * ADDR + 64 * 32 * 4 - 16) == 10
+    good = dict(batch=apart(ck), exp=24 * ADDR, work=16 * ADDR, work_len=ADDR)
+    for bad in (dict(out=24 * ADDR + 4096 * 4), dict(work=24 * ADDR + 16384), dict(out=17 * ADDR - 16),
+                dict(out=16 * ADDR - 6 * 128 * 8 + 16)):
+        assert call(ck, "ck_paged_attention", attention_args(ck), **{**good, **bad}) == 10
