@@ -193,7 +193,7 @@ def paged_store(cache, layer, batch, q, k, v, rope, half=False, out=None, stream
         raise ValueError(f"rope: want [positions][rot / 2][2], got {tuple(rope.shape)}")
     _check("rope", rope, torch.int32, rope.shape, device)
     cols, kv_cols = q.shape[1], cache.kv_heads * hd
-    if cols % hd or k.shape[1] != kv_cols or v.shape[1] != kv_cols:
+    if not hd or cols % hd or k.shape[1] != kv_cols or v.shape[1] != kv_cols:
         raise ValueError("q, k and v: columns do not match the cache's heads")
     if out is None:
         out = _empty(stream, (rows, cols), torch.int64, device)
@@ -219,7 +219,7 @@ def paged_attention(cache, layer, batch, q, exp_table, inv_sqrt, out=None, work=
     step = _check_rows("q", q, rows, device)
     _check("exp_table", exp_table, torch.int32, (4097,), device)
     cols = q.shape[1]
-    if cols == 0 or cols % (hd * cache.kv_heads):
+    if cols == 0 or hd * cache.kv_heads == 0 or cols % (hd * cache.kv_heads):
         raise ValueError("q: columns are no multiple of the cache's heads")
     if out is None:
         out = _empty(stream, (rows, cols), torch.int64, device)

@@ -1087,3 +1087,64 @@ def test_what_plans_and_caches_allocated_stays_in_use_on_another_current_stream(
     k[8] = q.cpu().numpy()
     assert np.array_equal(out.cpu().numpy()[0], plain_attention(k[8], k, k, 1 << 22))
     assert all((t == 3).all() for t in other)
+
+
+def test_a_pool_without_heads_or_elements_is_refused(ck):
+    s = Setup(ck, [20], [2], 2, 2, 16, 8)
+    q, exp = cuda(np.zeros((2, 32), np.int64)), cuda(EXP.view(np.int32))
+    for shape in ((3, 1, 2, 8, 0), (3, 1, 0, 8, 16)):
+        cache = ck.PagedCache.empty(*shape)
+        with pytest.raises(ValueError):
+            ck.paged_attention(cache, 0, s.batch, q, exp, 1)
+        with pytest.raises(ValueError):
+            ck.paged_store(cache, 0, s.batch, q, q, q, cuda(rope_of(20, 16)))
+
+
+def test_sequences_longer_than_their_tables_are_skipped(ck):
+    """Lengths within max_len that the tables have no entries for, in all three kernels and the store."""
+    import torch
+    for lens, news, heads, kv, hd, page in (([40, 33], [2, 2], 4, 2, 32, 8), ([900, 700], [70, 129], 32, 8, 64, 16)):
+        s = Setup(ck, lens, news, heads, kv, hd, page, seed=2, max_len=lens[0] + 500)
+        at = s.table.shape[1] * page
+        s.batch.lens.copy_(cuda(np.array([at + 1, lens[1]], np.int32)))
+        assert on_tiles(ck, s) == (hd == 64)
+        q = (s.rng.standard_normal((s.rows, heads * hd)) * 65536).astype(np.int64)
+        want = s.attention(1, q, 1 << 21)
+        out = torch.full((s.rows, heads * hd), 5, dtype=torch.int64, device="cuda")
+        rc, _ = ck.paged_attention(s.cache, 1, s.batch, cuda(q), cuda(EXP.view(np.int32)), 1 << 21, out=out)
+        assert rc == 0 and s.batch.errors() == [(0, 1, 1, 0), None]
+        got = out.cpu().numpy()
+        assert (got[:news[0]] == 5).all() and np.array_equal(got[news[0]:], want[news[0]:])
+        k, before = cuda(q[:, :kv * hd]), s.cache.k.clone()
+        s.batch.status.fill_(-1)
+        out.fill_(5)
+        rc, _ = ck.paged_store(s.cache, 0, s.batch, cuda(q), k, k, cuda(rope_of(at + 1, 0)), out=out)
+        assert rc == 0 and s.batch.errors() == [(0, 0, 1, 0), None]
+        assert (out[:news[0]] == 5).all() and torch.equal(out[news[0]:], cuda(q)[news[0]:])
+        mine = [int(p) for p in s.table[0] if p >= 0]
+        assert torch.equal(s.cache.k[mine], before[mine])
+    s = single_rows(ck, [400, 30], [317, 3], 16, 300_000)
+    s.batch = ck.PagedBatch(s.batch.table[:, :300_000 // 8].contiguous(), cuda(np.array([300_000, 30], np.int32)), s.batch.starts,
+                            None, s.rows, 320, 300_001)
+    s.batch.lens[0] = 300_001
+    q = (s.rng.standard_normal((s.rows, 64)) * 65536).astype(np.int64)
+    out = torch.full((s.rows, 64), 5, dtype=torch.int64, device="cuda")
+    assert ck.paged_attention_work(s.cache, s.batch, 4).numel() >= 608 * 300_000 * 8
+    rc, _ = ck.paged_attention(s.cache, 0, s.batch, cuda(q), cuda(EXP.view(np.int32)), 1 << 22, out=out)
+    assert rc == 0 and s.batch.errors() == [(0, 0, 1, 0), None]
+    assert (out[:317] == 5).all() and np.array_equal(out[317:].cpu().numpy(), s.attention(0, q, 1 << 22)[317:])
+
+
+@pytest.mark.parametrize("groups,beams,vocab", [(1, 64, 1), (3, 64, 2), (1000, 64, 3), (65536, 1, 2)])
+def test_beams_with_hardly_a_vocabulary(ck, groups, beams, vocab):
+    rng = np.random.default_rng(beams)
+    rows = groups * beams
+    logits = rng.integers(-2**17, 2**17, (rows, vocab))
+    scores, done = -rng.integers(0, 5 << 16, rows), (rng.random(rows) < 0.2).astype(np.uint8)
+    rc, got = ck.BeamPlan(groups, beams, vocab).select(cuda(logits), cuda(scores), cuda(done), cuda(EXP.view(np.int32)))
+    assert rc == 0
+    got = list(zip(*(t.tolist() for t in got)))
+    for g in sorted({0, 1 % groups, groups // 3, groups - 1}):
+        at = slice(g * beams, (g + 1) * beams)
+        want = plain_beam(logits[at], scores[at], done[at], 1, beams, 0, False)
+        assert got[at] == [(s, r + g * beams if r >= 0 else r, t, d) for s, r, t, d in want]

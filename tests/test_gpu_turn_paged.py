@@ -246,3 +246,29 @@ def test_a_cache_of_another_model_is_refused(ck, gqa, change):
     long = ck.PagedBatch(i32([[0, 1]]), i32([3]), i32([0, 3]), None, 3, 3, 513)  # past the context
     with pytest.raises(ck.CkError):
         gqa.gpu.turn_paged_work(gqa.cache(ck, 4, 8), long)
+
+
+def test_more_sequences_than_rows(ck, gqa):
+    """Seventy sequences of which two have a new token, in a pass on another current stream: the
+    classifier runs for all of them, in more columns than the layers."""
+    import torch
+    ids = [[int(t) for t in synth.prompt_ids(gqa.spec, n, run=n)] for n in (6, 9)]
+    cache = gqa.cache(ck, 70, 16)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        first = ck.PagedBatch(i32([[5], [60]]), i32([5, 8]), i32([0, 5, 13]), None, 13, 8, 8)
+        rc, _ = gqa.gpu.turn_paged(cache, first, i32(ids[0][:5] + ids[1][:8]))
+        assert rc == 0
+        lens, starts, table = [0] * 70, [0] * 71, [[-1]] * 70
+        lens[3], lens[69], table[3], table[69] = 6, 9, [5], [60]
+        starts[4:70], starts[70] = [1] * 66, 2
+        batch = ck.PagedBatch(i32(table), i32(lens), i32(starts), None, 2, 1, 16)
+        logits = torch.full((70, 512), 7, dtype=torch.int64, device="cuda")
+        rc, _ = gqa.gpu.turn_paged(cache, batch, i32([ids[0][5], ids[1][8]]), logits=logits)
+        assert rc == 0 and batch.errors() == [None] * 70 and first.errors() == [None] * 2
+    torch.cuda.synchronize()
+    for at, run in ((3, ids[0]), (69, ids[1])):
+        assert np.array_equal(logits[at].cpu().numpy(), gqa.logits(run))
+    keep = [i for i in range(70) if i not in (3, 69)]
+    assert (logits[keep] == 7).all()
