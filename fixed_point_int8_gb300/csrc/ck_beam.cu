@@ -562,15 +562,15 @@ int ck_beam_select(const int64_t* dev_logits, size_t logits_stride, uint32_t gro
   if (logits_stride < vocab || logits_stride >> 40 || done_token >= vocab || (flags & ~CK_FLAG_STOP_TOKENS))
     return CK_INVALID_ARGUMENT;
   const uint64_t rows = (uint64_t)groups * beams;
-  const void* in[] = {dev_logits, dev_scores, dev_done};
-  const uint64_t in_bytes[] = {8 * ((rows - 1) * logits_stride + vocab), 8 * rows, rows};
+  const void* in[] = {dev_logits, dev_scores, dev_done, dev_exp};
+  const uint64_t in_bytes[] = {8 * ((rows - 1) * logits_stride + vocab), 8 * rows, rows, 4 * 4097};
   const void* out[] = {dev_scores_out, dev_parent, dev_token, dev_done_out, dev_work};
   const uint64_t out_bytes[] = {8 * rows, 4 * rows, 4 * rows, rows, work_len};
   const uintptr_t out_align[] = {8, 4, 4, 1, 256};
   if (!aligned_to(dev_logits, 8) || !aligned_to(dev_scores, 8) || !aligned_to(dev_exp, 4)) return CK_INVALID_ARGUMENT;
   for (int o = 0; o < 5; ++o) {
     if (!aligned_to(out[o], out_align[o])) return CK_INVALID_ARGUMENT;
-    for (int i = 0; i < 3; ++i)
+    for (int i = 0; i < 4; ++i)
       if (overlaps(out[o], out_bytes[o], in[i], in_bytes[i])) return CK_INVALID_ARGUMENT;
     for (int i = 0; i < o; ++i)
       if (overlaps(out[o], out_bytes[o], out[i], out_bytes[i])) return CK_INVALID_ARGUMENT;

@@ -580,7 +580,7 @@ int ck_pages_fork(const ck_paged_cache* cache, uint32_t rows_in, const uint32_t*
   const void* out[] = {dev_len_out, dev_table_out, dev_status, dev_work};
   const uint64_t out_bytes[] = {4ull * rows, 4ull * rows * stride, 4ull * rows, work_len};
   for (int o = 0; o < 4; ++o) {
-    if (!aligned_to(out[o], 4)) return CK_INVALID_ARGUMENT;
+    if (!aligned_to(out[o], 4) || on_pools(out[o], out_bytes[o], *cache)) return CK_INVALID_ARGUMENT;
     for (int i = 0; i < 5; ++i) {
       if (i < 4 && !aligned_to(in[i], 4)) return CK_INVALID_ARGUMENT;
       if (overlaps(out[o], out_bytes[o], in[i], in_bytes[i])) return CK_INVALID_ARGUMENT;
@@ -630,7 +630,7 @@ int ck_pages_compact(const ck_paged_cache* cache, uint32_t rows, const uint32_t*
   const void* out[] = {dev_used, dev_table_out, dev_status, dev_work};
   const uint64_t out_bytes[] = {4, 4ull * rows * stride, 4ull * rows, work_len};
   for (int o = 0; o < 4; ++o) {
-    if (!aligned_to(out[o], 4)) return CK_INVALID_ARGUMENT;
+    if (!aligned_to(out[o], 4) || on_pools(out[o], out_bytes[o], *cache)) return CK_INVALID_ARGUMENT;
     for (int i = 0; i < 2; ++i)
       if (!aligned_to(in[i], 4) || overlaps(out[o], out_bytes[o], in[i], in_bytes[i])) return CK_INVALID_ARGUMENT;
     for (int i = 0; i < o; ++i)

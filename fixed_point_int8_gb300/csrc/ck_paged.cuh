@@ -44,11 +44,14 @@ inline bool batch_ok(const ck_paged_batch* b) {
          aligned_to(b->dev_status, 8);
 }
 
-// Whether a call's output (or scratch) of n bytes lies on the pools or the batch's arrays.
-inline bool on_batch(const void* p, uint64_t n, const ck_paged_cache& c, const ck_paged_batch& b) {
+// Whether a call's output (or scratch) of n bytes lies on the pools, or on them or the batch's arrays.
+inline bool on_pools(const void* p, uint64_t n, const ck_paged_cache& c) {
   const uint64_t page = 4ull * c.layers * c.kv_heads * c.page * c.head_dim;  // at most 2^41 bytes
   const uint64_t pool = std::min<uint64_t>(c.pages, (1ull << 62) / page) * page;
-  return overlaps(p, n, c.dev_k, pool) || overlaps(p, n, c.dev_v, pool) || overlaps(p, n, b.dev_start, 4ull * (b.seqs + 1)) ||
+  return overlaps(p, n, c.dev_k, pool) || overlaps(p, n, c.dev_v, pool);
+}
+inline bool on_batch(const void* p, uint64_t n, const ck_paged_cache& c, const ck_paged_batch& b) {
+  return on_pools(p, n, c) || overlaps(p, n, b.dev_start, 4ull * (b.seqs + 1)) ||
          overlaps(p, n, b.dev_len, 4ull * b.seqs) || overlaps(p, n, b.dev_table, 4ull * b.seqs * b.stride) ||
          overlaps(p, n, b.dev_status, 8ull * b.seqs);
 }

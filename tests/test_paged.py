@@ -337,3 +337,21 @@ def test_outputs_on_tables_and_scratch_are_refused(ck):
     for bad in (dict(out=24 * ADDR + 4096 * 4), dict(work=24 * ADDR + 16384), dict(out=17 * ADDR - 16),
                 dict(out=16 * ADDR - 6 * 128 * 8 + 16)):
         assert call(ck, "ck_paged_attention", attention_args(ck), **{**good, **bad}) == 10
+
+
+def test_tables_on_pools_and_selections_on_the_exponentials_are_refused(ck):
+    for at in (ADDR, 2 * ADDR):
+        for place in (at + POOL - 4, at - 12):
+            # (the inputs elsewhere; outputs of 16 bytes and more)
+            moved = dict(len_in=30 * ADDR, table_in=31 * ADDR)
+            for name in ("len_out", "table_out", "status"):
+                assert call(ck, "ck_pages_fork", fork_args(ck), **{**moved, name: place}) == 10
+            moved = dict(len=30 * ADDR, table_in=31 * ADDR)
+            for name in ("table_out", "status"):
+                assert call(ck, "ck_pages_compact", compact_args(ck), **{**moved, name: place}) == 10
+        assert call(ck, "ck_pages_compact", compact_args(ck), len=30 * ADDR, table_in=31 * ADDR, used=at + 40) == 10
+        work = dict(work=at + POOL - 256)
+        assert call(ck, "ck_pages_fork", fork_args(ck), len_in=30 * ADDR, table_in=31 * ADDR, **work) == 10
+        assert call(ck, "ck_pages_compact", compact_args(ck), len=30 * ADDR, table_in=31 * ADDR, **work) == 10
+    for name in ("scores_out", "parent", "token", "done_out", "work"):
+        assert call(ck, "ck_beam_select", beam_args(ck), **{name: 4 * ADDR + 16384}) == 10
