@@ -32,8 +32,9 @@ __device__ __forceinline__ void load2(const int64_t* p, int64_t& a, int64_t& b) 
 // layout two pairs (j, j + rot / 2) and (j + 1, j + 1 + rot / 2), otherwise four in a row.  A
 // thread takes unit after unit, gridDim.y blocks' threads apart, the next one's words under way:
 // one block a row where rows fill the GPU (looking up a row's sequence and page for every 256
-// units took 29.5 us for 1,600 rows of 6,144 elements, once a row 27.6), a unit a thread where
-// they do not.  HBM bounds it.
+// units took 29.5 us for 1,600 rows of 6,144 elements, once a row 26.2), a unit a thread where
+// they do not.  The instructions bound it (over 200 a unit with a turned pair's 64-bit products,
+// checks and addresses: 63 % of the issue slots), with half of the warps resident at 58 registers.
 __global__ void __launch_bounds__(kStoreThreads) k_paged_store(const StoreParams p) {
   const uint32_t row = blockIdx.x, hd = p.pool.hd;
   const uint32_t shift = 31 - __clz((int)hd) - 2, kvh = p.pool.kv_heads;  // log2 of a head's units

@@ -30,7 +30,7 @@ __device__ __forceinline__ uint32_t exponential(const uint32_t* tab, unsigned lo
 // One (row, head) at a time a block, whatever the values and the lengths: the products are
 // 64-bit, the scores of the row lie in the block's part of the scratch.  Every row reads its
 // keys and values again, and 64-bit products bound it: one token over 8,191 positions of 32 heads
-// takes 883 us, 256 rows over 7,936 take 12.9 ms (the other kernels: 28.8 and 357 us).
+// takes 883 us, 256 rows over 7,936 take 12.9 ms (the other kernels: 28.9 and 358 us).
 __global__ void __launch_bounds__(kRowsThreads) k_pattn_rows(const RowsParams f) {
   const PAttnParams& p = f.a;
   if (f.away && *f.any == 0) return;
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kRowsThreads) k_pattn_rows(const RowsParams f)
 // 6,000 with eight).  Keys and then values stream through a ring of asynchronous copies, kBatch positions a
 // lane group each; a lane copies the words that it uses itself, so nothing waits on another
 // lane, and the values are on their way while the exponentials are formed.  One token over 8,191
-// positions of 32 heads: 134 MB in 28.8 us (4.7 TB/s); 64 runs of 65 to 191: 30.4 us, 20 of them
+// positions of 32 heads: 134 MB in 28.9 us (4.6 TB/s); 64 runs of 65 to 191: 30.1 us, 20 of them
 // without any load.
 constexpr uint32_t kMaxCluster = 16;
 constexpr int kNarrow = 64, kMiddle = 128, kBroad = 256;  // threads of a block

@@ -10,7 +10,8 @@
 //   values: a probability P (24 fraction bits) has the unsigned digits p0, p1, p2, and the P of
 //     a row add up to at most 2^24, so sum p1 <= 2^16 and sum p2 <= 2^8.  Over 256 positions the
 //     accumulator of weight 2^0 stays below 255 * 128 * 256, that of 2^8 below twice that (just
-//     under 2^24), that of 2^16 below 255 * 128 * 256 + 128 * 2^16 + 2^15 (under 2^24), and
+//     under 2^24), that of 2^16 at most 255 * 128 * 256 + 128 * 2^16 + 2^15 = 2^24, which f32 holds
+//     (and is below: the P add up to 2^24, so sum p1 <= 2^16 - 255 where sum p0 = 255 * 256), and
 //     those of 2^24 and 2^32 together, in units of 2^24, below 2^23 + 2^15: they share one.  The
 //     planes carry powers of two (2^-12, 2^-4, 2^4) so that the products come out aligned.
 //     After 256 positions the four accumulators move into 64-bit integers.
@@ -21,8 +22,8 @@
 //
 // The instructions around the products bound it (about 70 a score, a third of the issue slots in
 // phases that wait for one another), and the scratch's traffic where it is larger than L2: 256 rows
-// over 7,936 positions of 32 heads of 64 take 357 us, chunks of 201 and 151 rows over 2,047 and 777
-// of 32 heads of 128 take 249.  Twice the warps with 64 registers a thread were slower (447 against
+// over 7,936 positions of 32 heads of 64 take 358 us, chunks of 201 and 151 rows over 2,047 and 777
+// of 32 heads of 128 take 251.  Twice the warps with 64 registers a thread were slower (447 against
 // 388 us, 276 against 255 then), and so were 16-bit places in the table in the scratch for the
 // exponentials (346 against 338, 243 against 234 then).  A thread owns a row (its lane of tensor
 // memory), so maxima and sums need no exchange inside a warp.  A cluster splits a tile's positions,

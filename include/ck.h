@@ -408,7 +408,11 @@ int ck_paged_store(const ck_paged_cache* cache, uint32_t layer, const ck_paged_b
  * (q_stride words from row to row), dev_out i64 [rows][heads * head_dim], both 16-byte
  * aligned; heads a multiple of kv_heads, head h reading key head h / (heads / kv_heads).
  * dev_exp: the exponential table u32 [4097], entry 0 = 2^30 and none larger; inv_sqrt: one
- * over the square root of the head size, 24 fraction bits.  dev_out and dev_work may overlap neither
+ * over the square root of the head size, 24 fraction bits.  Chunks of new tokens with heads of 64 and
+ * 128 run on tensor cores 128 queries of a key head at a time, where the queries and all the words
+ * they meet lie within -128 * 65793 .. 127 * 65793 (-128.5 to 127.49 in value).  One word beyond takes
+ * its 128 queries through a kernel for all values, with the same bits in some 36 times the time.
+ * dev_out and dev_work may overlap neither
  * each other nor anything that the call reads.  Errors: 4 (work_len), 9, 10. */
 int ck_paged_attention_work(const ck_paged_cache* cache, const ck_paged_batch* batch, uint32_t heads,
                             size_t* out);
