@@ -90,17 +90,25 @@ def lib() -> ctypes.CDLL:
                                ctypes.c_int),
             "ck_paged_attention_work": ([vp, vp, u32, vp], ctypes.c_int),
             "ck_paged_attention": ([vp, u32, vp, vp, sz, u32, vp, u32, vp, vp, sz, vp], ctypes.c_int),
+            "ck_paged_window_attention_work": ([vp, vp, u32, vp, vp], ctypes.c_int),
+            "ck_paged_window_attention": ([vp, u32, vp, vp, sz, u32, vp, vp, u32, vp, vp, sz, vp], ctypes.c_int),
             "ck_pages_work": ([vp, u32, u32, vp], ctypes.c_int),
             "ck_pages_fork": ([vp, u32, vp, vp, u32, vp, vp, u32, vp, vp, vp, vp, vp, sz, vp], ctypes.c_int),
             "ck_pages_compact": ([vp, u32, vp, vp, u32, vp, vp, vp, vp, sz, vp], ctypes.c_int),
+            "ck_pages_advance": ([vp, u32, vp, vp, vp, u32, vp, vp, u32, vp, vp, vp, vp, vp, vp, vp, sz, vp],
+                                 ctypes.c_int),
+            "ck_sample": ([vp, sz, u32, u32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp], ctypes.c_int),
             "ck_beam_work": ([u32, u32, u32, vp], ctypes.c_int),
             "ck_beam_select": ([vp, sz, u32, u32, u32, vp, vp, vp, u32, u32, vp, vp, vp, vp, vp, sz, vp],
                                ctypes.c_int),
             "ck_set_beam_wait_limit": ([u32], ctypes.c_int),
             "ck_host_log_sum": ([u64], i64),
+            "ck_host_sample_place": ([u32, u32], u32),
             "ck_host_attention_plan": ([vp, vp, u32, u32, u32, vp, vp, vp], ctypes.c_int),
             "ck_turn_paged_work": ([vp, vp, vp, vp], ctypes.c_int),
             "ck_turn_paged": ([vp, vp, vp, vp, vp, sz, vp, sz, vp], ctypes.c_int),
+            "ck_turn_paged_window_work": ([vp, vp, vp, vp, vp], ctypes.c_int),
+            "ck_turn_paged_window": ([vp, vp, vp, vp, vp, vp, sz, vp, sz, vp], ctypes.c_int),
             "ck_model_tables": ([vp, vp, vp, vp], ctypes.c_int),
             "ck_version": ([], ctypes.c_char_p),
         }
@@ -265,16 +273,17 @@ class Model:
         rc = lib().ck_turn_noalloc(self._h, _ptr(state), state.numel(), _stream(stream), ctypes.byref(res))
         return rc, res.as_dict()
 
-    def turn_paged(self, cache, batch, tokens, logits=None, work=None, stream=None):
-        """A paged batch's new rows through the layers (ck_turn_paged): tokens int32 [rows].
-        Returns (rc, logits int64 [seqs][vocab] of each sequence's last row)."""
+    def turn_paged(self, cache, batch, tokens, logits=None, work=None, stream=None, window=None):
+        """A paged batch's new rows through the layers (ck_turn_paged): tokens int32 [rows]; window a
+        Window for all layers, or a list of one for each (ck_turn_paged_window).  Returns (rc, logits
+        int64 [seqs][vocab] of each sequence's last row)."""
         from . import paged
-        return paged.turn_paged(self, cache, batch, tokens, logits, work, stream)
+        return paged.turn_paged(self, cache, batch, tokens, logits, work, stream, window)
 
-    def turn_paged_work(self, cache, batch, stream=None):
-        """Scratch for turn_paged, as large as the batch's bounds need."""
+    def turn_paged_work(self, cache, batch, stream=None, window=None):
+        """Scratch for turn_paged, as large as the batch's bounds and the windows need."""
         from . import paged
-        return paged.turn_paged_work(self, cache, batch, stream)
+        return paged.turn_paged_work(self, cache, batch, stream, window)
 
     def exp_table(self):
         """The exponential table in device memory, int32 [4097] (a view of the model's memory)."""
@@ -390,10 +399,10 @@ def version() -> str:
     return lib().ck_version().decode()
 
 
-# The paged cache and beam search, loaded at their first use (they import torch).
+# The paged cache, beam search and sampling, loaded at their first use (they import torch).
 _PAGED = ("NO_PAGE", "BAD_SEQUENCE", "BAD_PAGE", "PAGE_RESERVED", "PAGE_SHARED", "BEAM_FAILED", "PagedCache", "PagedBatch",
           "PagePlan", "BeamPlan", "paged_store", "paged_attention_work", "paged_attention", "set_beam_wait_limit",
-          "host_log_sum")
+          "host_log_sum", "NO_TOKEN", "Window", "sample", "host_sample_place")
 
 
 def __getattr__(name):

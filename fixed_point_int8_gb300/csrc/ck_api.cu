@@ -1254,28 +1254,44 @@ int ck_turn_batch(ck_model* m, void* const* dev_states, const size_t* lens, uint
   return first;
 }
 
-// What both paged calls check; *attn: the attention's scratch.
-static int paged_pass_args(ck_model* m, const ck_paged_cache* cache, const ck_paged_batch* batch, size_t* attn) {
+// What the paged calls check; *attn: the attention's scratch, the largest of any layer's (equal
+// windows follow one another).
+static int paged_pass_args(ck_model* m, const ck_paged_cache* cache, const ck_paged_batch* batch,
+                           const ck_window* windows, size_t* attn) {
   if (!m || !cache_ok(cache) || !batch_sizes_ok(batch)) return CK_INVALID_ARGUMENT;
   if (cache->layers != m->cfg.layers || cache->kv_heads != m->cfg.kv_heads || cache->head_dim != m->head_dim ||
       batch->rows > kMaxPrefillChunk || batch->seqs > kMaxPrefillChunk || batch->max_len > m->cfg.context)
     return CK_INVALID_ARGUMENT;
   if (!prefill_supported(prefill_model(m), 1, (size_t)m->smem_optin)) return CK_INVALID_ARGUMENT;
-  return ck_paged_attention_work(cache, batch, m->cfg.heads, attn);
+  *attn = 0;
+  for (uint32_t l = 0; l < (windows ? m->cfg.layers : 1); ++l) {
+    const ck_window* w = windows ? windows + l : nullptr;
+    if (l && w->sinks == w[-1].sinks && w->window == w[-1].window) continue;
+    size_t one;
+    if (const int rc = ck_paged_window_attention_work(cache, batch, m->cfg.heads, w, &one)) return rc;
+    *attn = std::max(*attn, one);
+  }
+  return CK_OK;
 }
 
-int ck_turn_paged_work(ck_model* m, const ck_paged_cache* cache, const ck_paged_batch* batch, size_t* out) {
+int ck_turn_paged_window_work(ck_model* m, const ck_paged_cache* cache, const ck_paged_batch* batch,
+                              const ck_window* windows, size_t* out) {
   size_t attn;
   if (!out) return CK_INVALID_ARGUMENT;
-  if (const int rc = paged_pass_args(m, cache, batch, &attn)) return rc;
+  if (const int rc = paged_pass_args(m, cache, batch, windows, &attn)) return rc;
   *out = paged_pass_bytes(prefill_model(m), std::max(batch->rows, batch->seqs), attn);
   return CK_OK;
 }
 
-int ck_turn_paged(ck_model* m, const ck_paged_cache* cache, const ck_paged_batch* batch, const uint32_t* dev_tokens,
-                  int64_t* dev_logits, size_t logits_stride, void* dev_work, size_t work_len, void* stream) {
+int ck_turn_paged_work(ck_model* m, const ck_paged_cache* cache, const ck_paged_batch* batch, size_t* out) {
+  return ck_turn_paged_window_work(m, cache, batch, nullptr, out);
+}
+
+int ck_turn_paged_window(ck_model* m, const ck_paged_cache* cache, const ck_paged_batch* batch,
+                         const ck_window* windows, const uint32_t* dev_tokens, int64_t* dev_logits,
+                         size_t logits_stride, void* dev_work, size_t work_len, void* stream) {
   size_t attn;
-  if (const int rc = paged_pass_args(m, cache, batch, &attn)) return rc;
+  if (const int rc = paged_pass_args(m, cache, batch, windows, &attn)) return rc;
   if (!pools_ok(cache) || !batch_ok(batch) || !dev_tokens || !dev_logits || !dev_work) return CK_INVALID_ARGUMENT;
   if (!aligned_to(dev_tokens, 4) || !aligned_to(dev_logits, 8) || !aligned_to(dev_work, 256) ||
       logits_stride < m->cfg.vocab || logits_stride >> 40)
@@ -1291,9 +1307,15 @@ int ck_turn_paged(ck_model* m, const ck_paged_cache* cache, const ck_paged_batch
     CK_CUDA(configure_prefill((size_t)m->smem_optin));
     m->pf_configured = true;
   }
-  CK_CUDA(enqueue_paged_pass(pm, cache, batch, dev_tokens, dev_logits, logits_stride, attn,
+  CK_CUDA(enqueue_paged_pass(pm, cache, batch, windows, dev_tokens, dev_logits, logits_stride, attn,
                              static_cast<uint8_t*>(dev_work), S(stream)));
   return CK_OK;
+}
+
+int ck_turn_paged(ck_model* m, const ck_paged_cache* cache, const ck_paged_batch* batch, const uint32_t* dev_tokens,
+                  int64_t* dev_logits, size_t logits_stride, void* dev_work, size_t work_len, void* stream) {
+  return ck_turn_paged_window(m, cache, batch, nullptr, dev_tokens, dev_logits, logits_stride, dev_work, work_len,
+                              stream);
 }
 
 int ck_model_tables(const ck_model* m, const uint32_t** dev_exp, const int32_t** dev_rope, uint32_t* inv_sqrt) {

@@ -1206,6 +1206,7 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
 struct PagedPass {
   const ck_paged_cache* cache;
   const ck_paged_batch* batch;
+  const ck_window* windows;  // a layer's, or null
   const uint32_t* tokens;
   int64_t* qkv;
   uint8_t* attn_work;
@@ -1319,8 +1320,9 @@ cudaError_t enqueue_rows(const PrefillModel& m, const uint8_t* gate, const WorkL
       int rc = ck_paged_store(paged->cache, l, paged->batch, paged->qkv, pq.rows, paged->qkv + q_dim, pq.rows,
                               paged->qkv + q_dim + kv_dim, pq.rows, c.heads, m.rope, paged->rope_rows, m.head_dim, 0, Q, s);
       if (rc == CK_OK)
-        rc = ck_paged_attention(paged->cache, l, paged->batch, Q, c.dim, c.heads, m.exp_tab, m.inv_sqrt, O,
-                                paged->attn_work, paged->attn_len, s);
+        rc = ck_paged_window_attention(paged->cache, l, paged->batch, Q, c.dim, c.heads,
+                                       paged->windows ? paged->windows + l : nullptr, m.exp_tab, m.inv_sqrt, O,
+                                       paged->attn_work, paged->attn_len, s);
       if (rc != CK_OK) return cudaErrorUnknown;
       const uint64_t words = (uint64_t)P * c.dim;
       k_magnitudes<<<(uint32_t)std::min<uint64_t>((words + 4 * kRowThreads - 1) / (4 * kRowThreads), 1024), kRowThreads, 0, s>>>(
@@ -1443,10 +1445,10 @@ size_t paged_pass_bytes(const PrefillModel& m, uint32_t cap, size_t attn_bytes) 
 }
 
 cudaError_t enqueue_paged_pass(const PrefillModel& m, const ck_paged_cache* cache, const ck_paged_batch* batch,
-                               const uint32_t* tokens, int64_t* logits, size_t logits_stride, size_t attn_bytes,
+                               const ck_window* windows, const uint32_t* tokens, int64_t* logits, size_t logits_stride, size_t attn_bytes,
                                uint8_t* work, cudaStream_t s) {
   const PagedLayout l = paged_layout(m, std::max(batch->rows, batch->seqs), attn_bytes);
-  const PagedPass pass = {cache, batch, tokens, reinterpret_cast<int64_t*>(work + l.qkv), work + l.attn, attn_bytes,
+  const PagedPass pass = {cache, batch, windows, tokens, reinterpret_cast<int64_t*>(work + l.qkv), work + l.attn, attn_bytes,
                           m.cfg.context, logits, logits_stride};
   // rows of no sequence are not written by the attention
   cudaError_t e = cudaMemsetAsync(work + l.w.O, 0, 8ull * batch->rows * m.cfg.dim, s);

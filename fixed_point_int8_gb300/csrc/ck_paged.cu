@@ -451,6 +451,147 @@ __global__ void __launch_bounds__(kPlanThreads) k_compact_plan(const PagesParams
   }
 }
 
+// Between two passes: sequences give pages back, get pages for their new positions, and the rows
+// of the next pass their places.
+struct AdvanceParams {
+  const uint32_t* len_in;
+  const uint32_t* table_in;
+  const uint32_t* ask;
+  const uint8_t* held;
+  uint32_t* len_out;
+  uint32_t* table_out;
+  uint32_t* start;
+  int64_t* slot;
+  uint32_t* position;
+  uint32_t* status;
+  uint32_t seqs, stride, pages, page_shift, rows, sinks, window;
+  uint32_t* bits;             // pages that are not free
+  uint32_t* list;             // free pages
+  unsigned long long* before; // of each sequence the pages that those before it ask for
+};
+
+__device__ __forceinline__ uint32_t pages_of(const AdvanceParams& p, uint32_t len) {
+  return (len + (1u << p.page_shift) - 1) >> p.page_shift;
+}
+// Longest sequence a table row holds.
+__device__ __forceinline__ uint32_t longest(const AdvanceParams& p) {
+  return (uint32_t)min((unsigned long long)p.stride << p.page_shift, (unsigned long long)kMaxPositions);
+}
+
+// First step (a warp a sequence): checks it, takes over and marks the pages that its next position
+// or a later one sees.
+__device__ __forceinline__ void advance_mark(const AdvanceParams& p, uint32_t s, uint32_t lane) {
+  const uint32_t len = p.len_in[s];
+  uint32_t status = 0;
+  if (len > longest(p))
+    status = CK_INVALID_STATE;
+  else if ((unsigned long long)len + p.ask[s] > longest(p))
+    status = CK_CONTEXT_EXCEEDED;
+  const uint32_t have = status == CK_INVALID_STATE ? 0 : pages_of(p, len);
+  auto keeps = [&](uint32_t i) {
+    return i < have && ((unsigned long long)i << p.page_shift < p.sinks ||
+                        ((unsigned long long)(i + 1) << p.page_shift) + p.window > (unsigned long long)len + 1);
+  };
+  const uint32_t* from = p.table_in + (size_t)s * p.stride;
+  bool bad = false;
+  for (uint32_t i = lane; i < have; i += 32) bad |= keeps(i) && from[i] >= p.pages;
+  if (__any_sync(0xffffffffu, bad)) status = CK_INVALID_STATE;
+  uint32_t* to = p.table_out + (size_t)s * p.stride;
+  for (uint32_t i = lane; i < p.stride; i += 32) {
+    const uint32_t id = status != CK_INVALID_STATE && keeps(i) ? from[i] : CK_NO_PAGE;
+    to[i] = id;
+    if (id != CK_NO_PAGE) atomicOr(p.bits + (id >> 5), 1u << (id & 31));
+  }
+  if (lane == 0) p.status[s] = status;
+}
+// and the pages held outside the call (a warp 32 of them).
+__device__ __forceinline__ void advance_held(const AdvanceParams& p, uint32_t word, uint32_t lane) {
+  const uint32_t i = word * 32 + lane;
+  const uint32_t held = __ballot_sync(0xffffffffu, i < p.pages && p.held[i] != 0);
+  if (lane == 0 && held) atomicOr(p.bits + word, held);
+}
+
+// Second step (one block): the free pages in ascending order, as many as are asked for, which
+// sequences are served, and where their rows start.
+__device__ __forceinline__ void advance_plan(const AdvanceParams& p, unsigned long long* warp_sum) {
+  const uint32_t tid = threadIdx.x, words = (p.pages + 31) / 32;
+  auto need_of = [&](uint32_t s) { return pages_of(p, p.len_in[s] + p.ask[s]) - pages_of(p, p.len_in[s]); };
+  unsigned long long asked = 0, total;
+  for (uint32_t base = 0; base < p.seqs; base += kPlanThreads) {
+    const uint32_t s = base + tid;
+    const unsigned long long need = s < p.seqs && p.status[s] == 0 ? need_of(s) : 0;
+    const unsigned long long end = asked + block_scan(need, warp_sum, &total);
+    if (s < p.seqs) p.before[s] = end - need;
+    asked += total;
+  }
+  unsigned long long found = 0;
+  for (uint32_t base = 0; base < words && found < asked; base += kPlanThreads) {
+    const uint32_t w = base + tid;
+    uint32_t free = w < words ? ~p.bits[w] : 0;
+    if (w == words - 1 && (p.pages & 31)) free &= (1u << (p.pages & 31)) - 1;
+    unsigned long long at = found + block_scan(__popc(free), warp_sum, &total) - __popc(free);
+    for (; free && at < asked; free &= free - 1) p.list[at++] = w * 32 + __ffs((int)free) - 1;
+    found += total;
+  }
+  unsigned long long asked_rows = 0;
+  uint32_t rows = 0;
+  for (uint32_t base = 0; base < p.seqs; base += kPlanThreads) {
+    const uint32_t s = base + tid;
+    const bool fine = s < p.seqs && p.status[s] == 0;
+    const uint32_t ask = fine ? p.ask[s] : 0, need = fine ? need_of(s) : 0;
+    const unsigned long long end = asked_rows + block_scan(ask, warp_sum, &total);
+    asked_rows += total;
+    const bool served = fine && (need == 0 || p.before[s] + need <= found) && (ask == 0 || end <= p.rows);
+    const uint32_t mine = served ? ask : 0;
+    const uint32_t last = rows + (uint32_t)block_scan(mine, warp_sum, &total);
+    if (s < p.seqs) {
+      p.start[s] = last - mine;
+      if (fine && !served) p.status[s] = CK_BUFFER_TOO_SMALL;
+    }
+    rows += (uint32_t)total;
+  }
+  if (tid == 0) p.start[p.seqs] = rows;
+}
+
+// Third step (a warp a sequence): its new pages and its rows; and the rows behind the last.
+__device__ __forceinline__ void advance_fill(const AdvanceParams& p, uint32_t s, uint32_t lane) {
+  const uint32_t status = p.status[s], len = p.len_in[s], ask = status ? 0 : p.ask[s];
+  if (lane == 0) p.len_out[s] = status == CK_INVALID_STATE ? 0 : len + ask;
+  if (ask == 0) return;
+  const uint32_t have = pages_of(p, len), need = pages_of(p, len + ask) - have, start = p.start[s];
+  const uint32_t* fresh = p.list + (need ? p.before[s] : 0);
+  uint32_t* table = p.table_out + (size_t)s * p.stride;
+  for (uint32_t i = lane; i < need; i += 32) table[have + i] = fresh[i];
+  const uint32_t mask = (1u << p.page_shift) - 1;
+  for (uint32_t j = lane; j < ask; j += 32) {
+    const uint32_t pos = len + j, i = pos >> p.page_shift, id = i < have ? table[i] : fresh[i - have];
+    p.slot[start + j] = ((int64_t)id << p.page_shift) + (pos & mask);
+    p.position[start + j] = pos;
+  }
+}
+__device__ __forceinline__ void advance_rest(const AdvanceParams& p, uint32_t at, uint32_t step) {
+  for (uint32_t r = p.start[p.seqs] + at; r < p.rows; r += step) {
+    p.slot[r] = -1;
+    p.position[r] = CK_NO_PAGE;
+  }
+}
+
+__global__ void __launch_bounds__(kTableThreads) k_advance_mark(const AdvanceParams p) {
+  const uint32_t warps = gridDim.x * (kTableThreads / 32), lane = threadIdx.x & 31;
+  const uint32_t w = blockIdx.x * (kTableThreads / 32) + threadIdx.x / 32;
+  for (uint32_t s = w; s < p.seqs; s += warps) advance_mark(p, s, lane);
+  for (uint32_t i = w; p.held && i < (p.pages + 31) / 32; i += warps) advance_held(p, i, lane);
+}
+__global__ void __launch_bounds__(kPlanThreads) k_advance_plan(const AdvanceParams p) {
+  __shared__ unsigned long long warp_sum[kPlanThreads / 32];
+  advance_plan(p, warp_sum);
+}
+__global__ void __launch_bounds__(kTableThreads) k_advance_fill(const AdvanceParams p) {
+  const uint32_t s = blockIdx.x * (kTableThreads / 32) + threadIdx.x / 32;
+  if (s < p.seqs) advance_fill(p, s, threadIdx.x & 31);
+  advance_rest(p, blockIdx.x * kTableThreads + threadIdx.x, gridDim.x * kTableThreads);
+}
+
 int pages_args(const ck_paged_cache* cache, uint32_t rows, uint32_t stride, void* work, size_t work_len,
                PagesLayout* w) {
   if (!pools_ok(cache) || !work || !aligned_to(work, 256)) return CK_INVALID_ARGUMENT;
@@ -662,6 +803,62 @@ int ck_pages_compact(const ck_paged_cache* cache, uint32_t rows, const uint32_t*
   }
   CKP_CUDA(cudaGetLastError());
   return run_copies(cache, p, s);
+}
+
+int ck_pages_advance(const ck_paged_cache* cache, uint32_t seqs, const uint32_t* dev_len_in,
+                     const uint32_t* dev_table_in, const uint32_t* dev_new, uint32_t stride, const ck_window* window,
+                     const uint8_t* dev_held, uint32_t rows, uint32_t* dev_len_out, uint32_t* dev_table_out,
+                     uint32_t* dev_start, int64_t* dev_slot, uint32_t* dev_position, uint32_t* dev_status,
+                     void* dev_work, size_t work_len, void* stream) {
+  PagesLayout w;
+  if (const int rc = pages_args(cache, seqs, stride, dev_work, work_len, &w)) return rc;
+  if (rows < 1 || rows > (1u << 20) || !dev_len_in || !dev_table_in || !dev_new || !dev_len_out || !dev_table_out ||
+      !dev_start || !dev_slot || !dev_position || !dev_status || (window && window->window == 0))
+    return CK_INVALID_ARGUMENT;
+  const void* in[] = {dev_len_in, dev_table_in, dev_new, dev_held};
+  const uint64_t in_bytes[] = {4ull * seqs, 4ull * seqs * stride, 4ull * seqs, dev_held ? cache->pages : 0ull};
+  const void* out[] = {dev_slot, dev_len_out, dev_table_out, dev_start, dev_position, dev_status, dev_work};
+  const uint64_t out_bytes[] = {8ull * rows, 4ull * seqs, 4ull * seqs * stride, 4ull * (seqs + 1), 4ull * rows,
+                                4ull * seqs, work_len};
+  for (int o = 0; o < 7; ++o) {
+    if (!aligned_to(out[o], o ? 4 : 8) || on_pools(out[o], out_bytes[o], *cache)) return CK_INVALID_ARGUMENT;
+    for (int i = 0; i < 4; ++i)
+      if ((i < 3 && !aligned_to(in[i], 4)) || overlaps(out[o], out_bytes[o], in[i], in_bytes[i]))
+        return CK_INVALID_ARGUMENT;
+    for (int i = 0; i < o; ++i)
+      if (overlaps(out[o], out_bytes[o], out[i], out_bytes[i])) return CK_INVALID_ARGUMENT;
+  }
+  AdvanceParams p = {};
+  p.len_in = dev_len_in;
+  p.table_in = dev_table_in;
+  p.ask = dev_new;
+  p.held = dev_held;
+  p.len_out = dev_len_out;
+  p.table_out = dev_table_out;
+  p.start = dev_start;
+  p.slot = dev_slot;
+  p.position = dev_position;
+  p.status = dev_status;
+  p.seqs = seqs;
+  p.stride = stride;
+  p.pages = cache->pages;
+  p.page_shift = log2_of(cache->page);
+  p.rows = rows;
+  p.sinks = window ? window->sinks : 0;
+  p.window = window ? window->window : 0xFFFFFFFFu;
+  uint8_t* b = static_cast<uint8_t*>(dev_work);
+  p.bits = reinterpret_cast<uint32_t*>(b + w.bits);
+  p.list = reinterpret_cast<uint32_t*>(b + w.list);
+  p.before = reinterpret_cast<unsigned long long*>(b + w.before);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  CKP_CUDA(cudaMemsetAsync(p.bits, 0, 4ull * ((p.pages + 31) / 32), s));
+  constexpr uint32_t per = kTableThreads / 32;
+  const uint32_t blocks = (seqs + per - 1) / per;
+  k_advance_mark<<<blocks, kTableThreads, 0, s>>>(p);
+  k_advance_plan<<<1, kPlanThreads, 0, s>>>(p);
+  k_advance_fill<<<blocks, kTableThreads, 0, s>>>(p);
+  CKP_CUDA(cudaGetLastError());
+  return CK_OK;
 }
 
 }  // extern "C"

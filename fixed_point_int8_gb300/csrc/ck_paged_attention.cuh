@@ -13,7 +13,38 @@ struct PAttnParams {
   uint32_t heads, inv_sqrt;
   const uint32_t* exp_tab;
   int64_t* out;
+  uint32_t sinks, window;  // with a window: a row sees the first `sinks` positions and its last `window`
 };
+
+constexpr unsigned long long kOne = 1ull << 30;  // the table's first entry
+
+// A score's exponential: the table's, which is at most 2^30.
+__device__ __forceinline__ uint32_t exponential(const uint32_t* tab, unsigned long long d) {
+  const unsigned long long i = d >> 8;
+  return min(__ldg(tab + (i < 4096 ? i : 4096)), (uint32_t)kOne);
+}
+
+// What rows with windows see, the first of them at `pos0`, drawn together: place u is position u
+// below `edge` and position u + skip from there on.  Both parts begin and end at multiples of
+// eight (as pages do), so eight places from a multiple of eight on lie in one page.
+struct Span {
+  uint32_t edge, skip;
+  __device__ __forceinline__ uint32_t position(uint32_t u) const { return u < edge ? u : u + skip; }
+};
+__device__ __forceinline__ uint32_t window_begin(const PAttnParams& p, uint32_t pos) {  // the last `window`
+  return pos >= p.window ? pos - p.window + 1 : 0;
+}
+__device__ __forceinline__ Span window_span(const PAttnParams& p, uint32_t pos0) {
+  const uint32_t edge = (p.sinks + 7) & ~7u, low = window_begin(p, pos0) & ~7u;
+  return {edge, low > edge ? low - edge : 0};
+}
+// Whether the window leaves a call's sequences as they are, and the places that rows up to `apart`
+// positions from one another see at most.
+inline bool whole(const ck_window* w, uint32_t max_len) { return !w || w->window >= max_len || w->sinks >= max_len; }
+inline uint32_t window_places(const ck_window* w, uint32_t max_len, uint32_t apart) {
+  if (whole(w, max_len)) return max_len;
+  return (uint32_t)std::min<uint64_t>(max_len, ((w->sinks + 7ull) & ~7ull) + w->window + apart + 7);
+}
 
 // Tiles of 128 queries.  Scratch: a count of the tiles left to the kernel for all values and
 // a word a tile, then each block's scores and the sums it keeps between flushes.

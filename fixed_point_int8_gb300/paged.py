@@ -1,5 +1,5 @@
-"""The paged cache and beam search of ``libck.so`` (include/ck.h, "a cache in pages" and "beam
-search").  As the rest of the binding this module only marshals arguments; what the C side
+"""The paged cache, beam search and sampling of ``libck.so`` (include/ck.h, "a cache in pages", "beam
+search" and "sampling").  As the rest of the binding this module only marshals arguments; what the C side
 cannot see (a tensor's type, shape, strides and device) is checked here, and a wrong one raises
 ValueError.  Every call returns the library's error number first and enqueues its work on
 `stream` (the current one by default) without synchronising.  Arrays of u32 are int32 tensors;
@@ -21,6 +21,8 @@ BAD_SEQUENCE, BAD_PAGE = 1, 2
 PAGE_RESERVED, PAGE_SHARED = 1, 2
 # Beams.done of a search that failed (a wait of its kernel ran out)
 BEAM_FAILED = 255
+# a sampled row without a token
+NO_TOKEN = -1
 
 _vp, _sz, _u32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_uint32
 _device = torch.cuda.current_device
@@ -34,6 +36,35 @@ class _Cache(ctypes.Structure):
 class _Batch(ctypes.Structure):
     _fields_ = [(n, _vp) for n in ("dev_start", "dev_len", "dev_table", "dev_status")] + [
         (n, _u32) for n in ("seqs", "rows", "stride", "max_new", "max_len")]
+
+
+class _Window(ctypes.Structure):
+    _fields_ = [("sinks", _u32), ("window", _u32)]
+
+
+class Window(NamedTuple):
+    """What a row of attention sees: the sequence's first `sinks` positions and its last `window`, its own
+    among them."""
+    sinks: int
+    window: int
+
+
+def _window(w):
+    """A window as the library takes it (None: the whole cache)."""
+    if w is None:
+        return None
+    sinks, window = w
+    return ctypes.byref(_Window(_u32_of("sinks", sinks), _u32_of("window", window)))
+
+
+def _windows(w, layers):
+    """A window for every layer (one stands for all of them)."""
+    if w is None:
+        return None
+    each = [w] * layers if isinstance(w, Window) else list(w)
+    if len(each) != layers:
+        raise ValueError(f"window: {len(each)} of them, the model has {layers} layers")
+    return (_Window * layers)(*(_Window(_u32_of("sinks", s), _u32_of("window", n)) for s, n in each))
 
 
 def _u32_of(name, value):
@@ -206,15 +237,17 @@ def paged_store(cache, layer, batch, q, k, v, rope, half=False, out=None, stream
     return rc, out
 
 
-def paged_attention_work(cache, batch, heads, stream=None):
-    """Scratch for paged_attention on the stream, as large as the batch's bounds need."""
+def paged_attention_work(cache, batch, heads, stream=None, window=None):
+    """Scratch for paged_attention on the stream, as large as the batch's bounds and the window need."""
     device = _devices(cache, batch, stream)
-    return _empty(stream, _size("ck_paged_attention_work", cache._c, batch._c, heads), torch.uint8, device)
+    return _empty(stream, _size("ck_paged_window_attention_work", cache._c, batch._c, heads, _window(window)), torch.uint8,
+                  device)
 
 
-def paged_attention(cache, layer, batch, q, exp_table, inv_sqrt, out=None, work=None, stream=None):
-    """Attention of a batch's new rows over their sequences' pages (ck_paged_attention).  q: int64
-    rows of rotated queries; exp_table: int32 [4097].  Returns (rc, outputs)."""
+def paged_attention(cache, layer, batch, q, exp_table, inv_sqrt, out=None, work=None, stream=None, window=None):
+    """Attention of a batch's new rows over their sequences' pages (ck_paged_attention), or over a
+    Window of them (ck_paged_window_attention).  q: int64 rows of rotated queries; exp_table: int32
+    [4097].  Returns (rc, outputs)."""
     device, rows, hd = _devices(cache, batch, stream), batch.rows, cache.head_dim
     step = _check_rows("q", q, rows, device)
     _check("exp_table", exp_table, torch.int32, (4097,), device)
@@ -226,22 +259,23 @@ def paged_attention(cache, layer, batch, q, exp_table, inv_sqrt, out=None, work=
     else:
         _check("out", out, torch.int64, (rows, cols), device)
     if work is None:
-        work = paged_attention_work(cache, batch, cols // hd, stream)
+        work = paged_attention_work(cache, batch, cols // hd, stream, window)
     else:
         _check("work", work, torch.uint8, (work.numel(),), device)
     _keep(stream, q, exp_table, out, work, *cache._tensors, *batch._tensors)
-    rc = lib().ck_paged_attention(cache._c, _u32_of("layer", layer), batch._c, q.data_ptr(), step, cols // hd,
-                                  exp_table.data_ptr(), _u32_of("inv_sqrt", inv_sqrt), out.data_ptr(), work.data_ptr(), work.numel(),
-                                  _on(stream, device, cache, batch))
+    rc = lib().ck_paged_window_attention(cache._c, _u32_of("layer", layer), batch._c, q.data_ptr(), step, cols // hd,
+                                         _window(window), exp_table.data_ptr(), _u32_of("inv_sqrt", inv_sqrt),
+                                         out.data_ptr(), work.data_ptr(), work.numel(), _on(stream, device, cache, batch))
     return rc, out
 
 
-def turn_paged_work(model, cache, batch, stream=None):
+def turn_paged_work(model, cache, batch, stream=None, window=None):
     device = _devices(cache, batch, stream)
-    return _empty(stream, _size("ck_turn_paged_work", model._h, cache._c, batch._c), torch.uint8, device)
+    each = _windows(window, model.config["layers"])
+    return _empty(stream, _size("ck_turn_paged_window_work", model._h, cache._c, batch._c, each), torch.uint8, device)
 
 
-def turn_paged(model, cache, batch, tokens, logits=None, work=None, stream=None):
+def turn_paged(model, cache, batch, tokens, logits=None, work=None, stream=None, window=None):
     device, seqs, vocab = _devices(cache, batch, stream), batch.lens.shape[0], model.config["vocab"]
     if model.mem.get_device() != device:
         raise ValueError("the model is not on the current CUDA device")
@@ -251,13 +285,16 @@ def turn_paged(model, cache, batch, tokens, logits=None, work=None, stream=None)
     step = _check_rows("logits", logits, seqs, device)
     if logits.shape[1] != vocab:
         raise ValueError(f"logits: {logits.shape[1]} columns, the vocabulary is {vocab}")
+    if window is not None and not isinstance(window, Window):
+        window = list(window)
+    each = _windows(window, model.config["layers"])
     if work is None:
-        work = turn_paged_work(model, cache, batch, stream)
+        work = turn_paged_work(model, cache, batch, stream, window)
     else:
         _check("work", work, torch.uint8, (work.numel(),), device)
     _keep(stream, model.mem, tokens, logits, work, *cache._tensors, *batch._tensors)
-    rc = lib().ck_turn_paged(model._h, cache._c, batch._c, tokens.data_ptr(), logits.data_ptr(), step,
-                             work.data_ptr(), work.numel(), _on(stream, device, model, cache, batch))
+    rc = lib().ck_turn_paged_window(model._h, cache._c, batch._c, each, tokens.data_ptr(), logits.data_ptr(), step,
+                                    work.data_ptr(), work.numel(), _on(stream, device, model, cache, batch))
     return rc, logits
 
 
@@ -265,6 +302,15 @@ class Fork(NamedTuple):
     table: object   # int32 [rows][stride]
     lens: object    # int32 [rows], grown
     status: object  # int32 [rows]
+
+
+class Advance(NamedTuple):
+    table: object      # int32 [seqs][stride]
+    lens: object       # int32 [seqs], grown
+    starts: object     # int32 [seqs + 1]
+    slots: object      # int64 [rows], -1 for none
+    positions: object  # int32 [rows], -1 for none
+    status: object     # int32 [seqs]
 
 
 class Compact(NamedTuple):
@@ -313,6 +359,30 @@ class PagePlan:
                                  new_lens.data_ptr(), out.data_ptr(), status.data_ptr(), *self._args,
                                  _on(stream, device, self, self.cache))
         return rc, Fork(out, new_lens, status)
+
+    def advance(self, lens, table, new, rows, window=None, held=None, stream=None):
+        """ck_pages_advance: every sequence gives back the pages behind its Window (None: it keeps all) and
+        gets pages for new[s] more positions, at most `rows` of them together; held (uint8 [pages]):
+        nonzero pages are not handed out.  The outputs' tensors are a PagedBatch's.  Returns (rc, Advance)."""
+        device, seqs = self._begin(lens, table, stream)
+        if seqs > self.rows:
+            raise ValueError(f"table: {seqs} rows, the plan has room for {self.rows}")
+        _check("new", new, torch.int32, (seqs,), device)
+        if held is not None:
+            _check("held", held, torch.uint8, (self.cache.pages,), device)
+        rows = _u32_of("rows", rows)
+        if not 1 <= rows <= 2**20:
+            raise ValueError(f"rows: want a number from 1 to 2^20, got {rows}")
+        view = _window(window)
+        _keep(stream, self._work, lens, table, new, *(() if held is None else (held,)), *self.cache._tensors)
+        out, slots = _empty(stream, (seqs, self.stride), torch.int32, device), _empty(stream, (rows,), torch.int64, device)
+        new_lens, starts, positions, status = _empty(stream, (3 * seqs + 1 + rows,), torch.int32, device).split(
+            (seqs, seqs + 1, rows, seqs))
+        rc = lib().ck_pages_advance(self.cache._c, seqs, lens.data_ptr(), table.data_ptr(), new.data_ptr(), self.stride,
+                                    view, None if held is None else held.data_ptr(), rows, new_lens.data_ptr(),
+                                    out.data_ptr(), starts.data_ptr(), slots.data_ptr(), positions.data_ptr(),
+                                    status.data_ptr(), *self._args, _on(stream, device, self, self.cache))
+        return rc, Advance(out, new_lens, starts, slots, positions, status)
 
     def compact(self, lens, table, stream=None):
         """ck_pages_compact: the rows' pages move to the lowest page numbers.  Returns (rc, Compact)."""
@@ -372,9 +442,46 @@ class BeamPlan:
         return rc, Beams(new_scores, parent, token, new_done)
 
 
+class Samples(NamedTuple):
+    token: object  # int32 [rows], NO_TOKEN for none
+    prob: object   # int32 [rows], 24 fraction bits
+    kept: object   # int32 [rows]
+
+
+def sample(logits, temperature, random, exp_table, top_k=None, top_p=None, min_p=None, stream=None):
+    """A token of every row (ck_sample): logits int64 [rows][vocab] (rows may be further apart),
+    temperature int32 [rows] (16 fraction bits), random int64 [rows] (all 64 bits count), exp_table
+    int32 [4097]; top_k, top_p and min_p int32 [rows] (the latter two with 24 fraction bits) or None.
+    Returns (rc, Samples)."""
+    device = _call_device(stream)
+    if logits.dim() != 2:
+        raise ValueError(f"logits: want two dimensions, got {tuple(logits.shape)}")
+    rows, vocab = logits.shape
+    step = _check_rows("logits", logits, rows, device)
+    _check("temperature", temperature, torch.int32, (rows,), device)
+    _check("random", random, torch.int64, (rows,), device)
+    _check("exp_table", exp_table, torch.int32, (4097,), device)
+    filters = [("top_k", top_k), ("top_p", top_p), ("min_p", min_p)]
+    for name, f in filters:
+        if f is not None:
+            _check(name, f, torch.int32, (rows,), device)
+    _keep(stream, logits, temperature, random, exp_table, *(f for _, f in filters if f is not None))
+    token, prob, kept = _empty(stream, (3, rows), torch.int32, device)
+    rc = lib().ck_sample(logits.data_ptr(), step, rows, vocab, temperature.data_ptr(),
+                         *(None if f is None else f.data_ptr() for _, f in filters), random.data_ptr(),
+                         exp_table.data_ptr(), token.data_ptr(), prob.data_ptr(), kept.data_ptr(),
+                         _on(stream, device))
+    return rc, Samples(token, prob, kept)
+
+
 def set_beam_wait_limit(polls: int) -> int:
     """The process's limit on a row's wait for its cluster's maxima (ck_set_beam_wait_limit)."""
     return lib().ck_set_beam_wait_limit(_u32_of("polls", polls))
+
+
+def host_sample_place(distance: int, temperature: int) -> int:
+    """Host build of a distance's place in the exponential table as ck_sample takes it."""
+    return int(lib().ck_host_sample_place(_u32_of("distance", distance), _u32_of("temperature", temperature)))
 
 
 def host_log_sum(z: int) -> int:

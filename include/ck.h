@@ -420,6 +420,21 @@ int ck_paged_attention(const ck_paged_cache* cache, uint32_t layer, const ck_pag
                        const int64_t* dev_q, size_t q_stride, uint32_t heads, const uint32_t* dev_exp,
                        uint32_t inv_sqrt, int64_t* dev_out, void* dev_work, size_t work_len, void* stream);
 
+/* The same over a window of the cache: a row at position p sees the positions t <= p with t <
+ * sinks (the first ones, which stay visible) or p - t < window (its own and those before it).  Pages
+ * that no row of the batch sees are not looked up: their table entries may be CK_NO_PAGE, as
+ * ck_pages_advance leaves them.  A null window is the whole cache.  dev_work as large as the window's
+ * own *_work says.  Errors: those of ck_paged_attention, and 10 for a window of 0. */
+typedef struct ck_window {
+  uint32_t sinks, window;
+} ck_window;
+int ck_paged_window_attention_work(const ck_paged_cache* cache, const ck_paged_batch* batch, uint32_t heads,
+                                   const ck_window* window, size_t* out);
+int ck_paged_window_attention(const ck_paged_cache* cache, uint32_t layer, const ck_paged_batch* batch,
+                              const int64_t* dev_q, size_t q_stride, uint32_t heads, const ck_window* window,
+                              const uint32_t* dev_exp, uint32_t inv_sqrt, int64_t* dev_out, void* dev_work,
+                              size_t work_len, void* stream);
+
 /* The new rows of a batch through the model's layers (phases 3 to 18, "The forward pass, in
  * order"): dev_tokens u32 [rows] the rows' tokens; every layer's keys and values go into the
  * cache (the model's layers, key heads and head size), and dev_logits i64 [seqs][logits_stride]
@@ -434,6 +449,14 @@ int ck_paged_attention(const ck_paged_cache* cache, uint32_t layer, const ck_pag
 int ck_turn_paged_work(ck_model* m, const ck_paged_cache* cache, const ck_paged_batch* batch, size_t* out);
 int ck_turn_paged(ck_model* m, const ck_paged_cache* cache, const ck_paged_batch* batch, const uint32_t* dev_tokens,
                   int64_t* dev_logits, size_t logits_stride, void* dev_work, size_t work_len, void* stream);
+/* The same with a window for every layer: windows [layers] in host memory, read before the call
+ * returns.  Layers may differ; one whose window is longer than max_len sees the whole cache.  Errors: those
+ * of ck_turn_paged, and 10 for a window of 0. */
+int ck_turn_paged_window_work(ck_model* m, const ck_paged_cache* cache, const ck_paged_batch* batch,
+                              const ck_window* windows, size_t* out);
+int ck_turn_paged_window(ck_model* m, const ck_paged_cache* cache, const ck_paged_batch* batch,
+                         const ck_window* windows, const uint32_t* dev_tokens, int64_t* dev_logits,
+                         size_t logits_stride, void* dev_work, size_t work_len, void* stream);
 /* The model's exponential and rotary tables in device memory and its one over the square root
  * of the head size, for the single operators.  Errors: 10. */
 int ck_model_tables(const ck_model* m, const uint32_t** dev_exp, const int32_t** dev_rope, uint32_t* inv_sqrt);
@@ -475,6 +498,60 @@ int ck_pages_compact(const ck_paged_cache* cache, uint32_t rows, const uint32_t*
                      const uint32_t* dev_table_in, uint32_t stride, uint32_t* dev_table_out,
                      uint32_t* dev_used, uint32_t* dev_status, void* dev_work, size_t work_len,
                      void* stream);
+
+/* Between two passes: sequence s, dev_len_in[s] positions long with its pages in row s of
+ * dev_table_in, asks for dev_new[s] more (0: none).  With a window it gives back the pages that
+ * neither its next position nor a later one sees (no position below `sinks`, none among the
+ * window - 1 before the next): their entries come out as CK_NO_PAGE, and are not read here again.  (For
+ * layers that differ, give the widest window and the most sinks; null: every page stays.)  Free are the pages
+ * that no sequence keeps and that are not marked in dev_held (u8 [pages], nonzero: not handed out;
+ * may be null); they are handed out in ascending order, sequence after sequence.  Sequences may
+ * share whole pages; a part-filled page that a sequence goes on in has to be its own, as ck_pages_fork
+ * leaves it.  Outputs, ready for a ck_paged_batch: dev_table_out u32 [seqs][stride], dev_len_out
+ * u32 [seqs] (the new positions included), dev_start u32 [seqs + 1]; and for every row its place
+ * in the pools, dev_slot i64 [rows] (page number * page + place in the page), and its position,
+ * dev_position u32 [rows], -1 and CK_NO_PAGE behind the last row.  dev_status u32 [seqs]: 0; 7
+ * (the new length is above stride * page or 2^20 - 1) or 4 (it asks for pages, and those asked for
+ * up to it are more than there are free, or for rows, and those are more than `rows`): the sequence
+ * gets no rows, and keeps its length and the pages above; 3 (its length is above either bound, or an
+ * entry that it would keep lies outside the pool): its table comes out empty, its length 0.
+ * Sequences of status 3 and 7 ask for nothing.  The outputs may not overlap the inputs, the scratch (of
+ * ck_pages_work for seqs rows) or the pools.  Limits: seqs <= 65536, stride <= 2^17, rows <= 2^20.
+ * Errors: 4 (work_len), 9, 10. */
+int ck_pages_advance(const ck_paged_cache* cache, uint32_t seqs, const uint32_t* dev_len_in,
+                     const uint32_t* dev_table_in, const uint32_t* dev_new, uint32_t stride, const ck_window* window,
+                     const uint8_t* dev_held, uint32_t rows, uint32_t* dev_len_out, uint32_t* dev_table_out,
+                     uint32_t* dev_start, int64_t* dev_slot, uint32_t* dev_position, uint32_t* dev_status,
+                     void* dev_work, size_t work_len, void* stream);
+
+/* ---------------------------------------------------------------- sampling
+ * Phase 19 ("Sampling") for many rows at once, with the usual filters and given random numbers:
+ * dev_logits i64 [rows][logits_stride] (the first `vocab` used), dev_temperature u32 [rows] (16
+ * fraction bits, up to 16 << 16), dev_random u64 [rows].  A logit of the lowest int64 is masked: its
+ * token is never kept.  With m the row's largest logit, D = m - logit and t the temperature, a token
+ * weighs e = EXP[D >= 16 t ? 4096 : floor(256 D / t)], as in ck_turn.  In the order of (D, token) the
+ * first n = min(n_k, n_p, n_m) tokens are kept, at least one:
+ *   n_k: dev_top_k (0: all of them);
+ *   n_p: the fewest whose weights add up to floor(Z * dev_top_p / 2^24), Z the weight of the first n_k
+ *     (2^24 and above: all);
+ *   n_m: those with e * 2^24 >= dev_min_p * EXP[0] (0: all; values above 2^24 count as it).
+ * Each of the three arrays, u32 [rows], may be null: that filter is off.  The draw is dev_random
+ * modulo the weight W of the kept tokens, and the token the first, in the order of the vocabulary, of
+ * those kept whose weights up to it exceed the draw.  At temperature zero the first largest logit is the
+ * only one kept.  Outputs, u32 [rows]: dev_token, dev_prob = floor(e * 2^24 / W) of that token (2^24
+ * at temperature zero), dev_kept = n.  Where every logit is masked, or the temperature is above 16 <<
+ * 16: CK_NO_TOKEN, 0, 0.  dev_exp: the exponential table u32 [4097], entry 0 = 2^30 and none larger
+ * than the one before it.  With no filter and the generator's output as the random number the token
+ * is the one that ck_turn samples.  The outputs may not overlap each other or the inputs.  Nothing
+ * is allocated, and no scratch is needed.  Limits: rows <= 65536, vocab <= 2^20.  Errors: 9, 10. */
+#define CK_NO_TOKEN 0xFFFFFFFFu
+int ck_sample(const int64_t* dev_logits, size_t logits_stride, uint32_t rows, uint32_t vocab,
+              const uint32_t* dev_temperature, const uint32_t* dev_top_k, const uint32_t* dev_top_p,
+              const uint32_t* dev_min_p, const uint64_t* dev_random, const uint32_t* dev_exp, uint32_t* dev_token,
+              uint32_t* dev_prob, uint32_t* dev_kept, void* stream);
+/* A host build of a distance's place in the table at a temperature of 1 to 16 << 16, for tests
+ * without a GPU. */
+uint32_t ck_host_sample_place(uint32_t distance, uint32_t temperature);
 
 /* ---------------------------------------------------------------- beam search
  * One step of `groups` searches of `beams` beams each: of every search's beams times the

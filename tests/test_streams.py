@@ -1,0 +1,120 @@
+"""What windowed attention, the page tables' step between passes and sampling refuse, and their host
+routines: no GPU needed (every refusal is decided from the arguments alone, before any device
+call)."""
+import ctypes
+
+import numpy as np
+import pytest
+
+from test_paged import ADDR, BAD_BATCHES, BAD_CACHES, attention_args, batch, cache, call, ck  # noqa: F401
+
+
+def window(ck, sinks=4, size=16):
+    return ck.paged._Window(sinks, size)
+
+
+def window_args(ck):
+    args = attention_args(ck)
+    out = {}
+    for name, value in args.items():
+        if name == "exp":
+            out["window"] = window(ck)
+        out[name] = value
+    return out
+
+
+@pytest.mark.parametrize("bad", BAD_CACHES + BAD_BATCHES, ids=str)
+def test_wrong_caches_and_batches_are_refused(ck, bad):
+    key = "cache" if bad.keys() & {n for n, _ in ck.paged._Cache._fields_} else "batch"
+    value = cache(ck, **bad) if key == "cache" else batch(ck, **bad)
+    assert call(ck, "ck_paged_window_attention", window_args(ck), **{key: value}) == 10
+
+
+@pytest.mark.parametrize("bad", [dict(cache=None), dict(layer=2), dict(batch=None), dict(q=None), dict(exp=None),
+                                 dict(out=None), dict(work=None), dict(q=4 * ADDR + 8), dict(out=ADDR + 8),
+                                 dict(work=ADDR + 128), dict(exp=ADDR + 2), dict(q_stride=126), dict(q_stride=129),
+                                 dict(heads=3), dict(heads=0), dict(heads=65538), dict(out=4 * ADDR + 32),
+                                 dict(window=0)], ids=str)
+def test_wrong_window_calls_are_refused(ck, bad):
+    if bad == dict(window=0):
+        bad = dict(window=window(ck, 4, 0))
+    assert call(ck, "ck_paged_window_attention", window_args(ck), **bad) == 10
+
+
+def test_window_scratch_is_refused_for_wrong_arguments(ck):
+    n = ctypes.c_size_t()
+    L, good = ck.lib(), (ctypes.byref(cache(ck)), ctypes.byref(batch(ck)), 4, ctypes.byref(window(ck)), ctypes.byref(n))
+    for i, wrong in ((0, None), (1, None), (2, 3), (3, ctypes.byref(window(ck, 0, 0))), (4, None)):
+        assert L.ck_paged_window_attention_work(*good[:i], wrong, *good[i + 1:]) == 10
+    assert L.ck_turn_paged_window_work(None, good[0], good[1], good[3], good[4]) == 10
+    assert L.ck_turn_paged_window(None, good[0], good[1], good[3], ADDR, 2 * ADDR, 512, 3 * ADDR, 2**40, None) == 10
+
+
+def advance_args(ck):
+    return dict(cache=cache(ck, dev_k=40 * ADDR, dev_v=41 * ADDR), seqs=3, len_in=ADDR, table_in=2 * ADDR, new=3 * ADDR,
+                stride=4, window=window(ck), held=4 * ADDR, rows=6, len_out=5 * ADDR, table_out=6 * ADDR, start=7 * ADDR,
+                slot=8 * ADDR, position=9 * ADDR, status=10 * ADDR, work=16 * ADDR, work_len=2**20, stream=None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(cache=None), dict(seqs=0), dict(seqs=65537), dict(len_in=None), dict(table_in=None), dict(new=None),
+    dict(stride=0), dict(stride=2**17 + 1), dict(window="empty"), dict(rows=0), dict(rows=2**20 + 1), dict(len_out=None),
+    dict(table_out=None), dict(start=None), dict(slot=None), dict(position=None), dict(status=None), dict(work=None),
+    dict(work=16 * ADDR + 128), dict(slot=8 * ADDR + 4), dict(position=9 * ADDR + 2), dict(len_in=ADDR + 2),
+    # outputs on inputs, on one another, on the pools and on the scratch
+    dict(len_out=ADDR), dict(table_out=2 * ADDR + 44), dict(start=3 * ADDR - 12), dict(status=4 * ADDR + 4),
+    dict(slot=5 * ADDR - 40), dict(position=6 * ADDR + 44), dict(start=10 * ADDR + 8), dict(status=40 * ADDR + 64),
+    dict(slot=41 * ADDR), dict(work=8 * ADDR), dict(work=40 * ADDR), dict(len_out=16 * ADDR + 512)], ids=str)
+def test_wrong_steps_of_the_tables_are_refused(ck, bad):
+    if bad == dict(window="empty"):
+        bad = dict(window=window(ck, 4, 0))
+    assert call(ck, "ck_pages_advance", advance_args(ck), **bad) == 10
+
+
+def test_short_scratch_of_a_step_is_refused(ck):
+    n = ctypes.c_size_t()
+    assert ck.lib().ck_pages_work(ctypes.byref(cache(ck)), 3, 4, ctypes.byref(n)) == 0
+    assert call(ck, "ck_pages_advance", advance_args(ck), work_len=n.value - 1) == 4
+
+
+def sample_args():
+    return dict(logits=ADDR, stride=512, rows=3, vocab=512, temperature=2 * ADDR, top_k=3 * ADDR, top_p=4 * ADDR,
+                min_p=5 * ADDR, random=6 * ADDR, exp=7 * ADDR, token=8 * ADDR, prob=9 * ADDR, kept=10 * ADDR, stream=None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(logits=None), dict(logits=ADDR + 4), dict(stride=511), dict(stride=2**40), dict(rows=0), dict(rows=65537),
+    dict(vocab=0), dict(vocab=2**20 + 1, stride=2**21), dict(temperature=None), dict(temperature=2 * ADDR + 1),
+    dict(top_k=3 * ADDR + 2), dict(top_p=4 * ADDR + 2), dict(min_p=5 * ADDR + 1), dict(random=None),
+    dict(random=6 * ADDR + 4), dict(exp=None), dict(exp=7 * ADDR + 2), dict(token=None), dict(prob=None), dict(kept=None),
+    dict(token=8 * ADDR + 2), dict(token=ADDR + 4096), dict(prob=2 * ADDR + 8), dict(kept=3 * ADDR), dict(token=4 * ADDR),
+    dict(prob=5 * ADDR - 8), dict(kept=6 * ADDR + 16), dict(token=7 * ADDR + 16384), dict(prob=8 * ADDR + 8),
+    dict(kept=9 * ADDR - 8)], ids=str)
+def test_wrong_samplings_are_refused(ck, bad):
+    assert call(ck, "ck_sample", sample_args(), **bad) == 10
+
+
+def test_the_place_in_the_table_is_the_floored_quotient(ck):
+    """At every temperature's ends of places: floor(256 d / t) below 16 t, 4096 from there."""
+    rng = np.random.default_rng(5)
+    temperatures = [1, 2, 3, 5, 255, 256, 257, 4095, 65535, 65536, 65537, 98304, 2**20 - 1, 2**20]
+    temperatures += [int(t) for t in rng.integers(1, 2**20, 200)]
+    for t in temperatures:
+        places = np.concatenate([np.arange(0, 4097, 97), [1, 2, 4094, 4095, 4096], rng.integers(0, 4096, 50)])
+        first = [-(-int(b) * t // 256) for b in places]
+        for d in {x + o for x in first for o in (-1, 0, 1)} | {0, 16 * t - 1, 16 * t, 16 * t + 1, 2**32 - 1}:
+            if d >= 0:
+                assert ck.host_sample_place(d, t) == (4096 if d >= 16 * t else 256 * d // t), (d, t)
+
+
+def test_numbers_of_a_window_past_32_bits_are_refused(ck):
+    for bad in ((2**32, 5), (-1, 5), (4, 2**32), (4, -1)):
+        with pytest.raises(ValueError, match="sinks|window"):
+            ck.paged._window(ck.Window(*bad))
+        with pytest.raises(ValueError, match="sinks|window"):
+            ck.paged._windows(ck.Window(*bad), 3)
+    with pytest.raises(ValueError, match="3 layers"):
+        ck.paged._windows([ck.Window(0, 4)] * 2, 3)
+    assert ck.paged._window(None) is None and ck.paged._windows(None, 3) is None
+    each = ck.paged._windows([ck.Window(0, 4), ck.Window(2, 9), ck.Window(1, 1)], 3)
+    assert [(w.sinks, w.window) for w in each] == [(0, 4), (2, 9), (1, 1)]
