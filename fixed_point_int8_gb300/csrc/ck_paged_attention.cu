@@ -168,7 +168,7 @@ AttentionPlan attention_plan(const ck_paged_cache& c, const ck_paged_batch& b, u
   AttentionPlan w = {};
   w.window = !whole(window, b.max_len);
   w.line = window_places(window, b.max_len, 0);
-  if (!w.window) w.few = plan_few(c, b, heads, f);
+  w.few = plan_few(c, b, heads, window, f);
   if (!w.window && c.head_dim >= 64) {
     const double tiles = std::ceil((double)b.max_new * (heads / c.kv_heads) / 128) * b.seqs * c.kv_heads;
     const double few_us = 8 + 0.9e-6 * b.seqs * heads * b.max_new * b.max_len * c.head_dim;
@@ -206,6 +206,11 @@ bool work_args_ok(const ck_paged_cache* cache, const ck_paged_batch* batch, uint
 }
 
 }  // namespace
+
+cudaError_t launch_few_whole(const FewParams& p, const FewPlan& w, const DeviceFacts& f, cudaStream_t s) {
+  return launch_few_any<false>(p, w, f, s);
+}
+
 }  // namespace ck
 
 using namespace ck;
@@ -268,9 +273,7 @@ int ck_paged_window_attention(const ck_paged_cache* cache, uint32_t layer, const
   if (plan.few.use) {
     const FewParams fp = {p, reinterpret_cast<long long*>(work), plan.few.cap, plan.few.ids, plan.few.sc_smem,
                           log2_of(plan.few.C), 0, 0};
-    CKP_CUDA(plan.few.NT == kBroad    ? launch_few_r<kBroad>(fp, plan.few, f, s)
-             : plan.few.NT == kMiddle ? launch_few_r<kMiddle>(fp, plan.few, f, s)
-                                      : launch_few_r<kNarrow>(fp, plan.few, f, s));
+    CKP_CUDA(plan.window ? launch_few_window(fp, plan.few, f, s) : launch_few_whole(fp, plan.few, f, s));
     return CK_OK;
   }
   RowsParams rp = {p, reinterpret_cast<long long*>(work), plan.line, nullptr, nullptr, 0};

@@ -4,7 +4,6 @@
 #include "ck_paged_attention.cuh"
 
 namespace ck {
-namespace {
 
 // ------------------------------------------------------------------ a few queries a key head
 
@@ -20,6 +19,8 @@ namespace {
 // lane, and the values are on their way while the exponentials are formed.  One token over 8,191
 // positions of 32 heads: 134 MB in 28.9 us (4.6 TB/s); 64 runs of 65 to 191: 30.1 us, 20 of them
 // without any load.
+// With a window the places that any of the queries sees follow one another (Span), and the others
+// are neither read nor counted; of those, each query takes what it sees itself.
 constexpr uint32_t kMaxCluster = 16;
 constexpr int kNarrow = 64, kMiddle = 128, kBroad = 256;  // threads of a block
 constexpr unsigned long long kNowhere = ~0ull;
@@ -33,6 +34,28 @@ struct FewParams {
   uint32_t split;        // log2 of the cluster's blocks
   uint32_t seq0, z0;     // first sequence and first group of R queries of this launch
 };
+
+// Scores that do not fit shared memory take R * cap words of the scratch a block; those of every group
+// of queries at once would be gigabytes (4 GB for a chunk of 2,048 rows over 8,192 positions of 32 key
+// heads of 32).  Past kFewScratch, launches that follow one another share it, each of whole sequences
+// or, of one sequence, of some groups of queries.  Each ends with SMs idle: that chunk takes 11.8 ms in
+// two launches, 11.6 in one and 13.0 in eight of 512 MB; fewer blocks that loop took 16.6.
+constexpr uint64_t kFewScratch = 2ull << 30;
+constexpr uint64_t kFewLaunches = 64;
+struct FewPlan {
+  bool use;
+  uint32_t NT, R, C, z, cap, ids;
+  uint32_t seqs_each, z_each;  // sequences and groups of queries of one launch
+  bool sc_smem;
+  uint32_t smem;
+  uint64_t work;
+};
+
+// The launches of a plan, for the whole cache and for windows of it.
+cudaError_t launch_few_whole(const FewParams& p, const FewPlan& w, const DeviceFacts& f, cudaStream_t s);
+cudaError_t launch_few_window(const FewParams& p, const FewPlan& w, const DeviceFacts& f, cudaStream_t s);
+
+namespace {
 
 __device__ __forceinline__ uint32_t smem_of(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void cluster_sync() {
@@ -103,7 +126,7 @@ __device__ __forceinline__ unsigned long long warp_total(unsigned long long v) {
 }
 
 // LPP = 0: hd / 4 lanes a position (head sizes below 32).
-template <int LPP, int NCH, int R, int NT>
+template <int LPP, int NCH, int R, int NT, bool WINDOW>
 __global__ void __launch_bounds__(NT) k_pattn_few(const FewParams f) {
   constexpr int kStages = few_stages(NT, NCH), kBatch = few_batch(NT, R), kWarps = NT / 32;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -120,7 +143,7 @@ __global__ void __launch_bounds__(NT) k_pattn_few(const FewParams f) {
   const uint32_t group = p.heads / p.pool.kv_heads, queries = sq.count * group;
   if (v0 >= queries) return;
   // each query's row and head, and the positions it sees: those up to its row's own
-  uint32_t np[R], row[R], head[R], top = 0;
+  uint32_t np[R], row[R], head[R], top = 0, pos0 = 0xFFFFFFFFu;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const uint32_t token = group == 1 ? v0 + r : (v0 + r) / group, up = token + sq.len;  // position + count
@@ -129,7 +152,22 @@ __global__ void __launch_bounds__(NT) k_pattn_few(const FewParams f) {
     row[r] = sq.first + token;
     head[r] = kvh * group + (v0 + r - token * group);
     top = max(top, np[r]);
+    if (WINDOW && np[r]) pos0 = min(pos0, np[r] - 1);
   }
+  // with a window: from here on places, of which query r sees those below np[r] that are below
+  // `sinks` or not below from[r]
+  Span span = {0, 0};
+  uint32_t from[R];
+  if (WINDOW && top) {
+    span = window_span(p, pos0);
+    top -= span.skip;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      from[r] = np[r] ? window_begin(p, np[r] - 1) - span.skip : 0;
+      np[r] = np[r] ? np[r] - span.skip : 0;
+    }
+  }
+  auto sees = [&](int r, uint32_t u) { return u < np[r] && (!WINDOW || u < p.sinks || u >= from[r]); };
   const uint32_t per = (top + C - 1) >> f.split, c0 = min(top, rank * per), n = min(top, c0 + per) - c0;
   const FewLayout w = few_layout<NT, R>(NCH, hd, f.ids, f.cap, f.sc_smem);
   int4* ring = reinterpret_cast<int4*>(smem + w.ring);
@@ -145,12 +183,20 @@ __global__ void __launch_bounds__(NT) k_pattn_few(const FewParams f) {
 
   const uint32_t shift = p.pool.page_shift, mask = (1u << shift) - 1, page0 = c0 >> shift;
   const uint32_t* table = p.batch.table + (size_t)seq * p.batch.stride;
+  // The block's pages: those of its places below the span's edge, and from `second` on in the list those of
+  // the others, the first of which is page1.
+  uint32_t listed = n != 0 ? ((c0 + n - 1) >> shift) - page0 + 1 : 0, second = 0, page1 = 0;
+  if (WINDOW && n != 0) {
+    second = c0 < span.edge ? ((min(c0 + n, span.edge) - 1) >> shift) - page0 + 1 : 0;
+    page1 = (max(c0, span.edge) + span.skip) >> shift;
+    listed = second + (c0 + n > span.edge ? ((c0 + n - 1 + span.skip) >> shift) - page1 + 1 : 0);
+  }
   int holes = 0;  // a page outside the pool
-  for (uint32_t i = tid; n != 0 && i <= ((c0 + n - 1) >> shift) - page0; i += NT) {
-    const uint32_t id = table[page0 + i];
+  for (uint32_t i = tid; i < listed; i += NT) {
+    const uint32_t at = !WINDOW || i < second ? page0 + i : page1 + i - second, id = table[at];
     pages[i] = id < p.pool.pages ? 4 * page_word(p.pool, id, kvh) : kNowhere;
     if (id >= p.pool.pages) {
-      note(p.batch, seq, err_key((page0 + i) << shift, p.pool.layer, CK_PAGED_BAD_PAGE, 0));
+      note(p.batch, seq, err_key(at << shift, p.pool.layer, CK_PAGED_BAD_PAGE, 0));
       holes = 1;
     }
   }
@@ -182,7 +228,11 @@ __global__ void __launch_bounds__(NT) k_pattn_few(const FewParams f) {
       const uint32_t to = smem_of(ring + (sent % kStages) * NCH * kBatch * NT + tid);
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
-        const uint32_t u = (c0 & mask) + min(first + b * step, n - 1);  // from the first page's start
+        uint32_t u = (c0 & mask) + min(first + b * step, n - 1);  // from the first page's start
+        if (WINDOW) {  // (and here a page of the list and a place in it)
+          const uint32_t place = c0 + min(first + b * step, n - 1);
+          u = place < span.edge ? place - (page0 << shift) : place + span.skip - ((page1 - second) << shift);
+        }
         unsigned long long at = pages[u >> shift];
         uint32_t bytes = 16;
         if (holes && at == kNowhere) at = bytes = 0;
@@ -213,7 +263,7 @@ __global__ void __launch_bounds__(NT) k_pattn_few(const FewParams f) {
     if (i >= n) return;
     const long long v = wmul((long long)d >> 16, (int64_t)p.inv_sqrt) >> 24;
     sc[(size_t)r * f.cap + i] = v;
-    if (c0 + i < np[r]) m[r] = max(m[r], v);
+    if (sees(r, c0 + i)) m[r] = max(m[r], v);
   };
   for (uint32_t base = 0; base < n; base += round) {
     const int4* place = take();
@@ -303,7 +353,7 @@ __global__ void __launch_bounds__(NT) k_pattn_few(const FewParams f) {
     const uint32_t seen = np[r] > c0 ? min(n, np[r] - c0) : 0;
     long long* s = sc + (size_t)r * f.cap;
     for (uint32_t i = tid; i < n; i += NT) {
-      const uint32_t e = i < seen ? exponential(p.exp_tab, (unsigned long long)m[r] - (unsigned long long)s[i]) : 0;
+      const uint32_t e = (WINDOW ? sees(r, c0 + i) : i < seen) ? exponential(p.exp_tab, (unsigned long long)m[r] - (unsigned long long)s[i]) : 0;
       s[i] = e;
       z[r] += e;
     }
@@ -415,22 +465,6 @@ __global__ void __launch_bounds__(NT) k_pattn_few(const FewParams f) {
   cluster_sync();  // no block leaves while another reads its sums
 }
 
-// Scores that do not fit shared memory take R * cap words of the scratch a block; those of every group
-// of queries at once would be gigabytes (4 GB for a chunk of 2,048 rows over 8,192 positions of 32 key
-// heads of 32).  Past kFewScratch, launches that follow one another share it, each of whole sequences
-// or, of one sequence, of some groups of queries.  Each ends with SMs idle: that chunk takes 11.8 ms in
-// two launches, 11.6 in one and 13.0 in eight of 512 MB; fewer blocks that loop took 16.6.
-constexpr uint64_t kFewScratch = 2ull << 30;
-constexpr uint64_t kFewLaunches = 64;
-struct FewPlan {
-  bool use;
-  uint32_t NT, R, C, z, cap, ids;
-  uint32_t seqs_each, z_each;  // sequences and groups of queries of one launch
-  bool sc_smem;
-  uint32_t smem;
-  uint64_t work;
-};
-
 template <int NT>
 uint32_t few_smem(uint32_t R, uint32_t hd, uint32_t ids, uint32_t cap, bool sc_smem) {
   const int nch = hd >= 64 ? 2 : 1;
@@ -439,21 +473,23 @@ uint32_t few_smem(uint32_t R, uint32_t hd, uint32_t ids, uint32_t cap, bool sc_s
                   : few_layout<NT, 4>(nch, hd, ids, cap, sc_smem).size;
 }
 
-FewPlan plan_few(const ck_paged_cache& c, const ck_paged_batch& b, uint32_t heads, const DeviceFacts& f) {
+FewPlan plan_few(const ck_paged_cache& c, const ck_paged_batch& b, uint32_t heads, const ck_window* window,
+                 const DeviceFacts& f) {
   FewPlan w = {};
   const uint64_t queries = (uint64_t)b.max_new * (heads / c.kv_heads);
   w.R = queries == 1 ? 1 : queries == 2 ? 2 : 4;
   w.z = (uint32_t)((queries + w.R - 1) / w.R);
+  const uint32_t line = window_places(window, b.max_len, w.R - 1);
   // blocks of a cluster: until there are two an SM (one, for sixteen), while each has 256 positions
   const uint64_t items = (uint64_t)b.seqs * c.kv_heads * w.z;
   w.C = 1;
-  while (w.C < 8 && items * w.C < 2ull * f.sms && b.max_len / (2 * w.C) >= 256) w.C *= 2;
-  if (w.C == 8 && items * w.C < (uint64_t)f.sms && b.max_len >= 16 * 256) w.C = kMaxCluster;
-  w.NT = items * w.C <= (uint64_t)f.sms ? kBroad : items * w.C >= 8ull * f.sms && b.max_len <= 512 ? kNarrow : kMiddle;
+  while (w.C < 8 && items * w.C < 2ull * f.sms && line / (2 * w.C) >= 256) w.C *= 2;
+  if (w.C == 8 && items * w.C < (uint64_t)f.sms && line >= 16 * 256) w.C = kMaxCluster;
+  w.NT = items * w.C <= (uint64_t)f.sms ? kBroad : items * w.C >= 8ull * f.sms && line <= 512 ? kNarrow : kMiddle;
   // (whole rounds: what a block's lanes cover at once)
   const uint32_t lanes = c.head_dim == 128 ? 16 : c.head_dim == 64 ? 8 : c.head_dim / 4, round = w.NT / lanes * few_batch(w.NT, w.R);
-  w.cap = ((b.max_len + w.C - 1) / w.C + round - 1) / round * round;
-  w.ids = w.cap / c.page + 2;
+  w.cap = ((line + w.C - 1) / w.C + round - 1) / round * round;
+  w.ids = w.cap / c.page + (whole(window, b.max_len) ? 2 : 4);  // (a window: two runs of pages)
   auto smem = [&](bool sc) {
     return w.NT == kBroad    ? few_smem<kBroad>(w.R, c.head_dim, w.ids, w.cap, sc)
            : w.NT == kMiddle ? few_smem<kMiddle>(w.R, c.head_dim, w.ids, w.cap, sc)
@@ -475,15 +511,15 @@ FewPlan plan_few(const ck_paged_cache& c, const ck_paged_batch& b, uint32_t head
   return w;
 }
 
-template <int LPP, int NCH, int R, int NT>
+template <bool WINDOW, int LPP, int NCH, int R, int NT>
 cudaError_t launch_few(FewParams p, const FewPlan& w, const DeviceFacts& f, cudaStream_t s) {
   static std::atomic<bool> ready[64];
   if (!ready[f.dev].load(std::memory_order_relaxed)) {
     const cudaError_t e =
-        cudaFuncSetAttribute(k_pattn_few<LPP, NCH, R, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, f.optin);
+        cudaFuncSetAttribute(k_pattn_few<LPP, NCH, R, NT, WINDOW>, cudaFuncAttributeMaxDynamicSharedMemorySize, f.optin);
     if (e != cudaSuccess) return e;
     const cudaError_t e16 =  // clusters of sixteen
-        cudaFuncSetAttribute(k_pattn_few<LPP, NCH, R, NT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        cudaFuncSetAttribute(k_pattn_few<LPP, NCH, R, NT, WINDOW>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e16 != cudaSuccess) return e16;
     ready[f.dev].store(true, std::memory_order_relaxed);
   }
@@ -500,27 +536,34 @@ cudaError_t launch_few(FewParams p, const FewPlan& w, const DeviceFacts& f, cuda
   for (p.seq0 = 0; p.seq0 < p.a.batch.seqs; p.seq0 += w.seqs_each)
     for (p.z0 = 0; p.z0 < w.z; p.z0 += w.z_each) {
       cfg.gridDim = dim3(std::min(w.seqs_each, p.a.batch.seqs - p.seq0) * w.C, p.a.pool.kv_heads, std::min(w.z_each, w.z - p.z0));
-      const cudaError_t e = cudaLaunchKernelEx(&cfg, k_pattn_few<LPP, NCH, R, NT>, p);
+      const cudaError_t e = cudaLaunchKernelEx(&cfg, k_pattn_few<LPP, NCH, R, NT, WINDOW>, p);
       if (e != cudaSuccess) return e;
     }
   return cudaSuccess;
 }
 
-template <int R, int NT>
+template <bool WINDOW, int R, int NT>
 cudaError_t launch_few_lpp(const FewParams& p, const FewPlan& w, const DeviceFacts& f, cudaStream_t s) {
   switch (p.a.pool.hd) {
-    case 128: return launch_few<16, 2, R, NT>(p, w, f, s);
-    case 64: return launch_few<8, 2, R, NT>(p, w, f, s);
-    case 32: return launch_few<8, 1, R, NT>(p, w, f, s);
-    default: return launch_few<0, 1, R, NT>(p, w, f, s);
+    case 128: return launch_few<WINDOW, 16, 2, R, NT>(p, w, f, s);
+    case 64: return launch_few<WINDOW, 8, 2, R, NT>(p, w, f, s);
+    case 32: return launch_few<WINDOW, 8, 1, R, NT>(p, w, f, s);
+    default: return launch_few<WINDOW, 0, 1, R, NT>(p, w, f, s);
   }
 }
 
-template <int NT>
+template <bool WINDOW, int NT>
 cudaError_t launch_few_r(const FewParams& p, const FewPlan& w, const DeviceFacts& f, cudaStream_t s) {
-  return w.R == 1   ? launch_few_lpp<1, NT>(p, w, f, s)
-         : w.R == 2 ? launch_few_lpp<2, NT>(p, w, f, s)
-                    : launch_few_lpp<4, NT>(p, w, f, s);
+  return w.R == 1   ? launch_few_lpp<WINDOW, 1, NT>(p, w, f, s)
+         : w.R == 2 ? launch_few_lpp<WINDOW, 2, NT>(p, w, f, s)
+                    : launch_few_lpp<WINDOW, 4, NT>(p, w, f, s);
+}
+
+template <bool WINDOW>
+cudaError_t launch_few_any(const FewParams& p, const FewPlan& w, const DeviceFacts& f, cudaStream_t s) {
+  return w.NT == kBroad    ? launch_few_r<WINDOW, kBroad>(p, w, f, s)
+         : w.NT == kMiddle ? launch_few_r<WINDOW, kMiddle>(p, w, f, s)
+                           : launch_few_r<WINDOW, kNarrow>(p, w, f, s);
 }
 
 }  // namespace
