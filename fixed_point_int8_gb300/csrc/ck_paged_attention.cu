@@ -169,14 +169,14 @@ AttentionPlan attention_plan(const ck_paged_cache& c, const ck_paged_batch& b, u
   w.window = !whole(window, b.max_len);
   w.line = window_places(window, b.max_len, 0);
   w.few = plan_few(c, b, heads, window, f);
-  if (!w.window && c.head_dim >= 64) {
+  if (c.head_dim >= 64) {
     const double tiles = std::ceil((double)b.max_new * (heads / c.kv_heads) / 128) * b.seqs * c.kv_heads;
-    const double few_us = 8 + 0.9e-6 * b.seqs * heads * b.max_new * b.max_len * c.head_dim;
-    const double at = tiles * b.max_len, tiles_us = c.head_dim == 64 ? 30 + 0.66e-3 * at : 34 + 1.06e-3 * at;
+    const double few_us = 8 + 0.9e-6 * b.seqs * heads * b.max_new * w.line * c.head_dim;
+    const double at = tiles * tile_places(c, b, heads, window), tiles_us = c.head_dim == 64 ? 30 + 0.66e-3 * at : 34 + 1.06e-3 * at;
     if (!w.few.use || tiles_us < few_us) {
       int32_t clusters[kTileClusters] = {};
       resident(clusters);
-      w.tiles = plan_tiles(c, b, heads, f, clusters);
+      w.tiles = plan_tiles(c, b, heads, window, f, clusters);
     }
     if (w.tiles.use) w.few.use = false;
   }
@@ -283,7 +283,7 @@ int ck_paged_window_attention(const ck_paged_cache* cache, uint32_t layer, const
                             reinterpret_cast<uint32_t*>(work + plan.tiles.away_off),
                             reinterpret_cast<int32_t*>(work + plan.tiles.scores_off),
                             reinterpret_cast<unsigned long long*>(work + plan.tiles.sums_off)};
-    CKP_CUDA(launch_tiles(tp, plan.tiles, f, s));
+    CKP_CUDA(launch_tiles(tp, plan.tiles, plan.window, f, s));
     rp.scores = reinterpret_cast<long long*>(work + plan.tiles.scores_off);
     rp.any = tp.any;
     rp.away = tp.away;

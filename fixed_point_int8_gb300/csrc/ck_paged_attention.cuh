@@ -65,8 +65,13 @@ struct TilesParams {
 // device could not say; and the plan by them, of host values alone.
 constexpr int kTileClusters = 4;
 void resident_tiles(const ck_paged_cache& c, const DeviceFacts& f, int32_t* out);
-TilesPlan plan_tiles(const ck_paged_cache& c, const ck_paged_batch& b, uint32_t heads, const DeviceFacts& f,
-                     const int32_t* resident);
-cudaError_t launch_tiles(const TilesParams& p, const TilesPlan& w, const DeviceFacts& f, cudaStream_t s);
+TilesPlan plan_tiles(const ck_paged_cache& c, const ck_paged_batch& b, uint32_t heads, const ck_window* window,
+                     const DeviceFacts& f, const int32_t* resident);
+// Places that a tile goes through at most: its 128 queries are of so many tokens.
+inline uint32_t tile_places(const ck_paged_cache& c, const ck_paged_batch& b, uint32_t heads, const ck_window* window) {
+  const uint32_t group = heads / c.kv_heads;
+  return window_places(window, b.max_len, std::min(b.max_new - 1, (126 + group) / group));
+}
+cudaError_t launch_tiles(const TilesParams& p, const TilesPlan& w, bool window, const DeviceFacts& f, cudaStream_t s);
 
 }  // namespace ck

@@ -26,7 +26,9 @@
 // of 32 heads of 128 take 251.  Twice the warps with 64 registers a thread were slower (447 against
 // 388 us, 276 against 255 then), and so were 16-bit places in the table in the scratch for the
 // exponentials (346 against 338, 243 against 234 then).  A thread owns a row (its lane of tensor
-// memory), so maxima and sums need no exchange inside a warp.  A cluster splits a tile's positions,
+// memory), so maxima and sums need no exchange inside a warp.  With a window a tile
+// goes through the places that any of its rows sees (Span), and what a row does not see of them gets a
+// probability of zero.  A cluster splits a tile's positions,
 // which fills the GPU when tiles are few; it exchanges maxima, sums and the 64-bit sums of values
 // through distributed shared memory.
 #include "ck_paged_attention.cuh"
@@ -170,7 +172,7 @@ __device__ __forceinline__ void all_sync(uint32_t C) {  // the cluster's threads
     __syncthreads();
 }
 
-template <int HD>
+template <int HD, bool WINDOW>
 __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_tiles(const TilesParams f) {
   using T = Tile<HD>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -273,10 +275,28 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
       const uint32_t up = q / group + sq.len;
       return up >= sq.count ? up - sq.count + 1 : 0;
     };
-    const uint32_t top = seen_by(last), np = v < queries ? seen_by(v) : 0;
+    uint32_t top = seen_by(last), np = v < queries ? seen_by(v) : 0;
+    // with a window: places from here on, of which the row sees those below np that are below `sinks` or
+    // not below `from`
+    Span span = {0, 0};
+    uint32_t from = 0;
+    if (WINDOW && top) {
+      const uint32_t first = seen_by(v0);
+      span = window_span(p, first ? first - 1 : 0);
+      top -= span.skip;
+      if (np) {
+        from = window_begin(p, np - 1) - span.skip;
+        np -= span.skip;
+      }
+    }
     const uint32_t per = ((top + C - 1) / C + kBlockPos - 1) & ~(kBlockPos - 1);
     const uint32_t c0 = min(top, rank * per), n = min(top, c0 + per) - c0;
     const uint32_t lim = np > c0 ? min(n, np - c0) : 0;  // positions of this block that the row sees
+    const uint32_t early = WINDOW && p.sinks > c0 ? p.sinks - c0 : 0, late = WINDOW && from > c0 ? from - c0 : 0;
+    auto sees = [&](uint32_t at) { return at < lim && (!WINDOW || at < early || at >= late); };
+    auto sees_all = [&](uint32_t at, uint32_t count) {  // of `count` positions
+      return at + count <= lim && (!WINDOW || at >= late || at + count <= early);
+    };
     const uint32_t nt = (n + kTilePos - 1) / kTilePos, all_blocks = (n + kBlockPos - 1) / kBlockPos;
     const uint32_t* table = p.batch.table + (size_t)seq * p.batch.stride;
     if (tid == 0) *bad_s = 0;
@@ -330,17 +350,17 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
     int4 raw[2];
     uint32_t next_id = 0;
     auto page_of = [&](uint32_t at) {  // of position c0 + at
-      return at < n ? __ldg(table + ((c0 + at) >> shift)) : CK_NO_PAGE;
+      return at < n ? __ldg(table + ((WINDOW ? span.position(c0 + at) : c0 + at) >> shift)) : CK_NO_PAGE;
     };
     auto load_keys = [&](uint32_t i) {  // by the page looked up before, and looks the next one up
-      const uint32_t at = i * kTilePos + kpos, t = c0 + at, id = next_id;
+      const uint32_t at = i * kTilePos + kpos, t = WINDOW ? span.position(c0 + at) : c0 + at, id = next_id;
       raw[0] = raw[1] = make_int4(0, 0, 0, 0);
       if (id < p.pool.pages) {
         const int4* src = reinterpret_cast<const int4*>(p.pool.k + page_word(p.pool, id, kvh) +
                                                         (size_t)(t & pmask) * HD + 8 * kchunk);
         raw[0] = __ldg(src);
         raw[1] = __ldg(src + 1);
-      } else if (at < n && ((t & pmask) == 0 || at == 0)) {
+      } else if (at < n && ((t & pmask) == 0 || at == 0 || (WINDOW && c0 + at == span.edge))) {
         note(p.batch, seq, err_key((t >> shift) << shift, p.pool.layer, CK_PAGED_BAD_PAGE, 0));
       }
       next_id = page_of(at + kTilePos);
@@ -435,13 +455,13 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
             if (c[j] != s) c[j] = s < 0 ? INT32_MIN : INT32_MAX;
           }
         }
-        if (at + 8 <= lim) {
+        if (sees_all(at, 8)) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) m = max(m, c[j]);
         } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            if (at + j < lim) m = max(m, c[j]);
+            if (sees(at + j)) m = max(m, c[j]);
         }
         int4* dst = scores + (size_t)(at / 4) * kTileRows + r;
         dst[0] = make_int4(c[0], c[1], c[2], c[3]);
@@ -531,10 +551,10 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
           uint32_t e[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) e[j] = table_s[min(((uint32_t)m - (uint32_t)x[j]) >> 8, 4096u)];
-          if (4 * k + 4 > lim) {  // the last quad may be cut
+          if (!sees_all(4 * k, 4)) {  // the last quad may be cut, and those at a window's ends
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              if (4 * k + j >= lim) e[j] = 0;
+              if (!sees(4 * k + j)) e[j] = 0;
           }
           if (4 * k < lim) {
             z += (unsigned long long)(e[0] + e[1]) + (e[2] + e[3]);
@@ -575,7 +595,7 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
     int2 vraw[8];
     int4 sraw[2 * kChunks];
     auto load_values = [&](uint32_t b) {
-      const uint32_t at = b * kBlockPos + vchunk * 8, t = c0 + at, id = next_id;
+      const uint32_t at = b * kBlockPos + vchunk * 8, t = WINDOW ? span.position(c0 + at) : c0 + at, id = next_id;
 #pragma unroll
       for (int j = 0; j < 8; ++j) vraw[j] = make_int2(0, 0);
       if (id < p.pool.pages) {  // a page holds whole chunks of eight
@@ -784,12 +804,12 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(T::kTmem) : "memory");
 }
 
-template <int HD>
+template <int HD, bool WINDOW>
 cudaError_t configure_tiles(const DeviceFacts& f) {
   static std::atomic<bool> ready[64];
   if (ready[f.dev].load(std::memory_order_relaxed)) return cudaSuccess;
   const cudaError_t e =
-      cudaFuncSetAttribute(k_pattn_tiles<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, Tile<HD>::kSmem);
+      cudaFuncSetAttribute(k_pattn_tiles<HD, WINDOW>, cudaFuncAttributeMaxDynamicSharedMemorySize, Tile<HD>::kSmem);
   if (e == cudaSuccess) ready[f.dev].store(true, std::memory_order_relaxed);
   return e;
 }
@@ -808,19 +828,19 @@ void tiles_config(uint32_t blocks, uint32_t C, cudaLaunchConfig_t* cfg, cudaLaun
 }
 
 // Clusters of C blocks that are resident at once, looked up once for each C (the runtime counts one
-// block an SM; of head size 64 two run).  0 where the lookup fails: no plan then uses that C, and the
+// block an SM; of head size 64 two run; as many of the kernel for windows).  0 where the lookup fails: no plan then uses that C, and the
 // failure is not left for a later call to report.
 template <int HD>
 int32_t resident_clusters(uint32_t C, const DeviceFacts& f) {
   static std::atomic<int> known[64][9];  // the number and one more, zero before
   int n = known[f.dev][C].load(std::memory_order_relaxed) - 1;
   if (n < 0) {
-    cudaError_t e = configure_tiles<HD>(f);
+    cudaError_t e = configure_tiles<HD, false>(f);
     if (e == cudaSuccess) {
       cudaLaunchConfig_t cfg;
       cudaLaunchAttribute attr[1];
       tiles_config<HD>(C, C, &cfg, attr);
-      e = cudaOccupancyMaxActiveClusters(&n, k_pattn_tiles<HD>, &cfg);
+      e = cudaOccupancyMaxActiveClusters(&n, k_pattn_tiles<HD, false>, &cfg);
     }
     if (e != cudaSuccess) {
       cudaGetLastError();
@@ -832,15 +852,15 @@ int32_t resident_clusters(uint32_t C, const DeviceFacts& f) {
   return n;
 }
 
-template <int HD>
+template <int HD, bool WINDOW>
 cudaError_t launch_tiles_hd(const TilesParams& p, const TilesPlan& w, const DeviceFacts& f, cudaStream_t s) {
-  const cudaError_t e = configure_tiles<HD>(f);
+  const cudaError_t e = configure_tiles<HD, WINDOW>(f);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[1];
   tiles_config<HD>(w.clusters * w.C, w.C, &cfg, attr);
   cfg.stream = s;
-  return cudaLaunchKernelEx(&cfg, k_pattn_tiles<HD>, p);
+  return cudaLaunchKernelEx(&cfg, k_pattn_tiles<HD, WINDOW>, p);
 }
 
 }  // namespace
@@ -855,10 +875,11 @@ void resident_tiles(const ck_paged_cache& c, const DeviceFacts& f, int32_t* out)
     out[i] = !tiles_fit(c, f) ? 0 : c.head_dim == 64 ? resident_clusters<64>(1u << i, f) : resident_clusters<128>(1u << i, f);
 }
 
-TilesPlan plan_tiles(const ck_paged_cache& c, const ck_paged_batch& b, uint32_t heads, const DeviceFacts& f,
-                     const int32_t* resident) {
+TilesPlan plan_tiles(const ck_paged_cache& c, const ck_paged_batch& b, uint32_t heads, const ck_window* window,
+                     const DeviceFacts& f, const int32_t* resident) {
   TilesPlan w = {};
   const uint64_t queries = (uint64_t)b.max_new * (heads / c.kv_heads);
+  const uint32_t line = tile_places(c, b, heads, window);
   if (!tiles_fit(c, f)) return w;
   w.tiles = (uint32_t)((queries + kTileRows - 1) / kTileRows);
   const uint64_t items = (uint64_t)b.seqs * c.kv_heads * w.tiles;
@@ -867,13 +888,14 @@ TilesPlan plan_tiles(const ck_paged_cache& c, const ck_paged_batch& b, uint32_t 
   // equal tiles for one sequence; for several, whose lengths differ, three quarters of the bound
   // on average, but never less than the longest.  What surrounds a tile (queries, exchanges,
   // sums) measured as about 200 positions.
+  const double typical = line < b.max_len ? line : 0.75 * line;  // (windows are as long as one another)
   double best = 0;
   for (int i = 0; i < kTileClusters; ++i) {
     if (resident[i] <= 0) continue;
     const uint32_t C = 1u << i;
-    const double each = (double)b.max_len / C + 200, clusters = (double)std::min<uint64_t>(items, resident[i]);
+    const double each = (double)line / C + 200, clusters = (double)std::min<uint64_t>(items, resident[i]);
     const double cost = b.seqs == 1 ? std::ceil(items / clusters) * each
-                                    : std::max(each, items / clusters * (0.75 * b.max_len / C + 200));
+                                    : std::max(each, items / clusters * (typical / C + 200));
     if (!w.use || cost < 0.95 * best) {
       w.use = true;
       best = cost;
@@ -882,7 +904,7 @@ TilesPlan plan_tiles(const ck_paged_cache& c, const ck_paged_batch& b, uint32_t 
     }
   }
   if (!w.use) return w;
-  w.cap = ((b.max_len + w.C - 1) / w.C + kBlockPos - 1) & ~(kBlockPos - 1);
+  w.cap = ((line + w.C - 1) / w.C + kBlockPos - 1) & ~(kBlockPos - 1);
   w.any_off = 0;
   w.away_off = 256;
   w.scores_off = w.away_off + align256(4 * items);
@@ -891,8 +913,9 @@ TilesPlan plan_tiles(const ck_paged_cache& c, const ck_paged_batch& b, uint32_t 
   return w;
 }
 
-cudaError_t launch_tiles(const TilesParams& p, const TilesPlan& w, const DeviceFacts& f, cudaStream_t s) {
-  return p.a.pool.hd == 64 ? launch_tiles_hd<64>(p, w, f, s) : launch_tiles_hd<128>(p, w, f, s);
+cudaError_t launch_tiles(const TilesParams& p, const TilesPlan& w, bool window, const DeviceFacts& f, cudaStream_t s) {
+  if (window) return p.a.pool.hd == 64 ? launch_tiles_hd<64, true>(p, w, f, s) : launch_tiles_hd<128, true>(p, w, f, s);
+  return p.a.pool.hd == 64 ? launch_tiles_hd<64, false>(p, w, f, s) : launch_tiles_hd<128, false>(p, w, f, s);
 }
 
 }  // namespace ck

@@ -82,6 +82,7 @@ WINDOWS = [
     ([900], [3], 4, 4, 32, 8, 24, 257),
     ([50, 60], [1, 1], 4, 4, 64, 16, 100, 8),
     ([50, 60], [1, 1], 4, 4, 64, 16, 4, 2**32 - 1),
+    ([901], [300], 32, 8, 128, 128, 0, 1),
 ]
 # work enough for the tensor-core tiles
 WINDOW_TILES = [
@@ -92,19 +93,32 @@ WINDOW_TILES = [
     ([1077, 530], [90, 2], 48, 3, 64, 32, 1, 256),
     ([300, 1500, 5], [0, 65, 5], 32, 32, 64, 256, 300, 511),
     ([640], [640], 16, 4, 64, 64, 4, 64),
-    ([901], [300], 32, 8, 128, 128, 0, 1),
 ]
 
 
 @pytest.mark.parametrize("lens,news,heads,kv,hd,page,sinks,window", WINDOWS + WINDOW_TILES)
 def test_window_against_the_plain_form(ck, lens, news, heads, kv, hd, page, sinks, window):
     s = Windowed(ck, lens, news, heads, kv, hd, page, sinks, window, seed=hd + len(lens))
+    tiles = ck.paged_attention_work(s.cache, s.batch, heads, window=s.view).numel() > 1 << 20
+    assert tiles == ((lens, news, heads, kv, hd, page, sinks, window) in WINDOW_TILES)
     q, inv = s.queries(), synth.inv_sqrt_head(hd)
     for layer in (0, 1):
         rc, out = s.run(ck, q, inv, layer)
         assert rc == 0
         assert np.array_equal(out.cpu().numpy(), s.attention(layer, q, inv))
     assert s.batch.errors() == [None] * len(lens)
+
+
+@pytest.mark.parametrize("lens,news,heads,kv,hd,page,sinks,window", WINDOW_TILES)
+def test_windowed_tiles_give_the_same_bits_every_time(ck, lens, news, heads, kv, hd, page, sinks, window):
+    import torch
+    s = Windowed(ck, lens, news, heads, kv, hd, page, sinks, window, seed=5)
+    q, exp = cuda(s.queries()), cuda(EXP.view(np.int32))
+    rc, first = ck.paged_attention(s.cache, 0, s.batch, q, exp, 1 << 21, window=s.view)
+    assert rc == 0
+    for _ in range(100):
+        rc, out = ck.paged_attention(s.cache, 0, s.batch, q, exp, 1 << 21, window=s.view)
+        assert rc == 0 and torch.equal(out, first)
 
 
 @pytest.mark.parametrize("new", [1, 70])
