@@ -7,6 +7,8 @@
 // boundary: the sums of top-k's tokens, how many tokens reach the nucleus, and the place at whose
 // tokens the kept ones end, of which the nearest are then chosen by (D, token).  The draw walks
 // the kept tokens in the order of the vocabulary, by each warp's sums.
+#include <type_traits>
+
 #include "ck_paged.cuh"
 
 namespace ck {
@@ -28,17 +30,17 @@ struct SampleParams {
   uint32_t split;  // blocks of a row's cluster
 };
 
-constexpr int kDrawThreads = 256, kDrawWarps = kDrawThreads / 32;
-constexpr uint32_t kPer = 16;                              // logits a thread holds
-constexpr uint32_t kHold = kPer * kDrawThreads;            // and a block
-constexpr uint32_t kBins = 4097, kMine = 17;               // places, and those a thread adds up
+constexpr int kDrawThreads = 512, kDrawWarps = kDrawThreads / 32;
+constexpr int kDrawBlocks = 2;                             // resident on an SM
+constexpr uint32_t kPer = 16, kBatch = 32 * kPer;          // tokens a lane takes at once, and a warp
+constexpr uint32_t kMaxBatches = (1u << 20) / kBatch;
+constexpr uint32_t kBins = 4097, kMine = 9;                // places, and those a thread adds up
 constexpr uint32_t kRoom = kMine * kDrawThreads;
 constexpr uint32_t kList = 256;                            // tokens at the boundary that are ranked by counting
 constexpr uint32_t kMaxSplit = 8;
 constexpr uint32_t kOneQ24 = 1u << 24;
-// distances held in 32 bits: a masked token (or none), and one to be read again
-constexpr uint32_t kMasked = 0xFFFFFFFFu, kFar = 0xFFFFFFFEu;
 constexpr unsigned long long kNoBound = ~0ull;
+static_assert(kRoom >= kBins && kMaxBatches * 8 <= kRoom * 4 && kList <= kDrawThreads, "shared memory");
 
 __device__ __forceinline__ uint32_t remote(const void* p, uint32_t rank) {
   uint32_t a;
@@ -77,26 +79,47 @@ __device__ __forceinline__ long long warp_max(long long v) {
   const uint32_t lo = __reduce_max_sync(0xffffffffu, (int32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
   return (long long)((unsigned long long)(uint32_t)hi << 32 | lo);
 }
-__device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+// The sum of the warp's values, each at most 2^34, by 32-bit reductions.
+__device__ __forceinline__ unsigned long long warp_sum34(unsigned long long v) {
+  const uint32_t lo = __reduce_add_sync(0xffffffffu, (uint32_t)v & 0xFFFFFFu);
+  const uint32_t hi = __reduce_add_sync(0xffffffffu, (uint32_t)(v >> 24));
+  return ((unsigned long long)hi << 24) + lo;
 }
 
-// The place of a distance below 16 temperatures: floor(256 d / t) by the reciprocal r = floor(2^32
-// / t) (2^32 - 1 for t = 1), short of the quotient by less than one.
-__host__ __device__ __forceinline__ uint32_t reciprocal_of(uint32_t t) {
-  return t > 1 ? (uint32_t)((1ull << 32) / t) : 0xFFFFFFFFu;
+// The place of a distance, floor(256 d / t) up to 4096, by one product: with T = t << shift >= 512 and
+// D = min(d, 16 t) << shift it is (D * factor + add) >> (32 + down).  factor is 2^(40 + down) / T rounded
+// up (add 0), which is exact while 16 T times what the rounding adds to factor * T stays below 2^(32 +
+// down), or else rounded down (add = factor / 256: a 256th more in D), which is by the same bound: the two
+// add up to T, and 8 T^2 <= 2^(32 + down) with down = floor(log2 T) - 8.
+struct Places {
+  uint32_t far, factor, shift, down;
+  unsigned long long add;
+};
+__host__ __device__ inline Places places_of(uint32_t t) {
+  Places s;
+  s.far = 16 * t;
+  s.shift = t < 512 ? 9 : 0;
+  const unsigned long long T = (unsigned long long)t << s.shift;
+  s.down = 0;
+  while (T >> (s.down + 10)) ++s.down;  // floor(log2 T) - 9 ..
+  ++s.down;
+  unsigned long long N = 1ull << (40 + s.down), up = (N + T - 1) / T;
+  if (up >> 32) {  // (a power of two)
+    --s.down;
+    N >>= 1;
+    up = (N + T - 1) / T;
+  }
+  s.factor = (uint32_t)up;
+  s.add = 0;
+  if (16 * T * (up * T - N) >= 1ull << (32 + s.down)) {
+    s.factor = (uint32_t)(N / T);
+    s.add = s.factor >> 8;
+  }
+  return s;
 }
-__host__ __device__ __forceinline__ uint32_t place_of(uint32_t d, uint32_t t, uint32_t r) {
-  if (d >= 16 * t) return 4096;
-  const uint32_t n = d << 8;
-#ifdef __CUDA_ARCH__
-  const uint32_t q = __umulhi(n, r);
-#else
-  const uint32_t q = (uint32_t)(((uint64_t)n * r) >> 32);
-#endif
-  return q + (n - q * t >= t);
+__host__ __device__ __forceinline__ uint32_t place_of(uint32_t d, const Places& s) {
+  const uint32_t D = (d < s.far ? d : s.far) << s.shift;
+  return (uint32_t)(((unsigned long long)D * s.factor + s.add) >> 32) >> s.down;
 }
 // The first distance of a place.
 __device__ __forceinline__ unsigned long long first_of(uint32_t place, uint32_t t) {
@@ -115,164 +138,127 @@ __device__ __forceinline__ unsigned long long tail_first(uint32_t b) {
   return (1ull << e) + ((unsigned long long)(b & 63u) << (e - 6));
 }
 
-// What is kept: tokens nearer than d, and those at d up to the token.
+// A cluster of blocks a row (one block, where rows fill the GPU), warps taking batches of 512 tokens
+// in turn.  The logits are read in each pass: the first from HBM, the next from L2.  Rows whose logits fit
+// 32 bits (any that are not masked, in practice) go through them as 32-bit words.
+struct Shared {
+  uint32_t hist[kRoom];   // counts of this block; later the weights that are kept, by batch
+  uint32_t full[kRoom];   // counts of the row
+  uint32_t table[kRoom];  // the exponentials
+  unsigned long long near_d[kList];
+  uint32_t near_i[kList], n_near;
+  unsigned long long red[kDrawWarps], peak, found[3];
+  uint32_t red_c[kDrawWarps], red_i[kDrawWarps], least, tokens, wide;
+  uint32_t f_place, f_count, f_rest;
+  Places places;
+};
+
+// What is kept: tokens nearer than `first`, and of those from there to `last` the ones up to (d, token).
 struct Bound {
-  unsigned long long d;
+  unsigned long long first, last, d;
   uint32_t token;
 };
 
-template <bool ONE>
-__global__ void __launch_bounds__(kDrawThreads) k_sample_rows(const SampleParams p) {
-  __shared__ uint32_t hist[kRoom], full[kRoom];
-  __shared__ unsigned long long near_d[kList];
-  __shared__ uint32_t near_i[kList], n_near;
-  __shared__ unsigned long long sums[kMaxSplit * kDrawWarps], red[kDrawWarps], peak, found[3];
-  __shared__ uint32_t counts[kMaxSplit * kDrawWarps], red_c[kDrawWarps], red_i[kDrawWarps], least;
-  __shared__ uint32_t f_place, f_count, f_rest;
+template <bool WIDE>
+__device__ __forceinline__ void sample_row(const SampleParams& p, Shared& sm, long long m, uint32_t t, uint32_t top_k,
+                                           uint32_t top_p, uint32_t min_p, bool filtered) {
   const uint32_t S = p.split, rank = blockIdx.x % S, row = blockIdx.x / S;
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t per = (p.vocab + S - 1) / S, v0 = min(p.vocab, rank * per), n = min(p.vocab, v0 + per) - v0;
-  // a warp's tokens follow one another
-  const uint32_t each = ((n + kDrawWarps - 1) / kDrawWarps + 31) & ~31u, w0 = min(n, warp * each), wn = min(n, w0 + each) - w0;
-  const long long* l = reinterpret_cast<const long long*>(p.logits) + (size_t)row * p.stride + v0 + w0;
-  const uint32_t first = v0 + w0;  // the warp's first token
-
-  long long x[kPer];
-  auto load = [&](uint32_t base) {
-#pragma unroll
-    for (uint32_t j = 0; j < kPer; ++j) {
-      const uint32_t i = base + 32 * j + lane;
-      x[j] = i < wn ? __ldg(l + i) : LLONG_MIN;
-    }
+  const long long* l = reinterpret_cast<const long long*>(p.logits) + (size_t)row * p.stride;
+  const uint32_t batches = (p.vocab + kBatch - 1) / kBatch;
+  using Word = typename std::conditional<WIDE, long long, int32_t>::type;
+  using Distance = typename std::conditional<WIDE, unsigned long long, uint32_t>::type;
+  auto word = [&](uint32_t i) -> Word {  // (of a narrow logit its low half)
+    return WIDE ? (Word)__ldg(l + i) : (Word)__ldg(reinterpret_cast<const int32_t*>(l + i));
   };
-  if (ONE) load(0);
-  const uint32_t t = p.temperature[row];
-  const uint32_t top_k = p.top_k ? p.top_k[row] : 0, top_p = p.top_p ? min(p.top_p[row], kOneQ24) : kOneQ24;
-  const uint32_t min_p = p.min_p ? min(p.min_p[row], kOneQ24) : 0;
-  const bool filtered = (top_k != 0 && top_k < p.vocab) || top_p < kOneQ24 || min_p != 0;
-  auto weight_at = [&](uint32_t place) { return min(__ldg(p.exp_tab + place), 1u << 30); };
-  for (uint32_t i = tid; i < kRoom; i += kDrawThreads) hist[i] = filtered || i >= kBins ? 0 : weight_at(i);
-  if (tid == 0) n_near = 0;
-
-  // ---- the largest logit
-  long long m = LLONG_MIN;
-  for (uint32_t base = 0; base < (ONE ? 1 : wn); base += 32 * kPer) {
-    if (!ONE) load(base);
+  auto distance = [&](Word x) -> Distance { return (Distance)m - (Distance)x; };
+  auto there = [&](Word x) { return !WIDE || x != (Word)LLONG_MIN; };
+  const Places places = sm.places;
+  auto place = [&](Distance d) { return place_of(WIDE && d >> 31 ? 0x7FFFFFFFu : (uint32_t)d, places); };
+  // every batch of this warp: f(its number, its first token, whether it is whole, its words)
+  auto each_batch = [&](auto f) {
+    for (uint32_t b = rank * kDrawWarps + warp; b < batches; b += S * kDrawWarps) {
+      const uint32_t i0 = b * kBatch + lane;
+      Word x[kPer];
+      if (b * kBatch + kBatch <= p.vocab) {
 #pragma unroll
-    for (uint32_t j = 0; j < kPer; ++j) m = max(m, x[j]);
-  }
-  m = warp_max(m);
-  if (lane == 0) red[warp] = (unsigned long long)m;
-  __syncthreads();
+        for (uint32_t j = 0; j < kPer; ++j) x[j] = word(i0 + 32 * j);
+        f(b, i0, true, x);
+      } else {
 #pragma unroll
-  for (int w = 0; w < kDrawWarps; ++w) m = max(m, (long long)red[w]);
-  if (tid == 0) peak = (unsigned long long)m;
-  row_sync(S);
-  for (uint32_t k = 0; S > 1 && k < S; ++k) m = max(m, (long long)remote_u64(&peak, k));
-  if (m == LLONG_MIN || t > kMaxTemperature) {  // nothing to choose from (for every block of the row)
-    row_sync(S);
-    if (rank == 0 && tid == 0) {
-      p.token[row] = CK_NO_TOKEN;
-      p.prob[row] = 0;
-      p.kept[row] = 0;
-    }
-    return;
-  }
-
-  // ---- distances, in 32 bits
-  uint32_t d[kPer];
-  auto distances = [&] {
-#pragma unroll
-    for (uint32_t j = 0; j < kPer; ++j) {
-      const unsigned long long w = (unsigned long long)m - (unsigned long long)x[j];
-      d[j] = x[j] == LLONG_MIN ? kMasked : w < kFar ? (uint32_t)w : kFar;
-    }
-  };
-  if (ONE) distances();
-  // every token of this thread that is not masked: f(distance in 32 bits, its number in the warp)
-  auto all = [&](auto f) {
-    for (uint32_t base = 0; base < (ONE ? 1 : wn); base += 32 * kPer) {
-      if (!ONE) {
-        load(base);
-        distances();
+        for (uint32_t j = 0; j < kPer; ++j) x[j] = i0 + 32 * j < p.vocab ? word(i0 + 32 * j) : 0;
+        f(b, i0, false, x);
       }
+    }
+  };
+  // every token of this thread that is not masked: f(distance, token)
+  auto each = [&](auto f) {
+    each_batch([&](uint32_t, uint32_t i0, bool whole, Word (&x)[kPer]) {
 #pragma unroll
       for (uint32_t j = 0; j < kPer; ++j)
-        if (d[j] != kMasked) f(d[j], base + 32 * j + lane);
-    }
-  };
-  auto exact = [&](uint32_t w, uint32_t i) {
-    return w != kFar ? (unsigned long long)w : (unsigned long long)m - (unsigned long long)__ldg(l + i);
+        if ((whole || i0 + 32 * j < p.vocab) && there(x[j])) f(distance(x[j]), i0 + 32 * j);
+    });
   };
 
   if (t == 0) {  // the first largest
     uint32_t at = 0xFFFFFFFFu;
-    all([&](uint32_t w, uint32_t i) {
-      if (w == 0) at = min(at, first + i);
+    each([&](Distance d, uint32_t i) {
+      if (d == 0) at = min(at, i);
     });
     at = __reduce_min_sync(0xffffffffu, at);
-    if (lane == 0) red_i[warp] = at;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kDrawWarps; ++w) at = min(at, red_i[w]);
-    if (tid == 0) least = at;
-    row_sync(S);
-    if (rank == 0) {
-      for (uint32_t k = 0; S > 1 && k < S; ++k) at = min(at, remote_u32(&least, k));
-      if (tid == 0) {
-        p.token[row] = at;
-        p.prob[row] = kOneQ24;
-        p.kept[row] = 1;
-      }
+    if (lane == 0) {
+      if (S > 1)
+        asm volatile("red.shared::cluster.min.u32 [%0], %1;" ::"r"(remote(&sm.least, 0)), "r"(at) : "memory");
+      else
+        atomicMin(&sm.least, at);
     }
-    row_sync(S);  // no block leaves while another reads its minimum
+    row_sync(S);
+    if (rank == 0 && tid == 0) {
+      p.token[row] = sm.least;
+      p.prob[row] = kOneQ24;
+      p.kept[row] = 1;
+    }
     return;
   }
-  const uint32_t rt = reciprocal_of(t);
 
-  Bound bound = {kNoBound, 0xFFFFFFFFu};
-  uint32_t kept = 0;
+  Bound bound = {kNoBound, kNoBound, kNoBound, 0xFFFFFFFFu};
+  uint32_t kept = 0, listed = 0, rest = 0;
+  const uint32_t* full = S > 1 ? sm.full : sm.hist;
   if (filtered) {
-    // the row's counts of the buckets that f names, in every block's `full`
+    // the row's counts of the buckets that f names
     auto count_all = [&](auto f) {
       uint32_t last = 0;
-      all([&](uint32_t w, uint32_t i) {
-        const uint32_t b = f(w, i);
-        if (b == kBins - 1)
-          ++last;  // (often most of them)
-        else if (b < kBins)
-          atomicAdd(hist + b, 1u);
+      each([&](Distance d, uint32_t i) {
+        const uint32_t b = f(d, i);
+        if (b < kBins - 1)
+          atomicAdd(sm.hist + b, 1u);
+        else
+          last += b == kBins - 1;  // (often most of them)
       });
       last = __reduce_add_sync(0xffffffffu, last);
-      if (lane == 0 && last) atomicAdd(hist + kBins - 1, last);
+      if (lane == 0 && last) atomicAdd(sm.hist + kBins - 1, last);
       row_sync(S);
-      const uint32_t width = (kBins + S - 1) / S, b1 = min(kBins, (rank + 1) * width);
+      if (S == 1) return;
+      const uint32_t width = (kRoom + S - 1) / S, b1 = min(kRoom, (rank + 1) * width);
       for (uint32_t b = rank * width + tid; b < b1; b += kDrawThreads) {
         uint32_t part[kMaxSplit], c = 0;
 #pragma unroll
-        for (uint32_t k = 0; k < kMaxSplit; ++k) part[k] = k < S ? (S > 1 ? remote_u32(hist + b, k) : hist[b]) : 0;
+        for (uint32_t k = 0; k < kMaxSplit; ++k) part[k] = k < S ? remote_u32(sm.hist + b, k) : 0;
 #pragma unroll
         for (uint32_t k = 0; k < kMaxSplit; ++k) c += part[k];
-        for (uint32_t k = 0; k < S; ++k)
-          if (S > 1)
-            put_u32(full + b, k, c);
-          else
-            full[b] = c;
+        for (uint32_t k = 0; k < S; ++k) put_u32(sm.full + b, k, c);
       }
-      for (uint32_t b = kBins + tid; b < kRoom; b += kDrawThreads) full[b] = 0;
       row_sync(S);
     };
-    count_all([&](uint32_t w, uint32_t) { return place_of(w, t, rt); });
-    for (uint32_t i = tid; i < kBins; i += kDrawThreads) hist[i] = weight_at(i);
-    __syncthreads();
+    count_all([&](Distance d, uint32_t) { return place(d); });
     // counts and weights before this thread's places
     const uint32_t b0 = tid * kMine;
     uint32_t mine = 0, near = 0;
     unsigned long long heavy = 0;
-    const unsigned long long least_w = (unsigned long long)min_p * hist[0];
+    const unsigned long long least_w = (unsigned long long)min_p * sm.table[0];
 #pragma unroll
     for (uint32_t j = 0; j < kMine; ++j) {
-      const uint32_t c = full[b0 + j], e = b0 + j < kBins ? hist[b0 + j] : 0;
+      const uint32_t c = full[b0 + j], e = sm.table[b0 + j];
       mine += c;
       heavy += (unsigned long long)c * e;
       if ((unsigned long long)e << 24 >= least_w) near += c;
@@ -281,9 +267,9 @@ __global__ void __launch_bounds__(kDrawThreads) k_sample_rows(const SampleParams
     const unsigned long long weight_in = warp_inclusive_scan(heavy, lane);
     near = __reduce_add_sync(0xffffffffu, near);
     if (lane == 31) {
-      red_c[warp] = count_in;
-      red[warp] = weight_in;
-      red_i[warp] = near;
+      sm.red_c[warp] = count_in;
+      sm.red[warp] = weight_in;
+      sm.red_i[warp] = near;
     }
     __syncthreads();
     uint32_t before = count_in - mine, total = 0;
@@ -292,12 +278,12 @@ __global__ void __launch_bounds__(kDrawThreads) k_sample_rows(const SampleParams
 #pragma unroll
     for (uint32_t w = 0; w < kDrawWarps; ++w) {
       if (w < warp) {
-        before += red_c[w];
-        weight += red[w];
+        before += sm.red_c[w];
+        weight += sm.red[w];
       }
-      total += red_c[w];
-      z += red[w];
-      near += red_i[w];
+      total += sm.red_c[w];
+      z += sm.red[w];
+      near += sm.red_i[w];
     }
     uint32_t keep = top_k ? min(top_k, total) : total;
     if (top_p < kOneQ24) {
@@ -307,24 +293,23 @@ __global__ void __launch_bounds__(kDrawThreads) k_sample_rows(const SampleParams
           unsigned long long w = weight;
           for (uint32_t j = 0; j < kMine; ++j) {
             const uint32_t take = min(full[b0 + j], keep - c);
-            w += (unsigned long long)take * hist[b0 + j];
+            w += (unsigned long long)take * sm.table[b0 + j];
             c += take;
           }
-          found[0] = w;
+          sm.found[0] = w;
         }
         __syncthreads();
-        z = found[0];
+        z = sm.found[0];
       }
       const unsigned long long target = (z >> 24) * top_p + (((z & (kOneQ24 - 1)) * top_p) >> 24);
-      if (tid == 0) found[1] = 1;  // (a target of zero)
-      __syncthreads();
+      if (tid == 0 && target == 0) sm.found[1] = 1;
       if (weight < target && target <= weight + heavy) {
         uint32_t c = before;
         unsigned long long w = weight;
         for (uint32_t j = 0; j < kMine; ++j) {
-          const unsigned long long here = (unsigned long long)full[b0 + j] * hist[b0 + j];
+          const unsigned long long here = (unsigned long long)full[b0 + j] * sm.table[b0 + j];
           if (w + here >= target) {
-            found[1] = c + (target - w + hist[b0 + j] - 1) / hist[b0 + j];
+            sm.found[1] = c + (target - w + sm.table[b0 + j] - 1) / sm.table[b0 + j];
             break;
           }
           w += here;
@@ -332,168 +317,187 @@ __global__ void __launch_bounds__(kDrawThreads) k_sample_rows(const SampleParams
         }
       }
       __syncthreads();
-      keep = min(keep, (uint32_t)found[1]);
+      keep = min(keep, (uint32_t)sm.found[1]);
     }
     if (min_p) keep = max(1u, min(keep, near));
     // the place at which the kept ones end, and how many of it
     if (before < keep && keep <= before + mine) {
       uint32_t c = before, j = 0;
       while (c + full[b0 + j] < keep) c += full[b0 + j++];
-      f_place = b0 + j;
-      f_count = full[b0 + j];
-      f_rest = keep - c;
+      sm.f_place = b0 + j;
+      sm.f_count = full[b0 + j];
+      sm.f_rest = keep - c;
     }
     __syncthreads();
     kept = keep;
-    const uint32_t place = f_place;
-    uint32_t among = f_count, rest = f_rest;
-    unsigned long long lo = first_of(place, t), span = place < 4096 ? first_of(place + 1, t) - lo : 0 - lo;  // (2^64 - lo)
-    bound.d = place < 4096 ? lo + span - 1 : kNoBound;
-    // the nearest `rest` of the `among` at distances lo .. lo + span - 1, by distance and then by token
-    bool by_token = false, tail = place == 4096;
-    uint32_t t_lo = 0, t_span = p.vocab;
-    while (rest < among) {
-      if (!by_token && span == 1) by_token = true;
-      auto in = [&](uint32_t w, uint32_t i, unsigned long long* at) {
-        const unsigned long long e = exact(w, i);
-        *at = by_token ? first + i - t_lo : e - lo;
-        return e >= lo && e - lo < span && (!by_token || *at < t_span);
-      };
-      if (among <= kList) {
-        all([&](uint32_t w, uint32_t i) {
-          unsigned long long at;
-          if (!in(w, i, &at)) return;
-          const unsigned long long e = exact(w, i);
-          const uint32_t to = S > 1 ? remote_count(&n_near, 0) : atomicAdd(&n_near, 1u);
-          for (uint32_t k = 0; k < S; ++k) {
-            if (S > 1) {
-              put_u64(near_d + to, k, e);
-              put_u32(near_i + to, k, first + i);
-            } else {
-              near_d[to] = e;
-              near_i[to] = first + i;
-            }
-          }
+    const uint32_t end = sm.f_place;
+    uint32_t among = sm.f_count;
+    rest = sm.f_rest;
+    unsigned long long lo = first_of(end, t), span = end < 4096 ? first_of(end + 1, t) - lo : 0 - lo;  // (2^64 - lo)
+    if (rest == among) {
+      bound.first = end < 4096 ? lo + span : kNoBound;
+      bound.last = bound.d = end < 4096 ? lo + span - 1 : kNoBound;
+    } else if (among <= kList) {
+      listed = among;
+      bound.first = lo;
+      bound.last = lo + (span - 1);
+    } else {
+      // the nearest `rest` of the `among` at distances lo .. lo + span - 1, by distance and then by token: a step
+      // narrows either to one of up to 4,096 buckets
+      bool by_token = false, tail = end == 4096;
+      uint32_t t_lo = 0, t_span = p.vocab;
+      while (rest < among) {
+        if (!by_token && span == 1) by_token = true;
+        if (by_token && t_span == 1) break;  // (one token at one distance: not reached)
+        const unsigned long long range = by_token ? t_span : span;
+        uint32_t shift = 0;
+        while (((range - 1) >> shift) >= 4096) ++shift;
+        __syncthreads();  // the counts have been read
+        for (uint32_t i = tid; i < kRoom; i += kDrawThreads) sm.hist[i] = 0;
+        __syncthreads();
+        count_all([&](Distance d, uint32_t i) {
+          const unsigned long long at = by_token ? i - t_lo : d - lo;
+          if (d < lo || d - lo >= span || (by_token && (i < t_lo || at >= t_span))) return kBins;
+          return tail ? tail_bucket(at) : (uint32_t)(at >> shift);
         });
-        row_sync(S);
-        if (tid < among) {
-          const unsigned long long e = near_d[tid];
-          const uint32_t i = near_i[tid];
-          uint32_t r = 0;
-          for (uint32_t k = 0; k < among; ++k) r += near_d[k] < e || (near_d[k] == e && near_i[k] < i);
-          if (r == rest - 1) {
-            found[2] = e;
-            least = i;
-          }
+        uint32_t own = 0;
+        for (uint32_t j = 0; j < kMine; ++j) own += full[b0 + j];
+        const uint32_t upto = (uint32_t)warp_inclusive_scan((unsigned long long)own, lane);
+        if (lane == 31) sm.red_c[warp] = upto;
+        __syncthreads();
+        uint32_t c = upto - own;
+        for (uint32_t w = 0; w < warp; ++w) c += sm.red_c[w];
+        if (c < rest && rest <= c + own) {
+          uint32_t j = 0;
+          while (c + full[b0 + j] < rest) c += full[b0 + j++];
+          sm.f_place = b0 + j;
+          sm.f_count = full[b0 + j];
+          sm.f_rest = rest - c;
         }
         __syncthreads();
-        bound = {found[2], least};
-        break;
+        const uint32_t b = sm.f_place;
+        among = sm.f_count;
+        rest = sm.f_rest;
+        if (by_token) {
+          t_lo += b << shift;
+          t_span = min(1u << shift, t_span - (b << shift));
+        } else {
+          const unsigned long long from = tail ? tail_first(b) : (unsigned long long)b << shift;
+          const unsigned long long wide = tail ? (b < 64 ? 1ull : 1ull << ((b >> 6) - 1)) : 1ull << shift;
+          span = min(wide, span - from);
+          lo += from;
+          tail = false;
+        }
       }
-      // one more step towards it, in up to 4,096 buckets
-      const unsigned long long range = by_token ? t_span : span;
-      uint32_t shift = 0;
-      while (((range - 1) >> shift) >= 4096) ++shift;
-      for (uint32_t i = tid; i < kRoom; i += kDrawThreads) hist[i] = 0;
-      __syncthreads();
-      count_all([&](uint32_t w, uint32_t i) {
-        unsigned long long at;
-        if (!in(w, i, &at)) return kBins;
-        return tail ? tail_bucket(at) : (uint32_t)(at >> shift);
-      });
-      uint32_t own = 0;
-      for (uint32_t j = 0; j < kMine; ++j) own += full[b0 + j];
-      const uint32_t upto = (uint32_t)warp_inclusive_scan((unsigned long long)own, lane);
-      if (lane == 31) red_c[warp] = upto;
-      __syncthreads();
-      uint32_t c = upto - own;
-      for (uint32_t w = 0; w < warp; ++w) c += red_c[w];
-      if (c < rest && rest <= c + own) {
-        uint32_t j = 0;
-        while (c + full[b0 + j] < rest) c += full[b0 + j++];
-        f_place = b0 + j;
-        f_count = full[b0 + j];
-        f_rest = rest - c;
-      }
-      __syncthreads();
-      const uint32_t b = f_place;
-      among = f_count;
-      rest = f_rest;
-      if (by_token) {
-        t_lo += b << shift;
-        t_span = min(1u << shift, t_span - (b << shift));
-        bound.token = t_lo + t_span - 1;
-        bound.d = lo;
-      } else {
-        const unsigned long long from = tail ? tail_first(b) : (unsigned long long)b << shift;
-        const unsigned long long wide = tail ? (b < 64 ? 1ull : 1ull << ((b >> 6) - 1)) : 1ull << shift;
-        span = min(wide, span - from);
-        lo += from;
-        bound.d = lo + span - 1;
-        tail = false;
-      }
-      __syncthreads();
+      bound = {lo, lo + (span - 1), lo + (span - 1), by_token ? t_lo + t_span - 1 : 0xFFFFFFFFu};
     }
+    if (S == 1) __syncthreads();  // (the counts have been read: the weights by batch take their place)
   }
 
-  // ---- the weights that are kept, by warp
-  auto weight_of = [&](uint32_t w, uint32_t i) -> uint32_t {
-    if (filtered) {
-      const unsigned long long e = bound.d >= kFar ? exact(w, i) : w;
-      if (e > bound.d || (e == bound.d && first + i > bound.token)) return 0;
-      return weight_at(place_of(w, t, rt));
+  // ---- the weights that are kept, by batch, and the tokens at the boundary: all to the first block
+  unsigned long long* weights = reinterpret_cast<unsigned long long*>(sm.hist);
+  uint32_t tokens = 0;
+  each_batch([&](uint32_t b, uint32_t i0, bool whole, Word (&x)[kPer]) {
+    unsigned long long sum = 0;
+#pragma unroll
+    for (uint32_t j = 0; j < kPer; ++j) {
+      if ((!whole && i0 + 32 * j >= p.vocab) || !there(x[j])) continue;
+      const Distance d = distance(x[j]);
+      if (!filtered) {
+        sum += sm.table[place(d)];
+        if (WIDE) ++tokens;
+      } else if (d <= bound.last) {
+        if (d < bound.first || (!listed && (d < bound.d || (d == bound.d && i0 + 32 * j <= bound.token)))) {
+          sum += sm.table[place(d)];
+        } else if (listed) {
+          const uint32_t to = S > 1 ? remote_count(&sm.n_near, 0) : atomicAdd(&sm.n_near, 1u);
+          if (S > 1) {
+            put_u64(sm.near_d + to, 0, d);
+            put_u32(sm.near_i + to, 0, i0 + 32 * j);
+          } else {
+            sm.near_d[to] = d;
+            sm.near_i[to] = i0 + 32 * j;
+          }
+        }
+      }
     }
-    return hist[place_of(w, t, rt)];
-  };
-  unsigned long long sum = 0;
-  uint32_t some = 0;
-  all([&](uint32_t w, uint32_t i) {
-    sum += weight_of(w, i);
-    ++some;
+    if (!filtered || __any_sync(0xffffffffu, sum != 0)) sum = warp_sum34(sum);
+    if (lane == 0) {
+      if (S > 1)
+        put_u64(weights + b, 0, sum);
+      else
+        weights[b] = sum;
+    }
   });
-  sum = warp_sum(sum);
-  some = __reduce_add_sync(0xffffffffu, some);
-  if (lane < S) {  // to every block of the row
-    if (S > 1) {
-      put_u64(sums + rank * kDrawWarps + warp, lane, sum);
-      put_u32(counts + rank * kDrawWarps + warp, lane, some);
-    } else {
-      sums[warp] = sum;
-      counts[warp] = some;
+  if (WIDE && !filtered) {
+    tokens = __reduce_add_sync(0xffffffffu, tokens);
+    if (lane == 0) {
+      if (S > 1)
+        asm volatile("red.shared::cluster.add.u32 [%0], %1;" ::"r"(remote(&sm.tokens, 0)), "r"(tokens) : "memory");
+      else
+        atomicAdd(&sm.tokens, tokens);
     }
   }
   row_sync(S);
-  unsigned long long z = 0, ahead = 0;
-  uint32_t tokens = 0;
-  for (uint32_t k = 0; k < S * kDrawWarps; ++k) {
-    if (k < rank * kDrawWarps + warp) ahead += sums[k];
-    z += sums[k];
-    tokens += counts[k];
+  if (rank != 0) return;
+  if (listed) {  // the nearest `rest` of them, by distance and then by token
+    if (tid < listed) {
+      const unsigned long long d = sm.near_d[tid];
+      const uint32_t i = sm.near_i[tid];
+      uint32_t r = 0;
+      for (uint32_t k = 0; k < listed; ++k) r += sm.near_d[k] < d || (sm.near_d[k] == d && sm.near_i[k] < i);
+      if (r < rest) atomicAdd(weights + i / kBatch, (unsigned long long)sm.table[place((Distance)d)]);
+      if (r == rest - 1) {
+        sm.found[2] = d;
+        sm.least = i;
+      }
+    }
+    __syncthreads();
+    bound.d = sm.found[2];
+    bound.token = sm.least;
   }
+  if (warp != 0) return;
+  // ---- the draw, by the first warp: the lane whose batches hold it, the batch, its 32 tokens, the token
+  const uint32_t own = (batches + 31) / 32, g0 = min(batches, lane * own), g1 = min(batches, g0 + own);
+  unsigned long long sum = 0;
+  for (uint32_t g = g0; g < g1; ++g) sum += weights[g];
+  const unsigned long long upto = warp_inclusive_scan(sum, lane), z = __shfl_sync(0xffffffffu, upto, 31);
   if (z == 0) {  // (a table of zeros)
-    if (rank == 0 && tid == 0) {
+    if (lane == 0) {
       p.token[row] = CK_NO_TOKEN;
       p.prob[row] = 0;
       p.kept[row] = 0;
     }
     return;
   }
-  const unsigned long long r = p.random[row] % z;
-  if (r < ahead || r - ahead >= sum) return;
-  // ---- this warp's tokens hold the draw
-  unsigned long long rem = r - ahead;
-  for (uint32_t i0 = 0; i0 < wn; i0 += 32) {
-    const uint32_t i = i0 + lane;
-    const long long y = i < wn ? __ldg(l + i) : LLONG_MIN;
-    const unsigned long long w = (unsigned long long)m - (unsigned long long)y;
-    const uint32_t e = y == LLONG_MIN ? 0 : weight_of(w < kFar ? (uint32_t)w : kFar, i);
-    const unsigned long long upto = warp_inclusive_scan((unsigned long long)e, lane);
-    const unsigned long long here = __shfl_sync(0xffffffffu, upto, 31);
+  const unsigned long long draw = p.random[row] % z;
+  const int holder = __ffs((int)__ballot_sync(0xffffffffu, upto > draw)) - 1;
+  unsigned long long rem = draw - __shfl_sync(0xffffffffu, upto - sum, holder);
+  uint32_t batch = g0;
+  if ((int)lane == holder)
+    while (rem >= weights[batch]) rem -= weights[batch++];
+  rem = __shfl_sync(0xffffffffu, rem, holder);
+  batch = __shfl_sync(0xffffffffu, batch, holder);
+  const uint32_t i0 = batch * kBatch + lane;
+  uint32_t e[kPer];
+#pragma unroll
+  for (uint32_t j = 0; j < kPer; ++j) {
+    const uint32_t i = i0 + 32 * j;
+    const Word x = i < p.vocab ? word(i) : 0;
+    const Distance d = distance(x);
+    const bool in = i < p.vocab && there(x) &&
+                    (!filtered || d < bound.first || (d <= bound.last && (d < bound.d || (d == bound.d && i <= bound.token))));
+    e[j] = in ? sm.table[place(d)] : 0;
+  }
+#pragma unroll
+  for (uint32_t j = 0; j < kPer; ++j) {
+    const unsigned long long here = warp_sum34(e[j]);
     if (rem < here) {
-      if (lane == (uint32_t)__ffs((int)__ballot_sync(0xffffffffu, upto > rem)) - 1) {
-        p.token[row] = first + i;
-        p.prob[row] = (uint32_t)(((unsigned long long)e << 24) / z);
-        p.kept[row] = filtered ? kept : tokens;
+      const unsigned long long to = warp_inclusive_scan((unsigned long long)e[j], lane);
+      if (lane == (uint32_t)__ffs((int)__ballot_sync(0xffffffffu, to > rem)) - 1) {
+        p.token[row] = i0 + 32 * j;
+        p.prob[row] = (uint32_t)(((unsigned long long)e[j] << 24) / z);
+        p.kept[row] = filtered ? kept : WIDE ? sm.tokens : p.vocab;
       }
       return;
     }
@@ -501,9 +505,124 @@ __global__ void __launch_bounds__(kDrawThreads) k_sample_rows(const SampleParams
   }
 }
 
-cudaError_t launch_sample(const SampleParams& p, cudaStream_t s) {
-  k_sample_rows<false><<<p.rows, kDrawThreads, 0, s>>>(p);
-  return cudaGetLastError();
+__global__ void __launch_bounds__(kDrawThreads, kDrawBlocks) k_sample_rows(const SampleParams p) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  Shared& sm = *reinterpret_cast<Shared*>(smem);
+  const uint32_t S = p.split, rank = blockIdx.x % S, row = blockIdx.x / S;
+  const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const long long* l = reinterpret_cast<const long long*>(p.logits) + (size_t)row * p.stride;
+  const uint32_t batches = (p.vocab + kBatch - 1) / kBatch;
+  const uint32_t t = p.temperature[row];
+  const uint32_t top_k = p.top_k ? p.top_k[row] : 0, top_p = p.top_p ? min(p.top_p[row], kOneQ24) : kOneQ24;
+  const uint32_t min_p = p.min_p ? min(p.min_p[row], kOneQ24) : 0;
+  const bool filtered = (top_k != 0 && top_k < p.vocab) || top_p < kOneQ24 || min_p != 0;
+  // ---- the largest logit, of 32 bits, and whether any has more
+  int32_t m32 = INT32_MIN, more = 0;
+  for (uint32_t b = rank * kDrawWarps + warp; b < batches; b += S * kDrawWarps) {
+    const uint32_t i0 = b * kBatch + lane;
+    long long x[kPer];
+#pragma unroll
+    for (uint32_t j = 0; j < kPer; ++j) x[j] = i0 + 32 * j < p.vocab ? __ldg(l + i0 + 32 * j) : (long long)INT32_MIN;
+#pragma unroll
+    for (uint32_t j = 0; j < kPer; ++j) {
+      m32 = max(m32, (int32_t)x[j]);
+      more |= (int32_t)(x[j] >> 32) ^ ((int32_t)x[j] >> 31);
+    }
+  }
+  for (uint32_t i = tid; i < kRoom; i += kDrawThreads) {
+    sm.hist[i] = 0;
+    sm.table[i] = i < kBins ? min(__ldg(p.exp_tab + i), 1u << 30) : 0;
+  }
+  if (tid == 0) {
+    sm.n_near = 0;
+    sm.tokens = 0;
+    sm.least = 0xFFFFFFFFu;
+    if (t != 0 && t <= kMaxTemperature) sm.places = places_of(t);
+  }
+  m32 = __reduce_max_sync(0xffffffffu, m32);
+  if (lane == 0) sm.red_i[warp] = (uint32_t)m32;
+  bool wide = __syncthreads_or(more);
+#pragma unroll
+  for (int w = 0; w < kDrawWarps; ++w) m32 = max(m32, (int32_t)sm.red_i[w]);
+  if (tid == 0) sm.peak = (unsigned long long)(uint32_t)m32 | (unsigned long long)wide << 32;
+  row_sync(S);
+  for (uint32_t k = 0; S > 1 && k < S; ++k) {
+    const unsigned long long other = remote_u64(&sm.peak, k);
+    m32 = max(m32, (int32_t)other);
+    wide |= other >> 32 != 0;
+  }
+  if (t > kMaxTemperature) {
+    row_sync(S);
+    if (rank == 0 && tid == 0) {
+      p.token[row] = CK_NO_TOKEN;
+      p.prob[row] = 0;
+      p.kept[row] = 0;
+    }
+    return;
+  }
+  if (!wide) {
+    sample_row<false>(p, sm, m32, t, top_k, top_p, min_p, filtered);
+    return;
+  }
+  // ---- the largest of 64 bits
+  row_sync(S);  // the 32-bit ones have been read
+  long long m = LLONG_MIN;
+  for (uint32_t b = rank * kDrawWarps + warp; b < batches; b += S * kDrawWarps)
+#pragma unroll
+    for (uint32_t j = 0; j < kPer; ++j) {
+      const uint32_t i = b * kBatch + lane + 32 * j;
+      m = max(m, i < p.vocab ? __ldg(l + i) : LLONG_MIN);
+    }
+  m = warp_max(m);
+  if (lane == 0) sm.red[warp] = (unsigned long long)m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kDrawWarps; ++w) m = max(m, (long long)sm.red[w]);
+  if (tid == 0) sm.peak = (unsigned long long)m;
+  row_sync(S);
+  for (uint32_t k = 0; S > 1 && k < S; ++k) m = max(m, (long long)remote_u64(&sm.peak, k));
+  if (m == LLONG_MIN) {  // every token is masked
+    row_sync(S);
+    if (rank == 0 && tid == 0) {
+      p.token[row] = CK_NO_TOKEN;
+      p.prob[row] = 0;
+      p.kept[row] = 0;
+    }
+    return;
+  }
+  sample_row<true>(p, sm, m, t, top_k, top_p, min_p, filtered);
+}
+
+// Blocks of a row's cluster: as many as there are SMs for every row, of at least a batch a warp.
+uint32_t sample_split(uint32_t rows, uint32_t vocab, const DeviceFacts& f) {
+  uint32_t S = 1;
+  while (S < kMaxSplit && 2ull * S * rows <= (uint64_t)f.sms && 2 * S * kDrawWarps * kBatch <= 2 * vocab) S *= 2;
+  return S;
+}
+
+cudaError_t launch_sample(SampleParams p, cudaStream_t s) {
+  DeviceFacts f;
+  cudaError_t e = device_facts(&f);
+  if (e != cudaSuccess) return e;
+  static std::atomic<bool> ready[64];
+  if (!ready[f.dev].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(k_sample_rows, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Shared));
+    if (e != cudaSuccess) return e;
+    ready[f.dev].store(true, std::memory_order_relaxed);
+  }
+  p.split = sample_split(p.rows, p.vocab, f);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.rows * p.split);
+  cfg.blockDim = dim3(kDrawThreads);
+  cfg.dynamicSmemBytes = sizeof(Shared);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p.split;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_sample_rows, p);
 }
 
 }  // namespace
@@ -515,7 +634,7 @@ extern "C" {
 
 uint32_t ck_host_sample_place(uint32_t distance, uint32_t temperature) {
   const uint32_t t = std::min(std::max(temperature, 1u), kMaxTemperature);
-  return place_of(distance, t, reciprocal_of(t));
+  return place_of(distance, places_of(t));
 }
 
 int ck_sample(const int64_t* dev_logits, size_t logits_stride, uint32_t rows, uint32_t vocab,
