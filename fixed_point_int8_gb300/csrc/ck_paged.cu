@@ -273,7 +273,8 @@ __device__ __forceinline__ void clear_marks(const PagesParams& p) {
 // Inclusive sum over the block's warps of one value a thread; *total the block's sum.
 __device__ __forceinline__ unsigned long long block_scan(unsigned long long v, unsigned long long* warp_sum,
                                                          unsigned long long* total) {
-  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // (known to be the same in the warp: else the scan below, in a branch, collects the lanes at every step)
+  const uint32_t lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const unsigned long long inc = warp_inclusive_scan(v, lane);
   if (lane == 31) warp_sum[warp] = inc;
   __syncthreads();
@@ -478,95 +479,165 @@ __device__ __forceinline__ uint32_t longest(const AdvanceParams& p) {
   return (uint32_t)min((unsigned long long)p.stride << p.page_shift, (unsigned long long)kMaxPositions);
 }
 
-// First step (a warp a sequence): checks it, takes over and marks the pages that its next position
-// or a later one sees.
-__device__ __forceinline__ void advance_mark(const AdvanceParams& p, uint32_t s, uint32_t lane) {
-  const uint32_t len = p.len_in[s];
-  uint32_t status = 0;
-  if (len > longest(p))
-    status = CK_INVALID_STATE;
-  else if ((unsigned long long)len + p.ask[s] > longest(p))
-    status = CK_CONTEXT_EXCEEDED;
-  const uint32_t have = status == CK_INVALID_STATE ? 0 : pages_of(p, len);
-  auto keeps = [&](uint32_t i) {
-    return i < have && ((unsigned long long)i << p.page_shift < p.sinks ||
-                        ((unsigned long long)(i + 1) << p.page_shift) + p.window > (unsigned long long)len + 1);
-  };
-  const uint32_t* from = p.table_in + (size_t)s * p.stride;
-  bool bad = false;
-  for (uint32_t i = lane; i < have; i += 32) bad |= keeps(i) && from[i] >= p.pages;
-  if (__any_sync(0xffffffffu, bad)) status = CK_INVALID_STATE;
-  uint32_t* to = p.table_out + (size_t)s * p.stride;
-  for (uint32_t i = lane; i < p.stride; i += 32) {
-    const uint32_t id = status != CK_INVALID_STATE && keeps(i) ? from[i] : CK_NO_PAGE;
-    to[i] = id;
-    if (id != CK_NO_PAGE) atomicOr(p.bits + (id >> 5), 1u << (id & 31));
+// First step (a warp takes sequence first and every `step`-th behind it, 32 at a time): checks them, takes
+// over and marks the pages that their next position or a later one sees.
+constexpr uint32_t kEntries = 4;  // of a table row, a lane holds
+__device__ __forceinline__ void advance_mark(const AdvanceParams& p, uint32_t* bits, uint32_t first, uint32_t step, uint32_t lane) {
+  for (; first < p.seqs; first += 32 * step) {
+    const uint64_t at = first + (uint64_t)lane * step;  // this lane's sequence
+    const uint32_t lens = at < p.seqs ? p.len_in[at] : 0, asks = at < p.seqs ? p.ask[at] : 0;
+    const uint32_t many = min(32u, (p.seqs - first + step - 1) / step);
+    for (uint32_t k = 0; k < many; ++k) {
+      const uint32_t s = first + k * step, len = __shfl_sync(0xffffffffu, lens, k), ask = __shfl_sync(0xffffffffu, asks, k);
+      uint32_t status = 0;
+      if (len > longest(p))
+        status = CK_INVALID_STATE;
+      else if ((unsigned long long)len + ask > longest(p))
+        status = CK_CONTEXT_EXCEEDED;
+      const uint32_t have = status == CK_INVALID_STATE ? 0 : pages_of(p, len);
+      // kept: the pages with a position below `sinks`, and from that on which ends behind len - window
+      const uint32_t early = (uint32_t)min(((unsigned long long)p.sinks + (1u << p.page_shift) - 1) >> p.page_shift, (unsigned long long)have);
+      const uint32_t late = min(have, p.window <= len ? (len + 1 - p.window) >> p.page_shift : 0);
+      auto keeps = [&](uint32_t i) { return i < early || i - late < have - late; };
+      const uint32_t* from = p.table_in + (size_t)s * p.stride;
+      uint32_t* to = p.table_out + (size_t)s * p.stride;
+      constexpr uint32_t kStep = 32 * kEntries;
+      auto none = [&](uint32_t i0) { return i0 >= have || (i0 >= early && i0 + kStep <= late); };  // of a step's entries
+      uint32_t id[kEntries];
+      auto read = [&](uint32_t i0) {
+#pragma unroll
+        for (uint32_t j = 0; j < kEntries; ++j) id[j] = keeps(i0 + 32 * j + lane) ? __ldg(from + i0 + 32 * j + lane) : 0;
+      };
+      uint32_t last = 0;  // the step that id holds
+      bool bad = false;
+      for (uint32_t i0 = 0; i0 < have; i0 += kStep) {
+        if (none(i0)) continue;
+        read(last = i0);
+#pragma unroll
+        for (uint32_t j = 0; j < kEntries; ++j) bad |= id[j] >= p.pages;
+      }
+      if (__any_sync(0xffffffffu, bad)) status = CK_INVALID_STATE;
+      const bool live = status != CK_INVALID_STATE;
+      for (uint32_t i0 = 0; i0 < p.stride; i0 += kStep) {
+        const bool empty = !live || none(i0);
+        if (!empty && last != i0) read(i0);
+#pragma unroll
+        for (uint32_t j = 0; j < kEntries; ++j) {
+          const uint32_t i = i0 + 32 * j + lane;
+          const bool kept = !empty && keeps(i);
+          if (i < p.stride) to[i] = kept ? id[j] : CK_NO_PAGE;
+          if (kept) atomicOr(bits + (id[j] >> 5), 1u << (id[j] & 31));
+        }
+      }
+      if (lane == 0) p.status[s] = status;
+    }
   }
-  if (lane == 0) p.status[s] = status;
 }
-// and the pages held outside the call (a warp 32 of them).
-__device__ __forceinline__ void advance_held(const AdvanceParams& p, uint32_t word, uint32_t lane) {
-  const uint32_t i = word * 32 + lane;
-  const uint32_t held = __ballot_sync(0xffffffffu, i < p.pages && p.held[i] != 0);
-  if (lane == 0 && held) atomicOr(p.bits + word, held);
+// and the pages held outside the call: a warp takes the `first`-th eight words of 32 and every `step`-th
+// eight behind.
+__device__ __forceinline__ void advance_held(const AdvanceParams& p, uint32_t* bits, uint32_t first, uint32_t step, uint32_t lane) {
+  const uint32_t words = (p.pages + 31) / 32;
+  for (uint32_t w0 = 8 * first; w0 < words; w0 += 8 * step) {
+    uint8_t held[8];
+#pragma unroll
+    for (uint32_t j = 0; j < 8; ++j) held[j] = (w0 + j) * 32 + lane < p.pages ? __ldg(p.held + (w0 + j) * 32 + lane) : 0;
+#pragma unroll
+    for (uint32_t j = 0; j < 8; ++j) {
+      const uint32_t word = __ballot_sync(0xffffffffu, held[j] != 0);
+      if (lane == 0 && word) atomicOr(bits + w0 + j, word);
+    }
+  }
 }
 
 // Second step (one block): the free pages in ascending order, as many as are asked for, which
-// sequences are served, and where their rows start.
+// sequences are served, and where their rows start.  A thread takes sequences that follow one another, so
+// that there are three sums over the block.
 __device__ __forceinline__ void advance_plan(const AdvanceParams& p, unsigned long long* warp_sum) {
   const uint32_t tid = threadIdx.x, words = (p.pages + 31) / 32;
-  auto need_of = [&](uint32_t s) { return pages_of(p, p.len_in[s] + p.ask[s]) - pages_of(p, p.len_in[s]); };
-  unsigned long long asked = 0, total;
-  for (uint32_t base = 0; base < p.seqs; base += kPlanThreads) {
-    const uint32_t s = base + tid;
-    const unsigned long long need = s < p.seqs && p.status[s] == 0 ? need_of(s) : 0;
-    const unsigned long long end = asked + block_scan(need, warp_sum, &total);
-    if (s < p.seqs) p.before[s] = end - need;
-    asked += total;
+  const uint32_t each = (p.seqs + kPlanThreads - 1) / kPlanThreads, s0 = min(p.seqs, tid * each), s1 = min(p.seqs, s0 + each);
+  auto need_of = [&](uint32_t s, uint32_t ask) {
+    const uint32_t len = p.len_in[s];
+    return pages_of(p, len + ask) - pages_of(p, len);
+  };
+  unsigned long long need = 0, ask = 0, asked, total;
+  for (uint32_t s = s0; s < s1; ++s) {
+    const uint32_t rows = p.status[s] == 0 ? p.ask[s] : 0;
+    p.before[s] = need;
+    need += rows ? need_of(s, rows) : 0;
+    ask += rows;
   }
+  const unsigned long long need_before = block_scan(need, warp_sum, &asked) - need;
   unsigned long long found = 0;
-  for (uint32_t base = 0; base < words && found < asked; base += kPlanThreads) {
-    const uint32_t w = base + tid;
-    uint32_t free = w < words ? ~p.bits[w] : 0;
-    if (w == words - 1 && (p.pages & 31)) free &= (1u << (p.pages & 31)) - 1;
-    unsigned long long at = found + block_scan(__popc(free), warp_sum, &total) - __popc(free);
-    for (; free && at < asked; free &= free - 1) p.list[at++] = w * 32 + __ffs((int)free) - 1;
+  for (uint32_t base = 0; base < words && found < asked; base += 4 * kPlanThreads) {
+    uint32_t free[4], count = 0;
+#pragma unroll
+    for (uint32_t j = 0; j < 4; ++j) {
+      const uint32_t w = base + 4 * tid + j;
+      free[j] = w < words ? ~p.bits[w] : 0;
+      if (w == words - 1 && (p.pages & 31)) free[j] &= (1u << (p.pages & 31)) - 1;
+      count += __popc(free[j]);
+    }
+    unsigned long long at = found + block_scan(count, warp_sum, &total) - count;
+#pragma unroll
+    for (uint32_t j = 0; j < 4; ++j)
+      for (; free[j] && at < asked; free[j] &= free[j] - 1) p.list[at++] = (base + 4 * tid + j) * 32 + __ffs((int)free[j]) - 1;
     found += total;
   }
-  unsigned long long asked_rows = 0;
-  uint32_t rows = 0;
-  for (uint32_t base = 0; base < p.seqs; base += kPlanThreads) {
-    const uint32_t s = base + tid;
-    const bool fine = s < p.seqs && p.status[s] == 0;
-    const uint32_t ask = fine ? p.ask[s] : 0, need = fine ? need_of(s) : 0;
-    const unsigned long long end = asked_rows + block_scan(ask, warp_sum, &total);
-    asked_rows += total;
-    const bool served = fine && (need == 0 || p.before[s] + need <= found) && (ask == 0 || end <= p.rows);
-    const uint32_t mine = served ? ask : 0;
-    const uint32_t last = rows + (uint32_t)block_scan(mine, warp_sum, &total);
-    if (s < p.seqs) {
-      p.start[s] = last - mine;
-      if (fine && !served) p.status[s] = CK_BUFFER_TOO_SMALL;
-    }
-    rows += (uint32_t)total;
+  unsigned long long ask_before = block_scan(ask, warp_sum, &total) - ask;
+  uint32_t granted = 0;
+  for (uint32_t s = s0; s < s1; ++s) {
+    if (p.status[s] != 0) continue;
+    const uint32_t rows = p.ask[s], pages = need_of(s, rows);
+    const unsigned long long before = need_before + p.before[s];
+    p.before[s] = before;
+    ask_before += rows;
+    if ((pages == 0 || before + pages <= found) && (rows == 0 || ask_before <= p.rows))
+      granted += rows;
+    else
+      p.status[s] = CK_BUFFER_TOO_SMALL;
   }
-  if (tid == 0) p.start[p.seqs] = rows;
+  uint32_t start = (uint32_t)block_scan(granted, warp_sum, &total) - granted;
+  for (uint32_t s = s0; s < s1; ++s) {
+    p.start[s] = start;
+    start += p.status[s] == 0 ? p.ask[s] : 0;
+  }
+  if (tid == 0) p.start[p.seqs] = (uint32_t)total;
 }
 
-// Third step (a warp a sequence): its new pages and its rows; and the rows behind the last.
-__device__ __forceinline__ void advance_fill(const AdvanceParams& p, uint32_t s, uint32_t lane) {
-  const uint32_t status = p.status[s], len = p.len_in[s], ask = status ? 0 : p.ask[s];
-  if (lane == 0) p.len_out[s] = status == CK_INVALID_STATE ? 0 : len + ask;
-  if (ask == 0) return;
-  const uint32_t have = pages_of(p, len), need = pages_of(p, len + ask) - have, start = p.start[s];
-  const uint32_t* fresh = p.list + (need ? p.before[s] : 0);
-  uint32_t* table = p.table_out + (size_t)s * p.stride;
-  for (uint32_t i = lane; i < need; i += 32) table[have + i] = fresh[i];
+// Third step (as the first): their new pages and their rows; and the rows behind the last.
+__device__ __forceinline__ void advance_fill(const AdvanceParams& p, uint32_t first, uint32_t step, uint32_t lane) {
   const uint32_t mask = (1u << p.page_shift) - 1;
-  for (uint32_t j = lane; j < ask; j += 32) {
-    const uint32_t pos = len + j, i = pos >> p.page_shift, id = i < have ? table[i] : fresh[i - have];
-    p.slot[start + j] = ((int64_t)id << p.page_shift) + (pos & mask);
-    p.position[start + j] = pos;
+  for (; first < p.seqs; first += 32 * step) {
+    const uint64_t at = first + (uint64_t)lane * step;  // this lane's sequence
+    const bool there = at < p.seqs;
+    const uint32_t status = there ? p.status[at] : CK_INVALID_STATE, lens = there ? p.len_in[at] : 0;
+    const uint32_t wants = there ? p.ask[at] : 0, asks = status == 0 ? wants : 0, starts = there ? p.start[at] : 0;
+    const unsigned long long befores = there ? p.before[at] : 0;
+    // (the page that the first new position goes on in)
+    const uint32_t parts = there && status != CK_INVALID_STATE && (lens & mask) ? p.table_out[at * p.stride + (lens >> p.page_shift)] : 0;
+    if (there) p.len_out[at] = status == CK_INVALID_STATE ? 0 : lens + asks;
+    // a few new positions a lane by itself, more by the warp together
+    auto rows = [&](uint64_t s, uint32_t len, uint32_t ask, uint32_t start, uint32_t part, unsigned long long before,
+                    uint32_t j0, uint32_t dj) {
+      const uint32_t have = pages_of(p, len), need = pages_of(p, len + ask) - have;
+      const uint32_t* fresh = p.list + (need ? before : 0);
+      uint32_t* table = p.table_out + s * p.stride;
+#pragma unroll 1
+      for (uint32_t i = j0; i < need; i += dj) table[have + i] = fresh[i];
+#pragma unroll 1
+      for (uint32_t j = j0; j < ask; j += dj) {
+        const uint32_t pos = len + j, i = pos >> p.page_shift, id = i < have ? part : fresh[i - have];
+        p.slot[start + j] = ((int64_t)id << p.page_shift) + (pos & mask);
+        p.position[start + j] = pos;
+      }
+    };
+    constexpr uint32_t kFew = 4;
+    if (asks && asks <= kFew) rows(at, lens, asks, starts, parts, befores, 0, 1);
+    for (uint32_t left = __ballot_sync(0xffffffffu, asks > kFew); left; left &= left - 1) {
+      const uint32_t k = __ffs((int)left) - 1;
+      rows(first + (uint64_t)k * step, __shfl_sync(0xffffffffu, lens, k), __shfl_sync(0xffffffffu, asks, k),
+           __shfl_sync(0xffffffffu, starts, k), __shfl_sync(0xffffffffu, parts, k), __shfl_sync(0xffffffffu, befores, k), lane, 32);
+    }
   }
 }
 __device__ __forceinline__ void advance_rest(const AdvanceParams& p, uint32_t at, uint32_t step) {
@@ -578,18 +649,58 @@ __device__ __forceinline__ void advance_rest(const AdvanceParams& p, uint32_t at
 
 __global__ void __launch_bounds__(kTableThreads) k_advance_mark(const AdvanceParams p) {
   const uint32_t warps = gridDim.x * (kTableThreads / 32), lane = threadIdx.x & 31;
-  const uint32_t w = blockIdx.x * (kTableThreads / 32) + threadIdx.x / 32;
-  for (uint32_t s = w; s < p.seqs; s += warps) advance_mark(p, s, lane);
-  for (uint32_t i = w; p.held && i < (p.pages + 31) / 32; i += warps) advance_held(p, i, lane);
+  const uint32_t w = blockIdx.x * (kTableThreads / 32) + __shfl_sync(0xffffffffu, threadIdx.x / 32, 0);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  advance_mark(p, p.bits, w, warps, lane);
+  if (p.held) advance_held(p, p.bits, w, warps, lane);
 }
 __global__ void __launch_bounds__(kPlanThreads) k_advance_plan(const AdvanceParams p) {
   __shared__ unsigned long long warp_sum[kPlanThreads / 32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   advance_plan(p, warp_sum);
 }
 __global__ void __launch_bounds__(kTableThreads) k_advance_fill(const AdvanceParams p) {
-  const uint32_t s = blockIdx.x * (kTableThreads / 32) + threadIdx.x / 32;
-  if (s < p.seqs) advance_fill(p, s, threadIdx.x & 31);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  advance_fill(p, blockIdx.x * (kTableThreads / 32) + __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), gridDim.x * (kTableThreads / 32), threadIdx.x & 31);
   advance_rest(p, blockIdx.x * kTableThreads + threadIdx.x, gridDim.x * kTableThreads);
+}
+
+// All of it in one launch, by a cluster of blocks or one: the steps are separated by the cluster's barriers
+// (which order what its blocks write to global memory), the second is the first block's.  Every block marks
+// pages in its own shared memory (131,000 atomics on L2 from eight SMs take 17 us).
+__global__ void __launch_bounds__(kPlanThreads) k_advance(const AdvanceParams p, uint32_t blocks) {
+  __shared__ unsigned long long warp_sum[kPlanThreads / 32];
+  extern __shared__ __align__(16) uint32_t marks[];
+  const uint32_t tid = threadIdx.x, lane = tid & 31, warps = blocks * (kPlanThreads / 32), words = (p.pages + 31) / 32;
+  const uint32_t w = blockIdx.x * (kPlanThreads / 32) + __shfl_sync(0xffffffffu, tid / 32, 0);
+  auto sync = [&] {
+    if (blocks > 1)
+      asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    else
+      __syncthreads();
+  };
+  for (uint32_t i = tid; i < words; i += kPlanThreads) marks[i] = 0;
+  __syncthreads();
+  advance_mark(p, marks, w, warps, lane);
+  if (p.held) advance_held(p, marks, w, warps, lane);
+  sync();
+  const uint32_t share = (words + blocks - 1) / blocks, end = min(words, (blockIdx.x + 1) * share);
+  for (uint32_t i = blockIdx.x * share + tid; i < end; i += kPlanThreads) {
+    uint32_t word = marks[i];
+    for (uint32_t k = 1; k < blocks; ++k) {
+      uint32_t at = (uint32_t)__cvta_generic_to_shared(marks + i), other;
+      asm("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(at) : "r"((blockIdx.x + k) % blocks));
+      asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(other) : "r"(at) : "memory");
+      word |= other;
+    }
+    p.bits[i] = word;
+  }
+  sync();  // (and no block leaves while another reads its marks)
+  if (blockIdx.x == 0) advance_plan(p, warp_sum);
+  sync();
+  advance_fill(p, w, warps, lane);
+  advance_rest(p, blockIdx.x * kPlanThreads + tid, blocks * kPlanThreads);
 }
 
 int pages_args(const ck_paged_cache* cache, uint32_t rows, uint32_t stride, void* work, size_t work_len,
@@ -631,6 +742,12 @@ bool copies_alone(const ck_paged_cache* c, uint64_t pages) {
 // thread clears every 1,024th page); larger ones spread it over the GPU.
 bool table_work_alone(uint32_t rows, uint32_t stride, uint32_t pages) {
   return (uint64_t)rows * ((stride + 31) / 32) <= 1024 && pages <= 65536;
+}
+
+// One cluster does all of a step of up to 2 MB of tables and 2^20 pages (measured).
+constexpr uint32_t kAdvanceBlocks = 8, kAdvancePages = 1u << 20;
+bool advance_alone(uint32_t seqs, uint32_t stride, uint32_t pages) {
+  return (uint64_t)seqs * stride <= (1u << 19) && pages <= kAdvancePages;
 }
 
 PagesParams pages_params(const ck_paged_cache* c, const PagesLayout& w, void* work) {
@@ -851,12 +968,41 @@ int ck_pages_advance(const ck_paged_cache* cache, uint32_t seqs, const uint32_t*
   p.list = reinterpret_cast<uint32_t*>(b + w.list);
   p.before = reinterpret_cast<unsigned long long*>(b + w.before);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (advance_alone(seqs, stride, cache->pages)) {
+    const uint32_t blocks = seqs <= kPlanThreads / 32 && cache->pages <= 65536 ? 1 : kAdvanceBlocks;  // (a warp a sequence)
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(kPlanThreads);
+    DeviceFacts f;
+    CKP_CUDA(device_facts(&f));
+    static std::atomic<bool> ready[64];
+    if (!ready[f.dev].load(std::memory_order_relaxed)) {
+      CKP_CUDA(cudaFuncSetAttribute(k_advance, cudaFuncAttributeMaxDynamicSharedMemorySize, kAdvancePages / 8));
+      ready[f.dev].store(true, std::memory_order_relaxed);
+    }
+    cfg.dynamicSmemBytes = (cache->pages + 31) / 32 * 4;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = blocks;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    CKP_CUDA(cudaLaunchKernelEx(&cfg, k_advance, p, blocks));
+    return CK_OK;
+  }
   CKP_CUDA(cudaMemsetAsync(p.bits, 0, 4ull * ((p.pages + 31) / 32), s));
   constexpr uint32_t per = kTableThreads / 32;
   const uint32_t blocks = (seqs + per - 1) / per;
   k_advance_mark<<<blocks, kTableThreads, 0, s>>>(p);
-  k_advance_plan<<<1, kPlanThreads, 0, s>>>(p);
-  k_advance_fill<<<blocks, kTableThreads, 0, s>>>(p);
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(kPlanThreads);
+  CKP_CUDA(cudaLaunchKernelEx(&cfg, k_advance_plan, p));
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(kTableThreads);
+  CKP_CUDA(cudaLaunchKernelEx(&cfg, k_advance_fill, p));
   CKP_CUDA(cudaGetLastError());
   return CK_OK;
 }

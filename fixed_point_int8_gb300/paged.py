@@ -102,6 +102,14 @@ def _empty(stream, shape, dtype, device):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _like(stream, t):
+    """A tensor as `t` is, of the pool of the stream the call runs on."""
+    if stream is None:
+        return torch.empty_like(t)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(t)
+
+
 def _keep(stream, *tensors):
     """The tensors stay in use on the stream, whatever becomes of them after the call."""
     if stream is not None:
@@ -374,10 +382,11 @@ class PagePlan:
         if not 1 <= rows <= 2**20:
             raise ValueError(f"rows: want a number from 1 to 2^20, got {rows}")
         view = _window(window)
-        _keep(stream, self._work, lens, table, new, *(() if held is None else (held,)), *self.cache._tensors)
-        out, slots = _empty(stream, (seqs, self.stride), torch.int32, device), _empty(stream, (rows,), torch.int64, device)
-        new_lens, starts, positions, status = _empty(stream, (3 * seqs + 1 + rows,), torch.int32, device).split(
-            (seqs, seqs + 1, rows, seqs))
+        if stream is not None:
+            _keep(stream, self._work, lens, table, new, *(() if held is None else (held,)), *self.cache._tensors)
+        out, new_lens, status = _like(stream, table), _like(stream, lens), _like(stream, lens)
+        starts, positions = _empty(stream, (seqs + 1,), torch.int32, device), _empty(stream, (rows,), torch.int32, device)
+        slots = _empty(stream, (rows,), torch.int64, device)
         rc = lib().ck_pages_advance(self.cache._c, seqs, lens.data_ptr(), table.data_ptr(), new.data_ptr(), self.stride,
                                     view, None if held is None else held.data_ptr(), rows, new_lens.data_ptr(),
                                     out.data_ptr(), starts.data_ptr(), slots.data_ptr(), positions.data_ptr(),
@@ -457,20 +466,25 @@ def sample(logits, temperature, random, exp_table, top_k=None, top_p=None, min_p
     if logits.dim() != 2:
         raise ValueError(f"logits: want two dimensions, got {tuple(logits.shape)}")
     rows, vocab = logits.shape
-    step = _check_rows("logits", logits, rows, device)
-    _check("temperature", temperature, torch.int32, (rows,), device)
-    _check("random", random, torch.int64, (rows,), device)
+    step, each = _check_rows("logits", logits, rows, device), (rows,)
+    _check("temperature", temperature, torch.int32, each, device)
+    _check("random", random, torch.int64, each, device)
     _check("exp_table", exp_table, torch.int32, (4097,), device)
-    filters = [("top_k", top_k), ("top_p", top_p), ("min_p", min_p)]
-    for name, f in filters:
-        if f is not None:
-            _check(name, f, torch.int32, (rows,), device)
-    _keep(stream, logits, temperature, random, exp_table, *(f for _, f in filters if f is not None))
-    token, prob, kept = _empty(stream, (3, rows), torch.int32, device)
-    rc = lib().ck_sample(logits.data_ptr(), step, rows, vocab, temperature.data_ptr(),
-                         *(None if f is None else f.data_ptr() for _, f in filters), random.data_ptr(),
-                         exp_table.data_ptr(), token.data_ptr(), prob.data_ptr(), kept.data_ptr(),
-                         _on(stream, device))
+    k = p = m = None
+    if top_k is not None:
+        _check("top_k", top_k, torch.int32, each, device)
+        k = top_k.data_ptr()
+    if top_p is not None:
+        _check("top_p", top_p, torch.int32, each, device)
+        p = top_p.data_ptr()
+    if min_p is not None:
+        _check("min_p", min_p, torch.int32, each, device)
+        m = min_p.data_ptr()
+    if stream is not None:
+        _keep(stream, logits, temperature, random, exp_table, *(f for f in (top_k, top_p, min_p) if f is not None))
+    token, prob, kept = _like(stream, temperature), _like(stream, temperature), _like(stream, temperature)
+    rc = lib().ck_sample(logits.data_ptr(), step, rows, vocab, temperature.data_ptr(), k, p, m, random.data_ptr(),
+                         exp_table.data_ptr(), token.data_ptr(), prob.data_ptr(), kept.data_ptr(), _on(stream, device))
     return rc, Samples(token, prob, kept)
 
 
