@@ -508,7 +508,7 @@ __device__ __forceinline__ void advance_mark(const AdvanceParams& p, uint32_t* b
 #pragma unroll
         for (uint32_t j = 0; j < kEntries; ++j) id[j] = keeps(i0 + 32 * j + lane) ? __ldg(from + i0 + 32 * j + lane) : 0;
       };
-      uint32_t last = 0;  // the step that id holds
+      uint32_t last = 0xFFFFFFFFu;  // the step that id holds
       bool bad = false;
       for (uint32_t i0 = 0; i0 < have; i0 += kStep) {
         if (none(i0)) continue;
@@ -520,7 +520,7 @@ __device__ __forceinline__ void advance_mark(const AdvanceParams& p, uint32_t* b
       const bool live = status != CK_INVALID_STATE;
       for (uint32_t i0 = 0; i0 < p.stride; i0 += kStep) {
         const bool empty = !live || none(i0);
-        if (!empty && last != i0) read(i0);
+        if (!empty && last != i0) read(last = i0);
 #pragma unroll
         for (uint32_t j = 0; j < kEntries; ++j) {
           const uint32_t i = i0 + 32 * j + lane;

@@ -347,7 +347,12 @@ def test_advance_of_what_does_not_go(ck):
     (1, 8, 1, 1, 1, 1, None, False), (1, 256, 3, 5, 300, 250, None, False), (3, 16, 40, 200, 9, 3, (4, 37), True),
     (33, 8, 70, 900, 100, 5, (0, 1), False), (64, 16, 513, 5000, 64, 1, (4, 1000), True),
     (200, 16, 33, 3000, 2**20, 90, (70, 100), True), (1025, 32, 20, 40000, 3000, 4, None, False),
-    (2500, 8, 64, 70001, 5000, 3, (9, 200), True), (5000, 64, 3, 65537, 5000, 1, None, True)])
+    (2500, 8, 64, 70001, 5000, 3, (9, 200), True), (5000, 64, 3, 65537, 5000, 1, None, True),
+    # long tables: pages at their beginnings and in windows far behind, and all of them
+    (20, 8, 700, 30000, 2**20, 5, (20, 1500), True), (40, 16, 513, 30000, 2**20, 1, (4, 1024), False),
+    (9, 8, 1100, 12000, 2**20, 2, None, False), (70, 8, 300, 20000, 2**20, 9, (1200, 3), True),
+    # tables too large for one cluster
+    (1500, 8, 400, 400000, 2**20, 5, (20, 700), True), (600, 16, 1000, 250000, 2**20, 1, None, False)])
 def test_advance_step_after_step(ck, seqs, page, stride, pages, rows, new, view, held):
     """Several steps from empty tables, whatever is granted, against the plain form."""
     rng = np.random.default_rng(seqs + pages)
