@@ -53,7 +53,7 @@ struct Tile {
   static constexpr uint32_t kKeyPlane = kTilePos * 128, kKeyHalf = 12 * kKeyPlane, kKeys = (HD / 64) * kKeyHalf;
   static constexpr uint32_t kProbPlane = kTileRows * 128, kValuePlane = HD * 128;
   static constexpr uint32_t kValueBuf = 3 * (kProbPlane + kValuePlane);
-  static constexpr uint32_t kPitch = kTileRows + 1;  // of the 64-bit sums, [element][row]
+  static constexpr uint32_t kPitch = kTileRows + 2;  // of the 64-bit sums, [element][row]; two rows are read at once
   static constexpr uint32_t max3(uint32_t a, uint32_t b, uint32_t c) {
     return a > b ? (a > c ? a : c) : (b > c ? b : c);
   }
@@ -165,6 +165,13 @@ __device__ __forceinline__ unsigned long long peer64(const void* p, uint32_t ran
   asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
   return v;
 }
+__device__ __forceinline__ ulonglong2 peer128(const void* p, uint32_t rank) {
+  uint32_t a;
+  ulonglong2 v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v2.u64 {%0, %1}, [%2];" : "=l"(v.x), "=l"(v.y) : "r"(a) : "memory");
+  return v;
+}
 __device__ __forceinline__ void all_sync(uint32_t C) {  // the cluster's threads, or the block's
   if (C > 1)
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -202,7 +209,15 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
   uint32_t* next_s = reinterpret_cast<uint32_t*>(sm + T::kMiscOff + 60);
   uint32_t* bad_s = reinterpret_cast<uint32_t*>(sm + T::kMiscOff + 56);  // this block's reason to give the tile away
 
-  for (uint32_t i = tid; i < 4097; i += T::kThreads) table_s[i] = min(__ldg(p.exp_tab + i), 1u << 30);
+  {
+    constexpr uint32_t kEach = (4097 + T::kThreads - 1) / T::kThreads;  // (all asked for at once: 3 us less)
+    uint32_t e[kEach];
+#pragma unroll
+    for (uint32_t j = 0; j < kEach; ++j) e[j] = tid + j * T::kThreads < 4097 ? __ldg(p.exp_tab + tid + j * T::kThreads) : 0;
+#pragma unroll
+    for (uint32_t j = 0; j < kEach; ++j)
+      if (tid + j * T::kThreads < 4097) table_s[tid + j * T::kThreads] = min(e[j], 1u << 30);
+  }
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mb_init(full + i, T::kThreads / 32);
@@ -262,8 +277,9 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
       if (tid == 0 && rank == 0) note(p.batch, seq, err_key(0, p.pool.layer, CK_PAGED_BAD_SEQUENCE, 0));
     }
     const uint32_t queries = sq.ok ? sq.count * group : 0;
-    if (tid == 0 && rank == 0) *next_s = clusters + atomicAdd(f.any + 1, 1u);
+    const uint32_t drawn = tid == 0 && rank == 0 ? atomicAdd(f.any + 1, 1u) : 0;  // (needed at the tile's end)
     if (v0 >= queries) {  // (for every block of the cluster)
+      if (tid == 0 && rank == 0) *next_s = clusters + drawn;
       all_sync(C);
       const uint32_t then = C > 1 ? peer32(next_s, 0) : *next_s;
       all_sync(C);
@@ -337,6 +353,7 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
         tmem_st16(tmem + lane_base + k * (HD / 2) + 16 * cg, w);
       }
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      if (tid == 0 && rank == 0) *next_s = clusters + drawn;
       __syncthreads();  // the keys' operands go to the same place
       for (uint32_t i = tid; i < T::kKeys / 2 / 16; i += T::kThreads) {  // places 0, 1, 5, 6, 10 and 11
         const uint32_t half = i / (T::kKeyHalf / 2 / 16), in = i % (T::kKeyHalf / 2 / 16), at = in / (T::kKeyPlane / 16);
@@ -775,21 +792,31 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
     away |= *bad_s;
     for (uint32_t k = 0; C > 1 && k < C; ++k) away |= peer32(bad_s, k);
     const uint32_t then = C > 1 ? peer32(next_s, 0) : *next_s;
-    const uint32_t rows = kTileRows / C;
-    for (uint32_t i = tid; !away && i < rows * HD; i += T::kThreads) {
-      const uint32_t row = rank * rows + i / HD, e = i % HD, q = v0 + row;
+    // two rows at a time: 16 bytes of every block's sums
+    const uint32_t pairs = kTileRows / 2 / C;
+    for (uint32_t i = tid; !away && i < pairs * HD; i += T::kThreads) {
+      const uint32_t row = 2 * (rank * pairs + i / HD), e = i % HD, q = v0 + row;
       if (q >= queries) break;
-      unsigned long long t = 0;
+      ulonglong2 t = make_ulonglong2(0, 0);
       if (C > 1) {
-        unsigned long long part[8];
+        ulonglong2 part[8];
 #pragma unroll
-        for (uint32_t k = 0; k < 8; ++k) part[k] = k < C ? peer64(sums + (size_t)e * T::kPitch + row, k) : 0;
+        for (uint32_t k = 0; k < 8; ++k) part[k] = k < C ? peer128(sums + (size_t)e * T::kPitch + row, k) : make_ulonglong2(0, 0);
 #pragma unroll
-        for (uint32_t k = 0; k < 8; ++k) t += part[k];
+        for (uint32_t k = 0; k < 8; ++k) {
+          t.x += part[k].x;
+          t.y += part[k].y;
+        }
       } else {
-        t = sums[(size_t)e * T::kPitch + row];
+        t = *reinterpret_cast<const ulonglong2*>(sums + (size_t)e * T::kPitch + row);
       }
-      p.out[((size_t)(sq.first + q / group) * p.heads + kvh * group + q % group) * HD + e] = (long long)t >> 24;
+      const uint32_t token = group == 1 ? q : q / group, head = kvh * group + (q - token * group);
+      int64_t* out = p.out + ((size_t)(sq.first + token) * p.heads + head) * HD + e;
+      out[0] = (long long)t.x >> 24;
+      if (q + 1 < queries) {
+        const bool over = q + 1 - token * group == group;  // the next token's first head
+        out[over ? (size_t)(p.heads - group + 1) * HD : HD] = (long long)t.y >> 24;
+      }
     }
     if (rank == 0 && tid == 0) {
       f.away[item] = away;
