@@ -102,12 +102,12 @@ def _empty(stream, shape, dtype, device):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _like(stream, t):
-    """A tensor as `t` is, of the pool of the stream the call runs on."""
+def _made_on(stream, make, *args):
+    """What make(*args) allocates, from the pool of the stream the call runs on."""
     if stream is None:
-        return torch.empty_like(t)
+        return make(*args)
     with torch.cuda.stream(stream):
-        return torch.empty_like(t)
+        return make(*args)
 
 
 def _keep(stream, *tensors):
@@ -321,6 +321,11 @@ class Advance(NamedTuple):
     status: object     # int32 [seqs]
 
 
+def _advance_outputs(table, lens, rows):
+    return (torch.empty_like(table), torch.empty_like(lens), lens.new_empty(lens.shape[0] + 1),
+            lens.new_empty(rows, dtype=torch.int64), lens.new_empty(rows), torch.empty_like(lens))
+
+
 class Compact(NamedTuple):
     table: object
     used: object    # int32 scalar
@@ -384,14 +389,12 @@ class PagePlan:
         view = _window(window)
         if stream is not None:
             _keep(stream, self._work, lens, table, new, *(() if held is None else (held,)), *self.cache._tensors)
-        out, new_lens, status = _like(stream, table), _like(stream, lens), _like(stream, lens)
-        starts, positions = _empty(stream, (seqs + 1,), torch.int32, device), _empty(stream, (rows,), torch.int32, device)
-        slots = _empty(stream, (rows,), torch.int64, device)
+        got = out, new_lens, starts, slots, positions, status = _made_on(stream, _advance_outputs, table, lens, rows)
         rc = lib().ck_pages_advance(self.cache._c, seqs, lens.data_ptr(), table.data_ptr(), new.data_ptr(), self.stride,
                                     view, None if held is None else held.data_ptr(), rows, new_lens.data_ptr(),
                                     out.data_ptr(), starts.data_ptr(), slots.data_ptr(), positions.data_ptr(),
                                     status.data_ptr(), *self._args, _on(stream, device, self, self.cache))
-        return rc, Advance(out, new_lens, starts, slots, positions, status)
+        return rc, Advance(*got)
 
     def compact(self, lens, table, stream=None):
         """ck_pages_compact: the rows' pages move to the lowest page numbers.  Returns (rc, Compact)."""
@@ -457,6 +460,10 @@ class Samples(NamedTuple):
     kept: object   # int32 [rows]
 
 
+def _three(t):
+    return torch.empty_like(t), torch.empty_like(t), torch.empty_like(t)
+
+
 def sample(logits, temperature, random, exp_table, top_k=None, top_p=None, min_p=None, stream=None):
     """A token of every row (ck_sample): logits int64 [rows][vocab] (rows may be further apart),
     temperature int32 [rows] (16 fraction bits), random int64 [rows] (all 64 bits count), exp_table
@@ -482,7 +489,7 @@ def sample(logits, temperature, random, exp_table, top_k=None, top_p=None, min_p
         m = min_p.data_ptr()
     if stream is not None:
         _keep(stream, logits, temperature, random, exp_table, *(f for f in (top_k, top_p, min_p) if f is not None))
-    token, prob, kept = _like(stream, temperature), _like(stream, temperature), _like(stream, temperature)
+    token, prob, kept = _made_on(stream, _three, temperature)
     rc = lib().ck_sample(logits.data_ptr(), step, rows, vocab, temperature.data_ptr(), k, p, m, random.data_ptr(),
                          exp_table.data_ptr(), token.data_ptr(), prob.data_ptr(), kept.data_ptr(), _on(stream, device))
     return rc, Samples(token, prob, kept)
