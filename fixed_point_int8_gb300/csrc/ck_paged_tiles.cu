@@ -31,6 +31,8 @@
 // probability of zero.  A cluster splits a tile's positions,
 // which fills the GPU when tiles are few; it exchanges maxima, sums and the 64-bit sums of values
 // through distributed shared memory.
+#include <type_traits>
+
 #include "ck_paged_attention.cuh"
 #include "ck_tc.cuh"
 
@@ -41,6 +43,10 @@ constexpr uint32_t kTileRows = 128, kTilePos = 32, kBlockPos = 64, kFlushBlocks 
 constexpr uint32_t kDiags = 5;
 // scores on their way back: four stages of 32 positions, [position / 4][row][4] as in the scratch
 constexpr uint32_t kRing = 4, kStage = kTilePos * kTileRows * 4;
+
+constexpr uint32_t kQueue = 8;  // products that wait for their turn without holding up who issues them
+template <uint32_t N>
+using Const = std::integral_constant<uint32_t, N>;
 
 template <int HD>
 struct Tile {
@@ -402,12 +408,15 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
         *reinterpret_cast<uint4*>(dst + k * T::kKeyPlane) = make_uint4(d[k][0], d[k][1], d[k][2], d[k][3]);
       fence_operands();
     };
-    // A batch's products, by one thread of the warps in turn, once its operands are in place and
-    // its accumulators drained.
-    auto issue_scores = [&](uint32_t i) {
+    // Products FROM to TO of a batch, by one thread of the warps in turn, once its operands are in place
+    // and its accumulators drained.
+    constexpr uint32_t kScoreProducts = HD / 16 * 3;
+    auto issue_scores = [&](uint32_t i, auto FROM, auto TO) {
       if (warp_u == i % kWarps) {
-        wait_full(batch + i);
-        if (i >= T::kBufs) wait_drained(tiles + i - T::kBufs);
+        if (FROM == 0) {
+          wait_full(batch + i);
+          if (i >= T::kBufs) wait_drained(tiles + i - T::kBufs);
+        }
         const uint32_t leader = elected(), d0 = tmem_u + T::kScoreCol + (i % T::kBufs) * (kDiags * kTilePos);
         const uint64_t b0 = operands + ((2 + 5 * (i & 1u)) * T::kKeyPlane >> 4);
         // A query plane times five places side by side, the three key planes and zeros, adds to the
@@ -415,19 +424,20 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
         // shape into the same accumulators are done in order; of several shapes into parts of
         // them, which measured 234 against 249 us and 337 against 357, they need not be.
 #pragma unroll
-        for (uint32_t kk = 0; kk < HD / 16; ++kk)
-#pragma unroll
-          for (uint32_t qp = 0; qp < 3; ++qp)
-            mma_ts(leader, d0, tmem_u + qp * (HD / 2) + 8 * kk,
-                   b0 + ((kk >> 2) * T::kKeyHalf >> 4) - (qp * T::kKeyPlane >> 4) + 2 * (kk & 3u),
-                   tile_idesc(kDiags * kTilePos), kk + qp != 0);
-        commit(leader, done + ((batch + i) & 1u));
+        for (uint32_t n = FROM; n < TO; ++n) {
+          const uint32_t kk = n / 3, qp = n % 3;
+          mma_ts(leader, d0, tmem_u + qp * (HD / 2) + 8 * kk,
+                 b0 + ((kk >> 2) * T::kKeyHalf >> 4) - (qp * T::kKeyPlane >> 4) + 2 * (kk & 3u),
+                 tile_idesc(kDiags * kTilePos), n != 0);
+        }
+        if (TO == kScoreProducts) commit(leader, done + ((batch + i) & 1u));
       }
       __syncwarp();
     };
     int32_t m = INT32_MIN;
     constexpr uint32_t kCols = kTilePos / T::kGroups;  // columns a thread drains
-    auto drain_scores = [&](uint32_t i) {
+    static_assert(T::kBufs == 1 || kCols == 8, "the products between are issued once");
+    auto drain_scores = [&](uint32_t i, auto between) {
       const uint32_t base = tmem + lane_base + T::kScoreCol + (i % T::kBufs) * (kDiags * kTilePos) + cg * kCols;
 #pragma unroll
       for (uint32_t h = 0; h < kCols; h += 8) {
@@ -472,6 +482,7 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
             if (c[j] != s) c[j] = s < 0 ? INT32_MIN : INT32_MAX;
           }
         }
+        between();
         if (sees_all(at, 8)) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) m = max(m, c[j]);
@@ -491,19 +502,26 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
       put_keys(0);
       arrive(full + (batch & 1u));
       load_keys(1);
-      issue_scores(0);
+      issue_scores(0, Const<0>(), Const<kScoreProducts>());
     }
     for (uint32_t i = 0; i < nt; ++i) {
       if (i + 1 < nt) {
         put_keys((i + 1) & 1u);  // (the products that read the place before are done: tile i - 1's)
         arrive(full + ((batch + i + 1) & 1u));
         load_keys(i + 2);
-        if (T::kBufs == 2) issue_scores(i + 1);
+        if (T::kBufs == 2) issue_scores(i + 1, Const<0>(), Const<kQueue>());
       }
       wait_done(batch + i);
-      drain_scores(i);
+      // The next batch's other products go out between the steps of this one's scores: about eight fit the
+      // queue, and who issues more stands still until there is room, and with it the block, which waits for
+      // that warp's own share (1,400 of 3,500 cycles a tile).
+      constexpr uint32_t kNext = T::kBufs == 2 ? 2 * kQueue : kScoreProducts;
+      drain_scores(i, [&] {
+        if (T::kBufs == 2 && i + 1 < nt) issue_scores(i + 1, Const<kQueue>(), Const<kNext>());
+      });
+      if (T::kBufs == 2 && i + 1 < nt) issue_scores(i + 1, Const<kNext>(), Const<kScoreProducts>());
       arrive(drained + ((tiles + i) & 1u));
-      if (T::kBufs == 1 && i + 1 < nt) issue_scores(i + 1);
+      if (T::kBufs == 1 && i + 1 < nt) issue_scores(i + 1, Const<0>(), Const<kScoreProducts>());
     }
     batch += nt;
     tiles += nt;
@@ -654,9 +672,10 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
           *reinterpret_cast<uint4*>(dst + k * T::kValuePlane) = make_uint4(d[k][0], d[k][1], d[k][2], d[k][3]);
       }
     };
-    auto put_probs = [&](uint32_t b, uint8_t* planes) {
+    auto put_probs = [&](uint32_t b, uint8_t* planes, auto between) {
 #pragma unroll
       for (uint32_t c = 0; c < kChunks; ++c) {
+        if (c == kChunks / 2) between();
         const uint32_t chunk = cg * kChunks + c, at = b * kBlockPos + chunk * 8;
         const int4 s0 = sraw[2 * c], s1 = sraw[2 * c + 1];
         const uint32_t s[8] = {(uint32_t)s0.x, (uint32_t)s0.y, (uint32_t)s0.z, (uint32_t)s0.w,
@@ -731,28 +750,29 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
         }
       }
     };
-    auto issue_values = [&](uint32_t b) {
+    constexpr uint32_t kValueProducts = kBlockPos / 16 * 9;
+    auto issue_values = [&](uint32_t b, auto FROM, auto TO) {
       if (warp_u == b % kWarps) {
-        wait_full(batch + b);
+        if (FROM == 0) wait_full(batch + b);
         const uint32_t leader = elected();
         const uint64_t a0 = operands + (b % T::kBufs) * (T::kValueBuf >> 4), b0 = a0 + (3 * T::kProbPlane >> 4);
         const uint32_t go_on = b % kFlushBlocks != 0;
         // The products of a weight have one shape and their accumulator to themselves; that of the
         // highest weight shares the last.
 #pragma unroll
-        for (uint32_t kk = 0; kk < kBlockPos / 16; ++kk)
-#pragma unroll
-          for (uint32_t pp = 0; pp < 3; ++pp)
-#pragma unroll
-            for (uint32_t vp = 0; vp < 3; ++vp) {
-              const uint32_t g = min(pp + vp, 3u);
-              const bool begins = kk == 0 && (pp == 0 || (pp == 1 && vp == 2));
-              mma_ss(leader, tmem_u + g * HD, a0 + ((pp * T::kProbPlane + kk * 32) >> 4),
-                     b0 + ((vp * T::kValuePlane + kk * 32) >> 4), tile_idesc(HD), begins ? go_on : 1u);
-            }
-        commit(leader, done + ((batch + b) & 1u));
+        for (uint32_t n = FROM; n < TO; ++n) {
+          const uint32_t kk = n / 9, pp = n / 3 % 3, vp = n % 3, g = min(pp + vp, 3u);
+          const bool begins = kk == 0 && (pp == 0 || (pp == 1 && vp == 2));
+          mma_ss(leader, tmem_u + g * HD, a0 + ((pp * T::kProbPlane + kk * 32) >> 4),
+                 b0 + ((vp * T::kValuePlane + kk * 32) >> 4), tile_idesc(HD), begins ? go_on : 1u);
+        }
+        if (TO == kValueProducts) commit(leader, done + ((batch + b) & 1u));
       }
       __syncwarp();
+    };
+    // (as the scores' products: the rest of a block's goes out between the steps of the next)
+    auto more_values = [&](uint32_t b, auto FROM, auto TO) {
+      if (T::kBufs == 2 && b > 0) issue_values(b - 1, FROM, TO);
     };
     if (nb) {
       next_id = page_of(vchunk * 8);
@@ -763,8 +783,11 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
       uint8_t* planes = sm + (b % T::kBufs) * T::kValueBuf;
       if (b >= T::kBufs) wait_done(batch + b - T::kBufs);  // the place is free
       put_values(planes + 3 * T::kProbPlane);
+      more_values(b, Const<kQueue>(), Const<15>());
       load_values(b + 1);
-      put_probs(b, planes);
+      more_values(b, Const<15>(), Const<22>());
+      put_probs(b, planes, [&] { more_values(b, Const<22>(), Const<29>()); });
+      more_values(b, Const<29>(), Const<kValueProducts>());
       if (b + 1 < nb) load_scores(b + 1);
       fence_operands();
       if (b > 0 && b % kFlushBlocks == 0) {
@@ -772,8 +795,9 @@ __global__ void __launch_bounds__(Tile<HD>::kThreads, HD == 64 ? 2 : 1) k_pattn_
         flush(b == kFlushBlocks, false);
       }
       arrive(full + ((batch + b) & 1u));
-      issue_values(b);
+      issue_values(b, Const<0>(), Const<T::kBufs == 2 ? kQueue : kValueProducts>());
     }
+    more_values(nb, Const<kQueue>(), Const<kValueProducts>());
     if (T::kBufs == 2 && nb > 1) wait_done(batch + nb - 2);  // (another thread's products)
     if (nb) wait_done(batch + nb - 1);
     batch += nb;
