@@ -150,7 +150,8 @@ __global__ void __launch_bounds__(kRowsThreads) k_pattn_rows(const RowsParams f)
 // 1.06 ns.  (Measured, few against tiles: head size 64, 32 heads: 32 rows over 200 positions 21 and
 // 31 us, over 1,000 68 and 51, four sequences of 16 rows over 1,500 144 and 146, of 8 rows 89 and
 // 142; head size 128: 16 rows over 2,000 117 and 98, 128 rows over 128 44 and 49, 32 sequences of
-// one row and four heads a key head over 2,000 179 and 494.)  k_pattn_rows follows the tiles for those
+// one row and four heads a key head over 2,000 179 and 494.)  With a window the places that a row, or a tile,
+// sees stand for the length.  k_pattn_rows follows the tiles for those
 // with values beyond their digits, and takes calls that k_pattn_few's grid or shared memory does
 // not hold.
 struct AttentionPlan {

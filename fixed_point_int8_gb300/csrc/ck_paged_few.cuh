@@ -20,7 +20,9 @@ namespace ck {
 // positions of 32 heads: 134 MB in 28.9 us (4.6 TB/s); 64 runs of 65 to 191: 30.1 us, 20 of them
 // without any load.
 // With a window the places that any of the queries sees follow one another (Span), and the others
-// are neither read nor counted; of those, each query takes what it sees itself.
+// are neither read nor counted; of those, each query takes what it sees itself.  One token with the last
+// 2,048 of 8,191 positions and the first four, 32 heads: 34 MB in 14.4 us (in clusters of four with twice
+// the threads 16.4); 64 streams with 1,024 and four: 1.08 GB in 172 us (6.3 TB/s, 92 % of the copy rate).
 constexpr uint32_t kMaxCluster = 16;
 constexpr int kNarrow = 64, kMiddle = 128, kBroad = 256;  // threads of a block
 constexpr unsigned long long kNowhere = ~0ull;

@@ -22,8 +22,9 @@
 //
 // The instructions around the products bound it (about 70 a score, a third of the issue slots in
 // phases that wait for one another), and the scratch's traffic where it is larger than L2: 256 rows
-// over 7,936 positions of 32 heads of 64 take 358 us, chunks of 201 and 151 rows over 2,047 and 777
-// of 32 heads of 128 take 251.  Twice the warps with 64 registers a thread were slower (447 against
+// over 7,936 positions of 32 heads of 64 take 345 us, chunks of 201 and 151 rows over 2,047 and 777
+// of 32 heads of 128 take 222; with windows of 2,048 and of 509 and four first positions 119 and 106.  A
+// warp of its own for the products left 96 registers a thread (17 warps): 134 and 169 us with the windows.  Twice the warps with 64 registers a thread were slower (447 against
 // 388 us, 276 against 255 then), and so were 16-bit places in the table in the scratch for the
 // exponentials (346 against 338, 243 against 234 then).  A thread owns a row (its lane of tensor
 // memory), so maxima and sums need no exchange inside a warp.  With a window a tile

@@ -62,8 +62,8 @@ def _windows(w, layers):
     if w is None:
         return None
     each = [w] * layers if isinstance(w, Window) else list(w)
-    if len(each) != layers:
-        raise ValueError(f"window: {len(each)} of them, the model has {layers} layers")
+    if len(each) != layers or not all(isinstance(one, tuple) and len(one) == 2 for one in each):
+        raise ValueError(f"window: want a Window, or one for each of the model's {layers} layers, got {w!r}")
     return (_Window * layers)(*(_Window(_u32_of("sinks", s), _u32_of("window", n)) for s, n in each))
 
 

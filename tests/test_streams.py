@@ -113,8 +113,9 @@ def test_numbers_of_a_window_past_32_bits_are_refused(ck):
             ck.paged._window(ck.Window(*bad))
         with pytest.raises(ValueError, match="sinks|window"):
             ck.paged._windows(ck.Window(*bad), 3)
-    with pytest.raises(ValueError, match="3 layers"):
-        ck.paged._windows([ck.Window(0, 4)] * 2, 3)
+    for wrong in ([ck.Window(0, 4)] * 2, (0, 4), [], [4, 4, 4], [ck.Window(0, 4), None, ck.Window(0, 4)]):
+        with pytest.raises(ValueError, match="3 layers"):
+            ck.paged._windows(wrong, 3)
     assert ck.paged._window(None) is None and ck.paged._windows(None, 3) is None
     each = ck.paged._windows([ck.Window(0, 4), ck.Window(2, 9), ck.Window(1, 1)], 3)
     assert [(w.sinks, w.window) for w in each] == [(0, 4), (2, 9), (1, 1)]
