@@ -168,7 +168,7 @@ __device__ __forceinline__ unsigned long long tail_first(uint32_t b) {
 // flight leave L2), two half rows an SM 48 and 72.  Atomics on shared memory bound the counts, a gather from the
 // table the weights.
 struct Shared {
-  uint32_t hist[kRoom];   // this block's counts
+  uint32_t hist[kRoom];   // this block's counts, then the row's
   uint32_t table[kRoom];  // the exponentials
   unsigned long long near_d[kList];
   unsigned long long weights[kMaxSplit * kHold / kBatch];  // that are kept, by batch
@@ -266,7 +266,7 @@ __device__ __forceinline__ void sample_row(const SampleParams& p, long long m, u
   Bound bound = {kNoBound, kNoBound, kNoBound, 0xFFFFFFFFu};
   uint32_t kept = 0, listed = 0, rest = 0;
   if (filtered) {
-    // The row's counts of this thread's buckets, b0 and those behind it, of the buckets that f names.
+    // The row's counts of this thread's buckets, b0 and those behind it, as f names a token's bucket.
     const uint32_t b0 = tid * kMine;
     auto count_all = [&](auto at_once, auto f, uint32_t (&c)[kMine]) {
       uint32_t last = 0;
@@ -280,7 +280,7 @@ __device__ __forceinline__ void sample_row(const SampleParams& p, long long m, u
       last = __reduce_add_sync(0xffffffffu, last);
       if (lane == 0 && last) atomicAdd(sm.hist + kBins - 1, last);
       row_sync(S);
-if (S > 1) {
+      if (S > 1) {
         // each block adds up its share of the places, four a thread, and hands it to all: nobody else touches
         // these words of any block.  (Every thread reading its own places from every block took 10 to 60 us.)
         constexpr uint32_t kQuads = kRoom / 4;

@@ -381,6 +381,39 @@ def test_advance_keeps_pages_that_sequences_share(ck):
     assert got.table.tolist() == [[-1, -1, 5, 0], [-1, 4, 6, -1]]
 
 
+def test_advance_of_a_pool_past_2_20_pages(ck):
+    """Few sequences and more pages than one cluster keeps apart."""
+    pages = 2**20 + 77
+    held = np.ones(pages, np.uint8)
+    held[[5, 9, 2**20 - 1, 2**20, 2**20 + 76]] = 0
+    table = [[2**20 + 70, 2**20 + 75, -1, -1], [2**20 + 76, -1, -1, -1]]
+    got = check_advance(ck, [16, 3], table, [10, 6], 20, 8, pages, None, held)
+    assert got.table.tolist() == [[2**20 + 70, 2**20 + 75, 5, 9], [2**20 + 76, 2**20 - 1, -1, -1]]
+    check_advance(ck, [16, 3], table, [17, 6], 20, 8, pages, ck.Window(0, 2), held)
+
+
+def test_advance_on_two_streams_at_once(ck):
+    """Two plans of one pool's shape, small tables and ones past a cluster, each on its stream."""
+    import torch
+    rng = np.random.default_rng(8)
+    for seqs, stride, pages in ((30, 20, 500), (1500, 400, 300000)):
+        cache = ck.PagedCache.empty(pages, 1, 1, 8, 4)
+        plans, streams = [ck.PagePlan(cache, seqs, stride) for _ in range(2)], [torch.cuda.Stream() for _ in range(2)]
+        state, want, outs = [], [], []
+        for _ in range(2):
+            new = rng.integers(0, 90, seqs)
+            state.append((cuda(np.zeros(seqs, np.int32)), cuda(np.full((seqs, stride), -1, np.int32)),
+                          cuda(new.astype(np.int32))))
+            want.append(plain_advance([0] * seqs, [[-1] * stride] * seqs, new.tolist(), 2**17, 8, pages, (3, 20)))
+        torch.cuda.synchronize()
+        for turn in range(12):
+            i = turn % 2
+            outs.append(plans[i].advance(*state[i], 2**17, window=ck.Window(3, 20), stream=streams[i]))
+        torch.cuda.synchronize()
+        for turn, (rc, got) in enumerate(outs):
+            assert rc == 0 and [x.tolist() for x in got] == list(want[turn % 2])
+
+
 def test_advance_captured_on_another_stream_and_refusals(ck):
     import torch
     cache = ck.PagedCache.empty(40, 1, 1, 8, 4)
@@ -487,6 +520,40 @@ def test_sampling_against_the_plain_form(ck, rows, vocab, spread):
     check_sample(ck, logits, t, None, None, m)
     logits[rng.random((rows, vocab)) < 0.7] = MIN
     check_sample(ck, logits, t, k, p, m)
+
+
+@pytest.mark.parametrize("rows,vocab", [(4, 262143), (4, 262144), (4, 262145), (3, 300001), (1, 2**20)])
+def test_sampling_of_vocabularies_past_a_clusters_memory(ck, rows, vocab):
+    """Rows whose words fit the shared memory of a cluster and the ones behind: drawn ones, ones of
+    ties, distances past 32 bits, masks, with filters and without."""
+    rng = np.random.default_rng(vocab)
+    logits = (rng.standard_normal((rows, vocab)) * 2 * 65536).astype(np.int64)
+    logits[-1, 1::2] = MIN
+    t = [65536, 30000, 1 << 20, 65536][:rows]
+    check_sample(ck, logits, t, [0, 900, 7, vocab // 3][:rows], [ONE // 2, ONE, ONE - 1, ONE][:rows], [0, 9000, 0, 0][:rows])
+    check_sample(ck, logits, t)
+    if rows > 1:
+        logits[0] = 77
+        logits[1] = rng.integers(-2**62, 2**62, vocab)
+        logits[2] >>= 14
+        check_sample(ck, logits, [0] + t[1:], [3, vocab // 5, vocab // 2, 5][:rows], [ONE, ONE, ONE - 1, ONE][:rows])
+        check_sample(ck, logits, t, [vocab - 1] * rows)
+
+
+@pytest.mark.parametrize("vocab", [3, 512, 40000, 300000])
+def test_sampling_keeps_everything_where_filters_ask_for_more(ck, vocab):
+    """A top-k of the vocabulary and above, a top-p of one and above, a min-p of nothing: the rows
+    without filters."""
+    import torch
+    rng = np.random.default_rng(vocab)
+    logits = cuda((rng.standard_normal((6, vocab)) * 65536).astype(np.int64))
+    i32 = lambda *a: cuda(np.array(a, np.uint32).view(np.int32))
+    random, exp, t = cuda(rng.integers(-2**63, 2**63, 6)), cuda(EXP.view(np.int32)), i32(*[65536] * 6)
+    rc, want = ck.sample(logits, t, random, exp)
+    assert rc == 0 and want.kept.tolist() == [vocab] * 6
+    rc, got = ck.sample(logits, t, random, exp, top_k=i32(vocab, vocab + 1, 2**32 - 1, 0, vocab, 2**31),
+                        top_p=i32(ONE, ONE + 1, 2**32 - 1, 2**31, ONE, ONE), min_p=i32(*[0] * 6))
+    assert rc == 0 and all(torch.equal(a, b) for a, b in zip(got, want))
 
 
 def test_the_oracle_samples_the_same(ck):
