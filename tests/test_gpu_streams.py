@@ -262,6 +262,40 @@ def test_window_scratch_too_small_is_refused(ck):
     assert rc == 10
 
 
+def test_windows_and_steps_beyond_32_bits_of_words(ck):
+    """Pages at the far end of pools of over 2^32 words each: a step hands them out, its slots are
+    stored to, windows read them (chunks, chunks of large queries, single tokens)."""
+    import torch
+    page, hd, pages, n = 256, 128, 131072 + 64, 300
+    if torch.cuda.mem_get_info()[0] < 60e9:
+        pytest.skip("needs 36 GB of device memory")
+    cache = ck.PagedCache.empty(pages, 1, 1, page, hd)
+    rng = np.random.default_rng(9)
+    top, view, inv, exp = pages - 1, ck.Window(3, 40), synth.inv_sqrt_head(hd), cuda(EXP.view(np.int32))
+    held = torch.ones(pages, dtype=torch.uint8, device="cuda")
+    held[[top - 40, top]] = 0
+    plan = ck.PagePlan(cache, 1, 4)
+    rc, step = plan.advance(cuda(np.zeros(1, np.int32)), cuda(np.full((1, 4), -1, np.int32)), cuda(np.array([n], np.int32)), n,
+                            window=view, held=held)
+    assert rc == 0 and step.status.tolist() == [0] and step.table.tolist() == [[top - 40, top, -1, -1]]
+    slots = np.concatenate([(top - 40) * page + np.arange(page), top * page + np.arange(n - page)])
+    assert np.array_equal(step.slots.cpu().numpy(), slots)
+    k, v = ((rng.standard_normal((n, hd)) * 65536).astype(np.int64) for _ in range(2))
+    for pool, words in ((cache.k, k), (cache.v, v)):
+        pool.view(-1, hd)[step.slots] = cuda(words.astype(np.int32))
+    for spread, new in ((65536, n), (2**40, n), (65536, 1)):
+        q = (rng.standard_normal((new, 32 * hd)) * spread).astype(np.int64)
+        batch = ck.PagedBatch(step.table, step.lens, cuda(np.array([0, new], np.int32)), None, new, new, n)
+        assert (ck.paged_attention_work(cache, batch, 32, window=view).numel() > 1 << 20) == (new > 1)  # the tiles
+        rc, out = ck.paged_attention(cache, 0, batch, cuda(q), exp, inv, window=view)
+        assert rc == 0 and batch.errors() == [None]
+        for row in {0, 130, 299} if new > 1 else (0,):
+            t = seen(n - new + row, *view)
+            for h in (0, 17, 31):
+                c = slice(h * hd, (h + 1) * hd)
+                assert np.array_equal(out[row, c].cpu().numpy(), plain_attention(q[row, c], k[t], v[t], inv))
+
+
 # ---------------------------------------------------------------- the tables between passes
 
 def plain_advance(lens, table, new, rows, page, pages, view=None, held=()):
@@ -643,6 +677,19 @@ def test_sampling_with_other_tables(ck):
     for args in ({}, dict(top_k=i32(k), top_p=i32(p), min_p=i32(m))):
         rc, got = ck.sample(cuda(logits), i32(np.maximum(t, 1)), cuda(np.arange(30)), zeros, **args)
         assert rc == 0 and ((got.token >= -1) & (got.token < 3000)).all()
+
+
+def test_sampling_of_rows_beyond_32_bits_apart(ck):
+    """Three rows of a matrix whose rows are 2^30 words apart, in blocks of their own and in clusters."""
+    import torch
+    if torch.cuda.mem_get_info()[0] < 40e9:
+        pytest.skip("needs 26 GB of device memory")
+    rng = np.random.default_rng(6)
+    wide = torch.empty(3, 2**30 + 3, dtype=torch.int64, device="cuda")
+    for vocab in (700, 33000):
+        wide[:, :vocab] = cuda((rng.standard_normal((3, vocab)) * 65536).astype(np.int64))
+        check_sample(ck, wide[:, :vocab], [65536] * 3, [40, 0, 9], [ONE // 2] * 3, [0, 7, 0])
+        check_sample(ck, wide[:, :vocab], [65536] * 3)
 
 
 def test_sampling_of_rows_apart_on_other_streams_and_captured(ck):
