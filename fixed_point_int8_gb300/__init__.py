@@ -95,6 +95,8 @@ def lib() -> ctypes.CDLL:
             "ck_pages_work": ([vp, u32, u32, vp], ctypes.c_int),
             "ck_pages_fork": ([vp, u32, vp, vp, u32, vp, vp, u32, vp, vp, vp, vp, vp, sz, vp], ctypes.c_int),
             "ck_pages_compact": ([vp, u32, vp, vp, u32, vp, vp, vp, vp, sz, vp], ctypes.c_int),
+            "ck_pages_window_fork": ([vp, u32, vp, vp, u32, vp, vp, u32, vp, vp, vp, vp, vp, vp, sz, vp], ctypes.c_int),
+            "ck_pages_window_compact": ([vp, u32, vp, vp, u32, vp, vp, vp, vp, vp, sz, vp], ctypes.c_int),
             "ck_pages_advance": ([vp, u32, vp, vp, vp, u32, vp, vp, u32, vp, vp, vp, vp, vp, vp, vp, sz, vp],
                                  ctypes.c_int),
             "ck_sample": ([vp, sz, u32, u32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp], ctypes.c_int),

@@ -209,7 +209,7 @@ struct PagesParams {
   uint32_t* table_out;
   uint32_t* status;
   uint32_t* used_out;
-  uint32_t rows_in, rows, stride, pages, page_shift;
+  uint32_t rows_in, rows, stride, pages, page_shift, sinks, window;
   uint32_t* owner;      // pages: rows - the lowest row that holds the page part-filled (0: none)
   uint32_t* bits;       // pages that a row holds whole (packing: holds at all)
   uint32_t* copied;     // number of copies
@@ -224,8 +224,20 @@ constexpr int kPlanThreads = 1024;
 
 __device__ __forceinline__ bool bit_of(const uint32_t* bits, uint32_t i) { return (bits[i >> 5] >> (i & 31)) & 1u; }
 
-// Forking, first step (a warp a row): checks the row, takes over the parent's whole pages and
-// marks them, and bids for its part-filled page.
+// Of a sequence of `len` positions on `have` pages the ones that its next position or a later one sees: those
+// with a position below `sinks`, and from the one on that ends behind len - window.  The page that the next
+// position goes on in is one of them, whatever the window.
+struct Kept {
+  uint32_t early, late, have;
+  __device__ __forceinline__ bool operator()(uint32_t i) const { return i < early || i - late < have - late; }
+};
+__device__ __forceinline__ Kept kept_pages(uint32_t len, uint32_t have, uint32_t sinks, uint32_t window, uint32_t page_shift) {
+  const uint32_t early = (uint32_t)min(((unsigned long long)sinks + (1u << page_shift) - 1) >> page_shift, (unsigned long long)have);
+  return {early, min(have, window <= len ? (len + 1 - window) >> page_shift : 0), have};
+}
+
+// Forking, first step (a warp a row): checks the row, takes over those of the parent's whole pages that its
+// window keeps and marks them, and bids for its part-filled page.
 __device__ __forceinline__ void fork_mark(const PagesParams& p, uint32_t r, uint32_t lane) {
   const uint32_t parent = p.parent[r];
   uint32_t status = 0, old = 0;
@@ -240,15 +252,16 @@ __device__ __forceinline__ void fork_mark(const PagesParams& p, uint32_t r, uint
   }
   const uint32_t full = old >> p.page_shift, part = old & ((1u << p.page_shift) - 1);
   const uint32_t* from = p.table_in + (size_t)parent * p.stride;
+  const Kept keeps = kept_pages(old, full + (part != 0), p.sinks, p.window, p.page_shift);
   if (status == 0 && parent != CK_NO_PAGE) {
     bool bad = false;
-    for (uint32_t i = lane; i < full + (part != 0); i += 32) bad |= from[i] >= p.pages;
+    for (uint32_t i = lane; i < keeps.have; i += 32) bad |= keeps(i) && from[i] >= p.pages;
     if (__any_sync(0xffffffffu, bad)) status = CK_INVALID_STATE;
   }
   const bool live = status == 0 && parent != CK_NO_PAGE;
   uint32_t* to = p.table_out + (size_t)r * p.stride;
   for (uint32_t i = lane; i < p.stride; i += 32) {
-    const uint32_t id = live && i < full ? from[i] : CK_NO_PAGE;
+    const uint32_t id = live && i < full && keeps(i) ? from[i] : CK_NO_PAGE;
     to[i] = id;
     if (id != CK_NO_PAGE) atomicOr(p.bits + (id >> 5), 1u << (id & 31));
   }
@@ -372,11 +385,13 @@ __device__ __forceinline__ void compact_mark(const PagesParams& p, uint32_t r, u
   if (len > kMaxPositions || len > ((uint64_t)p.stride << p.page_shift)) status = CK_CONTEXT_EXCEEDED;
   const uint32_t n = status ? 0u : (len + (1u << p.page_shift) - 1) >> p.page_shift;
   const uint32_t* from = p.table_in + (size_t)r * p.stride;
+  const Kept keeps = kept_pages(len, n, p.sinks, p.window, p.page_shift);
   bool bad = false;
-  for (uint32_t i = lane; i < n; i += 32) bad |= from[i] >= p.pages;
+  for (uint32_t i = lane; i < n; i += 32) bad |= keeps(i) && from[i] >= p.pages;
   if (__any_sync(0xffffffffu, bad)) status = CK_INVALID_STATE;
   if (status == 0)
-    for (uint32_t i = lane; i < n; i += 32) atomicOr(p.bits + (from[i] >> 5), 1u << (from[i] & 31));
+    for (uint32_t i = lane; i < n; i += 32)
+      if (keeps(i)) atomicOr(p.bits + (from[i] >> 5), 1u << (from[i] & 31));
   if (lane == 0) p.status[r] = status;
 }
 __global__ void __launch_bounds__(kTableThreads) k_compact_mark(const PagesParams p) {
@@ -387,9 +402,10 @@ __global__ void __launch_bounds__(kTableThreads) k_compact_mark(const PagesParam
 // Third step (a warp a row): the row's pages by their new numbers.
 __device__ __forceinline__ void compact_table(const PagesParams& p, uint32_t r, uint32_t lane, uint32_t used) {
   const uint32_t n = p.status[r] ? 0u : (p.len_in[r] + (1u << p.page_shift) - 1) >> p.page_shift;
+  const Kept keeps = kept_pages(p.len_in[r], n, p.sinks, p.window, p.page_shift);
   for (uint32_t i = lane; i < p.stride; i += 32) {
     uint32_t id = CK_NO_PAGE;
-    if (i < n) {
+    if (i < n && keeps(i)) {
       id = p.table_in[(size_t)r * p.stride + i];
       if (id >= used) id = p.owner[id];
     }
@@ -495,14 +511,11 @@ __device__ __forceinline__ void advance_mark(const AdvanceParams& p, uint32_t* b
       else if ((unsigned long long)len + ask > longest(p))
         status = CK_CONTEXT_EXCEEDED;
       const uint32_t have = status == CK_INVALID_STATE ? 0 : pages_of(p, len);
-      // kept: the pages with a position below `sinks`, and from that on which ends behind len - window
-      const uint32_t early = (uint32_t)min(((unsigned long long)p.sinks + (1u << p.page_shift) - 1) >> p.page_shift, (unsigned long long)have);
-      const uint32_t late = min(have, p.window <= len ? (len + 1 - p.window) >> p.page_shift : 0);
-      auto keeps = [&](uint32_t i) { return i < early || i - late < have - late; };
+      const Kept keeps = kept_pages(len, have, p.sinks, p.window, p.page_shift);
       const uint32_t* from = p.table_in + (size_t)s * p.stride;
       uint32_t* to = p.table_out + (size_t)s * p.stride;
       constexpr uint32_t kStep = 32 * kEntries;
-      auto none = [&](uint32_t i0) { return i0 >= have || (i0 >= early && i0 + kStep <= late); };  // of a step's entries
+      auto none = [&](uint32_t i0) { return i0 >= have || (i0 >= keeps.early && i0 + kStep <= keeps.late); };  // of a step's entries
       uint32_t id[kEntries];
       auto read = [&](uint32_t i0) {
 #pragma unroll
@@ -752,11 +765,13 @@ bool advance_alone(uint32_t seqs, uint32_t stride, uint32_t pages) {
   return (uint64_t)seqs * stride <= (1u << 19) && pages <= kAdvancePages;
 }
 
-PagesParams pages_params(const ck_paged_cache* c, const PagesLayout& w, void* work) {
+PagesParams pages_params(const ck_paged_cache* c, const ck_window* window, const PagesLayout& w, void* work) {
   uint8_t* b = static_cast<uint8_t*>(work);
   PagesParams p = {};
   p.pages = c->pages;
   p.page_shift = log2_of(c->page);
+  p.sinks = window ? window->sinks : 0;
+  p.window = window ? window->window : 0xFFFFFFFFu;
   p.owner = reinterpret_cast<uint32_t*>(b + w.owner);
   p.bits = reinterpret_cast<uint32_t*>(b + w.bits);
   p.copied = reinterpret_cast<uint32_t*>(b + w.counters);
@@ -825,15 +840,15 @@ int ck_pages_work(const ck_paged_cache* cache, uint32_t rows, uint32_t stride, s
   return CK_OK;
 }
 
-int ck_pages_fork(const ck_paged_cache* cache, uint32_t rows_in, const uint32_t* dev_len_in,
-                  const uint32_t* dev_table_in, uint32_t rows, const uint32_t* dev_parent,
-                  const uint32_t* dev_grow, uint32_t stride, const uint8_t* dev_held,
-                  uint32_t* dev_len_out, uint32_t* dev_table_out, uint32_t* dev_status, void* dev_work,
-                  size_t work_len, void* stream) {
+int ck_pages_window_fork(const ck_paged_cache* cache, uint32_t rows_in, const uint32_t* dev_len_in,
+                         const uint32_t* dev_table_in, uint32_t rows, const uint32_t* dev_parent,
+                         const uint32_t* dev_grow, uint32_t stride, const ck_window* window, const uint8_t* dev_held,
+                         uint32_t* dev_len_out, uint32_t* dev_table_out, uint32_t* dev_status, void* dev_work,
+                         size_t work_len, void* stream) {
   PagesLayout w;
   if (const int rc = pages_args(cache, rows, stride, dev_work, work_len, &w)) return rc;
   if (rows_in < 1 || rows_in > 65536 || !dev_len_in || !dev_table_in || !dev_parent || !dev_grow || !dev_len_out ||
-      !dev_table_out || !dev_status)
+      !dev_table_out || !dev_status || (window && window->window == 0))
     return CK_INVALID_ARGUMENT;
   const void* in[] = {dev_len_in, dev_table_in, dev_parent, dev_grow, dev_held};
   const uint64_t in_bytes[] = {4ull * rows_in, 4ull * rows_in * stride, 4ull * rows, 4ull * rows,
@@ -849,7 +864,7 @@ int ck_pages_fork(const ck_paged_cache* cache, uint32_t rows_in, const uint32_t*
     for (int i = 0; i < o; ++i)
       if (overlaps(out[o], out_bytes[o], out[i], out_bytes[i])) return CK_INVALID_ARGUMENT;
   }
-  PagesParams p = pages_params(cache, w, dev_work);
+  PagesParams p = pages_params(cache, window, w, dev_work);
   p.len_in = dev_len_in;
   p.table_in = dev_table_in;
   p.parent = dev_parent;
@@ -879,13 +894,23 @@ int ck_pages_fork(const ck_paged_cache* cache, uint32_t rows_in, const uint32_t*
   return run_copies(cache, p, s);
 }
 
-int ck_pages_compact(const ck_paged_cache* cache, uint32_t rows, const uint32_t* dev_len,
-                     const uint32_t* dev_table_in, uint32_t stride, uint32_t* dev_table_out,
-                     uint32_t* dev_used, uint32_t* dev_status, void* dev_work, size_t work_len,
-                     void* stream) {
+int ck_pages_fork(const ck_paged_cache* cache, uint32_t rows_in, const uint32_t* dev_len_in,
+                  const uint32_t* dev_table_in, uint32_t rows, const uint32_t* dev_parent,
+                  const uint32_t* dev_grow, uint32_t stride, const uint8_t* dev_held,
+                  uint32_t* dev_len_out, uint32_t* dev_table_out, uint32_t* dev_status, void* dev_work,
+                  size_t work_len, void* stream) {
+  return ck_pages_window_fork(cache, rows_in, dev_len_in, dev_table_in, rows, dev_parent, dev_grow, stride, nullptr,
+                              dev_held, dev_len_out, dev_table_out, dev_status, dev_work, work_len, stream);
+}
+
+int ck_pages_window_compact(const ck_paged_cache* cache, uint32_t rows, const uint32_t* dev_len,
+                            const uint32_t* dev_table_in, uint32_t stride, const ck_window* window,
+                            uint32_t* dev_table_out, uint32_t* dev_used, uint32_t* dev_status, void* dev_work,
+                            size_t work_len, void* stream) {
   PagesLayout w;
   if (const int rc = pages_args(cache, rows, stride, dev_work, work_len, &w)) return rc;
-  if (!dev_len || !dev_table_in || !dev_table_out || !dev_used || !dev_status) return CK_INVALID_ARGUMENT;
+  if (!dev_len || !dev_table_in || !dev_table_out || !dev_used || !dev_status || (window && window->window == 0))
+    return CK_INVALID_ARGUMENT;
   const void* in[] = {dev_len, dev_table_in};
   const uint64_t in_bytes[] = {4ull * rows, 4ull * rows * stride};
   const void* out[] = {dev_used, dev_table_out, dev_status, dev_work};
@@ -897,7 +922,7 @@ int ck_pages_compact(const ck_paged_cache* cache, uint32_t rows, const uint32_t*
     for (int i = 0; i < o; ++i)
       if (overlaps(out[o], out_bytes[o], out[i], out_bytes[i])) return CK_INVALID_ARGUMENT;
   }
-  PagesParams p = pages_params(cache, w, dev_work);
+  PagesParams p = pages_params(cache, window, w, dev_work);
   p.len_in = dev_len;
   p.table_in = dev_table_in;
   p.table_out = dev_table_out;
@@ -922,6 +947,14 @@ int ck_pages_compact(const ck_paged_cache* cache, uint32_t rows, const uint32_t*
   }
   CKP_CUDA(cudaGetLastError());
   return run_copies(cache, p, s);
+}
+
+int ck_pages_compact(const ck_paged_cache* cache, uint32_t rows, const uint32_t* dev_len,
+                     const uint32_t* dev_table_in, uint32_t stride, uint32_t* dev_table_out,
+                     uint32_t* dev_used, uint32_t* dev_status, void* dev_work, size_t work_len,
+                     void* stream) {
+  return ck_pages_window_compact(cache, rows, dev_len, dev_table_in, stride, nullptr, dev_table_out, dev_used, dev_status,
+                                 dev_work, work_len, stream);
 }
 
 int ck_pages_advance(const ck_paged_cache* cache, uint32_t seqs, const uint32_t* dev_len_in,

@@ -351,11 +351,12 @@ class PagePlan:
         _check("lens", lens, torch.int32, (rows,), device)
         return device, rows
 
-    def fork(self, parent, lens, table, grow, held=None, stream=None):
+    def fork(self, parent, lens, table, grow, held=None, stream=None, window=None):
         """ck_pages_fork: output row r takes over input row parent[r] (-1: none) and gets pages for
         grow[r] more positions; held (uint8 [pages]): PAGE_RESERVED pages are not handed out,
         PAGE_SHARED ones, of sequences that live on outside the call, are also copied where a row
-        has them part-filled.  Returns (rc, Fork)."""
+        has them part-filled.  window: the Window of sequences that advance() moves on
+        (ck_pages_window_fork).  Returns (rc, Fork)."""
         device, rows_in = self._begin(lens, table, stream)
         rows = parent.numel()
         if rows > self.rows:
@@ -364,13 +365,14 @@ class PagePlan:
         _check("grow", grow, torch.int32, (rows,), device)
         if held is not None:
             _check("held", held, torch.uint8, (self.cache.pages,), device)
+        view = _window(window)
         _keep(stream, self._work, parent, lens, table, grow, *(() if held is None else (held,)), *self.cache._tensors)
         out = _empty(stream, (rows, self.stride), torch.int32, device)
         new_lens, status = _empty(stream, (rows,), torch.int32, device), _empty(stream, (rows,), torch.int32, device)
-        rc = lib().ck_pages_fork(self.cache._c, rows_in, lens.data_ptr(), table.data_ptr(), rows, parent.data_ptr(),
-                                 grow.data_ptr(), self.stride, None if held is None else held.data_ptr(),
-                                 new_lens.data_ptr(), out.data_ptr(), status.data_ptr(), *self._args,
-                                 _on(stream, device, self, self.cache))
+        rc = lib().ck_pages_window_fork(self.cache._c, rows_in, lens.data_ptr(), table.data_ptr(), rows,
+                                        parent.data_ptr(), grow.data_ptr(), self.stride, view,
+                                        None if held is None else held.data_ptr(), new_lens.data_ptr(), out.data_ptr(),
+                                        status.data_ptr(), *self._args, _on(stream, device, self, self.cache))
         return rc, Fork(out, new_lens, status)
 
     def advance(self, lens, table, new, rows, window=None, held=None, stream=None):
@@ -396,18 +398,20 @@ class PagePlan:
                                     status.data_ptr(), *self._args, _on(stream, device, self, self.cache))
         return rc, Advance(*got)
 
-    def compact(self, lens, table, stream=None):
-        """ck_pages_compact: the rows' pages move to the lowest page numbers.  Returns (rc, Compact)."""
+    def compact(self, lens, table, stream=None, window=None):
+        """ck_pages_compact: the rows' pages move to the lowest page numbers; window: as fork's
+        (ck_pages_window_compact).  Returns (rc, Compact)."""
         device, rows = self._begin(lens, table, stream)
         if rows > self.rows:
             raise ValueError(f"table: {rows} rows, the plan has room for {self.rows}")
+        view = _window(window)
         _keep(stream, self._work, lens, table, *self.cache._tensors)
         out = _empty(stream, (rows, self.stride), torch.int32, device)
         status = _empty(stream, (rows,), torch.int32, device)
         used = _empty(stream, (), torch.int32, device)
-        rc = lib().ck_pages_compact(self.cache._c, rows, lens.data_ptr(), table.data_ptr(), self.stride,
-                                    out.data_ptr(), used.data_ptr(), status.data_ptr(), *self._args,
-                                    _on(stream, device, self, self.cache))
+        rc = lib().ck_pages_window_compact(self.cache._c, rows, lens.data_ptr(), table.data_ptr(), self.stride, view,
+                                           out.data_ptr(), used.data_ptr(), status.data_ptr(), *self._args,
+                                           _on(stream, device, self, self.cache))
         return rc, Compact(out, used, status)
 
 

@@ -499,10 +499,28 @@ int ck_pages_compact(const ck_paged_cache* cache, uint32_t rows, const uint32_t*
                      uint32_t* dev_used, uint32_t* dev_status, void* dev_work, size_t work_len,
                      void* stream);
 
+/* The same for streams with windows, whose tables ck_pages_advance has left without the pages behind them:
+ * of a sequence `len` positions long (forking: before it grows) the pages that its position `len` or a
+ * later one sees are its pages (one with a position below `sinks`, or with one of the window - 1 before
+ * `len`); the others are given back, their entries are not read and come out as CK_NO_PAGE.  (For layers
+ * that differ, give the widest window and the most sinks; null: the calls above, for which an empty entry is
+ * one outside the pool.  Packing without the window takes such a row's pages from it.)  Errors: those of the
+ * calls above, and 10 for a window of 0. */
+int ck_pages_window_fork(const ck_paged_cache* cache, uint32_t rows_in, const uint32_t* dev_len_in,
+                         const uint32_t* dev_table_in, uint32_t rows, const uint32_t* dev_parent,
+                         const uint32_t* dev_grow, uint32_t stride, const ck_window* window, const uint8_t* dev_held,
+                         uint32_t* dev_len_out, uint32_t* dev_table_out, uint32_t* dev_status, void* dev_work,
+                         size_t work_len, void* stream);
+int ck_pages_window_compact(const ck_paged_cache* cache, uint32_t rows, const uint32_t* dev_len,
+                            const uint32_t* dev_table_in, uint32_t stride, const ck_window* window,
+                            uint32_t* dev_table_out, uint32_t* dev_used, uint32_t* dev_status, void* dev_work,
+                            size_t work_len, void* stream);
+
 /* Between two passes: sequence s, dev_len_in[s] positions long with its pages in row s of
  * dev_table_in, asks for dev_new[s] more (0: none).  With a window it gives back the pages that
  * neither its next position nor a later one sees (no position below `sinks`, none among the
- * window - 1 before the next): their entries come out as CK_NO_PAGE, and are not read here again.  (For
+ * window - 1 before the next): their entries come out as CK_NO_PAGE, and are not read here again (nor by
+ * ck_pages_window_fork and ck_pages_window_compact, which such tables go to from then on).  (For
  * layers that differ, give the widest window and the most sinks; null: every page stays.)  Free are the pages
  * that no sequence keeps and that are not marked in dev_held (u8 [pages], nonzero: not handed out;
  * may be null); they are handed out in ascending order, sequence after sequence.  Sequences may

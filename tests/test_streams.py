@@ -6,7 +6,7 @@ import ctypes
 import numpy as np
 import pytest
 
-from test_paged import ADDR, BAD_BATCHES, BAD_CACHES, attention_args, batch, cache, call, ck  # noqa: F401
+from test_paged import ADDR, BAD_BATCHES, BAD_CACHES, attention_args, batch, cache, call, ck, compact_args, fork_args  # noqa: F401
 
 
 def window(ck, sinks=4, size=16):
@@ -119,3 +119,34 @@ def test_numbers_of_a_window_past_32_bits_are_refused(ck):
     assert ck.paged._window(None) is None and ck.paged._windows(None, 3) is None
     each = ck.paged._windows([ck.Window(0, 4), ck.Window(2, 9), ck.Window(1, 1)], 3)
     assert [(w.sinks, w.window) for w in each] == [(0, 4), (2, 9), (1, 1)]
+
+
+@pytest.mark.parametrize("bad", [
+    dict(cache=None), dict(rows_in=0), dict(rows=65537), dict(stride=0), dict(len_in=None), dict(table_in=None),
+    dict(parent=None), dict(grow=None), dict(len_out=None), dict(table_out=None), dict(status=None), dict(work=None),
+    dict(table_out=2 * ADDR + 60), dict(len_out=ADDR), dict(status=5 * ADDR), dict(held=8 * ADDR), dict(window="empty"),
+    dict(work_len=64)], ids=str)
+def test_wrong_forks_of_streams_are_refused(ck, bad):
+    args = {}
+    for name, value in fork_args(ck).items():
+        if name == "held":
+            args["window"] = window(ck)
+        args[name] = value
+    if bad == dict(window="empty"):
+        bad = dict(window=window(ck, 4, 0))
+    assert call(ck, "ck_pages_window_fork", args, **bad) == (4 if "work_len" in bad else 10)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(cache=None), dict(rows=0), dict(stride=2**17 + 1), dict(len=None), dict(table_in=None), dict(table_out=None),
+    dict(used=None), dict(status=None), dict(work=None), dict(table_out=2 * ADDR), dict(window="empty"), dict(work_len=64)],
+    ids=str)
+def test_wrong_packings_of_streams_are_refused(ck, bad):
+    args = {}
+    for name, value in compact_args(ck).items():
+        if name == "table_out":
+            args["window"] = window(ck)
+        args[name] = value
+    if bad == dict(window="empty"):
+        bad = dict(window=window(ck, 4, 0))
+    assert call(ck, "ck_pages_window_compact", args, **bad) == (4 if "work_len" in bad else 10)
