@@ -482,9 +482,13 @@ struct AdvanceParams {
   uint32_t* position;
   uint32_t* status;
   uint32_t seqs, stride, pages, page_shift, rows, sinks, window;
-  uint32_t* bits;             // pages that are not free
+  uint32_t* bits;             // pages that a sequence keeps, but for
+  uint32_t* parts;            // those that one goes on in
+  uint32_t* apart;            // those held outside the call, where there are any
   uint32_t* list;             // free pages
-  unsigned long long* before; // of each sequence the pages that those before it ask for
+  // of each sequence the part-filled page that it goes on in, CK_NO_PAGE for none; from the second step on the
+  // pages that those before it ask for
+  unsigned long long* before;
 };
 
 __device__ __forceinline__ uint32_t pages_of(const AdvanceParams& p, uint32_t len) {
@@ -496,13 +500,17 @@ __device__ __forceinline__ uint32_t longest(const AdvanceParams& p) {
 }
 
 // First step (a warp takes sequence first and every `step`-th behind it, 32 at a time): checks them, takes
-// over and marks the pages that their next position or a later one sees.
+// over and marks the pages that their next position or a later one sees.  The part-filled ones that sequences go
+// on in have marks of their own, so that a page with both marks is not such a sequence's alone; two of them on a
+// page leave both, too.
 constexpr uint32_t kEntries = 4;  // of a table row, a lane holds
-__device__ __forceinline__ void advance_mark(const AdvanceParams& p, uint32_t* bits, uint32_t first, uint32_t step, uint32_t lane) {
+__device__ __forceinline__ void advance_mark(const AdvanceParams& p, uint32_t* bits, uint32_t* parts, uint32_t first,
+                                             uint32_t step, uint32_t lane) {
   for (; first < p.seqs; first += 32 * step) {
     const uint64_t at = first + (uint64_t)lane * step;  // this lane's sequence
     const uint32_t lens = at < p.seqs ? p.len_in[at] : 0, asks = at < p.seqs ? p.ask[at] : 0;
     const uint32_t many = min(32u, (p.seqs - first + step - 1) / step);
+    uint32_t my_status = 0, my_part = CK_NO_PAGE;  // this lane's
     for (uint32_t k = 0; k < many; ++k) {
       const uint32_t s = first + k * step, len = __shfl_sync(0xffffffffu, lens, k), ask = __shfl_sync(0xffffffffu, asks, k);
       uint32_t status = 0;
@@ -531,6 +539,9 @@ __device__ __forceinline__ void advance_mark(const AdvanceParams& p, uint32_t* b
       }
       if (__any_sync(0xffffffffu, bad)) status = CK_INVALID_STATE;
       const bool live = status != CK_INVALID_STATE;
+      // the part-filled page that the sequence goes on in
+      const uint32_t part_at = status == 0 && ask && (len & ((1u << p.page_shift) - 1)) ? have - 1 : CK_NO_PAGE;
+      uint32_t part = 0;
       for (uint32_t i0 = 0; i0 < p.stride; i0 += kStep) {
         const bool empty = !live || none(i0);
         if (!empty && last != i0) read(last = i0);
@@ -539,27 +550,55 @@ __device__ __forceinline__ void advance_mark(const AdvanceParams& p, uint32_t* b
           const uint32_t i = i0 + 32 * j + lane;
           const bool kept = !empty && keeps(i);
           if (i < p.stride) to[i] = kept ? id[j] : CK_NO_PAGE;
-          if (kept) atomicOr(bits + (id[j] >> 5), 1u << (id[j] & 31));
+          if (i == part_at) part = id[j];
+          if (kept && i != part_at) atomicOr(bits + (id[j] >> 5), 1u << (id[j] & 31));
         }
       }
-      if (lane == 0) p.status[s] = status;
+      part = __shfl_sync(0xffffffffu, part, part_at & 31);
+      if (lane == k) {
+        my_status = status;
+        my_part = part_at == CK_NO_PAGE ? CK_NO_PAGE : part;
+      }
+    }
+    if (at < p.seqs) {
+      p.status[at] = my_status;
+      p.before[at] = my_part;
+      const uint32_t bit = 1u << (my_part & 31);
+      if (my_part != CK_NO_PAGE && (atomicOr(parts + (my_part >> 5), bit) & bit)) atomicOr(bits + (my_part >> 5), bit);
     }
   }
 }
-// and the pages held outside the call: a warp takes the `first`-th eight words of 32 and every `step`-th
-// eight behind.
+// and the pages held outside the call (in words of their own: a sequence may go on in one that is not handed out), of
+// which those shared with a sequence there are marked as well: a warp takes the `first`-th eight words of 32 and
+// every `step`-th eight behind.
 __device__ __forceinline__ void advance_held(const AdvanceParams& p, uint32_t* bits, uint32_t first, uint32_t step, uint32_t lane) {
   const uint32_t words = (p.pages + 31) / 32;
   for (uint32_t w0 = 8 * first; w0 < words; w0 += 8 * step) {
     uint8_t held[8];
+    uint32_t mine = 0, shared = 0;  // lane j's words
 #pragma unroll
     for (uint32_t j = 0; j < 8; ++j) held[j] = (w0 + j) * 32 + lane < p.pages ? __ldg(p.held + (w0 + j) * 32 + lane) : 0;
 #pragma unroll
     for (uint32_t j = 0; j < 8; ++j) {
       const uint32_t word = __ballot_sync(0xffffffffu, held[j] != 0);
-      if (lane == 0 && word) atomicOr(bits + w0 + j, word);
+      const uint32_t theirs = __ballot_sync(0xffffffffu, held[j] & CK_PAGE_SHARED);
+      if (lane == j) {
+        mine = word;
+        shared = theirs;
+      }
     }
+    if (lane < 8 && w0 + lane < words) p.apart[w0 + lane] = mine;
+    if (shared) atomicOr(bits + w0 + lane, shared);
   }
+}
+
+// Before the second step (one block): the sequences that would go on in a page with both marks are refused.
+__device__ __forceinline__ void advance_refuse(const AdvanceParams& p) {
+  for (uint32_t s = threadIdx.x; s < p.seqs; s += kPlanThreads) {
+    const uint32_t part = (uint32_t)p.before[s];
+    if (part != CK_NO_PAGE && bit_of(p.bits, part)) p.status[s] = CK_INVALID_ARGUMENT;
+  }
+  __syncthreads();
 }
 
 // Second step (one block): the free pages in ascending order, as many as are asked for, which
@@ -586,7 +625,7 @@ __device__ __forceinline__ void advance_plan(const AdvanceParams& p, unsigned lo
 #pragma unroll
     for (uint32_t j = 0; j < 4; ++j) {
       const uint32_t w = base + 4 * tid + j;
-      free[j] = w < words ? ~p.bits[w] : 0;
+      free[j] = w < words ? ~(p.bits[w] | p.parts[w] | (p.held ? p.apart[w] : 0)) : 0;
       if (w == words - 1 && (p.pages & 31)) free[j] &= (1u << (p.pages & 31)) - 1;
       count += __popc(free[j]);
     }
@@ -664,13 +703,14 @@ __global__ void __launch_bounds__(kTableThreads) k_advance_mark(const AdvancePar
   const uint32_t warps = gridDim.x * (kTableThreads / 32), lane = threadIdx.x & 31;
   const uint32_t w = blockIdx.x * (kTableThreads / 32) + __shfl_sync(0xffffffffu, threadIdx.x / 32, 0);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  advance_mark(p, p.bits, w, warps, lane);
+  advance_mark(p, p.bits, p.parts, w, warps, lane);
   if (p.held) advance_held(p, p.bits, w, warps, lane);
 }
 __global__ void __launch_bounds__(kPlanThreads) k_advance_plan(const AdvanceParams p) {
   __shared__ unsigned long long warp_sum[kPlanThreads / 32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  advance_refuse(p);
   advance_plan(p, warp_sum);
 }
 __global__ void __launch_bounds__(kTableThreads) k_advance_fill(const AdvanceParams p) {
@@ -682,37 +722,59 @@ __global__ void __launch_bounds__(kTableThreads) k_advance_fill(const AdvancePar
 // All of it in one launch, by a cluster of blocks or one: the steps are separated by the cluster's barriers
 // (which order what its blocks write to global memory), the second is the first block's.  Every block marks
 // pages in its own shared memory (131,000 atomics on L2 from eight SMs take 17 us).  The chain of loads and
-// sums bounds it: 4.5 us for 4 sequences, 11 for 64 with 512 table entries each, 24 for 2,048 with 128 (four
-// launches over the whole GPU: 12, 16 and 16 on the device, but 43 for the host's calls against 25).
+// sums bounds it: 4.8 us for 4 sequences, 14 for 64 with 512 table entries each, 25 for 2,048 with 128, of which the
+// marks for parts take 0.3, 1 and 3 (waiting for what every entry's atomic returns took 5).
+constexpr uint32_t kAdvanceBlocks = 8;
 __global__ void __launch_bounds__(kPlanThreads) k_advance(const AdvanceParams p, uint32_t blocks) {
   __shared__ unsigned long long warp_sum[kPlanThreads / 32];
   extern __shared__ __align__(16) uint32_t marks[];
   const uint32_t tid = threadIdx.x, lane = tid & 31, warps = blocks * (kPlanThreads / 32), words = (p.pages + 31) / 32;
   const uint32_t w = blockIdx.x * (kPlanThreads / 32) + __shfl_sync(0xffffffffu, tid / 32, 0);
+  uint32_t* parts = marks + words;
+  __shared__ uint32_t refusals;  // the first block's: some page has both marks
+  if (tid == 0) refusals = 0;
   auto sync = [&] {
     if (blocks > 1)
       asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
     else
       __syncthreads();
   };
-  for (uint32_t i = tid; i < words; i += kPlanThreads) marks[i] = 0;
+  for (uint32_t i = tid; i < 2 * words; i += kPlanThreads) marks[i] = 0;
   __syncthreads();
-  advance_mark(p, marks, w, warps, lane);
+  advance_mark(p, marks, parts, w, warps, lane);
   if (p.held) advance_held(p, marks, w, warps, lane);
   sync();
   const uint32_t share = (words + blocks - 1) / blocks, end = min(words, (blockIdx.x + 1) * share);
   for (uint32_t i = blockIdx.x * share + tid; i < end; i += kPlanThreads) {
-    uint32_t word = marks[i];
-    for (uint32_t k = 1; k < blocks; ++k) {
-      uint32_t at = (uint32_t)__cvta_generic_to_shared(marks + i), other;
-      asm("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(at) : "r"((blockIdx.x + k) % blocks));
-      asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(other) : "r"(at) : "memory");
-      word |= other;
+    uint32_t word = marks[i], part = parts[i], others[kAdvanceBlocks], other_parts[kAdvanceBlocks];
+#pragma unroll
+    for (uint32_t k = 1; k < kAdvanceBlocks; ++k) {  // (all asked for at once)
+      others[k] = other_parts[k] = 0;
+      if (k < blocks) {
+        uint32_t at = (uint32_t)__cvta_generic_to_shared(marks + i);
+        asm("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(at) : "r"((blockIdx.x + k) % blocks));
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(others[k]) : "r"(at) : "memory");
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(other_parts[k]) : "r"(at + 4 * words) : "memory");
+      }
+    }
+#pragma unroll
+    for (uint32_t k = 1; k < kAdvanceBlocks; ++k) {
+      word |= others[k] | (part & other_parts[k]);
+      part |= other_parts[k];
     }
     p.bits[i] = word;
+    p.parts[i] = part;
+    if (word & part) {
+      uint32_t at = (uint32_t)__cvta_generic_to_shared(&refusals);
+      asm("mapa.shared::cluster.u32 %0, %0, 0;" : "+r"(at));
+      asm volatile("st.shared::cluster.u32 [%0], 1;" ::"r"(at) : "memory");
+    }
   }
   sync();  // (and no block leaves while another reads its marks)
-  if (blockIdx.x == 0) advance_plan(p, warp_sum);
+  if (blockIdx.x == 0) {
+    if (refusals) advance_refuse(p);
+    advance_plan(p, warp_sum);
+  }
   sync();
   advance_fill(p, w, warps, lane);
   advance_rest(p, blockIdx.x * kPlanThreads + tid, blocks * kPlanThreads);
@@ -759,8 +821,9 @@ bool table_work_alone(uint32_t rows, uint32_t stride, uint32_t pages) {
   return (uint64_t)rows * ((stride + 31) / 32) <= 1024 && pages <= 65536;
 }
 
-// One cluster does all of a step of up to 2 MB of tables and 2^20 pages (measured).
-constexpr uint32_t kAdvanceBlocks = 8, kAdvancePages = 1u << 20;
+// One cluster does all of a step of up to 2 MB of tables (measured) and as many pages as two marks each in shared
+// memory allow.
+constexpr uint32_t kAdvancePages = 7u << 17;
 bool advance_alone(uint32_t seqs, uint32_t stride, uint32_t pages) {
   return (uint64_t)seqs * stride <= (1u << 19) && pages <= kAdvancePages;
 }
@@ -999,7 +1062,10 @@ int ck_pages_advance(const ck_paged_cache* cache, uint32_t seqs, const uint32_t*
   p.sinks = window ? window->sinks : 0;
   p.window = window ? window->window : 0xFFFFFFFFu;
   uint8_t* b = static_cast<uint8_t*>(dev_work);
+  const uint32_t words = (p.pages + 31) / 32;
   p.bits = reinterpret_cast<uint32_t*>(b + w.bits);
+  p.parts = p.bits - words;  // (at the end of the owners, which a step doesn't use, as it doesn't the second list)
+  p.apart = reinterpret_cast<uint32_t*>(b + w.list2);
   p.list = reinterpret_cast<uint32_t*>(b + w.list);
   p.before = reinterpret_cast<unsigned long long*>(b + w.before);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1016,17 +1082,17 @@ int ck_pages_advance(const ck_paged_cache* cache, uint32_t seqs, const uint32_t*
     CKP_CUDA(device_facts(&f));
     static std::atomic<bool> ready[64];
     if (!ready[f.dev].load(std::memory_order_relaxed)) {
-      CKP_CUDA(cudaFuncSetAttribute(k_advance, cudaFuncAttributeMaxDynamicSharedMemorySize, kAdvancePages / 8));
+      CKP_CUDA(cudaFuncSetAttribute(k_advance, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * kAdvancePages / 8));
       ready[f.dev].store(true, std::memory_order_relaxed);
     }
-    cfg.dynamicSmemBytes = (cache->pages + 31) / 32 * 4;
+    cfg.dynamicSmemBytes = 8 * words;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = blocks;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     CKP_CUDA(cudaLaunchKernelEx(&cfg, k_advance, p, blocks));
     return CK_OK;
   }
-  CKP_CUDA(cudaMemsetAsync(p.bits, 0, 4ull * ((p.pages + 31) / 32), s));
+  CKP_CUDA(cudaMemsetAsync(p.parts, 0, 8ull * words, s));  // and the bits behind it
   constexpr uint32_t per = kTableThreads / 32;
   const uint32_t blocks = (seqs + per - 1) / per;
   k_advance_mark<<<blocks, kTableThreads, 0, s>>>(p);

@@ -378,7 +378,9 @@ class PagePlan:
     def advance(self, lens, table, new, rows, window=None, held=None, stream=None):
         """ck_pages_advance: every sequence gives back the pages behind its Window (None: it keeps all) and
         gets pages for new[s] more positions, at most `rows` of them together; held (uint8 [pages]):
-        nonzero pages are not handed out.  The outputs' tensors are a PagedBatch's.  Returns (rc, Advance)."""
+        nonzero pages are not handed out.  A sequence whose part-filled page another entry names, or that
+        is PAGE_SHARED, gets no rows (status 10).  The outputs' tensors are a PagedBatch's.  Returns (rc,
+        Advance)."""
         device, seqs = self._begin(lens, table, stream)
         if seqs > self.rows:
             raise ValueError(f"table: {seqs} rows, the plan has room for {self.rows}")

@@ -525,15 +525,16 @@ int ck_pages_window_compact(const ck_paged_cache* cache, uint32_t rows, const ui
  * that no sequence keeps and that are not marked in dev_held (u8 [pages], nonzero: not handed out;
  * may be null); they are handed out in ascending order, sequence after sequence.  Sequences may
  * share whole pages; a part-filled page that a sequence goes on in has to be its own, as ck_pages_fork
- * leaves it.  Outputs, ready for a ck_paged_batch: dev_table_out u32 [seqs][stride], dev_len_out
+ * leaves it (status 10).  Outputs, ready for a ck_paged_batch: dev_table_out u32 [seqs][stride], dev_len_out
  * u32 [seqs] (the new positions included), dev_start u32 [seqs + 1]; and for every row its place
  * in the pools, dev_slot i64 [rows] (page number * page + place in the page), and its position,
  * dev_position u32 [rows], -1 and CK_NO_PAGE behind the last row.  dev_status u32 [seqs]: 0; 7
  * (the new length is above stride * page or 2^20 - 1) or 4 (it asks for pages, and those asked for
- * up to it are more than there are free, or for rows, and those are more than `rows`): the sequence
- * gets no rows, and keeps its length and the pages above; 3 (its length is above either bound, or an
+ * up to it are more than there are free, or for rows, and those are more than `rows`) or 10 (the part-filled
+ * page that it would go on in is also named by another kept entry, or marked CK_PAGE_SHARED in dev_held): the
+ * sequence gets no rows, and keeps its length and the pages above; 3 (its length is above either bound, or an
  * entry that it would keep lies outside the pool): its table comes out empty, its length 0.
- * Sequences of status 3 and 7 ask for nothing.  The outputs may not overlap the inputs, the scratch (of
+ * Sequences of status 3, 7 and 10 ask for nothing.  The outputs may not overlap the inputs, the scratch (of
  * ck_pages_work for seqs rows) or the pools.  Limits: seqs <= 65536, stride <= 2^17, rows <= 2^20.
  * Errors: 4 (work_len), 9, 10. */
 int ck_pages_advance(const ck_paged_cache* cache, uint32_t seqs, const uint32_t* dev_len_in,

@@ -260,3 +260,87 @@ def test_attention_after_windowed_forks_and_packing(ck, hd):
         graph.replay()
         assert np.array_equal(out.cpu().numpy(), want) and fork.status.tolist() == [0] * 6
     assert status.tolist() == [-1] * 6
+
+
+# ---------------------------------------------------------------- pages that two sequences would go on in
+
+def plain_owned_advance(lens, table, new, rows, page, pages, view, held):
+    """The step where a part-filled page that a sequence would go on in is named by another kept entry, or
+    shared with a sequence outside the call: it asks for nothing, and its status is 10."""
+    most = min(len(table[0]) * page, 2**20 - 1)
+    names, refused = [], []
+    for n, row in zip(lens, table):
+        mine = [] if n > most else [row[i] for i in kept(n, page, view)]
+        names += mine if all(0 <= w < pages for w in mine) else []
+    for s, (n, row, ask) in enumerate(zip(lens, table, new)):
+        if ask and n % page and n + ask <= most and all(0 <= row[i] < pages for i in kept(n, page, view)):
+            last = row[n // page]
+            if names.count(last) > 1 or held[last] & 2:
+                refused.append(s)
+    asks = [0 if s in refused else ask for s, ask in enumerate(new)]
+    out, lens, starts, slots, positions, status = plain_advance(lens, table, asks, rows, page, pages, view, held)
+    return out, lens, starts, slots, positions, [10 if s in refused else rc for s, rc in enumerate(status)]
+
+
+def check_owned(ck, lens, table, new, rows, page, pages, view=None, held=None):
+    plan = ck.PagePlan(ck.PagedCache.empty(pages, 1, 1, page, 4), len(lens), len(table[0]))
+    marks = np.zeros(pages, np.uint8) if held is None else np.array(held, np.uint8)
+    rc, got = plan.advance(i32(lens), i32(table), i32(new), rows, window=view, held=None if held is None else cuda(marks))
+    assert rc == 0
+    want = plain_owned_advance(lens, table, list(new), rows, page, pages, view, marks)
+    for name, a, b in zip(got._fields, got, want):
+        assert a.tolist() == b, name
+    return got
+
+
+def test_a_part_filled_page_of_two_sequences_is_handed_to_neither(ck):
+    """By hand: slots of one page are never given to two sequences, and the others go on."""
+    table = [[5, 9, -1], [3, 9, -1], [2, 4, -1], [9, 6, -1], [7, 7, -1], [8, 10, -1]]
+    got = check_owned(ck, [10, 12, 11, 5, 9, 16], table, [2, 1, 1, 3, 1, 1], 9, 8, 16)
+    assert got.status.tolist() == [10, 10, 0, 10, 10, 0] and got.lens.tolist() == [10, 12, 12, 5, 9, 17]
+    assert got.slots.tolist() == [35, 0] + [-1] * 7 and got.table.tolist()[0] == [5, 9, -1]
+    # one of the two stands still; one holds the page whole; one no longer sees it
+    for lens, new, view in (([10, 12], [0, 1], None), ([16, 12], [1, 1], None), ([17, 12], [1, 1], ck.Window(0, 2))):
+        got = check_owned(ck, lens, [[5, 9, 4], [3, 9, -1]], new, 9, 8, 16, view)
+        assert got.status.tolist() == [0, 0 if view else 10]
+    # marks: a page that is not handed out, and one that a sequence outside the call has
+    for mark, status in ((1, 0), (2, 10), (3, 10)):
+        held = np.zeros(16, np.uint8)
+        held[[9, 5]] = mark
+        got = check_owned(ck, [10, 8], [[5, 9, 4], [5, -1, -1]], [7, 1], 9, 8, 16, None, held)
+        assert got.status.tolist() == [status, 0]
+
+
+@pytest.mark.parametrize("seqs,stride,pages,view", [
+    (3, 4, 30, None), (20, 6, 200, (3, 9)), (60, 40, 4000, None), (300, 130, 60000, (9, 500)), (2050, 20, 70000, (2, 40)),
+    (40, 9, 917504, None), (40, 9, 917505, (0, 30)), (700, 800, 600000, (20, 3000))])
+def test_pages_named_twice_at_random(ck, seqs, stride, pages, view):
+    """Entries of other sequences in some places, whole pages and part-filled ones, in one block, in
+    a cluster and over the GPU."""
+    rng = np.random.default_rng(seqs + stride)
+    view = view and ck.Window(*view)
+    for turn in range(3):
+        lens = rng.integers(0, 8 * stride - 8, seqs)
+        table = rng.permutation(pages)[:seqs * stride].reshape(seqs, stride).astype(np.int64)
+        for s in rng.choice(seqs, max(1, seqs // 3)):  # the last page, or any, of another
+            other, i = int(rng.integers(seqs)), int(rng.integers(stride))
+            table[s, lens[s] // 8 if turn != 1 else i] = table[other, lens[other] // 8 if turn else i]
+        held = np.where(rng.random(pages) < 0.05, rng.integers(1, 4, pages), 0) if turn else None
+        new = rng.integers(0, 4, seqs)
+        got = check_owned(ck, lens.tolist(), table.tolist(), new.tolist(), 4 * seqs, 8, pages, view, held)
+        if turn != 1 and seqs > 3:
+            assert 10 in got.status.tolist() and 0 in got.status.tolist()
+
+
+def test_what_a_fork_leaves_goes_on(ck):
+    """Every row of a fork has its part-filled page to itself, also where the parent lives on outside."""
+    cache = ck.PagedCache.empty(64, 1, 1, 8, 4)
+    plan = ck.PagePlan(cache, 6, 6)
+    table, held = [[40, 41, 42, -1, -1, -1], [50, 51, -1, -1, -1, -1]], np.zeros(64, np.uint8)
+    held[[40, 41, 42]] = 3
+    rc, fork = plan.fork(i32([0, 0, 1, 1, 0, 1]), i32([21, 11]), i32(table), i32([0] * 6), held=cuda(held))
+    assert rc == 0 and fork.status.tolist() == [0] * 6
+    rc, got = plan.advance(fork.lens, fork.table, i32([1, 2, 3, 1, 9, 1]), 32, held=cuda(held))
+    assert rc == 0 and got.status.tolist() == [0] * 6
+    slots = got.slots.tolist()[:17]
+    assert len(set(slots)) == 17 and not {s // 8 for s in slots} & {40, 41, 42}
