@@ -107,6 +107,7 @@ def lib() -> ctypes.CDLL:
             "ck_host_log_sum": ([u64], i64),
             "ck_host_sample_place": ([u32, u32], u32),
             "ck_host_attention_plan": ([vp, vp, u32, u32, u32, vp, vp, vp], ctypes.c_int),
+            "ck_host_window_attention_plan": ([vp, vp, u32, vp, u32, u32, vp, vp, vp], ctypes.c_int),
             "ck_turn_paged_work": ([vp, vp, vp, vp], ctypes.c_int),
             "ck_turn_paged": ([vp, vp, vp, vp, vp, sz, vp, sz, vp], ctypes.c_int),
             "ck_turn_paged_window_work": ([vp, vp, vp, vp, vp], ctypes.c_int),

@@ -232,17 +232,24 @@ int ck_paged_attention_work(const ck_paged_cache* cache, const ck_paged_batch* b
   return ck_paged_window_attention_work(cache, batch, heads, nullptr, out);
 }
 
-int ck_host_attention_plan(const ck_paged_cache* cache, const ck_paged_batch* batch, uint32_t heads, uint32_t sms,
-                           uint32_t smem, const int32_t* clusters, uint32_t* kernel, size_t* work) {
-  if (!clusters || !kernel || !work || sms < 1 || sms > 65536 || smem > (1u << 20) || !work_args_ok(cache, batch, heads))
+int ck_host_window_attention_plan(const ck_paged_cache* cache, const ck_paged_batch* batch, uint32_t heads,
+                                  const ck_window* window, uint32_t sms, uint32_t smem, const int32_t* clusters,
+                                  uint32_t* kernel, size_t* work) {
+  if (!clusters || !kernel || !work || sms < 1 || sms > 65536 || smem > (1u << 20) ||
+      !work_args_ok(cache, batch, heads) || (window && window->window == 0))
     return CK_INVALID_ARGUMENT;
   const DeviceFacts f = {0, (int)sms, (int)smem};
-  const AttentionPlan plan = attention_plan(*cache, *batch, heads, nullptr, f, [&](int32_t* out) {
+  const AttentionPlan plan = attention_plan(*cache, *batch, heads, window, f, [&](int32_t* out) {
     std::copy(clusters, clusters + kTileClusters, out);
   });
   *kernel = plan.few.use ? 0 : plan.tiles.use ? 1 : 2;
   *work = plan.work;
   return CK_OK;
+}
+
+int ck_host_attention_plan(const ck_paged_cache* cache, const ck_paged_batch* batch, uint32_t heads, uint32_t sms,
+                           uint32_t smem, const int32_t* clusters, uint32_t* kernel, size_t* work) {
+  return ck_host_window_attention_plan(cache, batch, heads, nullptr, sms, smem, clusters, kernel, work);
 }
 
 int ck_paged_window_attention(const ck_paged_cache* cache, uint32_t layer, const ck_paged_batch* batch,

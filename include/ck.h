@@ -625,6 +625,10 @@ uint64_t ck_host_probability(uint64_t e, uint64_t z);
  * for tiles, 2 for single rows, *work the scratch in bytes.  Errors: 10. */
 int ck_host_attention_plan(const ck_paged_cache* cache, const ck_paged_batch* batch, uint32_t heads, uint32_t sms,
                            uint32_t smem, const int32_t* clusters, uint32_t* kernel, size_t* work);
+/* And ck_paged_window_attention.  Errors: 10. */
+int ck_host_window_attention_plan(const ck_paged_cache* cache, const ck_paged_batch* batch, uint32_t heads,
+                                  const ck_window* window, uint32_t sms, uint32_t smem, const int32_t* clusters,
+                                  uint32_t* kernel, size_t* work);
 
 /* Library version string. */
 const char* ck_version(void);

@@ -150,3 +150,80 @@ def test_wrong_packings_of_streams_are_refused(ck, bad):
     if bad == dict(window="empty"):
         bad = dict(window=window(ck, 4, 0))
     assert call(ck, "ck_pages_window_compact", args, **bad) == (4 if "work_len" in bad else 10)
+
+
+CLUSTERS = (304, 152, 76, 38)
+
+
+def window_plan(ck, view, seqs, new, length, heads, kv_heads, hd, page=16, rows=None):
+    """The kernel (0 a few queries, 1 tiles, 2 single rows) and the scratch of a call with a window (None:
+    without) on a device of 152 multiprocessors."""
+    kernel, work = ctypes.c_uint32(), ctypes.c_size_t()
+    c = cache(ck, kv_heads=kv_heads, page=page, head_dim=hd)
+    b = batch(ck, seqs=seqs, rows=rows or seqs * new, stride=2**17, max_new=new, max_len=length)
+    w = None if view is None else ctypes.byref(window(ck, *view))
+    rc = ck.lib().ck_host_window_attention_plan(ctypes.byref(c), ctypes.byref(b), heads, w, 152, 232448,
+                                                (ctypes.c_int32 * 4)(*CLUSTERS), ctypes.byref(kernel), ctypes.byref(work))
+    assert rc == 0
+    return kernel.value, work.value
+
+
+PLANS = [(1, 1, 8192, 32, 32, 64), (64, 1, 8192, 32, 8, 32), (2, 201, 2047, 32, 32, 128), (1, 256, 7936, 32, 32, 64),
+         (1, 2048, 8192, 32, 32, 32), (8, 512, 32768, 32, 8, 16), (4096, 1, 32768, 32, 32, 32), (3, 40, 900, 8, 2, 8),
+         (1, 1, 130001, 4, 1, 4)]
+
+
+@pytest.mark.parametrize("shape", PLANS, ids=str)
+def test_a_window_that_holds_everything_plans_as_the_whole_cache(ck, shape):
+    length = shape[2]
+    whole = window_plan(ck, None, *shape)
+    for view in ((0, length), (length, 1), (2**32 - 1, 2**32 - 1), (7, 2**32 - 1)):
+        assert window_plan(ck, view, *shape) == whole
+
+
+@pytest.mark.parametrize("seqs,new,length,heads,kv,hd", PLANS)
+@pytest.mark.parametrize("sinks,size", [(0, 1), (4, 100), (5, 511), (70, 700), (4, 4000), (0, 30000), (9, 120000)])
+def test_the_scratch_of_a_window_holds_the_places_that_are_seen(ck, seqs, new, length, heads, kv, hd, sinks, size):
+    """A few queries: none, or the scores of every query's places, up to 2 GB of them at a time.  Tiles: the
+    scores of 128 rows' places and the sums of every cluster, of one of the sizes.  Single rows: a row's places."""
+    kernel, work = window_plan(ck, (sinks, size), seqs, new, length, heads, kv, hd)
+    group = heads // kv
+    places = min(length, sinks + size)
+    if kernel == 0:
+        assert 256 <= work <= 2**31
+        scores = 8 * seqs * heads * new * places
+        assert work == 256 or work >= min(scores, 2**30)
+        # 227 KB of shared memory hold no more than this of up to four queries, of sixteen blocks
+        if 8 * places * min(4, new * group) > 16 * 232448:
+            assert work > 256
+    elif kernel == 1:
+        tiles = seqs * kv * -(-new * group // 128)
+        places = min(length, sinks + size + min(new - 1, 127 // group))
+        sizes = [min(tiles, n) * (4 * 128 * places + 8 * 128 * hd * 2**i) for i, n in enumerate(CLUSTERS)]
+        assert hd >= 64 and work >= min(sizes)
+    else:
+        assert work >= 8 * places
+    # a window takes no more than the whole cache does through the same kernel
+    other, most = window_plan(ck, None, seqs, new, length, heads, kv, hd)
+    if kernel == other == 0 and work > 256 and most > 256:
+        assert work <= max(most, 2**31)
+
+
+def test_windows_whose_scores_take_several_launches(ck):
+    """Two gigabytes at a time where all would be more; single rows where the launches would be too many."""
+    for shape in ((2, 300, 20500, 32, 8, 4), (1, 500, 20500, 32, 8, 4)):
+        kernel, work = window_plan(ck, (3, 19999), *shape)
+        seqs, new, _, heads = shape[:4]
+        assert kernel == 0 and 2**30 < work <= 2**31 < 8 * seqs * heads * new * 20000
+    kernel, work = window_plan(ck, (0, 2**19), 65535, 1000, 2**20 - 1, 32, 32, 32, page=256, rows=70000)
+    assert kernel == 2 and 8 * 2**19 <= work <= 4 * 152 * 8 * (2**19 + 16)
+
+
+def test_wrong_arguments_of_a_window_plan_are_refused(ck):
+    kernel, work, n = ctypes.c_uint32(), ctypes.c_size_t(), (ctypes.c_int32 * 4)(1, 1, 1, 1)
+    good = dict(cache=cache(ck), batch=batch(ck), heads=4, window=window(ck), sms=152, smem=232448, clusters=n,
+                kernel=ctypes.byref(kernel), work=ctypes.byref(work))
+    assert call(ck, "ck_host_window_attention_plan", good) == 0
+    for bad in (dict(cache=None), dict(batch=None), dict(heads=3), dict(sms=0), dict(smem=2**21), dict(clusters=None),
+                dict(kernel=None), dict(work=None), dict(window=window(ck, 4, 0))):
+        assert call(ck, "ck_host_window_attention_plan", good, **bad) == 10
