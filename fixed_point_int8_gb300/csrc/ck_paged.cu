@@ -722,7 +722,7 @@ __global__ void __launch_bounds__(kTableThreads) k_advance_fill(const AdvancePar
 // All of it in one launch, by a cluster of blocks or one: the steps are separated by the cluster's barriers
 // (which order what its blocks write to global memory), the second is the first block's.  Every block marks
 // pages in its own shared memory (131,000 atomics on L2 from eight SMs take 17 us).  The chain of loads and
-// sums bounds it: 4.8 us for 4 sequences, 14 for 64 with 512 table entries each, 25 for 2,048 with 128, of which the
+// sums bounds it: 5 us for 4 sequences, 14 for 64 with 512 table entries each, 25 for 2,048 with 128, of which the
 // marks for parts take 0.3, 1 and 3 (waiting for what every entry's atomic returns took 5).
 constexpr uint32_t kAdvanceBlocks = 8;
 __global__ void __launch_bounds__(kPlanThreads) k_advance(const AdvanceParams p, uint32_t blocks) {
@@ -821,8 +821,11 @@ bool table_work_alone(uint32_t rows, uint32_t stride, uint32_t pages) {
   return (uint64_t)rows * ((stride + 31) / 32) <= 1024 && pages <= 65536;
 }
 
-// One cluster does all of a step of up to 2 MB of tables (measured) and as many pages as two marks each in shared
-// memory allow.
+// One cluster does all of a step of up to 2 MB of tables and as many pages as two marks each in shared memory
+// allow.  That goes by the time of a call, which the host bounds: 30 us against 35 by a memset and three kernels.  On
+// the device, where a captured step is paid, it is 5 against 10 for 4 sequences, 14 and 13 for 64 with 512
+// entries each, 16 and 14 for 512 with 256, but 25 and 15 for 2,048 with 128.  A row is a warp's in either:
+// one of 131,072 entries takes 590 and 550.
 constexpr uint32_t kAdvancePages = 7u << 17;
 bool advance_alone(uint32_t seqs, uint32_t stride, uint32_t pages) {
   return (uint64_t)seqs * stride <= (1u << 19) && pages <= kAdvancePages;

@@ -23,7 +23,8 @@ constexpr int kRowsThreads = 256, kRowsWarps = kRowsThreads / 32;
 // One (row, head) at a time a block, whatever the values and the lengths: the products are
 // 64-bit, the scores of the row lie in the block's part of the scratch.  Every row reads its
 // keys and values again, and 64-bit products bound it: one token over 8,191 positions of 32 heads
-// takes 883 us, 256 rows over 7,936 take 12.9 ms (the other kernels: 28.9 and 358 us).
+// takes 883 us, 256 rows over 7,936 take 13.0 ms (the other kernels: 28.9 and 345 us), with windows of
+// 2,048 and four first positions 3.0 (119 us).
 template <bool WINDOW>
 __global__ void __launch_bounds__(kRowsThreads) k_pattn_rows(const RowsParams f) {
   const PAttnParams& p = f.a;
@@ -147,11 +148,14 @@ __global__ void __launch_bounds__(kRowsThreads) k_pattn_rows(const RowsParams f)
 // Which kernel a call takes.  Head sizes 64 and 128 compare what k_pattn_few and the tensor-core
 // tiles would take, by the launch's bounds: 8 us and 0.9 us a million products of a query's and a
 // key's element, against 30 us and 0.66 ns a tile and position (head size 64) or 34 us and
-// 1.06 ns.  (Measured, few against tiles: head size 64, 32 heads: 32 rows over 200 positions 21 and
-// 31 us, over 1,000 68 and 51, four sequences of 16 rows over 1,500 144 and 146, of 8 rows 89 and
-// 142; head size 128: 16 rows over 2,000 117 and 98, 128 rows over 128 44 and 49, 32 sequences of
-// one row and four heads a key head over 2,000 179 and 494.)  With a window the places that a row, or a tile,
-// sees stand for the length.  k_pattn_rows follows the tiles for those
+// 1.06 ns.  (Measured with cold caches, few against tiles, 32 heads: head size 64: 32 rows over 200 positions 25
+// and 41 us, over 1,000 73 and 61, four sequences of 16 rows over 1,500 160 and 159, of 8 rows 101 and
+// 156; head size 128: 16 rows over 2,000 122 and 96, 32 over 800 103 and 62, 128 over 128 50 and 49, 32 sequences of
+// one row and four heads a key head over 2,000 214 and 536.)  With a window the places that a row, or a tile,
+// sees stand for the length.  (With four first positions, head size 64: 16 rows with a window of 2,048 81 and 104
+// us, 32 with 512 60 and 55 (the one pair here that goes the other way), with 1,024 81 and 73, 64 with 128 38 and
+// 41, with 256 50 and 47; head size 128: 16 rows with 512 44 and 55, with 2,048 128 and 108, 32 with 128 27 and 43,
+// with 512 81 and 57, 64 with 128 48 and 45.)  k_pattn_rows follows the tiles for those
 // with values beyond their digits, and takes calls that k_pattn_few's grid or shared memory does
 // not hold.
 struct AttentionPlan {

@@ -163,7 +163,8 @@ __device__ __forceinline__ unsigned long long tail_first(uint32_t b) {
 // not fit 32 bits, and vocabularies above 262,144, are read in every pass.  A block fills an SM, so many rows
 // follow one another in steps that wait (a row of 32,000: loads 10,000 cycles, counts 7,000, sums 4,500, kept
 // weights 5,000, draw 2,500), and the next row's logits are asked for meanwhile: 512 rows take 49 us by
-// temperature (2.7 TB/s) and 67 with a nucleus and a least probability, 64 rows 18 on the device, one 13.
+// temperature (2.7 TB/s) and 67 with a nucleus and a least probability, 64 rows 18 on the device, one 13.  Rows
+// with masked logits read theirs twice, and those past 32 bits in every pass: 512 take 74 and 89 by temperature.
 // Two rows an SM, with 16-bit places in shared memory and the logits read twice, took 55 and 69 us (304 rows in
 // flight leave L2), two half rows an SM 48 and 72.  Atomics on shared memory bound the counts, a gather from the
 // table the weights.

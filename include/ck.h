@@ -450,8 +450,9 @@ int ck_turn_paged_work(ck_model* m, const ck_paged_cache* cache, const ck_paged_
 int ck_turn_paged(ck_model* m, const ck_paged_cache* cache, const ck_paged_batch* batch, const uint32_t* dev_tokens,
                   int64_t* dev_logits, size_t logits_stride, void* dev_work, size_t work_len, void* stream);
 /* The same with a window for every layer: windows [layers] in host memory, read before the call
- * returns.  Layers may differ; one whose window is longer than max_len sees the whole cache.  Errors: those
- * of ck_turn_paged, and 10 for a window of 0. */
+ * returns.  Layers may differ; one whose window is longer than max_len sees the whole cache.  Positions are
+ * the sequences' own, windows or not, so max_len ends at the model's context here too.  Errors: those of
+ * ck_turn_paged, and 10 for a window of 0. */
 int ck_turn_paged_window_work(ck_model* m, const ck_paged_cache* cache, const ck_paged_batch* batch,
                               const ck_window* windows, size_t* out);
 int ck_turn_paged_window(ck_model* m, const ck_paged_cache* cache, const ck_paged_batch* batch,
